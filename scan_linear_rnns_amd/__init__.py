@@ -14,13 +14,19 @@ Ops (see include/mgs.h for the definitions and their sources on the pages):
   * mgs_givens_scan_fwd / mgs_givens_scan_bwd           same, A_t = sigmoid(s_t) R(theta_t) formed in-kernel
   * mgs_block_matrix_scan_fwd / mgs_block_matrix_scan_bwd   P_t = A_t P_{t-1}
   * mgs_delta_fwd                                       delta rule (DeltaNet), chunked WY forward
+Layer operators (layers.py; include/mgs_layers.h for the definitions):
+  * mgs_linattn_fwd / mgs_linattn_bwd / mgs_linattn_step    linear attention with a decay per head
+  * mgs_rmsnorm_fwd / mgs_rmsnorm_fwd_fp8 / mgs_rmsnorm_bwd root-mean-square norm with the residual's addition
+  * mgs_clip_norm                                       global gradient norm, and clipping by it
 """
 from __future__ import annotations
 
 import ctypes
 
 from . import _lib
+from . import layers
 from ._lib import MgsError, check, declared_functions, load, status_string  # noqa: F401
+from .layers import *  # noqa: F401,F403
 
 __all__ = [
     "MgsError", "load", "workspace", "mgs_workspace_check", "mgs_workspace_set_waits",
@@ -31,7 +37,7 @@ __all__ = [
     "mgs_givens_scan_workspace_size", "mgs_givens_scan_fwd", "mgs_givens_scan_bwd",
     "mgs_block_matrix_scan_workspace_size", "mgs_block_matrix_scan_fwd", "mgs_block_matrix_scan_bwd",
     "mgs_delta_workspace_size", "mgs_delta_fwd",
-]
+] + layers.__all__
 
 
 def _ptr(t):

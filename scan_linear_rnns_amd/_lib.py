@@ -13,11 +13,25 @@ import re
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("MGS_LIBRARY", os.path.join(HERE, "libmgs.so"))
 HEADER = os.path.join(os.path.dirname(HERE), "include", "mgs.h")
+LAYERS_HEADER = os.path.join(os.path.dirname(HERE), "include", "mgs_layers.h")
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _INT = ctypes.c_int
+_F32 = ctypes.c_float
+
+
+class LinattnDesc(ctypes.Structure):
+    """mgs_linattn_desc of include/mgs_layers.h."""
+    _fields_ = [(n, _I64) for n in ("B", "T", "H", "Hk", "dk", "dv")] + [
+        ("dtype", _INT), ("decay_per_head", _INT), ("scale", _F32)] + [
+        (n, _I64 * 3) for n in ("q_stride", "k_stride", "v_stride", "do_stride", "g_stride")]
+
+
+_DESC = ctypes.POINTER(LinattnDesc)
+_PP = ctypes.POINTER(_P)
+_I64P = ctypes.POINTER(_I64)
 
 SIGNATURES = {
     "mgs_version": ([], _INT),
@@ -47,6 +61,17 @@ SIGNATURES = {
     "mgs_block_matrix_scan_bwd": ([_P, _P, _P, _I64, _I64, _I64, _I64, _P, _SZ, _INT, _P], _INT),
     "mgs_delta_workspace_size": ([_I64, _I64, _I64, ctypes.POINTER(_SZ)], _INT),
     "mgs_delta_fwd": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P], _INT),
+    # include/mgs_layers.h
+    "mgs_linattn_workspace_size": ([_DESC, _INT, ctypes.POINTER(_SZ)], _INT),
+    "mgs_linattn_fwd": ([_DESC] + [_P] * 8 + [_P, _SZ, _P], _INT),
+    "mgs_linattn_bwd": ([_DESC] + [_P] * 13 + [_P, _SZ, _P], _INT),
+    "mgs_linattn_step": ([_DESC] + [_P] * 5 + [_I64, _P, _P, _P], _INT),
+    "mgs_rmsnorm_fwd": ([_P] * 6 + [_I64] * 4 + [_F32, _INT, _P], _INT),
+    "mgs_rmsnorm_fwd_fp8": ([_P] * 6 + [_I64] * 4 + [_F32, _I64, _INT, _P], _INT),
+    "mgs_rmsnorm_workspace_size": ([_I64, _I64, ctypes.POINTER(_SZ)], _INT),
+    "mgs_rmsnorm_bwd": ([_P] * 7 + [_I64, _I64, _INT, _P, _SZ, _P], _INT),
+    "mgs_clip_norm_workspace_size": ([_I64, _I64P, ctypes.POINTER(_SZ)], _INT),
+    "mgs_clip_norm": ([_I64, _PP, _PP, _I64P, ctypes.POINTER(_INT), _F32, _P, _P, _SZ, _P], _INT),
 }
 
 _lib = None
@@ -86,8 +111,8 @@ def check(status: int, where: str) -> None:
         raise MgsError(status, where)
 
 
-def declared_functions():
-    """Names of every function declared in include/mgs.h."""
-    text = open(HEADER).read()
+def declared_functions(header=HEADER):
+    """Names of every function declared in a header (include/mgs.h by default)."""
+    text = open(header).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     return sorted(set(re.findall(r"\b(mgs_[a-z0-9_]+)\s*\(", text)))

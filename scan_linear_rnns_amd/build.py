@@ -23,7 +23,11 @@ OBJ_DIR = os.path.join(HERE, "_build")   # object files of the last build (the s
 SOURCES = [("mgs_api.cpp", "mgs_api", ()),
            ("elem_scan.hip", "elem_scan", ()),
            ("block_scan.hip", "block_scan", ()),
-           ("delta_scan.hip", "delta_scan", ())] + [
+           ("delta_scan.hip", "delta_scan", ()),
+           ("layers_api.cpp", "layers_api", ()),
+           ("linattn.hip", "linattn", ()),
+           ("rmsnorm.hip", "rmsnorm", ()),
+           ("clip_norm.hip", "clip_norm", ())] + [
           ("block_scan_k.hip", f"block_scan_k{k}", (f"-DMGS_ROWS_K={k}",)) for k in (1, 2, 4, 16)]
 JOBS = int(os.environ.get("MGS_BUILD_JOBS", "8"))
 ARCH = os.environ.get("MGS_OFFLOAD_ARCH", "gfx950")

@@ -1,0 +1,210 @@
+// clip_norm.hip -- the global norm of many tensors, and clipping by it (gfx950).
+//
+//     norm = sqrt(sum_i sum g_i^2),   out_i = in_i min(1, max_norm / (norm + 1e-6))
+//
+// Two passes over the data: one partial sum for each tile of 16384 elements,
+// then the scaling.  Both are bound by HBM; what costs beside that is the
+// number of launches, so a launch covers up to 128 tensors (their addresses
+// and sizes travel in its arguments, nothing is copied to the device).  Squares
+// are added in fp32 over the 8 elements of one access and in fp64 beyond, in
+// an order that depends on the sizes alone.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "device.hpp"
+#include "layers.hpp"
+
+namespace mgs {
+namespace {
+
+typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
+typedef float f8v __attribute__((ext_vector_type(8), aligned(16)));
+
+constexpr int kTile = static_cast<int>(kClipTile);
+// Up to this many partials every workgroup of the scaling adds them up itself;
+// beyond, one workgroup does it first, in a launch of its own.
+constexpr int64_t kClipFew = 1024;
+
+struct ClipTable {
+    const void *in[kClipTensors];
+    void *out[kClipTensors];
+    int64_t size[kClipTensors];
+    int first[kClipTensors];   // first tile of each tensor, in this launch
+    uint8_t bf16[kClipTensors], vec[kClipTensors];
+    int n;
+    int64_t base;              // this launch's first tile among all
+};
+
+__device__ __forceinline__ int tensor_of(const ClipTable &t, int tile)
+{
+    int lo = 0, hi = t.n - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (t.first[mid] <= tile) lo = mid;
+        else hi = mid - 1;
+    }
+    return lo;
+}
+
+__device__ __forceinline__ double block_sum(double v, double *lds)
+{
+#pragma unroll
+    for (int off = 32; off; off >>= 1) v += __shfl_xor(v, off, 64);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
+__device__ __forceinline__ f8v widen(f8v v) { return v; }
+__device__ __forceinline__ f8v widen(bf8v v) { return __builtin_convertvector(v, f8v); }
+
+template <typename T, typename V> __device__ __forceinline__ double tile_squares(const T *p, int n, bool vec)
+{
+    double sum = 0.0;
+    if (vec && n == kTile) {
+#pragma unroll
+        for (int i = 0; i < kTile / 2048; ++i) {
+            const f8v x = widen(*reinterpret_cast<const V *>(p + i * 2048 + threadIdx.x * 8));
+            float s = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s = __builtin_fmaf(x[e], x[e], s);
+            sum += static_cast<double>(s);
+        }
+    } else {
+        for (int i = threadIdx.x; i < n; i += 256) {
+            const float x = static_cast<float>(p[i]);
+            sum += static_cast<double>(x * x);
+        }
+    }
+    return sum;
+}
+
+__global__ void __launch_bounds__(256) squares_kernel(ClipTable t, double *part)
+{
+    __shared__ double lds[4];
+    const int i = tensor_of(t, blockIdx.x);
+    const int64_t at = static_cast<int64_t>(static_cast<int>(blockIdx.x) - t.first[i]) * kTile;
+    const int n = static_cast<int>(min(static_cast<int64_t>(kTile), t.size[i] - at));
+    double s = t.bf16[i] ? tile_squares<__bf16, bf8v>(static_cast<const __bf16 *>(t.in[i]) + at, n, t.vec[i])
+                         : tile_squares<float, f8v>(static_cast<const float *>(t.in[i]) + at, n, t.vec[i]);
+    s = block_sum(s, lds);
+    if (threadIdx.x == 0) part[t.base + blockIdx.x] = s;
+}
+
+// the norm from n partials, in order, by one workgroup
+__device__ __forceinline__ float norm_of(const double *part, int64_t n, double *lds)
+{
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < n; i += 256) s += part[i];
+    return static_cast<float>(sqrt(block_sum(s, lds)));
+}
+
+__global__ void __launch_bounds__(256) norm_kernel(const double *part, int64_t n, float *norm)
+{
+    __shared__ double lds[4];
+    const float v = norm_of(part, n, lds);
+    if (threadIdx.x == 0) *norm = v;
+}
+
+template <typename T, typename V>
+__device__ __forceinline__ void tile_scale(const T *p, T *o, int n, float c, bool vec)
+{
+    if (vec && n == kTile) {
+#pragma unroll
+        for (int i = 0; i < kTile / 2048; ++i) {
+            const int e = i * 2048 + threadIdx.x * 8;
+            *reinterpret_cast<V *>(o + e) = __builtin_convertvector(widen(*reinterpret_cast<const V *>(p + e)) * c, V);
+        }
+    } else {
+        for (int i = threadIdx.x; i < n; i += 256) o[i] = static_cast<T>(static_cast<float>(p[i]) * c);
+    }
+}
+
+// few != 0: the norm is added up here, and workgroup 0 of the first launch writes it
+__global__ void __launch_bounds__(256) scale_kernel(ClipTable t, const double *part, int64_t n_part, float max_norm,
+                                                    float *norm, int few)
+{
+    __shared__ double lds[4];
+    float v;
+    if (few) {
+        v = norm_of(part, n_part, lds);
+        if (t.base + blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
+    } else {
+        v = *norm;
+    }
+    float c = max_norm / (v + 1e-6f);
+    if (!(c < 1.0f) || !isfinite(v)) c = 1.0f;
+    const int i = tensor_of(t, blockIdx.x);
+    if (c == 1.0f && t.in[i] == t.out[i]) return;
+    const int64_t at = static_cast<int64_t>(static_cast<int>(blockIdx.x) - t.first[i]) * kTile;
+    const int n = static_cast<int>(min(static_cast<int64_t>(kTile), t.size[i] - at));
+    if (t.bf16[i])
+        tile_scale<__bf16, bf8v>(static_cast<const __bf16 *>(t.in[i]) + at, static_cast<__bf16 *>(t.out[i]) + at, n, c, t.vec[i]);
+    else
+        tile_scale<float, f8v>(static_cast<const float *>(t.in[i]) + at, static_cast<float *>(t.out[i]) + at, n, c, t.vec[i]);
+}
+
+// Calls f(table, tiles) for each group of up to kClipTensors non-empty tensors
+// whose tiles fit one grid.
+template <typename F>
+hipError_t each_launch(int64_t n, const void *const *in, void *const *out, const int64_t *sizes, const int *dtypes, F f)
+{
+    ClipTable t{};
+    int64_t base = 0, tiles = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        if (sizes[i] == 0) continue;
+        t.in[t.n] = in[i];
+        t.out[t.n] = out ? out[i] : nullptr;
+        t.size[t.n] = sizes[i];
+        t.first[t.n] = static_cast<int>(tiles);
+        t.bf16[t.n] = dtypes[i] == MGS_BF16;
+        t.vec[t.n] = ((reinterpret_cast<uintptr_t>(in[i]) | reinterpret_cast<uintptr_t>(t.out[t.n])) & 15u) == 0;
+        ++t.n;
+        tiles += (sizes[i] + kTile - 1) / kTile;
+        if (t.n == kClipTensors) {
+            t.base = base;
+            const hipError_t e = f(t, static_cast<unsigned>(tiles));
+            if (e != hipSuccess) return e;
+            base += tiles;
+            tiles = 0;
+            t.n = 0;
+        }
+    }
+    if (t.n == 0) return hipSuccess;
+    t.base = base;
+    return f(t, static_cast<unsigned>(tiles));
+}
+
+}  // namespace
+
+int64_t clip_tiles(int64_t n, const int64_t *sizes)
+{
+    int64_t tiles = 0;
+    for (int64_t i = 0; i < n; ++i) tiles += (sizes[i] + kTile - 1) / kTile;
+    return tiles;
+}
+
+hipError_t launch_clip_norm(int64_t n, const void *const *in, void *const *out, const int64_t *sizes,
+                            const int *dtypes, float max_norm, float *norm, void *ws, int64_t tiles, hipStream_t s)
+{
+    double *part = static_cast<double *>(ws);
+    hipError_t e = each_launch(n, in, nullptr, sizes, dtypes, [&](const ClipTable &t, unsigned grid) {
+        hipLaunchKernelGGL(squares_kernel, dim3(grid), dim3(256), 0, s, t, part);
+        return hipGetLastError();
+    });
+    if (e != hipSuccess) return e;
+    const int few = out && tiles > 0 && tiles <= kClipFew;
+    if (!few) {
+        hipLaunchKernelGGL(norm_kernel, dim3(1), dim3(256), 0, s, part, tiles, norm);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (!out) return hipSuccess;
+    return each_launch(n, in, out, sizes, dtypes, [&](const ClipTable &t, unsigned grid) {
+        hipLaunchKernelGGL(scale_kernel, dim3(grid), dim3(256), 0, s, t, part, tiles, max_norm, norm, few);
+        return hipGetLastError();
+    });
+}
+
+}  // namespace mgs

@@ -1,0 +1,1106 @@
+// linattn.hip -- linear attention with a decay for each head (gfx950).
+//
+//     S_t = a_t S_{t-1} + v_t k_t^T,   o_t = s S_t q_t,   a_t = exp(g_t),
+// S (dv x dk) per sequence and head.  Within a chunk of C = 64 steps entered
+// with state S, and G_i the sum of the chunk's g up to step i,
+//     o_i = s [ e^{G_i} S q_i + sum_{j<=i} e^{G_i - G_j} (q_i . k_j) v_j ],
+//     S  <- e^{G_C} S + sum_j e^{G_C - G_j} v_j k_j^T:
+// matrix products over the chunk.  All exponents are differences of sums of
+// the same chunk, kept in base 2 as two floats (a double rounded to head and
+// tail), so a decay is good to an ulp wherever it counts however long the
+// chunk's sums grow, and e^{-inf} (a cleared state) is an exact zero.
+//
+// The three gradients are the same walk with other operands.  With do in the
+// query's place, v in the key's and k in the value's, the walk's output is dq
+// (its state is S transposed).  Backwards in time, with each step's decay
+// applied one step later, (k; q, do) gives dv from the state
+// R_t = a_{t+1} D_{t+1} (D = dL/dS) and (v; do, q) gives dk from R transposed.
+// One kernel serves all four; the three gradient walks go in one launch.
+//
+// Along the steps a sequence is cut into segments when there are too few
+// (sequence, head) pairs to fill the chip: a first pass forms each segment's
+// own contribution to the state, a second chains them (elementwise), and the
+// walks start from the chained states.
+//
+// The gradient of g: with x_t = q_t . dq_t and y_t = k_t . dk_t, scaling all
+// decays from step t on shows
+//     dg_t = sum_{s=t}^{e} (x_s - y_s) + <R_e, S_e>
+// for any e >= t.  e is the end of t's segment (at most 512 steps): rounding
+// in the sum grows with its length.
+//
+// MFMA layout: lane l supplies row (or column) l % 16 of an operand; its
+// elements of a 16-wide reduction block are 4 (l / 16) .. + 3, and register r
+// of a result is row 4 (l / 16) + r, column l % 16.  A result tile is thus an
+// operand of the next product as it stands.  bf16 takes two blocks per
+// v_mfma_f32_16x16x32_bf16, fp32 four v_mfma_f32_16x16x4f32 per block.
+// Where an fp32 value (a decayed score, a state, a weighted value) meets bf16
+// inputs it is split into three bf16 terms, head, middle and tail, which hold
+// its 24 bits: the states and dg keep fp32 accuracy.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "device.hpp"
+#include "layers.hpp"
+
+namespace mgs {
+namespace {
+
+constexpr int kC = kAttnChunk;
+constexpr int kThreads = 256;
+constexpr float kLog2e = 1.44269504088896340736f;
+
+typedef float f4v __attribute__((ext_vector_type(4)));
+typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef short s4v __attribute__((ext_vector_type(4)));
+
+template <typename T> struct Num;
+
+template <> struct Num<float> {
+    using Frag = f4v;                    // 4 elements of a reduction block
+    static constexpr int NS = 1;         // terms an fp32 value is split into
+    static constexpr int PAD = 4;        // elements between LDS rows, 16 bytes
+    struct Vec8 { f4v a, b; };
+};
+template <> struct Num<__bf16> {
+    using Frag = bf4;
+    static constexpr int NS = 3;
+    static constexpr int PAD = 8;
+    struct Vec8 { bf8 a; };
+};
+
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__bf16 x) { return static_cast<float>(x); }
+
+// reduction blocks 2m, 2m + 1 of D += A B
+__device__ __forceinline__ f4v mma2(f4v a0, f4v a1, f4v b0, f4v b1, f4v c)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a0[j], b0[j], c, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a1[j], b1[j], c, 0, 0, 0);
+    return c;
+}
+
+__device__ __forceinline__ f4v mma2(bf4 a0, bf4 a1, bf4 b0, bf4 b1, f4v c)
+{
+    const bf8 a = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
+    const bf8 b = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// an fp32 fragment as NS fragments of T that sum to it
+__device__ __forceinline__ void split(f4v x, f4v (&out)[1]) { out[0] = x; }
+
+__device__ __forceinline__ void split(f4v x, bf4 (&out)[3])
+{
+    out[0] = __builtin_convertvector(x, bf4);
+    x -= __builtin_convertvector(out[0], f4v);
+    out[1] = __builtin_convertvector(x, bf4);
+    x -= __builtin_convertvector(out[1], f4v);
+    out[2] = __builtin_convertvector(x, bf4);
+}
+
+// 4 contiguous elements in LDS (aligned to the fragment)
+template <typename T> __device__ __forceinline__ typename Num<T>::Frag frag(const T *p)
+{
+    return *reinterpret_cast<const typename Num<T>::Frag *>(p);
+}
+
+// The fragment of a column: elements (row0 + 4 lq + r, col0 + li), r = 0..3, of
+// row-major LDS.  For 16-bit elements one transposing read: each of 16 lanes
+// addresses 4 elements of a row, and lane i gets column i of the 4 x 16 block.
+template <int LD> __device__ __forceinline__ f4v frag_t(const float *m, int row0, int col0, int li, int lq)
+{
+    const float *p = m + (row0 + 4 * lq) * LD + col0 + li;
+    return f4v{p[0], p[LD], p[2 * LD], p[3 * LD]};
+}
+
+template <int LD> __device__ __forceinline__ bf4 frag_t(const __bf16 *m, int row0, int col0, int li, int lq)
+{
+    typedef __attribute__((address_space(3))) s4v *lds_ptr;
+    const __bf16 *p = m + (row0 + 4 * lq + (li >> 2)) * LD + col0 + 4 * (li & 3);
+    const s4v r = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p));
+    return __builtin_bit_cast(bf4, r);
+}
+
+// ------------------------------------------------------------------- walks
+
+struct Operand {
+    const void *p;           // element (b, t, h, c) at b sb + t st + (h / div) sh + c
+    int64_t sb, st, sh;
+    int div, cols;
+};
+
+struct Role {
+    Operand q, k, v;
+    Operand dot;             // dots of the output rows with this, or p == NULL
+    void *out;               // (B,T,H,v.cols) dense: T, or fp32 with out_f32
+    float *xdot;             // (B,H,T)
+    const float *state;      // entering states, or NULL (zeros): + bh st_bh + seg st_seg
+    float *final;            // state after the walk (+ bh * sc-by-sk elements), or NULL
+    float *local;            // state-only pass: segment contributions, like `state`
+    int64_t st_bh, st_seg;
+    int sc, sk;              // element strides of the state's output column and reduction index
+    float intra, inter, src; // factors of the chunk's own part, the state's part, the sources
+    int rev, out_f32;
+};
+
+struct WalkArgs {
+    Role role[3];
+    const float *g;
+    int64_t gb, gt, gh;
+    const int32_t *lengths;
+    float *dec;              // state-only pass: decay over each segment (bh, seg), by the forward role
+    int64_t items;           // (b, h, segment) triples
+    int nRoles, T, H, nC, nSeg, segLen, vec;
+};
+
+template <typename T> __device__ __forceinline__ void zero8(typename Num<T>::Vec8 &x);
+template <> __device__ __forceinline__ void zero8<float>(Num<float>::Vec8 &x) { x.a = x.b = f4v{0, 0, 0, 0}; }
+template <> __device__ __forceinline__ void zero8<__bf16>(Num<__bf16>::Vec8 &x)
+{
+    x.a = __builtin_bit_cast(bf8, f4v{0, 0, 0, 0});
+}
+
+// elements c .. c + 7 of a row of `cols`, zeros past its end; vec: 16-byte
+// accesses are aligned and cols is a multiple of 8
+template <typename T>
+__device__ __forceinline__ typename Num<T>::Vec8 load8(const T *row, int c, int cols, bool vec)
+{
+    typename Num<T>::Vec8 x;
+    if (vec) {
+        zero8<T>(x);
+        if (c < cols) x = *reinterpret_cast<const typename Num<T>::Vec8 *>(row + c);
+    } else {
+        T e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = c + i < cols ? row[c + i] : static_cast<T>(0.0f);
+        __builtin_memcpy(&x, e, sizeof(x));
+    }
+    return x;
+}
+
+// One 64-row tile on its way from global memory to LDS: DIM columns, 8 per
+// thread and turn.  Row r is step t0 + r, or t1 - 1 - r backwards; rows past
+// the chunk or the sequence's length are zeros and are not read.
+template <typename T, int DIM> struct Stage {
+    static constexpr int LD = DIM + Num<T>::PAD;
+    static constexpr int PER = kC * DIM / 8 / kThreads;
+    typename Num<T>::Vec8 x[PER];
+
+    __device__ __forceinline__ void load(const Operand &o, int64_t b, int h, int t0, int t1, int len, int rev, bool vec)
+    {
+        const T *base = static_cast<const T *>(o.p) + b * o.sb + (h / o.div) * o.sh;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int idx = threadIdx.x + kThreads * i;
+            const int r = idx / (DIM / 8), c = (idx % (DIM / 8)) * 8;
+            const int t = rev ? t1 - 1 - r : t0 + r;
+            zero8<T>(x[i]);
+            if (r < t1 - t0 && t < len) x[i] = load8<T>(base + t * o.st, c, o.cols, vec);
+        }
+    }
+    __device__ __forceinline__ void store(T *lds) const
+    {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const int idx = threadIdx.x + kThreads * i;
+            *reinterpret_cast<typename Num<T>::Vec8 *>(lds + (idx / (DIM / 8)) * LD + (idx % (DIM / 8)) * 8) = x[i];
+        }
+    }
+};
+
+// The chunk's decay sums in base 2, by wave 0, lane = row.  Forward G_r
+// includes row r's own decay, backward (rows in reverse order) it does not.
+// A decay below 2^-20000 clears the state as -inf does (the clamp keeps the
+// differences finite); NaN passes the comparison and propagates.
+struct Decays {
+    float hi[kC], lo[kC];    // G
+    float src[kC];           // factor of source j: e^{total - G_j}, times the role's
+    float row[kC];           // factor of the state's part of row i: e^{G_i}, times the role's
+    float total;             // e^{total}
+    float log2_total;
+};
+
+__device__ __forceinline__ void chunk_decays(const WalkArgs &a, const Role &ro, int64_t b, int h, int t0, int t1, int len,
+                                             Decays &d)
+{
+    const int r = threadIdx.x;   // < 64
+    const int t = ro.rev ? t1 - 1 - r : t0 + r;
+    double x = 0.0;
+    if (r < t1 - t0 && t < len) {
+        const float gt = a.g[b * a.gb + t * a.gt + h * a.gh];
+        x = static_cast<double>(gt) * 1.4426950408889634074;
+        if (x < -20000.0) x = -20000.0;
+    }
+    double G = x;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const double y = __shfl_up(G, off, 64);
+        if (r >= off) G += y;
+    }
+    const double total = __shfl(G, 63, 64);
+    if (ro.rev) G = __shfl_up(G, 1, 64);
+    if (ro.rev && r == 0) G = 0.0;
+    const float hi = static_cast<float>(G);
+    d.hi[r] = hi;
+    d.lo[r] = static_cast<float>(G - static_cast<double>(hi));
+    d.src[r] = ro.src * __builtin_amdgcn_exp2f(static_cast<float>(total - G));
+    d.row[r] = ro.inter * __builtin_amdgcn_exp2f(hi);
+    if (r == 0) {
+        d.total = __builtin_amdgcn_exp2f(static_cast<float>(total));
+        d.log2_total = static_cast<float>(total);
+    }
+}
+
+// Zeros in place of the non-finite elements of a wave's value fragments (rows
+// 16 jb + 4 lq + r, column li of tile ct), and NaN in the output tiles (row
+// 16 i + li, columns 4 lq + r) from their rows on.
+template <typename T, int NCT>
+__device__ __forceinline__ void drop_non_finite(typename Num<T>::Frag (&vf)[4][NCT], f4v (&O)[4][NCT], int li, int lq)
+{
+#pragma unroll
+    for (int ct = 0; ct < NCT; ++ct) {
+        int first = kC;   // of column li
+#pragma unroll
+        for (int jb = 3; jb >= 0; --jb)
+#pragma unroll
+            for (int r = 3; r >= 0; --r)
+                if (!isfinite(to_f32(vf[jb][ct][r]))) {
+                    first = 16 * jb + 4 * lq + r;
+                    vf[jb][ct][r] = static_cast<T>(0.0f);
+                }
+        first = min(first, __shfl_xor(first, 16, 64));
+        first = min(first, __shfl_xor(first, 32, 64));
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int f = __shfl(first, 4 * lq + r, 64);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (16 * i + li >= f) O[i][ct][r] = __builtin_nanf("");
+        }
+    }
+}
+
+// The ten 16 x 16 score tiles on or below the diagonal, tile = 4 i + j, one per nibble.
+constexpr uint64_t kScoreTiles = 0xFEDCA98540ull;
+
+// KD, VD: the reduction dimension and the output columns, padded.  Each of the
+// 4 waves owns VD / 4 output columns: of the state it keeps S^T tiles
+// (reduction index x column) in accumulators, and it forms the same columns of
+// the output, transposed, so that a lane holds 4 neighbouring columns of a row.
+// The scores are formed once per workgroup and shared through LDS.
+// STATE_ONLY: the walk from a zero state without outputs.
+template <typename T, int KD, int VD, bool STATE_ONLY>
+__global__ void __launch_bounds__(kThreads) walk_kernel(WalkArgs a)
+{
+    using N = Num<T>;
+    using Frag = typename N::Frag;
+    constexpr int NS = N::NS;
+    constexpr int NCT = VD / 64;       // 16-column tiles per wave
+    constexpr int NKB = KD / 16;       // reduction blocks
+    constexpr int LK = KD + N::PAD, LV = VD + N::PAD, LA = kC + N::PAD;
+    __shared__ __align__(16) T sQ[STATE_ONLY ? 8 : kC * LK];
+    __shared__ __align__(16) T sK[kC * LK];
+    __shared__ __align__(16) T sV[kC * LV];
+    __shared__ __align__(16) T sA[STATE_ONLY ? 1 : NS][STATE_ONLY ? 8 : kC * LA];
+    __shared__ __align__(16) Decays sD;
+    __shared__ float sX[STATE_ONLY ? 1 : 4][kC];
+
+    const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int li = lane & 15, lq = lane >> 4;
+    // the roles of 8 neighbouring items run side by side, an item's on one XCD:
+    // they read the same rows
+    const int64_t rest = blockIdx.x >> 3;
+    const int64_t item = (rest / a.nRoles) * 8 + (blockIdx.x & 7);
+    if (item >= a.items) return;
+    const Role &ro = a.role[rest % a.nRoles];
+    const int seg = static_cast<int>(item % a.nSeg);
+    const int64_t bh = item / a.nSeg;
+    const int64_t b = bh / a.H;
+    const int h = static_cast<int>(bh - b * a.H);
+    int len = a.T;
+    if (a.lengths) len = max(0, min(a.T, a.lengths[b]));
+    const int c_lo = seg * a.segLen, c_hi = min(a.nC, c_lo + a.segLen);
+    const bool vec = a.vec != 0;
+
+    const int col0 = wv * (16 * NCT);   // this wave's first column
+    f4v S[NKB][NCT];
+#pragma unroll
+    for (int t = 0; t < NKB; ++t)
+#pragma unroll
+        for (int ct = 0; ct < NCT; ++ct) {
+            S[t][ct] = f4v{0, 0, 0, 0};
+            if (!STATE_ONLY && ro.state) {
+                const float *p = ro.state + bh * ro.st_bh + seg * ro.st_seg;
+                const int c = col0 + 16 * ct + li;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int kk = 16 * t + 4 * lq + r;
+                    if (c < ro.v.cols && kk < ro.k.cols) S[t][ct][r] = p[c * ro.sc + kk * ro.sk];
+                }
+            }
+        }
+    if constexpr (!STATE_ONLY) {   // the tiles above the diagonal stay zero
+#pragma unroll
+        for (int s = 0; s < NS; ++s)
+            for (int i = tid; i < kC * LA; i += kThreads) sA[s][i] = static_cast<T>(0.0f);
+    }
+
+    float seg_log2 = 0.0f;
+    for (int n = 0; n < c_hi - c_lo; ++n) {
+        const int ch = ro.rev ? c_hi - 1 - n : c_lo + n;
+        const int t0 = ch * kC, t1 = min(a.T, t0 + kC);
+        {
+            Stage<T, KD> k;
+            Stage<T, VD> v;
+            k.load(ro.k, b, h, t0, t1, len, ro.rev, vec);
+            v.load(ro.v, b, h, t0, t1, len, ro.rev, vec);
+            if constexpr (!STATE_ONLY) {
+                Stage<T, KD> q;
+                q.load(ro.q, b, h, t0, t1, len, ro.rev, vec);
+                q.store(sQ);
+            }
+            k.store(sK);
+            v.store(sV);
+        }
+        if (wv == 0) chunk_decays(a, ro, b, h, t0, t1, len, sD);
+        __syncthreads();
+
+        if constexpr (!STATE_ONLY) {
+            // scores: tile (i, j) with rows of q as columns, so that a lane holds
+            // 4 neighbouring sources of one row
+#pragma unroll
+            for (int it = 0; it < 3; ++it) {
+                const int slot = wv + 4 * it;
+                if (slot < 10) {
+                    const int tile = static_cast<int>((kScoreTiles >> (4 * slot)) & 15);
+                    const int i = tile >> 2, j = tile & 3;
+                    f4v p = {0, 0, 0, 0};
+#pragma unroll
+                    for (int m = 0; m < NKB / 2; ++m) {
+                        const T *kr = sK + (16 * j + li) * LK + 32 * m + 4 * lq;
+                        const T *qr = sQ + (16 * i + li) * LK + 32 * m + 4 * lq;
+                        p = mma2(frag(kr), frag(kr + 16), frag(qr), frag(qr + 16), p);
+                    }
+                    const int row = 16 * i + li, src = 16 * j + 4 * lq;
+                    const float gh = sD.hi[row], gl = sD.lo[row];
+                    f4v w;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const float e = __builtin_amdgcn_exp2f((gh - sD.hi[src + r]) + (gl - sD.lo[src + r]));
+                        w[r] = src + r <= row ? ro.intra * e * p[r] : 0.0f;
+                    }
+                    Frag ws[NS];
+                    split(w, ws);
+#pragma unroll
+                    for (int s = 0; s < NS; ++s) *reinterpret_cast<Frag *>(&sA[s][row * LA + src]) = ws[s];
+                }
+            }
+            __syncthreads();
+
+            // the state's part of the output, then the chunk's own
+            f4v O[4][NCT];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) O[i][ct] = f4v{0, 0, 0, 0};
+#pragma unroll
+            for (int m = 0; m < NKB / 2; ++m) {
+                Frag s0[NCT][NS], s1[NCT][NS];
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) {
+                    split(S[2 * m][ct], s0[ct]);
+                    split(S[2 * m + 1][ct], s1[ct]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const T *qr = sQ + (16 * i + li) * LK + 32 * m + 4 * lq;
+                    const Frag q0 = frag(qr), q1 = frag(qr + 16);
+#pragma unroll
+                    for (int s = 0; s < NS; ++s)
+#pragma unroll
+                        for (int ct = 0; ct < NCT; ++ct) O[i][ct] = mma2(s0[ct][s], s1[ct][s], q0, q1, O[i][ct]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) O[i][ct] *= sD.row[16 * i + li];
+            Frag vf[4][NCT];
+#pragma unroll
+            for (int jb = 0; jb < 4; ++jb)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) vf[jb][ct] = frag_t<LV>(sV, 16 * jb, col0 + 16 * ct, li, lq);
+            // A product with a zero weight would carry a non-finite value to rows ahead
+            // of its own: such values are taken out, and from their row on their
+            // column is NaN.
+            float probe = 0.0f;
+#pragma unroll
+            for (int jb = 0; jb < 4; ++jb)
+#pragma unroll
+                for (int ct = 0; ct < NCT; ++ct) {
+                    const f4v x = __builtin_convertvector(vf[jb][ct], f4v) * 0.0f;
+                    probe += (x[0] + x[1]) + (x[2] + x[3]);
+                }
+            if (__any(probe != 0.0f)) drop_non_finite<T, NCT>(vf, O, li, lq);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int m = 0; m <= i / 2; ++m)
+#pragma unroll
+                    for (int s = 0; s < NS; ++s) {
+                        const T *ar = &sA[s][(16 * i + li) * LA + 32 * m + 4 * lq];
+                        const Frag a0 = frag(ar), a1 = frag(ar + 16);
+#pragma unroll
+                        for (int ct = 0; ct < NCT; ++ct)
+                            O[i][ct] = mma2(vf[2 * m][ct], vf[2 * m + 1][ct], a0, a1, O[i][ct]);
+                    }
+
+            // rows of the output (zeros past the sequence's length) and their dots
+            const int cols = ro.v.cols;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int r = 16 * i + li;
+                const int t = ro.rev ? t1 - 1 - r : t0 + r;
+                float dot = 0.0f;
+                if (r < t1 - t0) {
+                    const int64_t o0 = ((b * a.T + t) * a.H + h) * cols;
+                    const bool live = t < len;
+#pragma unroll
+                    for (int ct = 0; ct < NCT; ++ct) {
+                        const int c = col0 + 16 * ct + 4 * lq;
+                        const f4v y = live ? O[i][ct] : f4v{0, 0, 0, 0};
+                        if (ro.dot.p && live) {
+                            const T *p = static_cast<const T *>(ro.dot.p) + b * ro.dot.sb + (h / ro.dot.div) * ro.dot.sh +
+                                         t * ro.dot.st;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                if (c + e < cols) dot = __builtin_fmaf(to_f32(p[c + e]), y[e], dot);
+                        }
+                        if (ro.out_f32) {
+                            float *op = static_cast<float *>(ro.out) + o0 + c;
+                            if ((cols & 3) == 0) {
+                                if (c < cols) *reinterpret_cast<f4v *>(op) = y;
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (c + e < cols) op[e] = y[e];
+                            }
+                        } else {
+                            T *op = static_cast<T *>(ro.out) + o0 + c;
+                            const Frag z = __builtin_convertvector(y, Frag);
+                            if (vec) {
+                                if (c < cols) *reinterpret_cast<Frag *>(op) = z;
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 4; ++e)
+                                    if (c + e < cols) op[e] = z[e];
+                            }
+                        }
+                    }
+                }
+                dot += __shfl_xor(dot, 16, 64);
+                dot += __shfl_xor(dot, 32, 64);
+                if (lq == 0) sX[wv][r] = dot;
+            }
+        }
+
+        // S <- e^{total} S + sum over the chunk of weighted sources
+        const float dec = sD.total;
+        Frag vw[4][NCT][NS];
+#pragma unroll
+        for (int jb = 0; jb < 4; ++jb) {
+            const f4v w = *reinterpret_cast<const f4v *>(&sD.src[16 * jb + 4 * lq]);
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                const Frag v = frag_t<LV>(sV, 16 * jb, col0 + 16 * ct, li, lq);
+                split(__builtin_convertvector(v, f4v) * w, vw[jb][ct]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < NKB; ++t) {
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) S[t][ct] *= dec;
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+                const Frag k0 = frag_t<LK>(sK, 32 * m, 16 * t, li, lq), k1 = frag_t<LK>(sK, 32 * m + 16, 16 * t, li, lq);
+#pragma unroll
+                for (int s = 0; s < NS; ++s)
+#pragma unroll
+                    for (int ct = 0; ct < NCT; ++ct)
+                        S[t][ct] = mma2(k0, k1, vw[2 * m][ct][s], vw[2 * m + 1][ct][s], S[t][ct]);
+            }
+        }
+        seg_log2 += sD.log2_total;
+        __syncthreads();
+        if constexpr (!STATE_ONLY) {
+            if (ro.xdot && tid < t1 - t0) {
+                const int t = ro.rev ? t1 - 1 - tid : t0 + tid;
+                ro.xdot[bh * a.T + t] = (sX[0][tid] + sX[1][tid]) + (sX[2][tid] + sX[3][tid]);
+            }
+        }
+    }
+
+    float *fin = STATE_ONLY ? ro.local : ro.final;
+    if (fin) {
+        fin += bh * ro.st_bh + (STATE_ONLY ? seg * ro.st_seg : 0);
+#pragma unroll
+        for (int t = 0; t < NKB; ++t)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                const int c = col0 + 16 * ct + li;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int kk = 16 * t + 4 * lq + r;
+                    if (c < ro.v.cols && kk < ro.k.cols) fin[c * ro.sc + kk * ro.sk] = S[t][ct][r];
+                }
+            }
+    }
+    if (STATE_ONLY && !ro.rev && tid == 0) a.dec[bh * a.nSeg + seg] = __builtin_amdgcn_exp2f(seg_log2);
+}
+
+// ---------------------------------------------------- chaining the segments
+// Forward (blockIdx.y == 0): slot n of S gets the state entering segment n,
+// slot nSeg and ST the last one.  Backward: slot n of R gets the state entering
+// segment n from the future, dS0 the one left at the start.  One thread per
+// state element; 8 segments of loads in flight.
+struct ChainArgs {
+    float *S, *R;
+    const float *dec, *S0, *dST;
+    float *ST, *dS0;
+    int64_t BH;
+    int nSeg, E;             // E = dv dk
+};
+
+__global__ void __launch_bounds__(256) chain_kernel(ChainArgs a)
+{
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (at >= a.BH * a.E) return;
+    const int64_t bh = at / a.E;
+    const int e = static_cast<int>(at - bh * a.E);
+    const bool rev = blockIdx.y != 0;
+    const int stride = rev ? -a.E : a.E;
+    const float *first = rev ? a.dST : a.S0;
+    float s = first ? first[at] : 0.0f;
+    float *p = rev ? a.R + (bh * a.nSeg + a.nSeg - 1) * a.E + e : a.S + bh * (a.nSeg + 1) * a.E + e;
+    const float *dec = a.dec + bh * a.nSeg + (rev ? a.nSeg - 1 : 0);
+    const int dd = rev ? -1 : 1;
+    for (int n0 = 0; n0 < a.nSeg; n0 += 8) {
+        float u[8], w[8];
+        const int m = min(8, a.nSeg - n0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int j = min(i, m - 1);   // past the end: the last one again, unused
+            u[i] = p[static_cast<int64_t>(n0 + j) * stride];
+            w[i] = dec[(n0 + j) * dd];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < m) {
+                p[static_cast<int64_t>(n0 + i) * stride] = s;
+                s = __builtin_fmaf(w[i], s, u[i]);
+            }
+    }
+    if (!rev) {
+        a.S[(bh * (a.nSeg + 1) + a.nSeg) * a.E + e] = s;
+        if (a.ST) a.ST[at] = s;
+    } else if (a.dS0) {
+        a.dS0[at] = s;
+    }
+}
+
+// --------------------------------------------------------------- dg and sums
+// dg of one (sequence, head, segment): the suffix sums of x - y from the
+// segment's end and <R, S> there, in double.  A step whose decay is zero has no
+// gradient (dg = a_t <D_t, S_{t-1}>).
+struct DgArgs {
+    const float *x, *y, *S, *R;   // S: entering states, segment n's end is slot n + 1; R may be NULL
+    const float *g;
+    int64_t gb, gt, gh;
+    const int32_t *lengths;
+    float *dg;                    // (B,T,H), or per-head partials (B,H,nSeg)
+    int64_t s_bh, s_seg, r_bh, r_seg;   // strides of S (from slot 1 on) and R
+    int T, H, nSeg, segLen, E, per_head;
+};
+
+__device__ __forceinline__ double block_sum(double v, double *lds)
+{
+#pragma unroll
+    for (int off = 32; off; off >>= 1) v += __shfl_xor(v, off, 64);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+}
+
+__global__ void __launch_bounds__(256) dg_kernel(DgArgs a)
+{
+    __shared__ double red[4];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int64_t item = blockIdx.x;
+    const int seg = static_cast<int>(item % a.nSeg);
+    const int64_t bh = item / a.nSeg, b = bh / a.H;
+    const int h = static_cast<int>(bh - b * a.H);
+    const int t_lo = seg * a.segLen * kC, t_hi = min(a.T, t_lo + a.segLen * kC);
+    int len = a.T;
+    if (a.lengths) len = max(0, min(a.T, a.lengths[b]));
+
+    double flux = 0.0;
+    if (a.R) {
+        const float *S = a.S + bh * a.s_bh + seg * a.s_seg, *R = a.R + bh * a.r_bh + seg * a.r_seg;
+        for (int e = tid; e < a.E; e += 256) flux += static_cast<double>(S[e]) * static_cast<double>(R[e]);
+    }
+    flux = block_sum(flux, red);
+
+    // 256 steps at a time, the latest first; thread i holds step hi - 1 - i
+    double sum = 0.0;
+    for (int hi = t_hi; hi > t_lo; hi -= 256) {
+        const int t = hi - 1 - tid;
+        double v = 0.0;
+        if (t >= t_lo) v = static_cast<double>(a.x[bh * a.T + t]) - static_cast<double>(a.y[bh * a.T + t]);
+#pragma unroll
+        for (int off = 1; off < 64; off <<= 1) {
+            const double u = __shfl_up(v, off, 64);
+            if (lane >= off) v += u;
+        }
+        __syncthreads();
+        if (lane == 63) red[tid >> 6] = v;
+        __syncthreads();
+        for (int w = 0; w < (tid >> 6); ++w) v += red[w];
+        const double all = (red[0] + red[1]) + (red[2] + red[3]);
+        double val = v + flux;
+        if (t >= t_lo) {
+            if (t >= len) val = 0.0;
+            else if (a.g[b * a.gb + t * a.gt + h * a.gh] < -104.0f) val = 0.0;
+            if (!a.per_head) a.dg[(b * a.T + t) * a.H + h] = static_cast<float>(val);
+            else sum += val;
+        }
+        flux += all;
+    }
+    if (a.per_head) {
+        sum = block_sum(sum, red);
+        if (tid == 0) a.dg[item] = static_cast<float>(sum);
+    }
+}
+
+// dg of a decay per head: the partials of all sequences and segments, in order
+__global__ void __launch_bounds__(256) dg_head_kernel(const float *part, float *dg, int64_t B, int H, int nSeg)
+{
+    __shared__ double red[4];
+    const int h = blockIdx.x;
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < B * nSeg; i += 256) s += part[((i / nSeg) * H + h) * nSeg + i % nSeg];
+    s = block_sum(s, red);
+    if (threadIdx.x == 0) dg[h] = static_cast<float>(s);
+}
+
+// dq, dk of a query/key head: its value heads' fp32 partials (B T,H,d) summed in order
+template <typename T>
+__global__ void __launch_bounds__(256) group_sum_kernel(const float *p0, const float *p1, T *o0, T *o1, int64_t n, int H,
+                                                        int Hk, int d)
+{
+    const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;   // of (B T,Hk,d)
+    if (at >= n) return;
+    const float *p = blockIdx.y ? p1 : p0;
+    const int per = H / Hk;
+    const int64_t row = at / (static_cast<int64_t>(Hk) * d);
+    const int rest = static_cast<int>(at - row * Hk * d), hk = rest / d, c = rest - hk * d;
+    p += (row * H + static_cast<int64_t>(hk) * per) * d + c;
+    float s = 0.0f;
+    for (int i = 0; i < per; ++i) s += p[static_cast<int64_t>(i) * d];
+    (blockIdx.y ? o1 : o0)[at] = static_cast<T>(s);
+}
+
+// -------------------------------------------------------------------- a step
+// One workgroup per (sequence, head, 16 rows of the state), a wave 4 rows: 16
+// lanes a row, each 4 (dk <= 64) or 2 x 4 elements.  The state is read and
+// written once; everything else is small.
+struct StepArgs {
+    const void *q, *k, *v;
+    const float *g;
+    float *S;
+    void *o;
+    const int32_t *slots;
+    int64_t qb, qh, kb, kh, vb, vh, gb, gh;
+    int64_t n_slots;
+    int H, div, dk, dv, tiles, vec;
+    float scale;
+};
+
+template <typename T, int NV>
+__global__ void __launch_bounds__(256) step_kernel(StepArgs a)
+{
+    const int tid = threadIdx.x, li = tid & 15, row = tid >> 4;
+    const int64_t bh = blockIdx.x / a.tiles;
+    const int r = static_cast<int>(blockIdx.x - bh * a.tiles) * 16 + row;
+    const int64_t b = bh / a.H;
+    const int h = static_cast<int>(bh - b * a.H);
+    const int64_t slot = a.slots ? a.slots[b] : b;
+    const bool live = slot >= 0 && slot < a.n_slots;
+    if (r >= a.dv) return;   // whole groups of 16 lanes, which the shuffles below stay within
+    T *o = static_cast<T *>(a.o) + (b * a.H + h) * static_cast<int64_t>(a.dv) + r;
+    if (!live) {
+        if (li == 0) *o = static_cast<T>(0.0f);
+        return;
+    }
+    const T *q = static_cast<const T *>(a.q) + b * a.qb + (h / a.div) * a.qh;
+    const T *k = static_cast<const T *>(a.k) + b * a.kb + (h / a.div) * a.kh;
+    const float v = to_f32(static_cast<const T *>(a.v)[b * a.vb + h * a.vh + r]);
+    const float dec = __builtin_amdgcn_exp2f(a.g[b * a.gb + h * a.gh] * kLog2e);
+    float *S = a.S + ((slot * a.H + h) * static_cast<int64_t>(a.dv) + r) * a.dk;
+    float dot = 0.0f;
+    const bool vec = a.vec != 0;   // 16-byte accesses of the state
+#pragma unroll
+    for (int n = 0; n < NV; ++n) {
+        const int c = 64 * n + 4 * li;
+        float s[4] = {0, 0, 0, 0};
+        if (vec) {
+            if (c < a.dk) {
+                const f4v x = *reinterpret_cast<const f4v *>(S + c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[e] = x[e];
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < a.dk) s[e] = S[c + e];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < a.dk) {
+                s[e] = __builtin_fmaf(v, to_f32(k[c + e]), dec * s[e]);
+                dot = __builtin_fmaf(s[e], to_f32(q[c + e]), dot);
+            }
+        if (vec) {
+            if (c < a.dk) *reinterpret_cast<f4v *>(S + c) = f4v{s[0], s[1], s[2], s[3]};
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (c + e < a.dk) S[c + e] = s[e];
+        }
+    }
+#pragma unroll
+    for (int off = 1; off < 16; off <<= 1) dot += __shfl_xor(dot, off, 64);
+    if (li == 0) *o = static_cast<T>(a.scale * dot);
+}
+
+// --------------------------------------------------------------------- host
+
+bool wide(const void *p, const int64_t *st, int n, size_t size)
+{
+    if (reinterpret_cast<uintptr_t>(p) & 15u) return false;
+    for (int i = 0; i < n; ++i)
+        if ((static_cast<size_t>(st[i]) * size) & 15u) return false;
+    return true;
+}
+
+unsigned walk_grid(int64_t items, int roles)
+{
+    return static_cast<unsigned>((items + 7) / 8 * 8 * roles);
+}
+
+template <typename T, bool STATE_ONLY>
+hipError_t launch_walk(const WalkArgs &a, int kdim, int vdim, hipStream_t s)
+{
+    const dim3 grid(walk_grid(a.items, a.nRoles)), block(kThreads);
+    if (kdim <= 64 && vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 64, STATE_ONLY>), grid, block, 0, s, a);
+    else if (kdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 128, STATE_ONLY>), grid, block, 0, s, a);
+    else if (vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 128, 64, STATE_ONLY>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((walk_kernel<T, 128, 128, STATE_ONLY>), grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+template <bool STATE_ONLY>
+hipError_t launch_walk(int dtype, const WalkArgs &a, int kdim, int vdim, hipStream_t s)
+{
+    return dtype == MGS_BF16 ? launch_walk<__bf16, STATE_ONLY>(a, kdim, vdim, s)
+                             : launch_walk<float, STATE_ONLY>(a, kdim, vdim, s);
+}
+
+size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
+}  // namespace
+
+// Segments: a walk takes one workgroup through its chunks in order, and the
+// chip holds 512 such workgroups (two a CU), so a long sequence of few heads is
+// cut until there are that many.  The backward also bounds a segment to 8
+// chunks, which bounds the rounding of dg's sums.
+AttnGeom attn_geometry(const mgs_linattn_desc &d, bool backward)
+{
+    AttnGeom g{};
+    g.BH = d.B * d.H;
+    g.nC = static_cast<int>((d.T + kC - 1) / kC);
+    const int64_t walks = std::max<int64_t>(1, g.BH * (backward ? 3 : 1));
+    int64_t seg = std::max<int64_t>(1, (512 + walks - 1) / walks);
+    int64_t len = std::max<int64_t>(1, (g.nC + seg - 1) / seg);
+    if (backward) len = std::min<int64_t>(len, 8);
+    g.segLen = static_cast<int>(len);
+    g.nSeg = static_cast<int>(std::max<int64_t>(1, (g.nC + len - 1) / len));
+    g.grouped = backward && d.H != d.Hk;
+    const size_t E = static_cast<size_t>(d.dk) * d.dv * 4, BH = static_cast<size_t>(g.BH);
+    const size_t steps = static_cast<size_t>(d.B) * d.T * d.H;
+    size_t at = 256;
+    auto take = [&](size_t bytes) {
+        const size_t off = at;
+        at += align_up(bytes);
+        return off;
+    };
+    if (g.nSeg > 1) {
+        g.off_S = take(BH * (g.nSeg + 1) * E);
+        if (backward) g.off_R = take(BH * g.nSeg * E);
+        g.off_dec = take(BH * g.nSeg * 4);
+    } else if (backward) {
+        g.off_S = take(BH * E);   // the final state
+    }
+    if (backward) {
+        g.off_x = take(steps * 4);
+        g.off_y = take(steps * 4);
+        g.off_dg = take(BH * g.nSeg * 4);
+        if (g.grouped) {
+            g.off_dq = take(steps * d.dk * 4);
+            g.off_dk = take(steps * d.dk * 4);
+        }
+    }
+    g.bytes = at;
+    return g;
+}
+
+namespace {
+
+Operand operand(const void *p, const int64_t *st, int64_t heads, int64_t H, int64_t cols)
+{
+    return Operand{p, st[0], st[1], st[2], static_cast<int>(H / heads), static_cast<int>(cols)};
+}
+
+WalkArgs walk_args(const AttnGeom &geo, const mgs_linattn_desc &d, const float *g, const int32_t *lengths, bool vec)
+{
+    WalkArgs a{};
+    a.g = g;
+    a.gb = d.decay_per_head ? 0 : d.g_stride[0];
+    a.gt = d.decay_per_head ? 0 : d.g_stride[1];
+    a.gh = d.decay_per_head ? 1 : d.g_stride[2];
+    a.lengths = lengths;
+    a.items = geo.BH * geo.nSeg;
+    a.T = static_cast<int>(d.T);
+    a.H = static_cast<int>(d.H);
+    a.nC = geo.nC;
+    a.nSeg = geo.nSeg;
+    a.segLen = geo.segLen;
+    a.vec = vec;
+    return a;
+}
+
+hipError_t launch_chain(const AttnGeom &geo, const ChainArgs &c, int directions, hipStream_t s)
+{
+    const int64_t n = geo.BH * c.E;
+    hipLaunchKernelGGL(chain_kernel, dim3(static_cast<unsigned>((n + 255) / 256), directions), dim3(256), 0, s, c);
+    return hipGetLastError();
+}
+
+hipError_t copy_state(const float *from, float *to, int64_t n, hipStream_t s);
+
+__global__ void __launch_bounds__(256) copy_state_kernel(const float *from, float *to, int64_t n)
+{
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    if (i < n) to[i] = from ? from[i] : 0.0f;
+}
+
+// `to` <- `from`, or zeros: states and gradients of empty sequences
+hipError_t copy_state(const float *from, float *to, int64_t n, hipStream_t s)
+{
+    if (!to || n == 0) return hipSuccess;
+    hipLaunchKernelGGL(copy_state_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, from, to, n);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_linattn_fwd(const AttnGeom &geo, const mgs_linattn_desc &d, const void *q, const void *k,
+                              const void *v, const float *g, const float *S0, const int32_t *lengths, void *o,
+                              float *ST, void *ws, hipStream_t s)
+{
+    const int dk = static_cast<int>(d.dk), dv = static_cast<int>(d.dv), E = dk * dv;
+    if (geo.nC == 0) return copy_state(S0, ST, geo.BH * E, s);
+    const size_t size = d.dtype == MGS_BF16 ? 2 : 4;
+    const bool vec = dk % 8 == 0 && dv % 8 == 0 && wide(q, d.q_stride, 3, size) && wide(k, d.k_stride, 3, size) &&
+                     wide(v, d.v_stride, 3, size) && wide(o, nullptr, 0, size);
+    WalkArgs a = walk_args(geo, d, g, lengths, vec);
+    a.nRoles = 1;
+    Role &r = a.role[0];
+    r.q = operand(q, d.q_stride, d.Hk, d.H, dk);
+    r.k = operand(k, d.k_stride, d.Hk, d.H, dk);
+    r.v = operand(v, d.v_stride, d.H, d.H, dv);
+    r.out = o;
+    r.sc = dk;
+    r.sk = 1;
+    r.intra = r.inter = d.scale;
+    r.src = 1.0f;
+    if (geo.nSeg == 1) {
+        r.state = S0;
+        r.final = ST;
+        r.st_bh = E;
+        return launch_walk<false>(d.dtype, a, dk, dv, s);
+    }
+    char *w = static_cast<char *>(ws);
+    float *S = reinterpret_cast<float *>(w + geo.off_S);
+    r.st_bh = static_cast<int64_t>(geo.nSeg + 1) * E;
+    r.st_seg = E;
+    r.local = S;
+    a.dec = reinterpret_cast<float *>(w + geo.off_dec);
+    hipError_t e = launch_walk<true>(d.dtype, a, dk, dv, s);
+    if (e != hipSuccess) return e;
+    ChainArgs c{};
+    c.S = S;
+    c.dec = a.dec;
+    c.S0 = S0;
+    c.ST = ST;
+    c.BH = geo.BH;
+    c.nSeg = geo.nSeg;
+    c.E = E;
+    e = launch_chain(geo, c, 1, s);
+    if (e != hipSuccess) return e;
+    r.state = S;
+    return launch_walk<false>(d.dtype, a, dk, dv, s);
+}
+
+hipError_t launch_linattn_bwd(const AttnGeom &geo, const mgs_linattn_desc &d, const void *q, const void *k,
+                              const void *v, const float *g, const void *do_, const float *S0, const float *dST,
+                              const int32_t *lengths, void *dq, void *dk_, void *dv_, float *dg, float *dS0,
+                              void *ws, hipStream_t s)
+{
+    const int dk = static_cast<int>(d.dk), dv = static_cast<int>(d.dv), E = dk * dv, H = static_cast<int>(d.H);
+    hipError_t e;
+    if (geo.nC == 0) {
+        if (d.decay_per_head && (e = copy_state(nullptr, dg, d.H, s)) != hipSuccess) return e;
+        return copy_state(dST, dS0, geo.BH * E, s);
+    }
+    char *w = static_cast<char *>(ws);
+    auto at = [&](size_t off) { return reinterpret_cast<float *>(w + off); };
+    float *S = at(geo.off_S), *R = geo.nSeg > 1 ? at(geo.off_R) : nullptr;
+    float *x = at(geo.off_x), *y = at(geo.off_y);
+    const size_t size = d.dtype == MGS_BF16 ? 2 : 4;
+    const bool vec = dk % 8 == 0 && dv % 8 == 0 && wide(q, d.q_stride, 3, size) && wide(k, d.k_stride, 3, size) &&
+                     wide(v, d.v_stride, 3, size) && wide(do_, d.do_stride, 3, size) && wide(dq, nullptr, 0, size) &&
+                     wide(dk_, nullptr, 0, size) && wide(dv_, nullptr, 0, size);
+    WalkArgs a = walk_args(geo, d, g, lengths, vec);
+    const Operand oq = operand(q, d.q_stride, d.Hk, d.H, dk), ok = operand(k, d.k_stride, d.Hk, d.H, dk);
+    const Operand ov = operand(v, d.v_stride, d.H, d.H, dv), oo = operand(do_, d.do_stride, d.H, d.H, dv);
+    const int64_t S_bh = static_cast<int64_t>(geo.nSeg > 1 ? geo.nSeg + 1 : 1) * E;
+    const int64_t R_bh = static_cast<int64_t>(geo.nSeg) * E;
+
+    Role rq{}, rk{}, rv{};   // of dq, dk, dv
+    rq.q = oo, rq.k = ov, rq.v = ok, rq.dot = oq;
+    rq.sc = 1, rq.sk = dk, rq.st_bh = S_bh, rq.st_seg = E;
+    rq.intra = rq.inter = d.scale, rq.src = 1.0f;
+    rq.xdot = x;
+    rk.q = ov, rk.k = oo, rk.v = oq, rk.dot = ok;
+    rk.sc = 1, rk.sk = dk;
+    rk.xdot = y;
+    rv.q = ok, rv.k = oq, rv.v = oo;
+    rv.sc = dk, rv.sk = 1;
+    for (Role *r : {&rk, &rv}) {
+        r->st_bh = R_bh, r->st_seg = E;
+        r->intra = r->src = d.scale, r->inter = 1.0f;
+        r->rev = 1;
+    }
+    rq.out = geo.grouped ? static_cast<void *>(at(geo.off_dq)) : dq;
+    rk.out = geo.grouped ? static_cast<void *>(at(geo.off_dk)) : dk_;
+    rq.out_f32 = rk.out_f32 = geo.grouped;
+    rv.out = dv_;
+
+    if (geo.nSeg > 1) {
+        // contributions of the segments to S (k, v) and R (q, do)
+        WalkArgs l = a;
+        l.nRoles = 2;
+        l.dec = at(geo.off_dec);
+        l.role[0].k = ok, l.role[0].v = ov, l.role[0].sc = dk, l.role[0].sk = 1, l.role[0].src = 1.0f;
+        l.role[0].local = S, l.role[0].st_bh = S_bh, l.role[0].st_seg = E;
+        l.role[1] = rv;
+        l.role[1].local = R;
+        if ((e = launch_walk<true>(d.dtype, l, dk, dv, s)) != hipSuccess) return e;
+        ChainArgs c{};
+        c.S = S, c.R = R, c.dec = l.dec, c.S0 = S0, c.dST = dST, c.dS0 = dS0;
+        c.BH = geo.BH, c.nSeg = geo.nSeg, c.E = E;
+        if ((e = launch_chain(geo, c, 2, s)) != hipSuccess) return e;
+        rq.state = S;
+        rk.state = rv.state = R;
+    } else {
+        rq.state = S0;
+        rq.final = S;
+        rk.state = rv.state = dST;
+        rv.final = dS0;
+    }
+    // the dq and dk walks reduce over dv, the dv walk over dk
+    a.role[0] = rq, a.role[1] = rk, a.role[2] = rv;
+    if ((dk <= 64) == (dv <= 64)) {
+        a.nRoles = 3;
+        if ((e = launch_walk<false>(d.dtype, a, dv, dk, s)) != hipSuccess) return e;
+    } else {
+        a.nRoles = 2;
+        if ((e = launch_walk<false>(d.dtype, a, dv, dk, s)) != hipSuccess) return e;
+        a.role[0] = rv;
+        a.nRoles = 1;
+        if ((e = launch_walk<false>(d.dtype, a, dk, dv, s)) != hipSuccess) return e;
+    }
+
+    DgArgs m{};
+    m.x = x, m.y = y;
+    m.S = geo.nSeg > 1 ? S + E : S;
+    m.R = geo.nSeg > 1 ? R : dST;
+    m.s_bh = S_bh, m.s_seg = E, m.r_bh = R_bh, m.r_seg = E;
+    m.g = g, m.gb = a.gb, m.gt = a.gt, m.gh = a.gh;
+    m.lengths = lengths;
+    m.dg = d.decay_per_head ? at(geo.off_dg) : dg;
+    m.T = a.T, m.H = H, m.nSeg = geo.nSeg, m.segLen = geo.segLen, m.E = E;
+    m.per_head = d.decay_per_head != 0;
+    hipLaunchKernelGGL(dg_kernel, dim3(static_cast<unsigned>(a.items)), dim3(256), 0, s, m);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    if (d.decay_per_head) {
+        hipLaunchKernelGGL(dg_head_kernel, dim3(H), dim3(256), 0, s, m.dg, dg, d.B, H, geo.nSeg);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (geo.grouped) {
+        const int64_t n = d.B * d.T * d.Hk * d.dk;
+        const dim3 grid(static_cast<unsigned>((n + 255) / 256), 2);
+        const int Hk = static_cast<int>(d.Hk);
+        if (d.dtype == MGS_BF16)
+            hipLaunchKernelGGL(group_sum_kernel<__bf16>, grid, dim3(256), 0, s, at(geo.off_dq), at(geo.off_dk),
+                               static_cast<__bf16 *>(dq), static_cast<__bf16 *>(dk_), n, H, Hk, dk);
+        else
+            hipLaunchKernelGGL(group_sum_kernel<float>, grid, dim3(256), 0, s, at(geo.off_dq), at(geo.off_dk),
+                               static_cast<float *>(dq), static_cast<float *>(dk_), n, H, Hk, dk);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+hipError_t launch_linattn_step(const mgs_linattn_desc &d, const void *q, const void *k, const void *v,
+                               const float *g, float *S, int64_t n_slots, const int32_t *slots, void *o,
+                               hipStream_t s)
+{
+    StepArgs a{};
+    a.q = q, a.k = k, a.v = v, a.g = g, a.S = S, a.o = o, a.slots = slots, a.n_slots = n_slots;
+    a.qb = d.q_stride[0], a.qh = d.q_stride[2], a.kb = d.k_stride[0], a.kh = d.k_stride[2];
+    a.vb = d.v_stride[0], a.vh = d.v_stride[2];
+    a.gb = d.decay_per_head ? 0 : d.g_stride[0];
+    a.gh = d.decay_per_head ? 1 : d.g_stride[2];
+    a.H = static_cast<int>(d.H), a.div = static_cast<int>(d.H / d.Hk);
+    a.dk = static_cast<int>(d.dk), a.dv = static_cast<int>(d.dv);
+    a.tiles = (a.dv + 15) / 16;
+    a.vec = (a.dk & 3) == 0 && wide(S, nullptr, 0, 4);
+    a.scale = d.scale;
+    const dim3 grid(static_cast<unsigned>(d.B * d.H * a.tiles)), block(256);
+    if (d.dtype == MGS_BF16) {
+        if (a.dk <= 64) hipLaunchKernelGGL((step_kernel<__bf16, 1>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((step_kernel<__bf16, 2>), grid, block, 0, s, a);
+    } else {
+        if (a.dk <= 64) hipLaunchKernelGGL((step_kernel<float, 1>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((step_kernel<float, 2>), grid, block, 0, s, a);
+    }
+    return hipGetLastError();
+}
+
+}  // namespace mgs

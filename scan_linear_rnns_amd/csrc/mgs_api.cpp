@@ -11,6 +11,7 @@
 #include <initializer_list>
 #include <mutex>
 
+#include "api_common.hpp"
 #include "device.hpp"
 #include "launch.hpp"
 
@@ -18,60 +19,18 @@ namespace {
 
 thread_local int g_last_hip_error = 0;
 
+using mgs::all_aligned;
+using mgs::any_alias;
+using mgs::as_stream;
+using mgs::check_workspace;
+using mgs::hip_status;
+using mgs::Range;
+
 constexpr int64_t kMaxElems = (int64_t(1) << 31) - 1;
 
-mgs_status hip_status(hipError_t e)
-{
-    if (e == hipSuccess) return MGS_OK;
-    g_last_hip_error = static_cast<int>(e);
-    return MGS_ERR_HIP;
-}
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Range {
-    const void *p;
-    size_t bytes;
-};
-
-bool overlaps(Range a, Range b)
-{
-    if (!a.p || !b.p || a.bytes == 0 || b.bytes == 0) return false;
-    const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-    return a0 < b0 + b.bytes && b0 < a0 + a.bytes;
-}
-
-// every output must be disjoint from every input and from the other outputs
-bool any_alias(const Range *in, int nin, const Range *out, int nout)
-{
-    for (int i = 0; i < nout; ++i) {
-        for (int j = 0; j < nin; ++j)
-            if (overlaps(out[i], in[j])) return true;
-        for (int j = i + 1; j < nout; ++j)
-            if (overlaps(out[i], out[j])) return true;
-    }
-    return false;
-}
-
-bool all_aligned(const Range *r, int n)
-{
-    for (int i = 0; i < n; ++i)
-        if (r[i].p && !aligned16(r[i].p)) return false;
-    return true;
-}
-
-// Product of non-negative tensor dimensions, or -1 when a dimension or the
-// product exceeds kMaxElems.  Each factor is bounded before it is multiplied
-// and the multiplications are overflow-checked, so caller-supplied sizes can
-// never wrap around to a small (or zero) element count.
 int64_t bounded_product(std::initializer_list<int64_t> dims)
 {
-    int64_t n = 1;
-    for (int64_t x : dims)
-        if (x > kMaxElems) return -1;
-    for (int64_t x : dims)
-        if (__builtin_mul_overflow(n, x, &n) || n > kMaxElems) return -1;
-    return n;
+    return mgs::bounded_product(dims, kMaxElems, kMaxElems);
 }
 
 // Element counts of the (B,T,d) and (B,d) tensors of an elementwise op.
@@ -87,16 +46,6 @@ mgs_status check_sizes(int64_t B, int64_t T, int64_t d, ElemSizes *out)
     *out = ElemSizes{n, s};
     return MGS_OK;
 }
-
-mgs_status check_workspace(const void *ws, size_t have, size_t need)
-{
-    if (!ws) return MGS_ERR_WORKSPACE;
-    if (have < need) return MGS_ERR_WORKSPACE;
-    if (!aligned16(ws)) return MGS_ERR_INVALID_VALUE;
-    return MGS_OK;
-}
-
-hipStream_t as_stream(void *s) { return static_cast<hipStream_t>(s); }
 
 // ------------------------------------------------ scratch of the no-allocation entry point
 // mgs_block_affine_scan_fwd_noalloc keeps its workspace in this file-scope
@@ -138,6 +87,13 @@ mgs_status noalloc_scratch(void **ptr)
 }
 
 }  // namespace
+
+mgs_status mgs::hip_status(hipError_t e)
+{
+    if (e == hipSuccess) return MGS_OK;
+    g_last_hip_error = static_cast<int>(e);
+    return MGS_ERR_HIP;
+}
 
 extern "C" {
 
