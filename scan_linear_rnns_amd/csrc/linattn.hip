@@ -15,7 +15,7 @@
 // (its state is S transposed).  Backwards in time, with each step's decay
 // applied one step later, (k; q, do) gives dv from the state
 // R_t = a_{t+1} D_{t+1} (D = dL/dS) and (v; do, q) gives dk from R transposed.
-// One kernel serves all four; the three gradient walks go in one launch.
+// One kernel serves all four.
 //
 // Along the steps a sequence is cut into segments when there are too few
 // (sequence, head) pairs to fill the chip: a first pass forms each segment's
@@ -51,6 +51,7 @@ constexpr int kThreads = 256;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 typedef float f4v __attribute__((ext_vector_type(4)));
+typedef float f8v __attribute__((ext_vector_type(8), aligned(16)));
 typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef short s4v __attribute__((ext_vector_type(4)));
@@ -61,13 +62,13 @@ template <> struct Num<float> {
     using Frag = f4v;                    // 4 elements of a reduction block
     static constexpr int NS = 1;         // terms an fp32 value is split into
     static constexpr int PAD = 4;        // elements between LDS rows, 16 bytes
-    struct Vec8 { f4v a, b; };
+    using Vec8 = f8v;
 };
 template <> struct Num<__bf16> {
     using Frag = bf4;
     static constexpr int NS = 3;
     static constexpr int PAD = 8;
-    struct Vec8 { bf8 a; };
+    using Vec8 = bf8;
 };
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
@@ -90,16 +91,16 @@ __device__ __forceinline__ f4v mma2(bf4 a0, bf4 a1, bf4 b0, bf4 b1, f4v c)
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
-// an fp32 fragment as NS fragments of T that sum to it
+// an fp32 fragment as fragments of T that sum to it, or to its first 16 bits (two of bf16)
 __device__ __forceinline__ void split(f4v x, f4v (&out)[1]) { out[0] = x; }
 
-__device__ __forceinline__ void split(f4v x, bf4 (&out)[3])
+template <int N> __device__ __forceinline__ void split(f4v x, bf4 (&out)[N])
 {
-    out[0] = __builtin_convertvector(x, bf4);
-    x -= __builtin_convertvector(out[0], f4v);
-    out[1] = __builtin_convertvector(x, bf4);
-    x -= __builtin_convertvector(out[1], f4v);
-    out[2] = __builtin_convertvector(x, bf4);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        out[i] = __builtin_convertvector(x, bf4);
+        x -= __builtin_convertvector(out[i], f4v);
+    }
 }
 
 // 4 contiguous elements in LDS (aligned to the fragment)
@@ -148,67 +149,153 @@ struct Role {
 };
 
 struct WalkArgs {
-    Role role[3];
+    Role role[2];
     const float *g;
     int64_t gb, gt, gh;
     const int32_t *lengths;
     float *dec;              // state-only pass: decay over each segment (bh, seg), by the forward role
-    int64_t items;           // (b, h, segment) triples
+    uint32_t items;          // (b, h, segment) triples
     int nRoles, T, H, nC, nSeg, segLen, vec;
 };
 
-template <typename T> __device__ __forceinline__ void zero8(typename Num<T>::Vec8 &x);
-template <> __device__ __forceinline__ void zero8<float>(Num<float>::Vec8 &x) { x.a = x.b = f4v{0, 0, 0, 0}; }
-template <> __device__ __forceinline__ void zero8<__bf16>(Num<__bf16>::Vec8 &x)
+// Cuts a workgroup-uniform value off from how it was computed.  Without it the
+// compiler keeps whole argument structures in scalar registers through the walk,
+// and the lane masks and products made from them, and spills.
+__device__ __forceinline__ int keep(int x)
 {
-    x.a = __builtin_bit_cast(bf8, f4v{0, 0, 0, 0});
-}
-
-// elements c .. c + 7 of a row of `cols`, zeros past its end; vec: 16-byte
-// accesses are aligned and cols is a multiple of 8
-template <typename T>
-__device__ __forceinline__ typename Num<T>::Vec8 load8(const T *row, int c, int cols, bool vec)
-{
-    typename Num<T>::Vec8 x;
-    if (vec) {
-        zero8<T>(x);
-        if (c < cols) x = *reinterpret_cast<const typename Num<T>::Vec8 *>(row + c);
-    } else {
-        T e[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = c + i < cols ? row[c + i] : static_cast<T>(0.0f);
-        __builtin_memcpy(&x, e, sizeof(x));
-    }
+    x = __builtin_amdgcn_readfirstlane(x);
+    asm volatile("" : "+s"(x));
     return x;
+}
+__device__ __forceinline__ float keep(float x) { return __int_as_float(keep(__float_as_int(x))); }
+__device__ __forceinline__ int64_t keep(int64_t x)
+{
+    const int lo = keep(static_cast<int>(x)), hi = keep(static_cast<int>(x >> 32));
+    return static_cast<int64_t>(static_cast<uint64_t>(static_cast<uint32_t>(hi)) << 32 | static_cast<uint32_t>(lo));
+}
+// addresses: plain numbers, turned into global pointers where they are used
+__device__ __forceinline__ int64_t keep(const void *p) { return keep(static_cast<int64_t>(reinterpret_cast<uintptr_t>(p))); }
+
+template <typename V> using Global = __attribute__((address_space(1))) V;
+
+// Buffer accesses, at a workgroup-uniform address plus a lane offset: a lane
+// whose offset is kNowhere reads zeros and writes nothing, with no branch, so
+// the number of accesses in flight is known and waiting for one does not mean
+// waiting for all (loads and stores share a counter).
+constexpr uint32_t kReach = 1u << 30, kNowhere = 1u << 31;
+
+typedef uint32_t u2v __attribute__((ext_vector_type(2)));
+typedef uint32_t u4v __attribute__((ext_vector_type(4)));
+
+struct Buffer {
+    __amdgpu_buffer_rsrc_t r;
+    __device__ __forceinline__ explicit Buffer(int64_t base)
+        : r(__builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void *>(base), 0, kReach, 0x00027000))
+    {
+    }
+    template <typename V> __device__ __forceinline__ V load(uint32_t off) const
+    {
+        if constexpr (sizeof(V) == 32) {
+            struct { u4v a, b; } x{__builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0),
+                                   __builtin_amdgcn_raw_buffer_load_b128(r, off, 16, 0)};
+            return __builtin_bit_cast(V, x);
+        } else if constexpr (sizeof(V) == 16) {
+            return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b128(r, off, 0, 0));
+        } else if constexpr (sizeof(V) == 8) {
+            return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+        } else {
+            static_assert(sizeof(V) == 4, "size");
+            return __builtin_bit_cast(V, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
+        }
+    }
+    template <typename V> __device__ __forceinline__ void store(uint32_t off, V v) const
+    {
+        if constexpr (sizeof(V) == 16) {
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4v, v), r, off, 0, 0);
+        } else {
+            static_assert(sizeof(V) == 8, "size");
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2v, v), r, off, 0, 0);
+        }
+    }
+};
+
+// Where a chunk lies: rows [lo, hi) of it are live (inside the sequence and its
+// length), row r is step tb + r, or tb + 63 - r backwards (tb may then lie
+// ahead of the sequence: only live rows are addressed).
+struct Chunk {
+    int64_t tb;
+    int lo, hi, rows;
+};
+
+__device__ __forceinline__ Chunk chunk_at(int ch, int T, int len, int rev)
+{
+    const int t0 = ch * kC, t1 = min(T, t0 + kC);
+    Chunk c;
+    c.rows = t1 - t0;
+    c.tb = rev ? t1 - kC : t0;
+    c.lo = rev ? min(c.rows, max(0, t1 - len)) : 0;
+    c.hi = rev ? c.rows : max(0, min(c.rows, len - t0));
+    return c;
 }
 
 // One 64-row tile on its way from global memory to LDS: DIM columns, 8 per
-// thread and turn.  Row r is step t0 + r, or t1 - 1 - r backwards; rows past
-// the chunk or the sequence's length are zeros and are not read.
-template <typename T, int DIM> struct Stage {
+// thread and turn.  Rows that are not live are zeros and are not read.  A wide
+// access is a workgroup-uniform chunk address plus a 32-bit lane offset that
+// stays the same from chunk to chunk.
+template <typename T, int DIM, bool VEC> struct Stage {
     static constexpr int LD = DIM + Num<T>::PAD;
     static constexpr int PER = kC * DIM / 8 / kThreads;
-    typename Num<T>::Vec8 x[PER];
+    static constexpr int TURN = kThreads / (DIM / 8);   // rows per turn
+    using Vec8 = typename Num<T>::Vec8;
+    Vec8 x[PER];
+    int64_t base;      // address of (b, 0, h, 0)
+    int64_t st;        // bytes from step to step
+    uint32_t off;      // bytes from the chunk's first step, first turn
+    uint32_t turn;     // bytes from turn to turn
+    int vrow;          // row of the first turn; of columns past the end, out of any chunk
+    int cols, rev;
 
-    __device__ __forceinline__ void load(const Operand &o, int64_t b, int h, int t0, int t1, int len, int rev, bool vec)
+    __device__ __forceinline__ void init(const Operand &o, int64_t b, int h, int rev_)
     {
-        const T *base = static_cast<const T *>(o.p) + b * o.sb + (h / o.div) * o.sh;
+        base = keep(static_cast<const T *>(o.p) + b * o.sb + (h / o.div) * o.sh);
+        st = keep(o.st * static_cast<int64_t>(sizeof(T)));
+        cols = keep(o.cols);
+        rev = rev_;
+        turn = static_cast<uint32_t>(st) * static_cast<uint32_t>(TURN);
+        if (rev) turn = 0u - turn;
+        const int r = row(0);
+        vrow = col() < cols ? r : kC;
+        off = (rev ? kC - 1 - r : r) * static_cast<uint32_t>(st) + static_cast<uint32_t>(col() * sizeof(T));
+    }
+    __device__ __forceinline__ int row(int i) const { return threadIdx.x / (DIM / 8) + TURN * i; }
+    __device__ __forceinline__ int col() const { return threadIdx.x % (DIM / 8) * 8; }
+
+    __device__ __forceinline__ void load(const Chunk &ck)
+    {
+        if constexpr (VEC) {
+            const Buffer p(base + ck.tb * st);
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int idx = threadIdx.x + kThreads * i;
-            const int r = idx / (DIM / 8), c = (idx % (DIM / 8)) * 8;
-            const int t = rev ? t1 - 1 - r : t0 + r;
-            zero8<T>(x[i]);
-            if (r < t1 - t0 && t < len) x[i] = load8<T>(base + t * o.st, c, o.cols, vec);
+            for (int i = 0; i < PER; ++i) {
+                const bool live = static_cast<uint32_t>(vrow + TURN * i - ck.lo) < static_cast<uint32_t>(ck.hi - ck.lo);
+                x[i] = p.template load<Vec8>(live ? off + i * turn : kNowhere);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                x[i] = Vec8(0);
+                const int r = row(i);
+                const Global<const T> *p = reinterpret_cast<const Global<const T> *>(base + (ck.tb + (rev ? kC - 1 - r : r)) * st);
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (r >= ck.lo && r < ck.hi && col() + j < cols) x[i][j] = p[col() + j];
+            }
         }
     }
     __device__ __forceinline__ void store(T *lds) const
     {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) {
-            const int idx = threadIdx.x + kThreads * i;
-            *reinterpret_cast<typename Num<T>::Vec8 *>(lds + (idx / (DIM / 8)) * LD + (idx % (DIM / 8)) * 8) = x[i];
-        }
+        for (int i = 0; i < PER; ++i)
+            *reinterpret_cast<Vec8 *>(lds + row(i) * LD + col()) = x[i];
     }
 };
 
@@ -219,40 +306,48 @@ template <typename T, int DIM> struct Stage {
 struct Decays {
     float hi[kC], lo[kC];    // G
     float src[kC];           // factor of source j: e^{total - G_j}, times the role's
-    float row[kC];           // factor of the state's part of row i: e^{G_i}, times the role's
     float total;             // e^{total}
     float log2_total;
 };
 
-__device__ __forceinline__ void chunk_decays(const WalkArgs &a, const Role &ro, int64_t b, int h, int t0, int t1, int len,
-                                             Decays &d)
+// x of the lane `ctrl` (a DPP lane shift) points at, 0 where there is none
+template <int CTRL, int ROWS> __device__ __forceinline__ double dpp(double x)
 {
-    const int r = threadIdx.x;   // < 64
-    const int t = ro.rev ? t1 - 1 - r : t0 + r;
-    double x = 0.0;
-    if (r < t1 - t0 && t < len) {
-        const float gt = a.g[b * a.gb + t * a.gt + h * a.gh];
-        x = static_cast<double>(gt) * 1.4426950408889634074;
-        if (x < -20000.0) x = -20000.0;
-    }
-    double G = x;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const double y = __shfl_up(G, off, 64);
-        if (r >= off) G += y;
-    }
-    const double total = __shfl(G, 63, 64);
-    if (ro.rev) G = __shfl_up(G, 1, 64);
-    if (ro.rev && r == 0) G = 0.0;
+    const int lo = __builtin_amdgcn_update_dpp(0, __double2loint(x), CTRL, ROWS, 0xf, false);
+    const int hi = __builtin_amdgcn_update_dpp(0, __double2hiint(x), CTRL, ROWS, 0xf, false);
+    return __hiloint2double(hi, lo);
+}
+
+__device__ __forceinline__ void chunk_decays(float g, float src, int rev, Decays &d)
+{
+    const int r = threadIdx.x & 63;
+    double x = static_cast<double>(g) * 1.4426950408889634074;
+    if (x < -20000.0) x = -20000.0;
+    double G = x;   // inclusive sums: within 16 lanes, then over the rows of 16
+    G += dpp<0x111, 0xf>(G);
+    G += dpp<0x112, 0xf>(G);
+    G += dpp<0x114, 0xf>(G);
+    G += dpp<0x118, 0xf>(G);
+    G += dpp<0x142, 0xa>(G);
+    G += dpp<0x143, 0xc>(G);
+    const double total = __hiloint2double(__builtin_amdgcn_readlane(__double2hiint(G), 63),
+                                          __builtin_amdgcn_readlane(__double2loint(G), 63));
+    if (rev) G = dpp<0x138, 0xf>(G);   // one lane up: row r without its own
     const float hi = static_cast<float>(G);
     d.hi[r] = hi;
     d.lo[r] = static_cast<float>(G - static_cast<double>(hi));
-    d.src[r] = ro.src * __builtin_amdgcn_exp2f(static_cast<float>(total - G));
-    d.row[r] = ro.inter * __builtin_amdgcn_exp2f(hi);
+    d.src[r] = src * __builtin_amdgcn_exp2f(static_cast<float>(total - G));
     if (r == 0) {
         d.total = __builtin_amdgcn_exp2f(static_cast<float>(total));
         d.log2_total = static_cast<float>(total);
     }
+}
+
+// Workgroup barrier that waits for this wave's LDS operations only: loads from
+// global memory (the next chunk's) stay in flight across it.
+__device__ __forceinline__ void lds_barrier()
+{
+    asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
 }
 
 // Zeros in place of the non-finite elements of a wave's value fragments (rows
@@ -292,82 +387,174 @@ constexpr uint64_t kScoreTiles = 0xFEDCA98540ull;
 // (reduction index x column) in accumulators, and it forms the same columns of
 // the output, transposed, so that a lane holds 4 neighbouring columns of a row.
 // The scores are formed once per workgroup and shared through LDS.
-// STATE_ONLY: the walk from a zero state without outputs.
-template <typename T, int KD, int VD, bool STATE_ONLY>
-__global__ void __launch_bounds__(kThreads) walk_kernel(WalkArgs a)
+// MODE: STATE, the walk from a zero state without outputs; OUT, outputs rounded
+// to T; DOTS, outputs in T or fp32 (partials of shared heads), and the dots of
+// their rows for dg.  An output rounded to bf16 takes two terms (16 bits) of the
+// states and scores, one whose dots make dg all three.
+enum { STATE, OUT, DOTS };
+
+template <typename T, int KD, int VD, int MODE, bool VEC>
+__global__ void __launch_bounds__(kThreads, 2) walk_kernel(WalkArgs a)
 {
     using N = Num<T>;
     using Frag = typename N::Frag;
-    constexpr int NS = N::NS;
+    constexpr bool STATE_ONLY = MODE == STATE;
+    constexpr int NS = N::NS;                                 // terms of the weighted values
+    constexpr int NO = NS == 3 && MODE != DOTS ? 2 : NS;      // terms of states and scores
     constexpr int NCT = VD / 64;       // 16-column tiles per wave
     constexpr int NKB = KD / 16;       // reduction blocks
-    constexpr int LK = KD + N::PAD, LV = VD + N::PAD, LA = kC + N::PAD;
+    constexpr int LK = KD + N::PAD, LV = VD + N::PAD, LA = kC + 4;
     __shared__ __align__(16) T sQ[STATE_ONLY ? 8 : kC * LK];
     __shared__ __align__(16) T sK[kC * LK];
     __shared__ __align__(16) T sV[kC * LV];
-    __shared__ __align__(16) T sA[STATE_ONLY ? 1 : NS][STATE_ONLY ? 8 : kC * LA];
-    __shared__ __align__(16) Decays sD;
-    __shared__ float sX[STATE_ONLY ? 1 : 4][kC];
+    __shared__ __align__(16) T sA[STATE_ONLY ? 1 : NO][STATE_ONLY ? 8 : kC * LA];
+    __shared__ __align__(16) Decays sDecays[2];
+    __shared__ float sX[MODE == DOTS ? 4 : 1][kC];
 
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int li = lane & 15, lq = lane >> 4;
     // the roles of 8 neighbouring items run side by side, an item's on one XCD:
     // they read the same rows
-    const int64_t rest = blockIdx.x >> 3;
-    const int64_t item = (rest / a.nRoles) * 8 + (blockIdx.x & 7);
+    const uint32_t rest = blockIdx.x >> 3;
+    const uint32_t item = (rest / a.nRoles) * 8 + (blockIdx.x & 7);
     if (item >= a.items) return;
     const Role &ro = a.role[rest % a.nRoles];
     const int seg = static_cast<int>(item % a.nSeg);
-    const int64_t bh = item / a.nSeg;
+    const uint32_t bh = item / a.nSeg;
     const int64_t b = bh / a.H;
-    const int h = static_cast<int>(bh - b * a.H);
+    const int h = static_cast<int>(bh % a.H);
     int len = a.T;
     if (a.lengths) len = max(0, min(a.T, a.lengths[b]));
-    const int c_lo = seg * a.segLen, c_hi = min(a.nC, c_lo + a.segLen);
-    const bool vec = a.vec != 0;
+    len = keep(len);
+    const int c_lo = seg * a.segLen, chunks = min(a.nC, c_lo + a.segLen) - c_lo;
+    const int rev = keep(ro.rev), cols = keep(ro.v.cols), kcols = keep(ro.k.cols);
+    const int T_ = keep(a.T), H_ = keep(a.H);
 
     const int col0 = wv * (16 * NCT);   // this wave's first column
     f4v S[NKB][NCT];
-#pragma unroll
-    for (int t = 0; t < NKB; ++t)
+    const float *state = STATE_ONLY ? nullptr : ro.state;
+    const int sc = keep(ro.sc), sk = keep(ro.sk);
+    if (state) {
+        // all loads in flight at once: out-of-range elements read the last one and
+        // are zeroed after
+        state += static_cast<int64_t>(bh) * ro.st_bh + seg * ro.st_seg;
 #pragma unroll
         for (int ct = 0; ct < NCT; ++ct) {
-            S[t][ct] = f4v{0, 0, 0, 0};
-            if (!STATE_ONLY && ro.state) {
-                const float *p = ro.state + bh * ro.st_bh + seg * ro.st_seg;
-                const int c = col0 + 16 * ct + li;
+            const int c = col0 + 16 * ct + li;
+            const float *p = state + min(c, cols - 1) * sc;
+            if (VEC && sk == 1) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int kk = 16 * t + 4 * lq + r;
-                    if (c < ro.v.cols && kk < ro.k.cols) S[t][ct][r] = p[c * ro.sc + kk * ro.sk];
-                }
+                for (int t = 0; t < NKB; ++t)
+                    S[t][ct] = *reinterpret_cast<const f4v *>(p + min(16 * t + 4 * lq, kcols - 4));
+            } else {
+#pragma unroll
+                for (int t = 0; t < NKB; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) S[t][ct][r] = p[min(16 * t + 4 * lq + r, kcols - 1) * sk];
             }
         }
+        if (cols < VD || kcols < KD) {
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct)
+#pragma unroll
+                for (int t = 0; t < NKB; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        S[t][ct][r] = col0 + 16 * ct + li < cols && 16 * t + 4 * lq + r < kcols ? S[t][ct][r] : 0.0f;
+        }
+    } else {
+#pragma unroll
+        for (int t = 0; t < NKB; ++t)
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) S[t][ct] = f4v{0, 0, 0, 0};
+    }
     if constexpr (!STATE_ONLY) {   // the tiles above the diagonal stay zero
 #pragma unroll
-        for (int s = 0; s < NS; ++s)
+        for (int s = 0; s < NO; ++s)
             for (int i = tid; i < kC * LA; i += kThreads) sA[s][i] = static_cast<T>(0.0f);
     }
 
+    Stage<T, KD, VEC> q, k;
+    Stage<T, VD, VEC> v;
+    k.init(ro.k, b, h, rev);
+    v.init(ro.v, b, h, rev);
+    if constexpr (!STATE_ONLY) q.init(ro.q, b, h, rev);
+    const int64_t gp = keep(a.g + b * a.gb + h * a.gh);
+    const int64_t gt = keep(a.gt * 4);
+    const float intra = keep(ro.intra), inter = keep(ro.inter), src_f = keep(ro.src);
+
+    // rows of the output and of what they are dotted with: lane offsets of row li
+    // (rows 16 i + li lie 16 i rows further on, or back), columns 4 lq
+    const int out_f32 = keep(MODE == DOTS && ro.out_f32 ? 1 : 0);
+    const int o_size = out_f32 ? 4 : static_cast<int>(sizeof(T));
+    const int64_t o_st = static_cast<int64_t>(H_) * cols * o_size, d_st = keep(ro.dot.st * static_cast<int64_t>(sizeof(T)));
+    const int orow = rev ? kC - 1 - li : li, o_step = rev ? -16 : 16;
+    const int c0 = col0 + 4 * lq;
+    const int64_t o_base = keep(static_cast<char *>(ro.out) + (b * T_ * H_ + h) * cols * o_size);
+    const int64_t d_base = keep(static_cast<const T *>(ro.dot.p) + b * ro.dot.sb + (MODE == DOTS ? h / ro.dot.div : 0) * ro.dot.sh);
+    const int64_t xdot = keep(ro.xdot + static_cast<int64_t>(bh) * T_);
+    // The rows of the next chunk travel while this one is worked on, and its decay
+    // sums are formed, by the waves in turn, while the others finish this one.
+    float g = 0.0f;
+    auto place = [&](int n) {
+        Chunk ck = chunk_at(rev ? c_lo + chunks - 1 - n : c_lo + n, T_, len, rev);
+        if (n >= chunks) ck.lo = ck.hi = 0;   // nothing to read
+        return ck;
+    };
+    auto load_g = [&](int n) {
+        const Chunk ck = place(n);
+        g = 0.0f;
+        if (lane >= ck.lo && lane < ck.hi)
+            g = *reinterpret_cast<const Global<const float> *>(gp + (ck.tb + (rev ? kC - 1 - lane : lane)) * gt);
+    };
+    auto load = [&](int n) {
+        const Chunk ck = place(n);
+        k.load(ck);
+        v.load(ck);
+        if constexpr (!STATE_ONLY) q.load(ck);
+    };
+    if (wv < 2) load_g(wv);
+    load(0);
+    if (wv == 0) chunk_decays(g, src_f, rev, sDecays[0]);
+
     float seg_log2 = 0.0f;
-    for (int n = 0; n < c_hi - c_lo; ++n) {
-        const int ch = ro.rev ? c_hi - 1 - n : c_lo + n;
-        const int t0 = ch * kC, t1 = min(a.T, t0 + kC);
-        {
-            Stage<T, KD> k;
-            Stage<T, VD> v;
-            k.load(ro.k, b, h, t0, t1, len, ro.rev, vec);
-            v.load(ro.v, b, h, t0, t1, len, ro.rev, vec);
-            if constexpr (!STATE_ONLY) {
-                Stage<T, KD> q;
-                q.load(ro.q, b, h, t0, t1, len, ro.rev, vec);
-                q.store(sQ);
+    for (int n = 0; n < chunks; ++n) {
+        const Decays &sD = sDecays[n & 1];
+        k.store(sK);
+        v.store(sV);
+        if constexpr (!STATE_ONLY) q.store(sQ);
+        lds_barrier();
+        const Chunk ck = place(n);
+
+        [[maybe_unused]] Frag dots[MODE == DOTS ? 4 : 1][NCT];
+        if constexpr (MODE == DOTS) {
+            {
+                [[maybe_unused]] const int64_t p = d_base + ck.tb * d_st;
+                const Buffer buf(p);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 16 * i + li;
+                    const bool live = r >= ck.lo && r < ck.hi;
+#pragma unroll
+                    for (int ct = 0; ct < NCT; ++ct) {
+                        const int c = c0 + 16 * ct;
+                        if constexpr (VEC) {
+                            const uint32_t at = (orow + o_step * i) * static_cast<uint32_t>(d_st) + c * static_cast<uint32_t>(sizeof(T));
+                            dots[i][ct] = buf.template load<Frag>(live && c < cols ? at : kNowhere);
+                        } else {
+                            const Global<const T> *x = reinterpret_cast<const Global<const T> *>(p + (orow + o_step * i) * d_st) + c;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                dots[i][ct][e] = static_cast<T>(0.0f);
+                                if (live && c + e < cols) dots[i][ct][e] = x[e];
+                            }
+                        }
+                    }
+                }
             }
-            k.store(sK);
-            v.store(sV);
         }
-        if (wv == 0) chunk_decays(a, ro, b, h, t0, t1, len, sD);
-        __syncthreads();
+        load(n + 1);
+        if (((n + 2) & 3) == wv) load_g(n + 2);
 
         if constexpr (!STATE_ONLY) {
             // scores: tile (i, j) with rows of q as columns, so that a lane holds
@@ -387,19 +574,20 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(WalkArgs a)
                     }
                     const int row = 16 * i + li, src = 16 * j + 4 * lq;
                     const float gh = sD.hi[row], gl = sD.lo[row];
+                    const f4v sh = *reinterpret_cast<const f4v *>(&sD.hi[src]), sl = *reinterpret_cast<const f4v *>(&sD.lo[src]);
                     f4v w;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float e = __builtin_amdgcn_exp2f((gh - sD.hi[src + r]) + (gl - sD.lo[src + r]));
-                        w[r] = src + r <= row ? ro.intra * e * p[r] : 0.0f;
+                        const float e = __builtin_amdgcn_exp2f((gh - sh[r]) + (gl - sl[r]));
+                        w[r] = src + r <= row ? intra * e * p[r] : 0.0f;
                     }
-                    Frag ws[NS];
+                    Frag ws[NO];
                     split(w, ws);
 #pragma unroll
-                    for (int s = 0; s < NS; ++s) *reinterpret_cast<Frag *>(&sA[s][row * LA + src]) = ws[s];
+                    for (int s = 0; s < NO; ++s) *reinterpret_cast<Frag *>(&sA[s][row * LA + src]) = ws[s];
                 }
             }
-            __syncthreads();
+            lds_barrier();
 
             // the state's part of the output, then the chunk's own
             f4v O[4][NCT];
@@ -409,7 +597,7 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(WalkArgs a)
                 for (int ct = 0; ct < NCT; ++ct) O[i][ct] = f4v{0, 0, 0, 0};
 #pragma unroll
             for (int m = 0; m < NKB / 2; ++m) {
-                Frag s0[NCT][NS], s1[NCT][NS];
+                Frag s0[NCT][NO], s1[NCT][NO];
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct) {
                     split(S[2 * m][ct], s0[ct]);
@@ -420,15 +608,17 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(WalkArgs a)
                     const T *qr = sQ + (16 * i + li) * LK + 32 * m + 4 * lq;
                     const Frag q0 = frag(qr), q1 = frag(qr + 16);
 #pragma unroll
-                    for (int s = 0; s < NS; ++s)
+                    for (int s = 0; s < NO; ++s)
 #pragma unroll
                         for (int ct = 0; ct < NCT; ++ct) O[i][ct] = mma2(s0[ct][s], s1[ct][s], q0, q1, O[i][ct]);
                 }
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+                const float w = inter * __builtin_amdgcn_exp2f(sD.hi[16 * i + li]);
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) O[i][ct] *= sD.row[16 * i + li];
+                for (int ct = 0; ct < NCT; ++ct) O[i][ct] *= w;
+            }
             Frag vf[4][NCT];
 #pragma unroll
             for (int jb = 0; jb < 4; ++jb)
@@ -436,22 +626,25 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(WalkArgs a)
                 for (int ct = 0; ct < NCT; ++ct) vf[jb][ct] = frag_t<LV>(sV, 16 * jb, col0 + 16 * ct, li, lq);
             // A product with a zero weight would carry a non-finite value to rows ahead
             // of its own: such values are taken out, and from their row on their
-            // column is NaN.
-            float probe = 0.0f;
+            // column is NaN.  A product with zeros alone finds them.
+            {
+                Frag z;
 #pragma unroll
-            for (int jb = 0; jb < 4; ++jb)
+                for (int e = 0; e < 4; ++e) z[e] = static_cast<T>(0.0f);
+                f4v probe = {0, 0, 0, 0};
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct) {
-                    const f4v x = __builtin_convertvector(vf[jb][ct], f4v) * 0.0f;
-                    probe += (x[0] + x[1]) + (x[2] + x[3]);
+                    probe = mma2(vf[0][ct], vf[1][ct], z, z, probe);
+                    probe = mma2(vf[2][ct], vf[3][ct], z, z, probe);
                 }
-            if (__any(probe != 0.0f)) drop_non_finite<T, NCT>(vf, O, li, lq);
+                if (__any((probe[0] + probe[1]) + (probe[2] + probe[3]) != 0.0f)) drop_non_finite<T, NCT>(vf, O, li, lq);
+            }
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int m = 0; m <= i / 2; ++m)
+                for (int i = 2 * m; i < 4; ++i)
 #pragma unroll
-                    for (int s = 0; s < NS; ++s) {
+                    for (int s = 0; s < NO; ++s) {
                         const T *ar = &sA[s][(16 * i + li) * LA + 32 * m + 4 * lq];
                         const Frag a0 = frag(ar), a1 = frag(ar + 16);
 #pragma unroll
@@ -460,106 +653,112 @@ __global__ void __launch_bounds__(kThreads) walk_kernel(WalkArgs a)
                     }
 
             // rows of the output (zeros past the sequence's length) and their dots
-            const int cols = ro.v.cols;
+            if (ck.hi - ck.lo < kC) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int ct = 0; ct < NCT; ++ct)
+                        if (16 * i + li < ck.lo || 16 * i + li >= ck.hi) O[i][ct] = f4v{0, 0, 0, 0};
+            }
+            const int64_t op = o_base + ck.tb * o_st;
+            const Buffer out(op);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int r = 16 * i + li;
-                const int t = ro.rev ? t1 - 1 - r : t0 + r;
-                float dot = 0.0f;
-                if (r < t1 - t0) {
-                    const int64_t o0 = ((b * a.T + t) * a.H + h) * cols;
-                    const bool live = t < len;
+                const int rr = orow + o_step * i;
 #pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct) {
-                        const int c = col0 + 16 * ct + 4 * lq;
-                        const f4v y = live ? O[i][ct] : f4v{0, 0, 0, 0};
-                        if (ro.dot.p && live) {
-                            const T *p = static_cast<const T *>(ro.dot.p) + b * ro.dot.sb + (h / ro.dot.div) * ro.dot.sh +
-                                         t * ro.dot.st;
+                for (int ct = 0; ct < NCT; ++ct) {
+                    const int c = c0 + 16 * ct;
+                    const f4v y = O[i][ct];
+                    const Frag z = __builtin_convertvector(y, Frag);
+                    if constexpr (VEC) {
+                        uint32_t at = static_cast<uint32_t>(rr) * static_cast<uint32_t>(o_st) + c * static_cast<uint32_t>(o_size);
+                        if (16 * i + li >= ck.rows || c >= cols) at = kNowhere;
+                        if (MODE == DOTS && out_f32) out.store(at, y);
+                        else out.store(at, z);
+                    } else if (16 * i + li < ck.rows) {
+                        const int64_t at = op + rr * o_st + c * o_size;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                if (c + e < cols) dot = __builtin_fmaf(to_f32(p[c + e]), y[e], dot);
-                        }
-                        if (ro.out_f32) {
-                            float *op = static_cast<float *>(ro.out) + o0 + c;
-                            if ((cols & 3) == 0) {
-                                if (c < cols) *reinterpret_cast<f4v *>(op) = y;
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (c + e < cols) op[e] = y[e];
+                        for (int e = 0; e < 4; ++e)
+                            if (c + e < cols) {
+                                if (out_f32) reinterpret_cast<Global<float> *>(at)[e] = y[e];
+                                else reinterpret_cast<Global<T> *>(at)[e] = z[e];
                             }
-                        } else {
-                            T *op = static_cast<T *>(ro.out) + o0 + c;
-                            const Frag z = __builtin_convertvector(y, Frag);
-                            if (vec) {
-                                if (c < cols) *reinterpret_cast<Frag *>(op) = z;
-                            } else {
-#pragma unroll
-                                for (int e = 0; e < 4; ++e)
-                                    if (c + e < cols) op[e] = z[e];
-                            }
-                        }
                     }
                 }
-                dot += __shfl_xor(dot, 16, 64);
-                dot += __shfl_xor(dot, 32, 64);
-                if (lq == 0) sX[wv][r] = dot;
+            }
+            if constexpr (MODE == DOTS) {
+                // columns past the end have zero dots, rows that are not live zero outputs
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    f4v x = {0, 0, 0, 0};
+#pragma unroll
+                    for (int ct = 0; ct < NCT; ++ct) x += __builtin_convertvector(dots[i][ct], f4v) * O[i][ct];
+                    float dot = (x[0] + x[1]) + (x[2] + x[3]);
+                    dot += __shfl_xor(dot, 16, 64);
+                    dot += __shfl_xor(dot, 32, 64);
+                    if (lq == 0) sX[wv][16 * i + li] = dot;
+                }
             }
         }
 
         // S <- e^{total} S + sum over the chunk of weighted sources
         const float dec = sD.total;
-        Frag vw[4][NCT][NS];
 #pragma unroll
-        for (int jb = 0; jb < 4; ++jb) {
-            const f4v w = *reinterpret_cast<const f4v *>(&sD.src[16 * jb + 4 * lq]);
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                const Frag v = frag_t<LV>(sV, 16 * jb, col0 + 16 * ct, li, lq);
-                split(__builtin_convertvector(v, f4v) * w, vw[jb][ct]);
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < NKB; ++t) {
+        for (int t = 0; t < NKB; ++t)
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) S[t][ct] *= dec;
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
+        for (int m = 0; m < 2; ++m) {
+            Frag v0[NCT][NS], v1[NCT][NS];
+            const f4v w0 = *reinterpret_cast<const f4v *>(&sD.src[32 * m + 4 * lq]);
+            const f4v w1 = *reinterpret_cast<const f4v *>(&sD.src[32 * m + 16 + 4 * lq]);
+#pragma unroll
+            for (int ct = 0; ct < NCT; ++ct) {
+                const Frag x0 = frag_t<LV>(sV, 32 * m, col0 + 16 * ct, li, lq);
+                const Frag x1 = frag_t<LV>(sV, 32 * m + 16, col0 + 16 * ct, li, lq);
+                split(__builtin_convertvector(x0, f4v) * w0, v0[ct]);
+                split(__builtin_convertvector(x1, f4v) * w1, v1[ct]);
+            }
+#pragma unroll
+            for (int t = 0; t < NKB; ++t) {
                 const Frag k0 = frag_t<LK>(sK, 32 * m, 16 * t, li, lq), k1 = frag_t<LK>(sK, 32 * m + 16, 16 * t, li, lq);
 #pragma unroll
                 for (int s = 0; s < NS; ++s)
 #pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct)
-                        S[t][ct] = mma2(k0, k1, vw[2 * m][ct][s], vw[2 * m + 1][ct][s], S[t][ct]);
+                    for (int ct = 0; ct < NCT; ++ct) S[t][ct] = mma2(k0, k1, v0[ct][s], v1[ct][s], S[t][ct]);
             }
         }
-        seg_log2 += sD.log2_total;
-        __syncthreads();
-        if constexpr (!STATE_ONLY) {
-            if (ro.xdot && tid < t1 - t0) {
-                const int t = ro.rev ? t1 - 1 - tid : t0 + tid;
-                ro.xdot[bh * a.T + t] = (sX[0][tid] + sX[1][tid]) + (sX[2][tid] + sX[3][tid]);
-            }
+        if constexpr (STATE_ONLY) seg_log2 += sD.log2_total;
+        if (((n + 1) & 3) == wv) chunk_decays(g, src_f, rev, sDecays[(n + 1) & 1]);
+        lds_barrier();
+        if constexpr (MODE == DOTS) {
+            if (tid < ck.rows)
+                reinterpret_cast<Global<float> *>(xdot)[ck.tb + (rev ? kC - 1 - tid : tid)] = (sX[0][tid] + sX[1][tid]) + (sX[2][tid] + sX[3][tid]);
         }
     }
 
     float *fin = STATE_ONLY ? ro.local : ro.final;
     if (fin) {
-        fin += bh * ro.st_bh + (STATE_ONLY ? seg * ro.st_seg : 0);
+        fin += static_cast<int64_t>(bh) * ro.st_bh + (STATE_ONLY ? seg * ro.st_seg : 0);
 #pragma unroll
-        for (int t = 0; t < NKB; ++t)
+        for (int ct = 0; ct < NCT; ++ct) {
+            const int c = col0 + 16 * ct + li;
+            if (c >= cols) continue;
+            float *p = fin + c * sc;
+            if (VEC && sk == 1) {
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                const int c = col0 + 16 * ct + li;
+                for (int t = 0; t < NKB; ++t)
+                    if (16 * t + 4 * lq < kcols) *reinterpret_cast<f4v *>(p + 16 * t + 4 * lq) = S[t][ct];
+            } else {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int kk = 16 * t + 4 * lq + r;
-                    if (c < ro.v.cols && kk < ro.k.cols) fin[c * ro.sc + kk * ro.sk] = S[t][ct][r];
-                }
+                for (int t = 0; t < NKB; ++t)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (16 * t + 4 * lq + r < kcols) p[(16 * t + 4 * lq + r) * sk] = S[t][ct][r];
             }
+        }
     }
-    if (STATE_ONLY && !ro.rev && tid == 0) a.dec[bh * a.nSeg + seg] = __builtin_amdgcn_exp2f(seg_log2);
+    if (STATE_ONLY && !rev && tid == 0) a.dec[static_cast<int64_t>(bh) * a.nSeg + seg] = __builtin_amdgcn_exp2f(seg_log2);
 }
 
 // ---------------------------------------------------- chaining the segments
@@ -789,12 +988,14 @@ __global__ void __launch_bounds__(256) step_kernel(StepArgs a)
 
 // --------------------------------------------------------------------- host
 
+// Whether rows at p, with strides of (b, t, h), take 16-byte accesses and 64 of
+// them lie within a buffer access's reach
 bool wide(const void *p, const int64_t *st, int n, size_t size)
 {
     if (reinterpret_cast<uintptr_t>(p) & 15u) return false;
     for (int i = 0; i < n; ++i)
         if ((static_cast<size_t>(st[i]) * size) & 15u) return false;
-    return true;
+    return n < 2 || st[1] < (int64_t(1) << 21);
 }
 
 unsigned walk_grid(int64_t items, int roles)
@@ -802,22 +1003,25 @@ unsigned walk_grid(int64_t items, int roles)
     return static_cast<unsigned>((items + 7) / 8 * 8 * roles);
 }
 
-template <typename T, bool STATE_ONLY>
+template <typename T, int MODE, bool VEC>
 hipError_t launch_walk(const WalkArgs &a, int kdim, int vdim, hipStream_t s)
 {
     const dim3 grid(walk_grid(a.items, a.nRoles)), block(kThreads);
-    if (kdim <= 64 && vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 64, STATE_ONLY>), grid, block, 0, s, a);
-    else if (kdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 128, STATE_ONLY>), grid, block, 0, s, a);
-    else if (vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 128, 64, STATE_ONLY>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((walk_kernel<T, 128, 128, STATE_ONLY>), grid, block, 0, s, a);
+    if (kdim <= 64 && vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 64, MODE, VEC>), grid, block, 0, s, a);
+    else if (kdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 128, MODE, VEC>), grid, block, 0, s, a);
+    else if (vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 128, 64, MODE, VEC>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((walk_kernel<T, 128, 128, MODE, VEC>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
-template <bool STATE_ONLY>
+template <int MODE>
 hipError_t launch_walk(int dtype, const WalkArgs &a, int kdim, int vdim, hipStream_t s)
 {
-    return dtype == MGS_BF16 ? launch_walk<__bf16, STATE_ONLY>(a, kdim, vdim, s)
-                             : launch_walk<float, STATE_ONLY>(a, kdim, vdim, s);
+    if (dtype == MGS_BF16)
+        return a.vec ? launch_walk<__bf16, MODE, true>(a, kdim, vdim, s)
+                     : launch_walk<__bf16, MODE, false>(a, kdim, vdim, s);
+    return a.vec ? launch_walk<float, MODE, true>(a, kdim, vdim, s)
+                 : launch_walk<float, MODE, false>(a, kdim, vdim, s);
 }
 
 size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -883,7 +1087,7 @@ WalkArgs walk_args(const AttnGeom &geo, const mgs_linattn_desc &d, const float *
     a.gt = d.decay_per_head ? 0 : d.g_stride[1];
     a.gh = d.decay_per_head ? 1 : d.g_stride[2];
     a.lengths = lengths;
-    a.items = geo.BH * geo.nSeg;
+    a.items = static_cast<uint32_t>(geo.BH * geo.nSeg);
     a.T = static_cast<int>(d.T);
     a.H = static_cast<int>(d.H);
     a.nC = geo.nC;
@@ -925,8 +1129,9 @@ hipError_t launch_linattn_fwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
     const int dk = static_cast<int>(d.dk), dv = static_cast<int>(d.dv), E = dk * dv;
     if (geo.nC == 0) return copy_state(S0, ST, geo.BH * E, s);
     const size_t size = d.dtype == MGS_BF16 ? 2 : 4;
-    const bool vec = dk % 8 == 0 && dv % 8 == 0 && wide(q, d.q_stride, 3, size) && wide(k, d.k_stride, 3, size) &&
-                     wide(v, d.v_stride, 3, size) && wide(o, nullptr, 0, size);
+    const bool vec = dk % 8 == 0 && dv % 8 == 0 && d.H < (1 << 14) && wide(q, d.q_stride, 3, size) && wide(k, d.k_stride, 3, size) &&
+                     wide(v, d.v_stride, 3, size) && wide(o, nullptr, 0, size) && wide(S0, nullptr, 0, 4) &&
+                     wide(ST, nullptr, 0, 4);
     WalkArgs a = walk_args(geo, d, g, lengths, vec);
     a.nRoles = 1;
     Role &r = a.role[0];
@@ -942,7 +1147,7 @@ hipError_t launch_linattn_fwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
         r.state = S0;
         r.final = ST;
         r.st_bh = E;
-        return launch_walk<false>(d.dtype, a, dk, dv, s);
+        return launch_walk<OUT>(d.dtype, a, dk, dv, s);
     }
     char *w = static_cast<char *>(ws);
     float *S = reinterpret_cast<float *>(w + geo.off_S);
@@ -950,7 +1155,7 @@ hipError_t launch_linattn_fwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
     r.st_seg = E;
     r.local = S;
     a.dec = reinterpret_cast<float *>(w + geo.off_dec);
-    hipError_t e = launch_walk<true>(d.dtype, a, dk, dv, s);
+    hipError_t e = launch_walk<STATE>(d.dtype, a, dk, dv, s);
     if (e != hipSuccess) return e;
     ChainArgs c{};
     c.S = S;
@@ -963,7 +1168,7 @@ hipError_t launch_linattn_fwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
     e = launch_chain(geo, c, 1, s);
     if (e != hipSuccess) return e;
     r.state = S;
-    return launch_walk<false>(d.dtype, a, dk, dv, s);
+    return launch_walk<OUT>(d.dtype, a, dk, dv, s);
 }
 
 hipError_t launch_linattn_bwd(const AttnGeom &geo, const mgs_linattn_desc &d, const void *q, const void *k,
@@ -982,9 +1187,10 @@ hipError_t launch_linattn_bwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
     float *S = at(geo.off_S), *R = geo.nSeg > 1 ? at(geo.off_R) : nullptr;
     float *x = at(geo.off_x), *y = at(geo.off_y);
     const size_t size = d.dtype == MGS_BF16 ? 2 : 4;
-    const bool vec = dk % 8 == 0 && dv % 8 == 0 && wide(q, d.q_stride, 3, size) && wide(k, d.k_stride, 3, size) &&
+    const bool vec = dk % 8 == 0 && dv % 8 == 0 && d.H < (1 << 14) && wide(q, d.q_stride, 3, size) && wide(k, d.k_stride, 3, size) &&
                      wide(v, d.v_stride, 3, size) && wide(do_, d.do_stride, 3, size) && wide(dq, nullptr, 0, size) &&
-                     wide(dk_, nullptr, 0, size) && wide(dv_, nullptr, 0, size);
+                     wide(dk_, nullptr, 0, size) && wide(dv_, nullptr, 0, size) && wide(S0, nullptr, 0, 4) &&
+                     wide(dST, nullptr, 0, 4) && wide(dS0, nullptr, 0, 4);
     WalkArgs a = walk_args(geo, d, g, lengths, vec);
     const Operand oq = operand(q, d.q_stride, d.Hk, d.H, dk), ok = operand(k, d.k_stride, d.Hk, d.H, dk);
     const Operand ov = operand(v, d.v_stride, d.H, d.H, dv), oo = operand(do_, d.do_stride, d.H, d.H, dv);
@@ -1020,7 +1226,7 @@ hipError_t launch_linattn_bwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
         l.role[0].local = S, l.role[0].st_bh = S_bh, l.role[0].st_seg = E;
         l.role[1] = rv;
         l.role[1].local = R;
-        if ((e = launch_walk<true>(d.dtype, l, dk, dv, s)) != hipSuccess) return e;
+        if ((e = launch_walk<STATE>(d.dtype, l, dk, dv, s)) != hipSuccess) return e;
         ChainArgs c{};
         c.S = S, c.R = R, c.dec = l.dec, c.S0 = S0, c.dST = dST, c.dS0 = dS0;
         c.BH = geo.BH, c.nSeg = geo.nSeg, c.E = E;
@@ -1034,17 +1240,12 @@ hipError_t launch_linattn_bwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
         rv.final = dS0;
     }
     // the dq and dk walks reduce over dv, the dv walk over dk
-    a.role[0] = rq, a.role[1] = rk, a.role[2] = rv;
-    if ((dk <= 64) == (dv <= 64)) {
-        a.nRoles = 3;
-        if ((e = launch_walk<false>(d.dtype, a, dv, dk, s)) != hipSuccess) return e;
-    } else {
-        a.nRoles = 2;
-        if ((e = launch_walk<false>(d.dtype, a, dv, dk, s)) != hipSuccess) return e;
-        a.role[0] = rv;
-        a.nRoles = 1;
-        if ((e = launch_walk<false>(d.dtype, a, dk, dv, s)) != hipSuccess) return e;
-    }
+    a.role[0] = rq, a.role[1] = rk;
+    a.nRoles = 2;
+    if ((e = launch_walk<DOTS>(d.dtype, a, dv, dk, s)) != hipSuccess) return e;
+    a.role[0] = rv;
+    a.nRoles = 1;
+    if ((e = launch_walk<OUT>(d.dtype, a, dk, dv, s)) != hipSuccess) return e;
 
     DgArgs m{};
     m.x = x, m.y = y;
