@@ -47,11 +47,14 @@ namespace mgs {
 namespace {
 
 constexpr int kC = kAttnChunk;
-constexpr int kThreads = 256;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 typedef float f4v __attribute__((ext_vector_type(4)));
 typedef float f8v __attribute__((ext_vector_type(8), aligned(16)));
+typedef float f2v __attribute__((ext_vector_type(2)));
+typedef __bf16 bf2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u2v __attribute__((ext_vector_type(2)));
+typedef uint32_t u4v __attribute__((ext_vector_type(4)));
 typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
 typedef short s4v __attribute__((ext_vector_type(4)));
@@ -94,12 +97,23 @@ __device__ __forceinline__ f4v mma2(bf4 a0, bf4 a1, bf4 b0, bf4 b1, f4v c)
 // an fp32 fragment as fragments of T that sum to it, or to its first 16 bits (two of bf16)
 __device__ __forceinline__ void split(f4v x, f4v (&out)[1]) { out[0] = x; }
 
+// two floats rounded to bf16, the first in the low half
+__device__ __forceinline__ uint32_t pack(float x, float y)
+{
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector((f2v{x, y}), bf2));
+}
+
 template <int N> __device__ __forceinline__ void split(f4v x, bf4 (&out)[N])
 {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        out[i] = __builtin_convertvector(x, bf4);
-        x -= __builtin_convertvector(out[i], f4v);
+        u2v p = {pack(x[0], x[1]), pack(x[2], x[3])};
+        // (opaque: the compiler would round each element again for its remainder)
+        asm volatile("" : "+v"(p));
+        out[i] = __builtin_bit_cast(bf4, p);
+        if (i + 1 < N)
+            x -= f4v{__uint_as_float(p[0] << 16), __uint_as_float(p[0] & 0xffff0000u), __uint_as_float(p[1] << 16),
+                     __uint_as_float(p[1] & 0xffff0000u)};
     }
 }
 
@@ -184,9 +198,6 @@ template <typename V> using Global = __attribute__((address_space(1))) V;
 // waiting for all (loads and stores share a counter).
 constexpr uint32_t kReach = 1u << 30, kNowhere = 1u << 31;
 
-typedef uint32_t u2v __attribute__((ext_vector_type(2)));
-typedef uint32_t u4v __attribute__((ext_vector_type(4)));
-
 struct Buffer {
     __amdgpu_buffer_rsrc_t r;
     __device__ __forceinline__ explicit Buffer(int64_t base)
@@ -242,10 +253,10 @@ __device__ __forceinline__ Chunk chunk_at(int ch, int T, int len, int rev)
 // thread and turn.  Rows that are not live are zeros and are not read.  A wide
 // access is a workgroup-uniform chunk address plus a 32-bit lane offset that
 // stays the same from chunk to chunk.
-template <typename T, int DIM, bool VEC> struct Stage {
+template <typename T, int DIM, int THREADS, bool VEC> struct Stage {
     static constexpr int LD = DIM + Num<T>::PAD;
-    static constexpr int PER = kC * DIM / 8 / kThreads;
-    static constexpr int TURN = kThreads / (DIM / 8);   // rows per turn
+    static constexpr int PER = kC * DIM / 8 / THREADS;
+    static constexpr int TURN = THREADS / (DIM / 8);   // rows per turn
     using Vec8 = typename Num<T>::Vec8;
     Vec8 x[PER];
     int64_t base;      // address of (b, 0, h, 0)
@@ -383,36 +394,51 @@ __device__ __forceinline__ void drop_non_finite(typename Num<T>::Frag (&vf)[4][N
 constexpr uint64_t kScoreTiles = 0xFEDCA98540ull;
 
 // KD, VD: the reduction dimension and the output columns, padded.  Each of the
-// 4 waves owns VD / 4 output columns: of the state it keeps S^T tiles
+// VD / 16 waves owns 16 output columns: of the state it keeps S^T tiles
 // (reduction index x column) in accumulators, and it forms the same columns of
 // the output, transposed, so that a lane holds 4 neighbouring columns of a row.
-// The scores are formed once per workgroup and shared through LDS.
+// The scores are formed once per workgroup and shared through LDS.  (With 32
+// columns a wave, half as many waves read LDS half as often, but their registers
+// leave two waves a SIMD, and waits and vector arithmetic then show.)
 // MODE: STATE, the walk from a zero state without outputs; OUT, outputs rounded
 // to T; DOTS, outputs in T or fp32 (partials of shared heads), and the dots of
 // their rows for dg.  An output rounded to bf16 takes two terms (16 bits) of the
 // states and scores, one whose dots make dg all three.
 enum { STATE, OUT, DOTS };
 
+// waves a SIMD that the registers are cut for: as many as LDS lets in
+template <typename T> constexpr int walk_waves(int KD, int VD, int mode)
+{
+    if (sizeof(T) == 4) return mode == STATE && KD + VD <= 192 ? 3 : 2;
+    return VD == 128 ? 4 : mode == STATE ? 4 : KD == 64 ? 3 : 2;
+}
+
 template <typename T, int KD, int VD, int MODE, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) walk_kernel(WalkArgs a)
+__global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kernel(WalkArgs a)
 {
     using N = Num<T>;
     using Frag = typename N::Frag;
     constexpr bool STATE_ONLY = MODE == STATE;
     constexpr int NS = N::NS;                                 // terms of the weighted values
     constexpr int NO = NS == 3 && MODE != DOTS ? 2 : NS;      // terms of states and scores
-    constexpr int NCT = VD / 64;       // 16-column tiles per wave
+    constexpr int kThreads = 4 * VD, NW = VD / 16;
     constexpr int NKB = KD / 16;       // reduction blocks
+    constexpr int NCT = 1;
     constexpr int LK = KD + N::PAD, LV = VD + N::PAD, LA = kC + 4;
     __shared__ __align__(16) T sQ[STATE_ONLY ? 8 : kC * LK];
     __shared__ __align__(16) T sK[kC * LK];
     __shared__ __align__(16) T sV[kC * LV];
     __shared__ __align__(16) T sA[STATE_ONLY ? 1 : NO][STATE_ONLY ? 8 : kC * LA];
     __shared__ __align__(16) Decays sDecays[2];
-    __shared__ float sX[MODE == DOTS ? 4 : 1][kC];
+
+    // the waves' partial dots of row r: in the 16 bytes of padding of the rows r of
+    // the q and k tiles
+    auto partial = [&](int w, int r) -> float & {
+        return reinterpret_cast<float *>((w < 4 ? sQ : sK) + r * LK + KD)[w & 3];
+    };
 
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int li = lane & 15, lq = lane >> 4;
+    int li = lane & 15, lq = lane >> 4;
     // the roles of 8 neighbouring items run side by side, an item's on one XCD:
     // they read the same rows
     const uint32_t rest = blockIdx.x >> 3;
@@ -430,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 2) walk_kernel(WalkArgs a)
     const int rev = keep(ro.rev), cols = keep(ro.v.cols), kcols = keep(ro.k.cols);
     const int T_ = keep(a.T), H_ = keep(a.H);
 
-    const int col0 = wv * (16 * NCT);   // this wave's first column
+    const int col0 = wv * 16;   // this wave's first column
     f4v S[NKB][NCT];
     const float *state = STATE_ONLY ? nullptr : ro.state;
     const int sc = keep(ro.sc), sk = keep(ro.sk);
@@ -474,8 +500,8 @@ __global__ void __launch_bounds__(kThreads, 2) walk_kernel(WalkArgs a)
             for (int i = tid; i < kC * LA; i += kThreads) sA[s][i] = static_cast<T>(0.0f);
     }
 
-    Stage<T, KD, VEC> q, k;
-    Stage<T, VD, VEC> v;
+    Stage<T, KD, kThreads, VEC> q, k;
+    Stage<T, VD, kThreads, VEC> v;
     k.init(ro.k, b, h, rev);
     v.init(ro.v, b, h, rev);
     if constexpr (!STATE_ONLY) q.init(ro.q, b, h, rev);
@@ -488,8 +514,7 @@ __global__ void __launch_bounds__(kThreads, 2) walk_kernel(WalkArgs a)
     const int out_f32 = keep(MODE == DOTS && ro.out_f32 ? 1 : 0);
     const int o_size = out_f32 ? 4 : static_cast<int>(sizeof(T));
     const int64_t o_st = static_cast<int64_t>(H_) * cols * o_size, d_st = keep(ro.dot.st * static_cast<int64_t>(sizeof(T)));
-    const int orow = rev ? kC - 1 - li : li, o_step = rev ? -16 : 16;
-    const int c0 = col0 + 4 * lq;
+    const int o_step = rev ? -16 : 16;
     const int64_t o_base = keep(static_cast<char *>(ro.out) + (b * T_ * H_ + h) * cols * o_size);
     const int64_t d_base = keep(static_cast<const T *>(ro.dot.p) + b * ro.dot.sb + (MODE == DOTS ? h / ro.dot.div : 0) * ro.dot.sh);
     const int64_t xdot = keep(ro.xdot + static_cast<int64_t>(bh) * T_);
@@ -519,6 +544,9 @@ __global__ void __launch_bounds__(kThreads, 2) walk_kernel(WalkArgs a)
 
     float seg_log2 = 0.0f;
     for (int n = 0; n < chunks; ++n) {
+        // (opaque: addresses made of them are cheaper to form again than to keep)
+        asm volatile("" : "+v"(li), "+v"(lq));
+        [[maybe_unused]] const int orow = rev ? kC - 1 - li : li, c0 = col0 + 4 * lq;
         const Decays &sD = sDecays[n & 1];
         k.store(sK);
         v.store(sV);
@@ -526,42 +554,15 @@ __global__ void __launch_bounds__(kThreads, 2) walk_kernel(WalkArgs a)
         lds_barrier();
         const Chunk ck = place(n);
 
-        [[maybe_unused]] Frag dots[MODE == DOTS ? 4 : 1][NCT];
-        if constexpr (MODE == DOTS) {
-            {
-                [[maybe_unused]] const int64_t p = d_base + ck.tb * d_st;
-                const Buffer buf(p);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int r = 16 * i + li;
-                    const bool live = r >= ck.lo && r < ck.hi;
-#pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct) {
-                        const int c = c0 + 16 * ct;
-                        if constexpr (VEC) {
-                            const uint32_t at = (orow + o_step * i) * static_cast<uint32_t>(d_st) + c * static_cast<uint32_t>(sizeof(T));
-                            dots[i][ct] = buf.template load<Frag>(live && c < cols ? at : kNowhere);
-                        } else {
-                            const Global<const T> *x = reinterpret_cast<const Global<const T> *>(p + (orow + o_step * i) * d_st) + c;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                dots[i][ct][e] = static_cast<T>(0.0f);
-                                if (live && c + e < cols) dots[i][ct][e] = x[e];
-                            }
-                        }
-                    }
-                }
-            }
-        }
-        load(n + 1);
-        if (((n + 2) & 3) == wv) load_g(n + 2);
+        if constexpr (STATE_ONLY) load(n + 1);
+        if (((n + 2) & (NW - 1)) == wv) load_g(n + 2);
 
         if constexpr (!STATE_ONLY) {
             // scores: tile (i, j) with rows of q as columns, so that a lane holds
             // 4 neighbouring sources of one row
 #pragma unroll
-            for (int it = 0; it < 3; ++it) {
-                const int slot = wv + 4 * it;
+            for (int it = 0; it < (10 + NW - 1) / NW; ++it) {
+                const int slot = wv + NW * it;
                 if (slot < 10) {
                     const int tile = static_cast<int>((kScoreTiles >> (4 * slot)) & 15);
                     const int i = tile >> 2, j = tile & 3;
@@ -578,8 +579,9 @@ __global__ void __launch_bounds__(kThreads, 2) walk_kernel(WalkArgs a)
                     f4v w;
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float e = __builtin_amdgcn_exp2f((gh - sh[r]) + (gl - sl[r]));
-                        w[r] = src + r <= row ? intra * e * p[r] : 0.0f;
+                        float e = intra * __builtin_amdgcn_exp2f((gh - sh[r]) + (gl - sl[r])) * p[r];
+                        asm volatile("" : "+v"(e));   // (computed for every lane: a branch costs more)
+                        w[r] = src + r <= row ? e : 0.0f;
                     }
                     Frag ws[NO];
                     split(w, ws);
@@ -613,6 +615,34 @@ __global__ void __launch_bounds__(kThreads, 2) walk_kernel(WalkArgs a)
                         for (int ct = 0; ct < NCT; ++ct) O[i][ct] = mma2(s0[ct][s], s1[ct][s], q0, q1, O[i][ct]);
                 }
             }
+            [[maybe_unused]] Frag dots[MODE == DOTS ? 4 : 1][NCT];
+            if constexpr (MODE == DOTS) {
+                {
+                    [[maybe_unused]] const int64_t p = d_base + ck.tb * d_st;
+                    const Buffer buf(p);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 16 * i + li;
+                        const bool live = r >= ck.lo && r < ck.hi;
+#pragma unroll
+                        for (int ct = 0; ct < NCT; ++ct) {
+                            const int c = c0 + 16 * ct;
+                            if constexpr (VEC) {
+                                const uint32_t at = (orow + o_step * i) * static_cast<uint32_t>(d_st) + c * static_cast<uint32_t>(sizeof(T));
+                                dots[i][ct] = buf.template load<Frag>(live && c < cols ? at : kNowhere);
+                            } else {
+                                const Global<const T> *x = reinterpret_cast<const Global<const T> *>(p + (orow + o_step * i) * d_st) + c;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    dots[i][ct][e] = static_cast<T>(0.0f);
+                                    if (live && c + e < cols) dots[i][ct][e] = x[e];
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+            load(n + 1);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float w = inter * __builtin_amdgcn_exp2f(sD.hi[16 * i + li]);
@@ -696,7 +726,7 @@ __global__ void __launch_bounds__(kThreads, 2) walk_kernel(WalkArgs a)
                     float dot = (x[0] + x[1]) + (x[2] + x[3]);
                     dot += __shfl_xor(dot, 16, 64);
                     dot += __shfl_xor(dot, 32, 64);
-                    if (lq == 0) sX[wv][16 * i + li] = dot;
+                    if (lq == 0) partial(wv, 16 * i + li) = dot;
                 }
             }
         }
@@ -729,11 +759,15 @@ __global__ void __launch_bounds__(kThreads, 2) walk_kernel(WalkArgs a)
             }
         }
         if constexpr (STATE_ONLY) seg_log2 += sD.log2_total;
-        if (((n + 1) & 3) == wv) chunk_decays(g, src_f, rev, sDecays[(n + 1) & 1]);
+        if (((n + 1) & (NW - 1)) == wv) chunk_decays(g, src_f, rev, sDecays[(n + 1) & 1]);
         lds_barrier();
         if constexpr (MODE == DOTS) {
-            if (tid < ck.rows)
-                reinterpret_cast<Global<float> *>(xdot)[ck.tb + (rev ? kC - 1 - tid : tid)] = (sX[0][tid] + sX[1][tid]) + (sX[2][tid] + sX[3][tid]);
+            if (tid < ck.rows) {
+                float x = 0.0f;
+#pragma unroll
+                for (int w = 0; w < NW; ++w) x += partial(w, tid);
+                reinterpret_cast<Global<float> *>(xdot)[ck.tb + (rev ? kC - 1 - tid : tid)] = x;
+            }
         }
     }
 
@@ -1006,7 +1040,7 @@ unsigned walk_grid(int64_t items, int roles)
 template <typename T, int MODE, bool VEC>
 hipError_t launch_walk(const WalkArgs &a, int kdim, int vdim, hipStream_t s)
 {
-    const dim3 grid(walk_grid(a.items, a.nRoles)), block(kThreads);
+    const dim3 grid(walk_grid(a.items, a.nRoles)), block(vdim <= 64 ? 256 : 512);
     if (kdim <= 64 && vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 64, MODE, VEC>), grid, block, 0, s, a);
     else if (kdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 128, MODE, VEC>), grid, block, 0, s, a);
     else if (vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 128, 64, MODE, VEC>), grid, block, 0, s, a);
