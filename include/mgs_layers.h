@@ -153,7 +153,7 @@ mgs_status mgs_rmsnorm_bwd(const void *dy, const void *h, const void *w, const f
  * equal in[i] (in place), and no other overlaps are allowed.  Where the norm is
  * not finite the tensors are passed through unscaled and norm says so.  With
  * out == NULL only the norm is computed.  max_norm < 0 or NaN is refused.
- *   norm : (1) fp32 out.
+ *   norm : one fp32 out.
  */
 mgs_status mgs_clip_norm_workspace_size(int64_t n, const int64_t *sizes, size_t *bytes);
 

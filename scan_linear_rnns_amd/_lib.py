@@ -29,10 +29,6 @@ class LinattnDesc(ctypes.Structure):
         (n, _I64 * 3) for n in ("q_stride", "k_stride", "v_stride", "do_stride", "g_stride")]
 
 
-_DESC = ctypes.POINTER(LinattnDesc)
-_PP = ctypes.POINTER(_P)
-_I64P = ctypes.POINTER(_I64)
-
 SIGNATURES = {
     "mgs_version": ([], _INT),
     "mgs_status_string": ([_INT], ctypes.c_char_p),
@@ -62,16 +58,16 @@ SIGNATURES = {
     "mgs_delta_workspace_size": ([_I64, _I64, _I64, ctypes.POINTER(_SZ)], _INT),
     "mgs_delta_fwd": ([_P, _P, _P, _P, _P, _P, _P, _I64, _I64, _I64, _P, _SZ, _P], _INT),
     # include/mgs_layers.h
-    "mgs_linattn_workspace_size": ([_DESC, _INT, ctypes.POINTER(_SZ)], _INT),
-    "mgs_linattn_fwd": ([_DESC] + [_P] * 8 + [_P, _SZ, _P], _INT),
-    "mgs_linattn_bwd": ([_DESC] + [_P] * 13 + [_P, _SZ, _P], _INT),
-    "mgs_linattn_step": ([_DESC] + [_P] * 5 + [_I64, _P, _P, _P], _INT),
+    "mgs_linattn_workspace_size": ([_P, _INT, ctypes.POINTER(_SZ)], _INT),
+    "mgs_linattn_fwd": ([_P] + [_P] * 8 + [_P, _SZ, _P], _INT),
+    "mgs_linattn_bwd": ([_P] + [_P] * 13 + [_P, _SZ, _P], _INT),
+    "mgs_linattn_step": ([_P] + [_P] * 5 + [_I64, _P, _P, _P], _INT),
     "mgs_rmsnorm_fwd": ([_P] * 6 + [_I64] * 4 + [_F32, _INT, _P], _INT),
     "mgs_rmsnorm_fwd_fp8": ([_P] * 6 + [_I64] * 4 + [_F32, _I64, _INT, _P], _INT),
     "mgs_rmsnorm_workspace_size": ([_I64, _I64, ctypes.POINTER(_SZ)], _INT),
     "mgs_rmsnorm_bwd": ([_P] * 7 + [_I64, _I64, _INT, _P, _SZ, _P], _INT),
-    "mgs_clip_norm_workspace_size": ([_I64, _I64P, ctypes.POINTER(_SZ)], _INT),
-    "mgs_clip_norm": ([_I64, _PP, _PP, _I64P, ctypes.POINTER(_INT), _F32, _P, _P, _SZ, _P], _INT),
+    "mgs_clip_norm_workspace_size": ([_I64, _P, ctypes.POINTER(_SZ)], _INT),
+    "mgs_clip_norm": ([_I64, _P, _P, _P, _P, _F32, _P, _P, _SZ, _P], _INT),
 }
 
 _lib = None

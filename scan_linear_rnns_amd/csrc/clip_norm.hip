@@ -36,15 +36,13 @@ struct ClipTable {
     int64_t base;              // this launch's first tile among all
 };
 
+// The tensor that holds a tile: every lane looks at two first tiles (which are
+// in rising order), so that the search is one load deep.
 __device__ __forceinline__ int tensor_of(const ClipTable &t, int tile)
 {
-    int lo = 0, hi = t.n - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (t.first[mid] <= tile) lo = mid;
-        else hi = mid - 1;
-    }
-    return lo;
+    const int lane = threadIdx.x & 63;
+    const bool a = lane < t.n && t.first[lane] <= tile, b = lane + 64 < t.n && t.first[lane + 64] <= tile;
+    return __builtin_amdgcn_readfirstlane(__popcll(__ballot(a)) + __popcll(__ballot(b)) - 1);
 }
 
 __device__ __forceinline__ double block_sum(double v, double *lds)
@@ -60,23 +58,35 @@ __device__ __forceinline__ double block_sum(double v, double *lds)
 __device__ __forceinline__ f8v widen(f8v v) { return v; }
 __device__ __forceinline__ f8v widen(bf8v v) { return __builtin_convertvector(v, f8v); }
 
+__device__ __forceinline__ double square8(f8v x)
+{
+    float s = 0.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = __builtin_fmaf(x[e], x[e], s);
+    return static_cast<double>(s);
+}
+
+// n elements of a tile: whole accesses of 8, those of a full tile all in flight;
+// single ones at the end, or where the address is not aligned
 template <typename T, typename V> __device__ __forceinline__ double tile_squares(const T *p, int n, bool vec)
 {
     double sum = 0.0;
-    if (vec && n == kTile) {
+    int done = 0;
+    if (vec) {
+        const V *v = reinterpret_cast<const V *>(p);
+        if (n == kTile) {
 #pragma unroll
-        for (int i = 0; i < kTile / 2048; ++i) {
-            const f8v x = widen(*reinterpret_cast<const V *>(p + i * 2048 + threadIdx.x * 8));
-            float s = 0.0f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s = __builtin_fmaf(x[e], x[e], s);
-            sum += static_cast<double>(s);
+            for (int i = 0; i < kTile / 2048; ++i) sum += square8(widen(v[i * 256 + threadIdx.x]));
+            return sum;
         }
-    } else {
-        for (int i = threadIdx.x; i < n; i += 256) {
-            const float x = static_cast<float>(p[i]);
-            sum += static_cast<double>(x * x);
-        }
+        done = n & ~7;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < done / 8; i += 256) sum += square8(widen(v[i]));
+    }
+#pragma unroll 8
+    for (int i = done + threadIdx.x; i < n; i += 256) {
+        const float x = static_cast<float>(p[i]);
+        sum += static_cast<double>(x * x);
     }
     return sum;
 }
@@ -111,18 +121,29 @@ __global__ void __launch_bounds__(256) norm_kernel(const double *part, int64_t n
 template <typename T, typename V>
 __device__ __forceinline__ void tile_scale(const T *p, T *o, int n, float c, bool vec)
 {
-    if (vec && n == kTile) {
+    int done = 0;
+    if (vec) {
+        const V *v = reinterpret_cast<const V *>(p);
+        V *w = reinterpret_cast<V *>(o);
+        if (n == kTile) {
+            V x[kTile / 2048];
 #pragma unroll
-        for (int i = 0; i < kTile / 2048; ++i) {
-            const int e = i * 2048 + threadIdx.x * 8;
-            *reinterpret_cast<V *>(o + e) = __builtin_convertvector(widen(*reinterpret_cast<const V *>(p + e)) * c, V);
+            for (int i = 0; i < kTile / 2048; ++i) x[i] = v[i * 256 + threadIdx.x];
+#pragma unroll
+            for (int i = 0; i < kTile / 2048; ++i) w[i * 256 + threadIdx.x] = __builtin_convertvector(widen(x[i]) * c, V);
+            return;
         }
-    } else {
-        for (int i = threadIdx.x; i < n; i += 256) o[i] = static_cast<T>(static_cast<float>(p[i]) * c);
+        done = n & ~7;
+#pragma unroll 4
+        for (int i = threadIdx.x; i < done / 8; i += 256) w[i] = __builtin_convertvector(widen(v[i]) * c, V);
     }
+#pragma unroll 8
+    for (int i = done + threadIdx.x; i < n; i += 256) o[i] = static_cast<T>(static_cast<float>(p[i]) * c);
 }
 
-// few != 0: the norm is added up here, and workgroup 0 of the first launch writes it
+// few != 0: the norm is added up here, and the first workgroup of the first launch
+// writes it.  The tensors come in the reverse of the first pass's order, and so do
+// the tiles of each: what that pass read last is still in the memory-side cache.
 __global__ void __launch_bounds__(256) scale_kernel(ClipTable t, const double *part, int64_t n_part, float max_norm,
                                                     float *norm, int few)
 {
@@ -130,7 +151,7 @@ __global__ void __launch_bounds__(256) scale_kernel(ClipTable t, const double *p
     float v;
     if (few) {
         v = norm_of(part, n_part, lds);
-        if (t.base + blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
+        if (t.base == 0 && blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
     } else {
         v = *norm;
     }
@@ -138,7 +159,8 @@ __global__ void __launch_bounds__(256) scale_kernel(ClipTable t, const double *p
     if (!(c < 1.0f) || !isfinite(v)) c = 1.0f;
     const int i = tensor_of(t, blockIdx.x);
     if (c == 1.0f && t.in[i] == t.out[i]) return;
-    const int64_t at = static_cast<int64_t>(static_cast<int>(blockIdx.x) - t.first[i]) * kTile;
+    const int64_t last = (t.size[i] - 1) / kTile;
+    const int64_t at = (last - (static_cast<int>(blockIdx.x) - t.first[i])) * kTile;
     const int n = static_cast<int>(min(static_cast<int64_t>(kTile), t.size[i] - at));
     if (t.bf16[i])
         tile_scale<__bf16, bf8v>(static_cast<const __bf16 *>(t.in[i]) + at, static_cast<__bf16 *>(t.out[i]) + at, n, c, t.vec[i]);
@@ -146,20 +168,22 @@ __global__ void __launch_bounds__(256) scale_kernel(ClipTable t, const double *p
         tile_scale<float, f8v>(static_cast<const float *>(t.in[i]) + at, static_cast<float *>(t.out[i]) + at, n, c, t.vec[i]);
 }
 
-// Calls f(table, tiles) for each group of up to kClipTensors non-empty tensors
-// whose tiles fit one grid.
+// Calls f(table, tiles) for each group of up to kClipTensors non-empty tensors,
+// from the first on, or from the last back.
 template <typename F>
-hipError_t each_launch(int64_t n, const void *const *in, void *const *out, const int64_t *sizes, const int *dtypes, F f)
+hipError_t each_launch(int64_t n, const void *const *in, void *const *out, const int64_t *sizes, const int *dtypes,
+                       bool back, F f)
 {
     ClipTable t{};
     int64_t base = 0, tiles = 0;
-    for (int64_t i = 0; i < n; ++i) {
+    for (int64_t j = 0; j < n; ++j) {
+        const int64_t i = back ? n - 1 - j : j;
         if (sizes[i] == 0) continue;
         t.in[t.n] = in[i];
         t.out[t.n] = out ? out[i] : nullptr;
         t.size[t.n] = sizes[i];
         t.first[t.n] = static_cast<int>(tiles);
-        t.bf16[t.n] = dtypes[i] == MGS_BF16;
+        t.bf16[t.n] = dtypes[i] == MGS_BF16 ? 1 : 0;
         t.vec[t.n] = ((reinterpret_cast<uintptr_t>(in[i]) | reinterpret_cast<uintptr_t>(t.out[t.n])) & 15u) == 0;
         ++t.n;
         tiles += (sizes[i] + kTile - 1) / kTile;
@@ -190,7 +214,7 @@ hipError_t launch_clip_norm(int64_t n, const void *const *in, void *const *out, 
                             const int *dtypes, float max_norm, float *norm, void *ws, int64_t tiles, hipStream_t s)
 {
     double *part = static_cast<double *>(ws);
-    hipError_t e = each_launch(n, in, nullptr, sizes, dtypes, [&](const ClipTable &t, unsigned grid) {
+    hipError_t e = each_launch(n, in, nullptr, sizes, dtypes, false, [&](const ClipTable &t, unsigned grid) {
         hipLaunchKernelGGL(squares_kernel, dim3(grid), dim3(256), 0, s, t, part);
         return hipGetLastError();
     });
@@ -201,7 +225,7 @@ hipError_t launch_clip_norm(int64_t n, const void *const *in, void *const *out, 
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (!out) return hipSuccess;
-    return each_launch(n, in, out, sizes, dtypes, [&](const ClipTable &t, unsigned grid) {
+    return each_launch(n, in, out, sizes, dtypes, true, [&](const ClipTable &t, unsigned grid) {
         hipLaunchKernelGGL(scale_kernel, dim3(grid), dim3(256), 0, s, t, part, tiles, max_norm, norm, few);
         return hipGetLastError();
     });

@@ -856,7 +856,7 @@ struct DgArgs {
     const int32_t *lengths;
     float *dg;                    // (B,T,H), or per-head partials (B,H,nSeg)
     int64_t s_bh, s_seg, r_bh, r_seg;   // strides of S (from slot 1 on) and R
-    int T, H, nSeg, segLen, E, per_head;
+    int T, H, nSeg, segLen, E, per_head, vec;   // vec: E is a multiple of 8, S and R are 16-byte aligned
 };
 
 __device__ __forceinline__ double block_sum(double v, double *lds)
@@ -884,7 +884,30 @@ __global__ void __launch_bounds__(256) dg_kernel(DgArgs a)
     double flux = 0.0;
     if (a.R) {
         const float *S = a.S + bh * a.s_bh + seg * a.s_seg, *R = a.R + bh * a.r_bh + seg * a.r_seg;
-        for (int e = tid; e < a.E; e += 256) flux += static_cast<double>(S[e]) * static_cast<double>(R[e]);
+        if (a.vec) {   // four wide loads of each in flight
+            double part[4] = {0.0, 0.0, 0.0, 0.0};
+            int e = 4 * tid;
+            for (; e + 3 * 1024 < a.E; e += 4 * 1024) {
+                f4v x[4], y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[i] = *reinterpret_cast<const f4v *>(S + e + 1024 * i);
+                    y[i] = *reinterpret_cast<const f4v *>(R + e + 1024 * i);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) part[i] += static_cast<double>(x[i][j]) * static_cast<double>(y[i][j]);
+            }
+            for (; e < a.E; e += 1024) {
+                const f4v x = *reinterpret_cast<const f4v *>(S + e), y = *reinterpret_cast<const f4v *>(R + e);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) part[j] += static_cast<double>(x[j]) * static_cast<double>(y[j]);
+            }
+            flux = (part[0] + part[1]) + (part[2] + part[3]);
+        } else {
+            for (int e = tid; e < a.E; e += 256) flux += static_cast<double>(S[e]) * static_cast<double>(R[e]);
+        }
     }
     flux = block_sum(flux, red);
 
@@ -948,9 +971,9 @@ __global__ void __launch_bounds__(256) group_sum_kernel(const float *p0, const f
 }
 
 // -------------------------------------------------------------------- a step
-// One workgroup per (sequence, head, 16 rows of the state), a wave 4 rows: 16
-// lanes a row, each 4 (dk <= 64) or 2 x 4 elements.  The state is read and
-// written once; everything else is small.
+// One workgroup per (sequence, head, 16 R rows of the state): 16 lanes a row,
+// each 4 (dk <= 64) or 2 x 4 neighbouring elements of R rows.  The state is
+// read and written once; everything else is small.
 struct StepArgs {
     const void *q, *k, *v;
     const float *g;
@@ -963,61 +986,89 @@ struct StepArgs {
     float scale;
 };
 
-template <typename T, int NV>
+template <typename T, int NV, int R, bool VEC>
 __global__ void __launch_bounds__(256) step_kernel(StepArgs a)
 {
-    const int tid = threadIdx.x, li = tid & 15, row = tid >> 4;
-    const int64_t bh = blockIdx.x / a.tiles;
-    const int r = static_cast<int>(blockIdx.x - bh * a.tiles) * 16 + row;
+    using Frag = typename Num<T>::Frag;
+    const int li = threadIdx.x & 15, row = threadIdx.x >> 4;
+    const uint32_t bh = blockIdx.x / a.tiles;
+    const int r0 = static_cast<int>(blockIdx.x - bh * a.tiles) * (16 * R) + row;
     const int64_t b = bh / a.H;
-    const int h = static_cast<int>(bh - b * a.H);
+    const int h = static_cast<int>(bh % a.H);
     const int64_t slot = a.slots ? a.slots[b] : b;
     const bool live = slot >= 0 && slot < a.n_slots;
-    if (r >= a.dv) return;   // whole groups of 16 lanes, which the shuffles below stay within
-    T *o = static_cast<T *>(a.o) + (b * a.H + h) * static_cast<int64_t>(a.dv) + r;
+    T *o = static_cast<T *>(a.o) + static_cast<int64_t>(bh) * a.dv;
     if (!live) {
-        if (li == 0) *o = static_cast<T>(0.0f);
+#pragma unroll
+        for (int j = 0; j < R; ++j)
+            if (li == 0 && r0 + 16 * j < a.dv) o[r0 + 16 * j] = static_cast<T>(0.0f);
         return;
     }
+    float *S = a.S + (slot * a.H + h) * static_cast<int64_t>(a.dv) * a.dk;
+    // the state first: all its loads in flight before anything waits
+    f4v s[R][NV];
+#pragma unroll
+    for (int j = 0; j < R; ++j)
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int r = r0 + 16 * j, c = 64 * n + 4 * li;
+            s[j][n] = f4v{0, 0, 0, 0};
+            if constexpr (VEC) {
+                if (r < a.dv && c < a.dk) s[j][n] = __builtin_nontemporal_load(reinterpret_cast<const f4v *>(S + r * a.dk + c));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (r < a.dv && c + e < a.dk) s[j][n][e] = S[r * a.dk + c + e];
+            }
+        }
     const T *q = static_cast<const T *>(a.q) + b * a.qb + (h / a.div) * a.qh;
     const T *k = static_cast<const T *>(a.k) + b * a.kb + (h / a.div) * a.kh;
-    const float v = to_f32(static_cast<const T *>(a.v)[b * a.vb + h * a.vh + r]);
-    const float dec = __builtin_amdgcn_exp2f(a.g[b * a.gb + h * a.gh] * kLog2e);
-    float *S = a.S + ((slot * a.H + h) * static_cast<int64_t>(a.dv) + r) * a.dk;
-    float dot = 0.0f;
-    const bool vec = a.vec != 0;   // 16-byte accesses of the state
+    const T *v = static_cast<const T *>(a.v) + b * a.vb + h * a.vh;
+    f4v qf[NV], kf[NV];
 #pragma unroll
     for (int n = 0; n < NV; ++n) {
         const int c = 64 * n + 4 * li;
-        float s[4] = {0, 0, 0, 0};
-        if (vec) {
+        qf[n] = kf[n] = f4v{0, 0, 0, 0};
+        if constexpr (VEC) {
             if (c < a.dk) {
-                const f4v x = *reinterpret_cast<const f4v *>(S + c);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s[e] = x[e];
+                qf[n] = __builtin_convertvector(*reinterpret_cast<const Frag *>(q + c), f4v);
+                kf[n] = __builtin_convertvector(*reinterpret_cast<const Frag *>(k + c), f4v);
             }
         } else {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (c + e < a.dk) s[e] = S[c + e];
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            if (c + e < a.dk) {
-                s[e] = __builtin_fmaf(v, to_f32(k[c + e]), dec * s[e]);
-                dot = __builtin_fmaf(s[e], to_f32(q[c + e]), dot);
-            }
-        if (vec) {
-            if (c < a.dk) *reinterpret_cast<f4v *>(S + c) = f4v{s[0], s[1], s[2], s[3]};
-        } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (c + e < a.dk) S[c + e] = s[e];
+                if (c + e < a.dk) {
+                    qf[n][e] = to_f32(q[c + e]);
+                    kf[n][e] = to_f32(k[c + e]);
+                }
         }
     }
+    const float dec = __builtin_amdgcn_exp2f(a.g[b * a.gb + h * a.gh] * kLog2e);
 #pragma unroll
-    for (int off = 1; off < 16; off <<= 1) dot += __shfl_xor(dot, off, 64);
-    if (li == 0) *o = static_cast<T>(a.scale * dot);
+    for (int j = 0; j < R; ++j) {
+        const int r = r0 + 16 * j;
+        const float vr = r < a.dv ? to_f32(v[r]) : 0.0f;
+        float dot = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            const int c = 64 * n + 4 * li;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                s[j][n][e] = __builtin_fmaf(vr, kf[n][e], dec * s[j][n][e]);
+                if (c + e < a.dk) dot = __builtin_fmaf(s[j][n][e], qf[n][e], dot);
+            }
+            if constexpr (VEC) {
+                if (r < a.dv && c < a.dk) __builtin_nontemporal_store(s[j][n], reinterpret_cast<f4v *>(S + r * a.dk + c));
+            } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (r < a.dv && c + e < a.dk) S[r * a.dk + c + e] = s[j][n][e];
+            }
+        }
+#pragma unroll
+        for (int off = 1; off < 16; off <<= 1) dot += __shfl_xor(dot, off, 64);
+        if (li == 0 && r < a.dv) o[r] = static_cast<T>(a.scale * dot);
+    }
 }
 
 // --------------------------------------------------------------------- host
@@ -1029,7 +1080,7 @@ bool wide(const void *p, const int64_t *st, int n, size_t size)
     if (reinterpret_cast<uintptr_t>(p) & 15u) return false;
     for (int i = 0; i < n; ++i)
         if ((static_cast<size_t>(st[i]) * size) & 15u) return false;
-    return n < 2 || st[1] < (int64_t(1) << 21);
+    return n < 3 || st[1] < (int64_t(1) << 21);
 }
 
 unsigned walk_grid(int64_t items, int roles)
@@ -1056,6 +1107,20 @@ hipError_t launch_walk(int dtype, const WalkArgs &a, int kdim, int vdim, hipStre
                      : launch_walk<__bf16, MODE, false>(a, kdim, vdim, s);
     return a.vec ? launch_walk<float, MODE, true>(a, kdim, vdim, s)
                  : launch_walk<float, MODE, false>(a, kdim, vdim, s);
+}
+
+template <typename T, int NV, int R> hipError_t launch_step(const StepArgs &a, int64_t heads, hipStream_t s)
+{
+    const dim3 grid(static_cast<unsigned>(heads * a.tiles)), block(256);
+    if (a.vec) hipLaunchKernelGGL((step_kernel<T, NV, R, true>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((step_kernel<T, NV, R, false>), grid, block, 0, s, a);
+    return hipGetLastError();
+}
+
+template <typename T> hipError_t launch_step(const StepArgs &a, int64_t heads, int rows, hipStream_t s)
+{
+    if (a.dk <= 64) return rows == 4 ? launch_step<T, 1, 4>(a, heads, s) : launch_step<T, 1, 1>(a, heads, s);
+    return rows == 4 ? launch_step<T, 2, 4>(a, heads, s) : launch_step<T, 2, 1>(a, heads, s);
 }
 
 size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -1291,6 +1356,7 @@ hipError_t launch_linattn_bwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
     m.dg = d.decay_per_head ? at(geo.off_dg) : dg;
     m.T = a.T, m.H = H, m.nSeg = geo.nSeg, m.segLen = geo.segLen, m.E = E;
     m.per_head = d.decay_per_head != 0;
+    m.vec = E % 8 == 0 && wide(dST, nullptr, 0, 4);
     hipLaunchKernelGGL(dg_kernel, dim3(static_cast<unsigned>(a.items)), dim3(256), 0, s, m);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if (d.decay_per_head) {
@@ -1324,18 +1390,16 @@ hipError_t launch_linattn_step(const mgs_linattn_desc &d, const void *q, const v
     a.gh = d.decay_per_head ? 1 : d.g_stride[2];
     a.H = static_cast<int>(d.H), a.div = static_cast<int>(d.H / d.Hk);
     a.dk = static_cast<int>(d.dk), a.dv = static_cast<int>(d.dv);
-    a.tiles = (a.dv + 15) / 16;
-    a.vec = (a.dk & 3) == 0 && wide(S, nullptr, 0, 4);
+    // 4 rows a thread keep more of the state in flight, 1 spreads a small batch
+    // over more of the chip
+    const int rows = d.B * d.H * ((a.dv + 15) / 16) >= 4096 ? 4 : 1;
+    a.tiles = (a.dv + 16 * rows - 1) / (16 * rows);
+    const size_t size = d.dtype == MGS_BF16 ? 2 : 4;
+    const int64_t sq[2] = {a.qb, a.qh}, sk[2] = {a.kb, a.kh};
+    a.vec = a.dk % 8 == 0 && wide(S, nullptr, 0, 4) && wide(q, sq, 2, size) && wide(k, sk, 2, size);
     a.scale = d.scale;
-    const dim3 grid(static_cast<unsigned>(d.B * d.H * a.tiles)), block(256);
-    if (d.dtype == MGS_BF16) {
-        if (a.dk <= 64) hipLaunchKernelGGL((step_kernel<__bf16, 1>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((step_kernel<__bf16, 2>), grid, block, 0, s, a);
-    } else {
-        if (a.dk <= 64) hipLaunchKernelGGL((step_kernel<float, 1>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((step_kernel<float, 2>), grid, block, 0, s, a);
-    }
-    return hipGetLastError();
+    if (d.dtype == MGS_BF16) return launch_step<__bf16>(a, d.B * d.H, rows, s);
+    return launch_step<float>(a, d.B * d.H, rows, s);
 }
 
 }  // namespace mgs

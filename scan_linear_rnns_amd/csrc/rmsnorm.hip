@@ -187,10 +187,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_fwd_kernel(NormArg
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             const int c = (i * TPR + t) * 8;
-            const float scale = fmaxf(m[i], kAmaxFloor) / kE4m3Max;
-            f8v q;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) q[e] = h[i][e] / scale;
+            // y / scale as y times 448 / max: one division a thread and turn; two ulps
+            // of fp32 ahead of a rounding to 4 bits
+            const float amax = fmaxf(m[i], kAmaxFloor), scale = amax / kE4m3Max, inv = kE4m3Max / amax;
+            const f8v q = h[i] * inv;
             uint32_t lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
             lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
             uint32_t hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
@@ -213,8 +213,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_fwd_kernel(NormArg
 
 // ---------------------------------------------------------------- gradient
 // A workgroup walks rows blockIdx.x RPW + sub, + gridDim.x RPW, ... and keeps
-// its sums of dw in registers; each writes one row of partials, which the
-// second kernel adds up in order.
+// its sums of dw in registers; it writes one row of partials, which the second
+// kernel adds up in order.
 struct NormBwdArgs {
     const void *dy, *h, *w, *dh;
     const float *rstd;
@@ -224,13 +224,33 @@ struct NormBwdArgs {
     int d, vec;
 };
 
+// 8 elements as they are stored
+template <typename T> struct Raw;
+template <> struct Raw<float> { using V = f8v; };
+template <> struct Raw<__bf16> { using V = bf8v; };
+
+template <typename T> __device__ __forceinline__ typename Raw<T>::V raw8(const T *p, int n, bool vec)
+{
+    typename Raw<T>::V v = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (vec) {
+        if (n > 0) v = *reinterpret_cast<const typename Raw<T>::V *>(p);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) v[i] = p[i];
+    }
+    return v;
+}
+
 template <typename T, int TPR, int ITER>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_bwd_kernel(NormBwdArgs a)
 {
     constexpr int RPW = TPR < 256 ? 256 / TPR : 1;
+    using V = typename Raw<T>::V;
     __shared__ float lds[16];
+    __shared__ __align__(16) float sum[RPW > 1 ? (RPW - 1) * TPR * 8 * ITER : 1];
     const int t = threadIdx.x % TPR, sub = threadIdx.x / TPR;
-    const bool vec = a.vec != 0;
+    const bool vec = a.vec != 0, more = a.dh != nullptr;
     f8v w[ITER], dw[ITER];
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
@@ -239,17 +259,33 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_bwd_kernel(NormBwd
         dw[i] = f8v{0, 0, 0, 0, 0, 0, 0, 0};
     }
     const int64_t step = static_cast<int64_t>(gridDim.x) * RPW;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * RPW + sub; row < a.rows; row += step) {
-        const T *dy = static_cast<const T *>(a.dy) + row * a.d, *h = static_cast<const T *>(a.h) + row * a.d;
-        const float rstd = a.rstd[row];
-        f8v hv[ITER], ev[ITER];
-        float dot = 0.0f;
+    // the next row's elements travel while this row's are reduced
+    V hn[ITER], en[ITER], dn[ITER];
+    float rn = 0.0f;
+    auto fetch = [&](int64_t row) {
+        if (row >= a.rows) return;
+        rn = a.rstd[row];
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             const int c = (i * TPR + t) * 8;
-            hv[i] = load8(h + c, a.d - c, vec);
-            ev[i] = load8(dy + c, a.d - c, vec);
+            hn[i] = raw8(static_cast<const T *>(a.h) + row * a.d + c, a.d - c, vec);
+            en[i] = raw8(static_cast<const T *>(a.dy) + row * a.d + c, a.d - c, vec);
+            if (more) dn[i] = raw8(static_cast<const T *>(a.dh) + row * a.d + c, a.d - c, vec);
         }
+    };
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * RPW + sub;
+    fetch(first);
+    for (int64_t row = first; row < a.rows; row += step) {
+        const float rstd = rn;
+        f8v hv[ITER], ev[ITER], dv[ITER];
+        float dot = 0.0f;
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            hv[i] = __builtin_convertvector(hn[i], f8v);
+            ev[i] = __builtin_convertvector(en[i], f8v);
+            if (more) dv[i] = __builtin_convertvector(dn[i], f8v);
+        }
+        fetch(row + step);
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             dw[i] += ev[i] * (hv[i] * rstd);
@@ -259,17 +295,27 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_bwd_kernel(NormBwd
         }
         dot = row_reduce<TPR, false>(dot, lds);
         const float f = rstd * rstd * (dot / static_cast<float>(a.d));
-        const T *dh = static_cast<const T *>(a.dh) + row * a.d;
         T *dx = static_cast<T *>(a.dx) + row * a.d;
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             const int c = (i * TPR + t) * 8;
             f8v v = rstd * (ev[i] - hv[i] * f);
-            if (a.dh) v += load8(dh + c, a.d - c, vec);
+            if (more) v += dv[i];
             store8(dx + c, v, a.d - c, vec);
         }
     }
-    float *part = a.part + (static_cast<int64_t>(blockIdx.x) * RPW + sub) * a.d;
+    if constexpr (RPW > 1) {   // the workgroup's rows share one row of partials
+        if (sub > 0)
+#pragma unroll
+            for (int i = 0; i < ITER; ++i) *reinterpret_cast<f8v *>(&sum[((sub - 1) * ITER + i) * TPR * 8 + t * 8]) = dw[i];
+        __syncthreads();
+        if (sub > 0) return;
+#pragma unroll
+        for (int j = 0; j + 1 < RPW; ++j)
+#pragma unroll
+            for (int i = 0; i < ITER; ++i) dw[i] += *reinterpret_cast<const f8v *>(&sum[(j * ITER + i) * TPR * 8 + t * 8]);
+    }
+    float *part = a.part + static_cast<int64_t>(blockIdx.x) * a.d;
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
         const int c = (i * TPR + t) * 8;
@@ -277,13 +323,13 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_bwd_kernel(NormBwd
     }
 }
 
-// dw: 64 columns per workgroup, each of its 4 waves a quarter of the partials
-__global__ void __launch_bounds__(256) dw_kernel(const float *part, float *dw, int n, int d)
+// dw: 64 columns per workgroup, each of its 16 waves a sixteenth of the partials
+__global__ void __launch_bounds__(1024) dw_kernel(const float *part, float *dw, int n, int d)
 {
-    __shared__ float lds[4][64];
+    __shared__ float lds[16][64];
     const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
     const int c = blockIdx.x * 64 + lane;
-    const int per = (n + 3) / 4, lo = wv * per, hi = min(n, lo + per);
+    const int per = (n + 15) / 16, lo = min(n, wv * per), hi = min(n, lo + per);
     float s[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     if (c < d) {
         const float *p = part + c;
@@ -295,7 +341,12 @@ __global__ void __launch_bounds__(256) dw_kernel(const float *part, float *dw, i
     }
     lds[wv][lane] = ((s[0] + s[1]) + (s[2] + s[3])) + ((s[4] + s[5]) + (s[6] + s[7]));
     __syncthreads();
-    if (wv == 0 && c < d) dw[c] = (lds[0][lane] + lds[1][lane]) + (lds[2][lane] + lds[3][lane]);
+    if (wv == 0 && c < d) {
+        float x = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x += lds[i][lane];
+        dw[c] = x;
+    }
 }
 
 bool wide(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -307,6 +358,7 @@ template <typename F> hipError_t by_width(int64_t d, F f)
     if (d <= 1024) return f(std::integral_constant<int, 64>{}, std::integral_constant<int, 2>{});
     if (d <= 2048) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 1>{});
     if (d <= 4096) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 2>{});
+    if (d <= 6144) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 3>{});
     if (d <= 8192) return f(std::integral_constant<int, 256>{}, std::integral_constant<int, 4>{});
     if (d <= 16384) return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 2>{});
     return f(std::integral_constant<int, 1024>{}, std::integral_constant<int, 8>{});
@@ -363,7 +415,7 @@ NormBwdGeom norm_bwd_geometry(int64_t rows, int64_t d)
     const int rpw = rows_per_group(d);
     g.blocks = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(512, (rows + rpw - 1) / rpw)));
     g.off_dw = 256;
-    g.bytes = g.off_dw + static_cast<size_t>(g.blocks) * rpw * d * sizeof(float);
+    g.bytes = g.off_dw + static_cast<size_t>(g.blocks) * d * sizeof(float);
     return g;
 }
 
@@ -378,8 +430,8 @@ hipError_t launch_rmsnorm_bwd(const NormBwdGeom &geo, const void *dy, const void
     a.vec = d % 8 == 0 && wide(dy) && wide(h) && wide(w) && wide(dh) && wide(dx);
     hipError_t e = dtype == MGS_BF16 ? launch_bwd<__bf16>(a, geo.blocks, s) : launch_bwd<float>(a, geo.blocks, s);
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL(dw_kernel, dim3(static_cast<unsigned>((d + 63) / 64)), dim3(256), 0, s, a.part, dw,
-                       geo.blocks * rows_per_group(d), a.d);
+    hipLaunchKernelGGL(dw_kernel, dim3(static_cast<unsigned>((d + 63) / 64)), dim3(1024), 0, s, a.part, dw,
+                       geo.blocks, a.d);
     return hipGetLastError();
 }
 
