@@ -64,13 +64,13 @@ template <typename T> struct Num;
 template <> struct Num<float> {
     using Frag = f4v;                    // 4 elements of a reduction block
     static constexpr int NS = 1;         // terms an fp32 value is split into
-    static constexpr int PAD = 4;        // elements between LDS rows, 16 bytes
+    static constexpr int PADQ = 4, PADK = 4, PADV = 8;
     using Vec8 = f8v;
 };
 template <> struct Num<__bf16> {
     using Frag = bf4;
     static constexpr int NS = 3;
-    static constexpr int PAD = 8;
+    static constexpr int PADQ = 4, PADK = 8, PADV = 16;
     using Vec8 = bf8;
 };
 
@@ -123,22 +123,42 @@ template <typename T> __device__ __forceinline__ typename Num<T>::Frag frag(cons
     return *reinterpret_cast<const typename Num<T>::Frag *>(p);
 }
 
-// The fragment of a column: elements (row0 + 4 lq + r, col0 + li), r = 0..3, of
-// row-major LDS.  For 16-bit elements one transposing read: each of 16 lanes
-// addresses 4 elements of a row, and lane i gets column i of the 4 x 16 block.
-template <int LD> __device__ __forceinline__ f4v frag_t(const float *m, int row0, int col0, int li, int lq)
-{
-    const float *p = m + (row0 + 4 * lq) * LD + col0 + li;
-    return f4v{p[0], p[LD], p[2 * LD], p[3 * LD]};
-}
-
-template <int LD> __device__ __forceinline__ bf4 frag_t(const __bf16 *m, int row0, int col0, int li, int lq)
-{
-    typedef __attribute__((address_space(3))) s4v *lds_ptr;
-    const __bf16 *p = m + (row0 + 4 * lq + (li >> 2)) * LD + col0 + 4 * (li & 3);
-    const s4v r = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p));
-    return __builtin_bit_cast(bf4, r);
-}
+// A tile of 64 rows of D elements in LDS, LD apart, read as fragments of rows (li
+// = row, block b of 16 columns) and of columns (rows row0 + 4 lq + r of column
+// 16 t + li).  For 16-bit elements a column fragment is one transposing read:
+// each of 16 lanes addresses 4 elements of a row, and lane i gets column i of the
+// 4 x 16 block.  16 lanes read 128 bytes in one go if they touch each of 32 banks
+// once: of bf16 rows LD = 4 (mod 64) elements apart for rows, 16 for columns; 8
+// costs both a second go, more seldom for columns.  q is read by rows, v by
+// columns, k by both, mostly columns.
+template <typename T, int D, int PAD> struct Tile {
+    using N = Num<T>;
+    static constexpr int LD = D + PAD, SIZE = kC * LD;
+    static __device__ __forceinline__ void store8(T *m, int r, int c, typename N::Vec8 x)
+    {
+        if constexpr (LD % 8 == 0) {
+            *reinterpret_cast<typename N::Vec8 *>(m + r * LD + c) = x;
+        } else {
+            *reinterpret_cast<typename N::Frag *>(m + r * LD + c) = __builtin_shufflevector(x, x, 0, 1, 2, 3);
+            *reinterpret_cast<typename N::Frag *>(m + r * LD + c + 4) = __builtin_shufflevector(x, x, 4, 5, 6, 7);
+        }
+    }
+    static __device__ __forceinline__ typename N::Frag row(const T *m, int row0, int b, int li, int lq)
+    {
+        return frag(m + (row0 + li) * LD + 16 * b + 4 * lq);
+    }
+    static __device__ __forceinline__ typename N::Frag col(const T *m, int row0, int t, int li, int lq)
+    {
+        if constexpr (sizeof(T) == 4) {
+            const T *p = m + (row0 + 4 * lq) * LD + 16 * t + li;
+            return f4v{p[0], p[LD], p[2 * LD], p[3 * LD]};
+        } else {
+            typedef __attribute__((address_space(3))) s4v *lds_ptr;
+            const T *p = m + (row0 + 4 * lq + (li >> 2)) * LD + 16 * t + 4 * (li & 3);
+            return __builtin_bit_cast(typename N::Frag, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_ptr)(p)));
+        }
+    }
+};
 
 // ------------------------------------------------------------------- walks
 
@@ -254,7 +274,6 @@ __device__ __forceinline__ Chunk chunk_at(int ch, int T, int len, int rev)
 // access is a workgroup-uniform chunk address plus a 32-bit lane offset that
 // stays the same from chunk to chunk.
 template <typename T, int DIM, int THREADS, bool VEC> struct Stage {
-    static constexpr int LD = DIM + Num<T>::PAD;
     static constexpr int PER = kC * DIM / 8 / THREADS;
     static constexpr int TURN = THREADS / (DIM / 8);   // rows per turn
     using Vec8 = typename Num<T>::Vec8;
@@ -302,11 +321,10 @@ template <typename T, int DIM, int THREADS, bool VEC> struct Stage {
             }
         }
     }
-    __device__ __forceinline__ void store(T *lds) const
+    template <typename Tile> __device__ __forceinline__ void store(T *lds) const
     {
 #pragma unroll
-        for (int i = 0; i < PER; ++i)
-            *reinterpret_cast<Vec8 *>(lds + row(i) * LD + col()) = x[i];
+        for (int i = 0; i < PER; ++i) Tile::store8(lds, row(i), col(), x[i]);
     }
 };
 
@@ -402,8 +420,11 @@ constexpr uint64_t kScoreTiles = 0xFEDCA98540ull;
 // leave two waves a SIMD, and waits and vector arithmetic then show.)
 // MODE: STATE, the walk from a zero state without outputs; OUT, outputs rounded
 // to T; DOTS, outputs in T or fp32 (partials of shared heads), and the dots of
-// their rows for dg.  An output rounded to bf16 takes two terms (16 bits) of the
-// states and scores, one whose dots make dg all three.
+// their rows for dg.
+// TERMS: how many bf16 terms the weighted values of the state's update take: 3
+// where the state itself, or dg, comes of it; 2 (16 bits) where only outputs
+// rounded to bf16 do.  Likewise states and scores on their way into an output: 2
+// in OUT, 3 in DOTS.
 enum { STATE, OUT, DOTS };
 
 // waves a SIMD that the registers are cut for: as many as LDS lets in
@@ -413,29 +434,29 @@ template <typename T> constexpr int walk_waves(int KD, int VD, int mode)
     return VD == 128 ? 4 : mode == STATE ? 4 : KD == 64 ? 3 : 2;
 }
 
-template <typename T, int KD, int VD, int MODE, bool VEC>
+template <typename T, int KD, int VD, int MODE, int TERMS, bool VEC>
 __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kernel(WalkArgs a)
 {
     using N = Num<T>;
     using Frag = typename N::Frag;
     constexpr bool STATE_ONLY = MODE == STATE;
-    constexpr int NS = N::NS;                                 // terms of the weighted values
-    constexpr int NO = NS == 3 && MODE != DOTS ? 2 : NS;      // terms of states and scores
+    constexpr int NS = N::NS == 3 ? TERMS : 1;                // terms of the weighted values
+    constexpr int NO = N::NS == 3 && MODE != DOTS ? 2 : N::NS;   // of states and scores
     constexpr int kThreads = 4 * VD, NW = VD / 16;
     constexpr int NKB = KD / 16;       // reduction blocks
     constexpr int NCT = 1;
-    constexpr int LK = KD + N::PAD, LV = VD + N::PAD, LA = kC + 4;
-    __shared__ __align__(16) T sQ[STATE_ONLY ? 8 : kC * LK];
-    __shared__ __align__(16) T sK[kC * LK];
-    __shared__ __align__(16) T sV[kC * LV];
+    using TQ = Tile<T, KD, N::PADQ>;
+    using TK = Tile<T, KD, N::PADK>;
+    using TV = Tile<T, VD, N::PADV>;
+    constexpr int LA = kC + 4;
+    __shared__ __align__(16) T sQ[STATE_ONLY ? 8 : TQ::SIZE];
+    __shared__ __align__(16) T sK[TK::SIZE];
+    __shared__ __align__(16) T sV[TV::SIZE];
     __shared__ __align__(16) T sA[STATE_ONLY ? 1 : NO][STATE_ONLY ? 8 : kC * LA];
     __shared__ __align__(16) Decays sDecays[2];
 
-    // the waves' partial dots of row r: in the 16 bytes of padding of the rows r of
-    // the q and k tiles
-    auto partial = [&](int w, int r) -> float & {
-        return reinterpret_cast<float *>((w < 4 ? sQ : sK) + r * LK + KD)[w & 3];
-    };
+    // the waves' partial dots of row r: in the 32 bytes after row r of the value tile
+    auto partial = [&](int w, int r) -> float & { return reinterpret_cast<float *>(sV + r * TV::LD + VD)[w]; };
 
     const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
     int li = lane & 15, lq = lane >> 4;
@@ -548,9 +569,9 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
         asm volatile("" : "+v"(li), "+v"(lq));
         [[maybe_unused]] const int orow = rev ? kC - 1 - li : li, c0 = col0 + 4 * lq;
         const Decays &sD = sDecays[n & 1];
-        k.store(sK);
-        v.store(sV);
-        if constexpr (!STATE_ONLY) q.store(sQ);
+        k.template store<TK>(sK);
+        v.template store<TV>(sV);
+        if constexpr (!STATE_ONLY) q.template store<TQ>(sQ);
         lds_barrier();
         const Chunk ck = place(n);
 
@@ -568,11 +589,9 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
                     const int i = tile >> 2, j = tile & 3;
                     f4v p = {0, 0, 0, 0};
 #pragma unroll
-                    for (int m = 0; m < NKB / 2; ++m) {
-                        const T *kr = sK + (16 * j + li) * LK + 32 * m + 4 * lq;
-                        const T *qr = sQ + (16 * i + li) * LK + 32 * m + 4 * lq;
-                        p = mma2(frag(kr), frag(kr + 16), frag(qr), frag(qr + 16), p);
-                    }
+                    for (int m = 0; m < NKB / 2; ++m)
+                        p = mma2(TK::row(sK, 16 * j, 2 * m, li, lq), TK::row(sK, 16 * j, 2 * m + 1, li, lq),
+                                 TQ::row(sQ, 16 * i, 2 * m, li, lq), TQ::row(sQ, 16 * i, 2 * m + 1, li, lq), p);
                     const int row = 16 * i + li, src = 16 * j + 4 * lq;
                     const float gh = sD.hi[row], gl = sD.lo[row];
                     const f4v sh = *reinterpret_cast<const f4v *>(&sD.hi[src]), sl = *reinterpret_cast<const f4v *>(&sD.lo[src]);
@@ -589,9 +608,8 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
                     for (int s = 0; s < NO; ++s) *reinterpret_cast<Frag *>(&sA[s][row * LA + src]) = ws[s];
                 }
             }
-            lds_barrier();
-
-            // the state's part of the output, then the chunk's own
+            // the state's part of the output (which needs no one's scores), then the
+            // chunk's own
             f4v O[4][NCT];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
@@ -607,39 +625,11 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const T *qr = sQ + (16 * i + li) * LK + 32 * m + 4 * lq;
-                    const Frag q0 = frag(qr), q1 = frag(qr + 16);
+                    const Frag q0 = TQ::row(sQ, 16 * i, 2 * m, li, lq), q1 = TQ::row(sQ, 16 * i, 2 * m + 1, li, lq);
 #pragma unroll
                     for (int s = 0; s < NO; ++s)
 #pragma unroll
                         for (int ct = 0; ct < NCT; ++ct) O[i][ct] = mma2(s0[ct][s], s1[ct][s], q0, q1, O[i][ct]);
-                }
-            }
-            [[maybe_unused]] Frag dots[MODE == DOTS ? 4 : 1][NCT];
-            if constexpr (MODE == DOTS) {
-                {
-                    [[maybe_unused]] const int64_t p = d_base + ck.tb * d_st;
-                    const Buffer buf(p);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = 16 * i + li;
-                        const bool live = r >= ck.lo && r < ck.hi;
-#pragma unroll
-                        for (int ct = 0; ct < NCT; ++ct) {
-                            const int c = c0 + 16 * ct;
-                            if constexpr (VEC) {
-                                const uint32_t at = (orow + o_step * i) * static_cast<uint32_t>(d_st) + c * static_cast<uint32_t>(sizeof(T));
-                                dots[i][ct] = buf.template load<Frag>(live && c < cols ? at : kNowhere);
-                            } else {
-                                const Global<const T> *x = reinterpret_cast<const Global<const T> *>(p + (orow + o_step * i) * d_st) + c;
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    dots[i][ct][e] = static_cast<T>(0.0f);
-                                    if (live && c + e < cols) dots[i][ct][e] = x[e];
-                                }
-                            }
-                        }
-                    }
                 }
             }
             load(n + 1);
@@ -649,11 +639,12 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
 #pragma unroll
                 for (int ct = 0; ct < NCT; ++ct) O[i][ct] *= w;
             }
+            lds_barrier();
             Frag vf[4][NCT];
 #pragma unroll
             for (int jb = 0; jb < 4; ++jb)
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) vf[jb][ct] = frag_t<LV>(sV, 16 * jb, col0 + 16 * ct, li, lq);
+                for (int ct = 0; ct < NCT; ++ct) vf[jb][ct] = TV::col(sV, 16 * jb, wv + ct, li, lq);
             // A product with a zero weight would carry a non-finite value to rows ahead
             // of its own: such values are taken out, and from their row on their
             // column is NaN.  A product with zeros alone finds them.
@@ -682,6 +673,33 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
                             O[i][ct] = mma2(vf[2 * m][ct], vf[2 * m + 1][ct], a0, a1, O[i][ct]);
                     }
 
+            [[maybe_unused]] Frag dots[MODE == DOTS ? 4 : 1][NCT];
+            if constexpr (MODE == DOTS) {
+                {
+                    [[maybe_unused]] const int64_t p = d_base + ck.tb * d_st;
+                    const Buffer buf(p);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int r = 16 * i + li;
+                        const bool live = r >= ck.lo && r < ck.hi;
+#pragma unroll
+                        for (int ct = 0; ct < NCT; ++ct) {
+                            const int c = c0 + 16 * ct;
+                            if constexpr (VEC) {
+                                const uint32_t at = (orow + o_step * i) * static_cast<uint32_t>(d_st) + c * static_cast<uint32_t>(sizeof(T));
+                                dots[i][ct] = buf.template load<Frag>(live && c < cols ? at : kNowhere);
+                            } else {
+                                const Global<const T> *x = reinterpret_cast<const Global<const T> *>(p + (orow + o_step * i) * d_st) + c;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    dots[i][ct][e] = static_cast<T>(0.0f);
+                                    if (live && c + e < cols) dots[i][ct][e] = x[e];
+                                }
+                            }
+                        }
+                    }
+                }
+            }
             // rows of the output (zeros past the sequence's length) and their dots
             if (ck.hi - ck.lo < kC) {
 #pragma unroll
@@ -744,14 +762,14 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
             const f4v w1 = *reinterpret_cast<const f4v *>(&sD.src[32 * m + 16 + 4 * lq]);
 #pragma unroll
             for (int ct = 0; ct < NCT; ++ct) {
-                const Frag x0 = frag_t<LV>(sV, 32 * m, col0 + 16 * ct, li, lq);
-                const Frag x1 = frag_t<LV>(sV, 32 * m + 16, col0 + 16 * ct, li, lq);
+                const Frag x0 = TV::col(sV, 32 * m, wv + ct, li, lq);
+                const Frag x1 = TV::col(sV, 32 * m + 16, wv + ct, li, lq);
                 split(__builtin_convertvector(x0, f4v) * w0, v0[ct]);
                 split(__builtin_convertvector(x1, f4v) * w1, v1[ct]);
             }
 #pragma unroll
             for (int t = 0; t < NKB; ++t) {
-                const Frag k0 = frag_t<LK>(sK, 32 * m, 16 * t, li, lq), k1 = frag_t<LK>(sK, 32 * m + 16, 16 * t, li, lq);
+                const Frag k0 = TK::col(sK, 32 * m, t, li, lq), k1 = TK::col(sK, 32 * m + 16, t, li, lq);
 #pragma unroll
                 for (int s = 0; s < NS; ++s)
 #pragma unroll
@@ -1088,25 +1106,29 @@ unsigned walk_grid(int64_t items, int roles)
     return static_cast<unsigned>((items + 7) / 8 * 8 * roles);
 }
 
-template <typename T, int MODE, bool VEC>
+template <typename T, int MODE, int TERMS, bool VEC>
 hipError_t launch_walk(const WalkArgs &a, int kdim, int vdim, hipStream_t s)
 {
     const dim3 grid(walk_grid(a.items, a.nRoles)), block(vdim <= 64 ? 256 : 512);
-    if (kdim <= 64 && vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 64, MODE, VEC>), grid, block, 0, s, a);
-    else if (kdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 128, MODE, VEC>), grid, block, 0, s, a);
-    else if (vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 128, 64, MODE, VEC>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((walk_kernel<T, 128, 128, MODE, VEC>), grid, block, 0, s, a);
+    if (kdim <= 64 && vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 64, MODE, TERMS, VEC>), grid, block, 0, s, a);
+    else if (kdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 128, MODE, TERMS, VEC>), grid, block, 0, s, a);
+    else if (vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 128, 64, MODE, TERMS, VEC>), grid, block, 0, s, a);
+    else hipLaunchKernelGGL((walk_kernel<T, 128, 128, MODE, TERMS, VEC>), grid, block, 0, s, a);
     return hipGetLastError();
 }
 
+// exact: whether a state that leaves the kernel, or dg, comes of the walk's state
 template <int MODE>
-hipError_t launch_walk(int dtype, const WalkArgs &a, int kdim, int vdim, hipStream_t s)
+hipError_t launch_walk(int dtype, const WalkArgs &a, int kdim, int vdim, bool exact, hipStream_t s)
 {
-    if (dtype == MGS_BF16)
-        return a.vec ? launch_walk<__bf16, MODE, true>(a, kdim, vdim, s)
-                     : launch_walk<__bf16, MODE, false>(a, kdim, vdim, s);
-    return a.vec ? launch_walk<float, MODE, true>(a, kdim, vdim, s)
-                 : launch_walk<float, MODE, false>(a, kdim, vdim, s);
+    if (dtype == MGS_BF16) {
+        if (!a.vec) return launch_walk<__bf16, MODE, 3, false>(a, kdim, vdim, s);
+        if constexpr (MODE != DOTS)
+            if (!exact) return launch_walk<__bf16, MODE, 2, true>(a, kdim, vdim, s);
+        return launch_walk<__bf16, MODE, 3, true>(a, kdim, vdim, s);
+    }
+    return a.vec ? launch_walk<float, MODE, 3, true>(a, kdim, vdim, s)
+                 : launch_walk<float, MODE, 3, false>(a, kdim, vdim, s);
 }
 
 template <typename T, int NV, int R> hipError_t launch_step(const StepArgs &a, int64_t heads, hipStream_t s)
@@ -1127,17 +1149,20 @@ size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 
-// Segments: a walk takes one workgroup through its chunks in order, and the
-// chip holds 512 such workgroups (two a CU), so a long sequence of few heads is
-// cut until there are that many.  The backward also bounds a segment to 8
-// chunks, which bounds the rounding of dg's sums.
+// Segments: a walk takes one workgroup through its chunks in order, and the chip
+// holds 512 such workgroups of 8 waves, or twice as many of 4 (up to 64 columns),
+// so a long sequence of few heads is cut until there are that many.  Half or twice
+// as many cost up to 15% (prompts of 8 x 1999 steps x 16 heads: 93, 82, 94 us).
+// The backward also bounds a segment to 8 chunks, which bounds the rounding of
+// dg's sums.
 AttnGeom attn_geometry(const mgs_linattn_desc &d, bool backward)
 {
     AttnGeom g{};
     g.BH = d.B * d.H;
     g.nC = static_cast<int>((d.T + kC - 1) / kC);
     const int64_t walks = std::max<int64_t>(1, g.BH * (backward ? 3 : 1));
-    int64_t seg = std::max<int64_t>(1, (512 + walks - 1) / walks);
+    const int64_t want = d.dk <= 64 && d.dv <= 64 ? 1024 : 512;
+    int64_t seg = std::max<int64_t>(1, (want + walks - 1) / walks);
     int64_t len = std::max<int64_t>(1, (g.nC + seg - 1) / seg);
     if (backward) len = std::min<int64_t>(len, 8);
     g.segLen = static_cast<int>(len);
@@ -1246,7 +1271,7 @@ hipError_t launch_linattn_fwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
         r.state = S0;
         r.final = ST;
         r.st_bh = E;
-        return launch_walk<OUT>(d.dtype, a, dk, dv, s);
+        return launch_walk<OUT>(d.dtype, a, dk, dv, ST != nullptr, s);
     }
     char *w = static_cast<char *>(ws);
     float *S = reinterpret_cast<float *>(w + geo.off_S);
@@ -1254,7 +1279,7 @@ hipError_t launch_linattn_fwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
     r.st_seg = E;
     r.local = S;
     a.dec = reinterpret_cast<float *>(w + geo.off_dec);
-    hipError_t e = launch_walk<STATE>(d.dtype, a, dk, dv, s);
+    hipError_t e = launch_walk<STATE>(d.dtype, a, dk, dv, ST != nullptr, s);
     if (e != hipSuccess) return e;
     ChainArgs c{};
     c.S = S;
@@ -1267,7 +1292,7 @@ hipError_t launch_linattn_fwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
     e = launch_chain(geo, c, 1, s);
     if (e != hipSuccess) return e;
     r.state = S;
-    return launch_walk<OUT>(d.dtype, a, dk, dv, s);
+    return launch_walk<OUT>(d.dtype, a, dk, dv, false, s);
 }
 
 hipError_t launch_linattn_bwd(const AttnGeom &geo, const mgs_linattn_desc &d, const void *q, const void *k,
@@ -1325,7 +1350,7 @@ hipError_t launch_linattn_bwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
         l.role[0].local = S, l.role[0].st_bh = S_bh, l.role[0].st_seg = E;
         l.role[1] = rv;
         l.role[1].local = R;
-        if ((e = launch_walk<STATE>(d.dtype, l, dk, dv, s)) != hipSuccess) return e;
+        if ((e = launch_walk<STATE>(d.dtype, l, dk, dv, true, s)) != hipSuccess) return e;
         ChainArgs c{};
         c.S = S, c.R = R, c.dec = l.dec, c.S0 = S0, c.dST = dST, c.dS0 = dS0;
         c.BH = geo.BH, c.nSeg = geo.nSeg, c.E = E;
@@ -1341,10 +1366,10 @@ hipError_t launch_linattn_bwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
     // the dq and dk walks reduce over dv, the dv walk over dk
     a.role[0] = rq, a.role[1] = rk;
     a.nRoles = 2;
-    if ((e = launch_walk<DOTS>(d.dtype, a, dv, dk, s)) != hipSuccess) return e;
+    if ((e = launch_walk<DOTS>(d.dtype, a, dv, dk, true, s)) != hipSuccess) return e;
     a.role[0] = rv;
     a.nRoles = 1;
-    if ((e = launch_walk<OUT>(d.dtype, a, dk, dv, s)) != hipSuccess) return e;
+    if ((e = launch_walk<OUT>(d.dtype, a, dk, dv, rv.final != nullptr, s)) != hipSuccess) return e;
 
     DgArgs m{};
     m.x = x, m.y = y;
