@@ -45,14 +45,18 @@ __device__ __forceinline__ int tensor_of(const ClipTable &t, int tile)
     return __builtin_amdgcn_readfirstlane(__popcll(__ballot(a)) + __popcll(__ballot(b)) - 1);
 }
 
-__device__ __forceinline__ double block_sum(double v, double *lds)
+// over a workgroup of W waves; lds: one slot per wave
+template <int W> __device__ __forceinline__ double block_sum(double v, double *lds)
 {
 #pragma unroll
     for (int off = 32; off; off >>= 1) v += __shfl_xor(v, off, 64);
     __syncthreads();
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
-    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+    v = lds[0];
+#pragma unroll
+    for (int w = 1; w < W; ++w) v += lds[w];
+    return v;
 }
 
 __device__ __forceinline__ f8v widen(f8v v) { return v; }
@@ -99,22 +103,23 @@ __global__ void __launch_bounds__(256) squares_kernel(ClipTable t, double *part)
     const int n = static_cast<int>(min(static_cast<int64_t>(kTile), t.size[i] - at));
     double s = t.bf16[i] ? tile_squares<__bf16, bf8v>(static_cast<const __bf16 *>(t.in[i]) + at, n, t.vec[i])
                          : tile_squares<float, f8v>(static_cast<const float *>(t.in[i]) + at, n, t.vec[i]);
-    s = block_sum(s, lds);
+    s = block_sum<4>(s, lds);
     if (threadIdx.x == 0) part[t.base + blockIdx.x] = s;
 }
 
-// the norm from n partials, in order, by one workgroup
-__device__ __forceinline__ float norm_of(const double *part, int64_t n, double *lds)
+// the norm from n partials, in a fixed order, by a workgroup of W waves
+template <int W> __device__ __forceinline__ float norm_of(const double *part, int64_t n, double *lds)
 {
     double s = 0.0;
-    for (int64_t i = threadIdx.x; i < n; i += 256) s += part[i];
-    return static_cast<float>(sqrt(block_sum(s, lds)));
+#pragma unroll 8
+    for (int64_t i = threadIdx.x; i < n; i += 64 * W) s += part[i];
+    return static_cast<float>(sqrt(block_sum<W>(s, lds)));
 }
 
-__global__ void __launch_bounds__(256) norm_kernel(const double *part, int64_t n, float *norm)
+__global__ void __launch_bounds__(1024) norm_kernel(const double *part, int64_t n, float *norm)
 {
-    __shared__ double lds[4];
-    const float v = norm_of(part, n, lds);
+    __shared__ double lds[16];
+    const float v = norm_of<16>(part, n, lds);
     if (threadIdx.x == 0) *norm = v;
 }
 
@@ -150,7 +155,7 @@ __global__ void __launch_bounds__(256) scale_kernel(ClipTable t, const double *p
     __shared__ double lds[4];
     float v;
     if (few) {
-        v = norm_of(part, n_part, lds);
+        v = norm_of<4>(part, n_part, lds);
         if (t.base == 0 && blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
     } else {
         v = *norm;
@@ -221,7 +226,7 @@ hipError_t launch_clip_norm(int64_t n, const void *const *in, void *const *out, 
     if (e != hipSuccess) return e;
     const int few = out && tiles > 0 && tiles <= kClipFew;
     if (!few) {
-        hipLaunchKernelGGL(norm_kernel, dim3(1), dim3(256), 0, s, part, tiles, norm);
+        hipLaunchKernelGGL(norm_kernel, dim3(1), dim3(1024), 0, s, part, tiles, norm);
         if ((e = hipGetLastError()) != hipSuccess) return e;
     }
     if (!out) return hipSuccess;

@@ -647,16 +647,21 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
                 for (int ct = 0; ct < NCT; ++ct) vf[jb][ct] = TV::col(sV, 16 * jb, wv + ct, li, lq);
             // A product with a zero weight would carry a non-finite value to rows ahead
             // of its own: such values are taken out, and from their row on their
-            // column is NaN.  A product with zeros alone finds them.
+            // column is NaN.  A product with zeros finds them.
             {
-                Frag z;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) z[e] = static_cast<T>(0.0f);
                 f4v probe = {0, 0, 0, 0};
+                if constexpr (sizeof(T) == 4) {
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) {
-                    probe = mma2(vf[0][ct], vf[1][ct], z, z, probe);
-                    probe = mma2(vf[2][ct], vf[3][ct], z, z, probe);
+                    for (int jb = 0; jb < 4; ++jb)
+#pragma unroll
+                        for (int ct = 0; ct < NCT; ++ct) probe += vf[jb][ct] * 0.0f;
+                } else {   // (by a matrix product with zeros)
+                    const Frag z = __builtin_bit_cast(Frag, uint64_t(0));
+#pragma unroll
+                    for (int ct = 0; ct < NCT; ++ct) {
+                        probe = mma2(vf[0][ct], vf[1][ct], z, z, probe);
+                        probe = mma2(vf[2][ct], vf[3][ct], z, z, probe);
+                    }
                 }
                 if (__any((probe[0] + probe[1]) + (probe[2] + probe[3]) != 0.0f)) drop_non_finite<T, NCT>(vf, O, li, lq);
             }
@@ -1151,8 +1156,10 @@ size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 // Segments: a walk takes one workgroup through its chunks in order, and the chip
 // holds 512 such workgroups of 8 waves, or twice as many of 4 (up to 64 columns),
-// so a long sequence of few heads is cut until there are that many.  Half or twice
-// as many cost up to 15% (prompts of 8 x 1999 steps x 16 heads: 93, 82, 94 us).
+// so a long sequence of few heads is cut until there are that many (512 of either
+// kind are left whole: cutting costs two more launches and reads k and v twice).
+// Half or twice as many cost up to 15% (prompts of 8 x 1999 steps x 16 heads: 93,
+// 82, 94 us).
 // The backward also bounds a segment to 8 chunks, which bounds the rounding of
 // dg's sums.
 AttnGeom attn_geometry(const mgs_linattn_desc &d, bool backward)
@@ -1162,7 +1169,7 @@ AttnGeom attn_geometry(const mgs_linattn_desc &d, bool backward)
     g.nC = static_cast<int>((d.T + kC - 1) / kC);
     const int64_t walks = std::max<int64_t>(1, g.BH * (backward ? 3 : 1));
     const int64_t want = d.dk <= 64 && d.dv <= 64 ? 1024 : 512;
-    int64_t seg = std::max<int64_t>(1, (want + walks - 1) / walks);
+    const int64_t seg = walks >= 512 ? 1 : (want + walks - 1) / walks;
     int64_t len = std::max<int64_t>(1, (g.nC + seg - 1) / seg);
     if (backward) len = std::min<int64_t>(len, 8);
     g.segLen = static_cast<int>(len);
