@@ -76,6 +76,14 @@ def _out(torch, name, t, shape, dtype, dev):
     return t
 
 
+def _like(name, t, x):
+    """t, or a new tensor of x's shape and type."""
+    if t is None:
+        return x.new_empty(x.shape)
+    _tensor(name, t, x.shape, x.dtype, x.get_device())
+    return t
+
+
 def _scratch(torch, ws, nbytes, dev):
     """ws, or a new workspace of nbytes() bytes (the operators here need no zero-fill)."""
     if ws is None:
@@ -131,7 +139,7 @@ def mgs_linattn_fwd(q, k, v, g, S0=None, lengths=None, scale=1.0, o=None, ST=Non
     import torch
     dims, dev, per_head = _attn_inputs(torch, q, k, v, g, S0, lengths)
     B, T, H, Hk, dk, dv = dims
-    o = _out(torch, "o", o, (B, T, H, dv), v.dtype, dev)
+    o = _like("o", o, v)
     if ST is not None or want_state:
         ST = _out(torch, "ST", ST, (B, H, dv, dk), torch.float32, dev)
     d = _pack_desc(*dims, _dtype(torch, v.dtype), per_head, scale, *q.stride()[:3], *k.stride()[:3], *v.stride()[:3],
@@ -188,7 +196,7 @@ def mgs_linattn_step(q, k, v, g, S, slots=None, scale=1.0, o=None, stream=None):
     _tensor("S", S, (n_slots, H, dv, dk), torch.float32, dev)
     if slots is not None:
         _tensor("slots", slots, (B,), torch.int32, dev)
-    o = _out(torch, "o", o, (B, H, dv), dt, dev)
+    o = _like("o", o, v)
     (qb, qh, _), (kb, kh, _), (vb, vh, _) = q.stride(), k.stride(), v.stride()
     gb, gh = (0, 0) if per_head else g.stride()
     d = _pack_desc(B, 1, H, Hk, dk, dv, _dtype(torch, dt), per_head, scale, qb, 0, qh, kb, 0, kh, vb, 0, vh, 0, 0, 0,
@@ -214,15 +222,18 @@ def _rows(name, t, d, dtype, dev):
 
 
 def _norm_inputs(torch, x, w, residual):
-    d, dev, dt = x.shape[-1], _device("x", x), x.dtype
-    code = _dtype(torch, dt)
-    xs = _rows("x", x, d, dt, dev)
+    shape, dev, dt = x.shape, _device("x", x), x.dtype
+    if not shape:
+        raise ValueError("x must have at least one dimension")
+    d, code = shape[-1], _dtype(torch, dt)
+    xs = rs = d
+    if not x.is_contiguous():
+        xs = _rows("x", x, d, dt, dev)
     _tensor("w", w, (d,), dt, dev)
-    rs = d
     if residual is not None:
-        if residual.shape != x.shape:
-            raise ValueError(f"residual has shape {tuple(residual.shape)}, expected {tuple(x.shape)}")
-        rs = _rows("residual", residual, d, dt, dev)
+        _tensor("residual", residual, shape, dt, dev, ANY)
+        if not residual.is_contiguous():
+            rs = _rows("residual", residual, d, dt, dev)
     return x.numel() // d if d else 0, d, xs, rs, dev, code
 
 
@@ -233,9 +244,9 @@ def mgs_rmsnorm_fwd(x, w, residual=None, eps=1e-6, y=None, h=None, rstd=None, st
     itself, not a copy, unless a buffer is passed.  h may be the residual's (or x's) own dense tensor."""
     import torch
     rows, d, xs, rs, dev, code = _norm_inputs(torch, x, w, residual)
-    y = _out(torch, "y", y, x.shape, x.dtype, dev)
+    y = _like("y", y, x)
     write_h = h is not None or residual is not None or not x.is_contiguous()
-    h_out = _out(torch, "h", h, x.shape, x.dtype, dev) if write_h else None
+    h_out = _like("h", h, x) if write_h else None
     rstd = _out(torch, "rstd", rstd, x.shape[:-1], torch.float32, dev)
     check(load().mgs_rmsnorm_fwd(x.data_ptr(), _ptr(residual), w.data_ptr(), y.data_ptr(), _ptr(h_out), rstd.data_ptr(),
                                  rows, d, xs, rs, eps, code, _raw_stream(torch, stream, dev)), "mgs_rmsnorm_fwd")
@@ -251,7 +262,7 @@ def mgs_rmsnorm_fwd_fp8(x, w, residual=None, eps=1e-6, group=0, y=None, scale=No
     n_scales = -(-d // group) if group > 0 else 1
     scale = _out(torch, "scale", scale, (*x.shape[:-1], n_scales), torch.float32, dev)
     write_h = h is not None or residual is not None or not x.is_contiguous()
-    h_out = _out(torch, "h", h, x.shape, x.dtype, dev) if write_h else None
+    h_out = _like("h", h, x) if write_h else None
     check(load().mgs_rmsnorm_fwd_fp8(x.data_ptr(), _ptr(residual), w.data_ptr(), y.data_ptr(), scale.data_ptr(),
                                      _ptr(h_out), rows, d, xs, rs, eps, group, code, _raw_stream(torch, stream, dev)),
           "mgs_rmsnorm_fwd_fp8")
@@ -276,7 +287,7 @@ def mgs_rmsnorm_bwd(dy, h, w, rstd, dh=None, dx=None, dw=None, ws=None, stream=N
     _tensor("rstd", rstd, h.shape[:-1], torch.float32, dev)
     if dh is not None:
         _tensor("dh", dh, h.shape, dt, dev)
-    dx = _out(torch, "dx", dx, h.shape, dt, dev)
+    dx = _like("dx", dx, h)
     dw = _out(torch, "dw", dw, (d,), torch.float32, dev)
     rows = rstd.numel()   # one for each row of h
     ws = _scratch(torch, ws, lambda: mgs_rmsnorm_workspace_size(rows, d), dev)
@@ -308,30 +319,33 @@ def mgs_clip_norm(tensors, max_norm=None, out=None, norm=None, ws=None, stream=N
     if not tensors:
         raise ValueError("no tensors")
     dev = _device("tensors[0]", tensors[0])
-    codes = {torch.float32: 0, torch.bfloat16: 1}
-    dtypes = array("i")
-    for i, t in enumerate(tensors):
-        code = codes.get(t.dtype)
-        if code is None or t.get_device() != dev or not t.is_contiguous():
+    of = torch.Tensor
+
+    def usable(ts):
+        return set(map(of.get_device, ts)) == {dev} and all(map(of.is_contiguous, ts))
+
+    kinds = [t.dtype for t in tensors]
+    if not set(kinds) <= {torch.float32, torch.bfloat16} or not usable(tensors):
+        for i, t in enumerate(tensors):
             _dtype(torch, t.dtype)
             _tensor(f"tensors[{i}]", t, t.shape, t.dtype, dev)
-        dtypes.append(code)
     outs = None
     if max_norm is not None:
         outs = tensors if out is None else list(out)
         if len(outs) != len(tensors):
             raise ValueError(f"out has {len(outs)} tensors, expected {len(tensors)}")
-        if out is not None:
+        if out is not None and not ([o.dtype for o in outs] == kinds and usable(outs) and
+                                    [o.shape for o in outs] == [t.shape for t in tensors]):
             for i, (o, t) in enumerate(zip(outs, tensors)):
-                if o.dtype is not t.dtype or o.shape != t.shape or o.get_device() != dev or not o.is_contiguous():
-                    _tensor(f"out[{i}]", o, t.shape, t.dtype, dev)
+                _tensor(f"out[{i}]", o, t.shape, t.dtype, dev)
     elif out is not None:
         raise ValueError("out needs max_norm")
+    dtypes = array("i", [int(k is torch.bfloat16) for k in kinds])
     norm = _out(torch, "norm", norm, (), torch.float32, dev)
-    counts = array("q", [t.numel() for t in tensors])
+    counts = array("q", map(of.numel, tensors))
     ws = _scratch(torch, ws, lambda: mgs_clip_norm_workspace_size(counts), dev)
-    ins = array("Q", [t.data_ptr() for t in tensors])
-    outp = array("Q", [t.data_ptr() for t in outs]) if outs is not None else None
+    ins = array("Q", map(of.data_ptr, tensors))
+    outp = array("Q", map(of.data_ptr, outs)) if outs is not None else None
     check(load().mgs_clip_norm(len(counts), ins.buffer_info()[0], outp.buffer_info()[0] if outp is not None else None,
                                counts.buffer_info()[0], dtypes.buffer_info()[0],
                                0.0 if max_norm is None else max_norm, norm.data_ptr(), ws.data_ptr(), ws.numel(),
