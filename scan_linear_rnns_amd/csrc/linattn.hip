@@ -183,7 +183,7 @@ struct Role {
 };
 
 struct WalkArgs {
-    Role role[2];
+    Role role[3];
     const float *g;
     int64_t gb, gt, gh;
     const int32_t *lengths;
@@ -380,31 +380,28 @@ __device__ __forceinline__ void lds_barrier()
 }
 
 // Zeros in place of the non-finite elements of a wave's value fragments (rows
-// 16 jb + 4 lq + r, column li of tile ct), and NaN in the output tiles (row
-// 16 i + li, columns 4 lq + r) from their rows on.
-template <typename T, int NCT>
-__device__ __forceinline__ void drop_non_finite(typename Num<T>::Frag (&vf)[4][NCT], f4v (&O)[4][NCT], int li, int lq)
+// 16 jb + 4 lq + r, column li), and NaN in the output tiles (row 16 i + li,
+// columns 4 lq + r) from their rows on.
+template <typename T>
+__device__ __forceinline__ void drop_non_finite(typename Num<T>::Frag (&vf)[4], f4v (&O)[4], int li, int lq)
 {
+    int first = kC;   // of column li
 #pragma unroll
-    for (int ct = 0; ct < NCT; ++ct) {
-        int first = kC;   // of column li
+    for (int jb = 3; jb >= 0; --jb)
 #pragma unroll
-        for (int jb = 3; jb >= 0; --jb)
+        for (int r = 3; r >= 0; --r)
+            if (!isfinite(to_f32(vf[jb][r]))) {
+                first = 16 * jb + 4 * lq + r;
+                vf[jb][r] = static_cast<T>(0.0f);
+            }
+    first = min(first, __shfl_xor(first, 16, 64));
+    first = min(first, __shfl_xor(first, 32, 64));
 #pragma unroll
-            for (int r = 3; r >= 0; --r)
-                if (!isfinite(to_f32(vf[jb][ct][r]))) {
-                    first = 16 * jb + 4 * lq + r;
-                    vf[jb][ct][r] = static_cast<T>(0.0f);
-                }
-        first = min(first, __shfl_xor(first, 16, 64));
-        first = min(first, __shfl_xor(first, 32, 64));
+    for (int r = 0; r < 4; ++r) {
+        const int f = __shfl(first, 4 * lq + r, 64);
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int f = __shfl(first, 4 * lq + r, 64);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (16 * i + li >= f) O[i][ct][r] = __builtin_nanf("");
-        }
+        for (int i = 0; i < 4; ++i)
+            if (16 * i + li >= f) O[i][r] = __builtin_nanf("");
     }
 }
 
@@ -419,8 +416,8 @@ constexpr uint64_t kScoreTiles = 0xFEDCA98540ull;
 // columns a wave, half as many waves read LDS half as often, but their registers
 // leave two waves a SIMD, and waits and vector arithmetic then show.)
 // MODE: STATE, the walk from a zero state without outputs; OUT, outputs rounded
-// to T; DOTS, outputs in T or fp32 (partials of shared heads), and the dots of
-// their rows for dg.
+// to T; DOTS, outputs in T or fp32 (partials of shared heads), and, of the roles
+// that ask for them, the dots of their rows for dg.
 // TERMS: how many bf16 terms the weighted values of the state's update take: 3
 // where the state itself, or dg, comes of it; 2 (16 bits) where only outputs
 // rounded to bf16 do.  Likewise states and scores on their way into an output: 2
@@ -444,7 +441,6 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
     constexpr int NO = N::NS == 3 && MODE != DOTS ? 2 : N::NS;   // of states and scores
     constexpr int kThreads = 4 * VD, NW = VD / 16;
     constexpr int NKB = KD / 16;       // reduction blocks
-    constexpr int NCT = 1;
     using TQ = Tile<T, KD, N::PADQ>;
     using TK = Tile<T, KD, N::PADK>;
     using TV = Tile<T, VD, N::PADV>;
@@ -478,42 +474,36 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
     const int T_ = keep(a.T), H_ = keep(a.H);
 
     const int col0 = wv * 16;   // this wave's first column
-    f4v S[NKB][NCT];
+    f4v S[NKB];
     const float *state = STATE_ONLY ? nullptr : ro.state;
     const int sc = keep(ro.sc), sk = keep(ro.sk);
     if (state) {
         // all loads in flight at once: out-of-range elements read the last one and
         // are zeroed after
         state += static_cast<int64_t>(bh) * ro.st_bh + seg * ro.st_seg;
+        const int c = col0 + li;
+        const float *p = state + min(c, cols - 1) * sc;
+        if (VEC && sk == 1) {
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) {
-            const int c = col0 + 16 * ct + li;
-            const float *p = state + min(c, cols - 1) * sc;
-            if (VEC && sk == 1) {
+            for (int t = 0; t < NKB; ++t)
+                S[t] = *reinterpret_cast<const f4v *>(p + min(16 * t + 4 * lq, kcols - 4));
+        } else {
 #pragma unroll
-                for (int t = 0; t < NKB; ++t)
-                    S[t][ct] = *reinterpret_cast<const f4v *>(p + min(16 * t + 4 * lq, kcols - 4));
-            } else {
+            for (int t = 0; t < NKB; ++t)
 #pragma unroll
-                for (int t = 0; t < NKB; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) S[t][ct][r] = p[min(16 * t + 4 * lq + r, kcols - 1) * sk];
-            }
+                for (int r = 0; r < 4; ++r) S[t][r] = p[min(16 * t + 4 * lq + r, kcols - 1) * sk];
         }
         if (cols < VD || kcols < KD) {
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct)
+            for (int t = 0; t < NKB; ++t)
 #pragma unroll
-                for (int t = 0; t < NKB; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        S[t][ct][r] = col0 + 16 * ct + li < cols && 16 * t + 4 * lq + r < kcols ? S[t][ct][r] : 0.0f;
+                for (int r = 0; r < 4; ++r)
+                    S[t][r] = col0 + li < cols && 16 * t + 4 * lq + r < kcols ? S[t][r] : 0.0f;
         }
     } else {
 #pragma unroll
         for (int t = 0; t < NKB; ++t)
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) S[t][ct] = f4v{0, 0, 0, 0};
+            S[t] = f4v{0, 0, 0, 0};
     }
     if constexpr (!STATE_ONLY) {   // the tiles above the diagonal stay zero
 #pragma unroll
@@ -533,11 +523,12 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
     // rows of the output and of what they are dotted with: lane offsets of row li
     // (rows 16 i + li lie 16 i rows further on, or back), columns 4 lq
     const int out_f32 = keep(MODE == DOTS && ro.out_f32 ? 1 : 0);
+    const int dots_on = keep(MODE == DOTS && ro.dot.p ? 1 : 0);
     const int o_size = out_f32 ? 4 : static_cast<int>(sizeof(T));
     const int64_t o_st = static_cast<int64_t>(H_) * cols * o_size, d_st = keep(ro.dot.st * static_cast<int64_t>(sizeof(T)));
     const int o_step = rev ? -16 : 16;
     const int64_t o_base = keep(static_cast<char *>(ro.out) + (b * T_ * H_ + h) * cols * o_size);
-    const int64_t d_base = keep(static_cast<const T *>(ro.dot.p) + b * ro.dot.sb + (MODE == DOTS ? h / ro.dot.div : 0) * ro.dot.sh);
+    const int64_t d_base = keep(static_cast<const T *>(ro.dot.p) + b * ro.dot.sb + (dots_on ? h / ro.dot.div : 0) * ro.dot.sh);
     const int64_t xdot = keep(ro.xdot + static_cast<int64_t>(bh) * T_);
     // The rows of the next chunk travel while this one is worked on, and its decay
     // sums are formed, by the waves in turn, while the others finish this one.
@@ -567,7 +558,7 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
     for (int n = 0; n < chunks; ++n) {
         // (opaque: addresses made of them are cheaper to form again than to keep)
         asm volatile("" : "+v"(li), "+v"(lq));
-        [[maybe_unused]] const int orow = rev ? kC - 1 - li : li, c0 = col0 + 4 * lq;
+        [[maybe_unused]] const int orow = rev ? kC - 1 - li : li, c = col0 + 4 * lq;
         const Decays &sD = sDecays[n & 1];
         k.template store<TK>(sK);
         v.template store<TV>(sV);
@@ -610,41 +601,34 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
             }
             // the state's part of the output (which needs no one's scores), then the
             // chunk's own
-            f4v O[4][NCT];
+            f4v O[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) O[i][ct] = f4v{0, 0, 0, 0};
+            for (int i = 0; i < 4; ++i) O[i] = f4v{0, 0, 0, 0};
 #pragma unroll
             for (int m = 0; m < NKB / 2; ++m) {
-                Frag s0[NCT][NO], s1[NCT][NO];
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) {
-                    split(S[2 * m][ct], s0[ct]);
-                    split(S[2 * m + 1][ct], s1[ct]);
-                }
+                Frag q0[4], q1[4], s0[NO], s1[NO];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const Frag q0 = TQ::row(sQ, 16 * i, 2 * m, li, lq), q1 = TQ::row(sQ, 16 * i, 2 * m + 1, li, lq);
-#pragma unroll
-                    for (int s = 0; s < NO; ++s)
-#pragma unroll
-                        for (int ct = 0; ct < NCT; ++ct) O[i][ct] = mma2(s0[ct][s], s1[ct][s], q0, q1, O[i][ct]);
+                    q0[i] = TQ::row(sQ, 16 * i, 2 * m, li, lq);
+                    q1[i] = TQ::row(sQ, 16 * i, 2 * m + 1, li, lq);
                 }
+                split(S[2 * m], s0);
+                split(S[2 * m + 1], s1);
+#pragma unroll
+                for (int s = 0; s < NO; ++s)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) O[i] = mma2(s0[s], s1[s], q0[i], q1[i], O[i]);
             }
             load(n + 1);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float w = inter * __builtin_amdgcn_exp2f(sD.hi[16 * i + li]);
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) O[i][ct] *= w;
+                O[i] *= w;
             }
             lds_barrier();
-            Frag vf[4][NCT];
+            Frag vf[4];
 #pragma unroll
-            for (int jb = 0; jb < 4; ++jb)
-#pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) vf[jb][ct] = TV::col(sV, 16 * jb, wv + ct, li, lq);
+            for (int jb = 0; jb < 4; ++jb) vf[jb] = TV::col(sV, 16 * jb, wv, li, lq);
             // A product with a zero weight would carry a non-finite value to rows ahead
             // of its own: such values are taken out, and from their row on their
             // column is NaN.  A product with zeros finds them.
@@ -652,55 +636,46 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
                 f4v probe = {0, 0, 0, 0};
                 if constexpr (sizeof(T) == 4) {
 #pragma unroll
-                    for (int jb = 0; jb < 4; ++jb)
-#pragma unroll
-                        for (int ct = 0; ct < NCT; ++ct) probe += vf[jb][ct] * 0.0f;
+                    for (int jb = 0; jb < 4; ++jb) probe += vf[jb] * 0.0f;
                 } else {   // (by a matrix product with zeros)
                     const Frag z = __builtin_bit_cast(Frag, uint64_t(0));
-#pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct) {
-                        probe = mma2(vf[0][ct], vf[1][ct], z, z, probe);
-                        probe = mma2(vf[2][ct], vf[3][ct], z, z, probe);
-                    }
+                    probe = mma2(vf[0], vf[1], z, z, probe);
+                    probe = mma2(vf[2], vf[3], z, z, probe);
                 }
-                if (__any((probe[0] + probe[1]) + (probe[2] + probe[3]) != 0.0f)) drop_non_finite<T, NCT>(vf, O, li, lq);
+                if (__any((probe[0] + probe[1]) + (probe[2] + probe[3]) != 0.0f)) drop_non_finite<T>(vf, O, li, lq);
             }
 #pragma unroll
             for (int m = 0; m < 2; ++m)
 #pragma unroll
-                for (int i = 2 * m; i < 4; ++i)
+                for (int s = 0; s < NO; ++s) {
+                    Frag a0[4], a1[4];
 #pragma unroll
-                    for (int s = 0; s < NO; ++s) {
+                    for (int i = 2 * m; i < 4; ++i) {
                         const T *ar = &sA[s][(16 * i + li) * LA + 32 * m + 4 * lq];
-                        const Frag a0 = frag(ar), a1 = frag(ar + 16);
-#pragma unroll
-                        for (int ct = 0; ct < NCT; ++ct)
-                            O[i][ct] = mma2(vf[2 * m][ct], vf[2 * m + 1][ct], a0, a1, O[i][ct]);
+                        a0[i] = frag(ar);
+                        a1[i] = frag(ar + 16);
                     }
+#pragma unroll
+                    for (int i = 2 * m; i < 4; ++i) O[i] = mma2(vf[2 * m], vf[2 * m + 1], a0[i], a1[i], O[i]);
+                }
 
-            [[maybe_unused]] Frag dots[MODE == DOTS ? 4 : 1][NCT];
+            [[maybe_unused]] Frag dots[MODE == DOTS ? 4 : 1];
             if constexpr (MODE == DOTS) {
-                {
-                    [[maybe_unused]] const int64_t p = d_base + ck.tb * d_st;
-                    const Buffer buf(p);
+                [[maybe_unused]] const int64_t p = d_base + ck.tb * d_st;
+                const Buffer buf(p);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int r = 16 * i + li;
-                        const bool live = r >= ck.lo && r < ck.hi;
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 16 * i + li;
+                    const bool live = r >= ck.lo && r < ck.hi && dots_on;
+                    if constexpr (VEC) {
+                        const uint32_t at = (orow + o_step * i) * static_cast<uint32_t>(d_st) + c * static_cast<uint32_t>(sizeof(T));
+                        dots[i] = buf.template load<Frag>(live && c < cols ? at : kNowhere);
+                    } else {
+                        const Global<const T> *x = reinterpret_cast<const Global<const T> *>(p + (orow + o_step * i) * d_st) + c;
 #pragma unroll
-                        for (int ct = 0; ct < NCT; ++ct) {
-                            const int c = c0 + 16 * ct;
-                            if constexpr (VEC) {
-                                const uint32_t at = (orow + o_step * i) * static_cast<uint32_t>(d_st) + c * static_cast<uint32_t>(sizeof(T));
-                                dots[i][ct] = buf.template load<Frag>(live && c < cols ? at : kNowhere);
-                            } else {
-                                const Global<const T> *x = reinterpret_cast<const Global<const T> *>(p + (orow + o_step * i) * d_st) + c;
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    dots[i][ct][e] = static_cast<T>(0.0f);
-                                    if (live && c + e < cols) dots[i][ct][e] = x[e];
-                                }
-                            }
+                        for (int e = 0; e < 4; ++e) {
+                            dots[i][e] = static_cast<T>(0.0f);
+                            if (live && c + e < cols) dots[i][e] = x[e];
                         }
                     }
                 }
@@ -709,43 +684,35 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
             if (ck.hi - ck.lo < kC) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-#pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct)
-                        if (16 * i + li < ck.lo || 16 * i + li >= ck.hi) O[i][ct] = f4v{0, 0, 0, 0};
+                    if (16 * i + li < ck.lo || 16 * i + li >= ck.hi) O[i] = f4v{0, 0, 0, 0};
             }
             const int64_t op = o_base + ck.tb * o_st;
             const Buffer out(op);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int rr = orow + o_step * i;
+                const f4v y = O[i];
+                const Frag z = __builtin_convertvector(y, Frag);
+                if constexpr (VEC) {
+                    uint32_t at = static_cast<uint32_t>(rr) * static_cast<uint32_t>(o_st) + c * static_cast<uint32_t>(o_size);
+                    if (16 * i + li >= ck.rows || c >= cols) at = kNowhere;
+                    if (MODE == DOTS && out_f32) out.store(at, y);
+                    else out.store(at, z);
+                } else if (16 * i + li < ck.rows) {
+                    const int64_t at = op + rr * o_st + c * o_size;
 #pragma unroll
-                for (int ct = 0; ct < NCT; ++ct) {
-                    const int c = c0 + 16 * ct;
-                    const f4v y = O[i][ct];
-                    const Frag z = __builtin_convertvector(y, Frag);
-                    if constexpr (VEC) {
-                        uint32_t at = static_cast<uint32_t>(rr) * static_cast<uint32_t>(o_st) + c * static_cast<uint32_t>(o_size);
-                        if (16 * i + li >= ck.rows || c >= cols) at = kNowhere;
-                        if (MODE == DOTS && out_f32) out.store(at, y);
-                        else out.store(at, z);
-                    } else if (16 * i + li < ck.rows) {
-                        const int64_t at = op + rr * o_st + c * o_size;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (c + e < cols) {
-                                if (out_f32) reinterpret_cast<Global<float> *>(at)[e] = y[e];
-                                else reinterpret_cast<Global<T> *>(at)[e] = z[e];
-                            }
-                    }
+                    for (int e = 0; e < 4; ++e)
+                        if (c + e < cols) {
+                            if (out_f32) reinterpret_cast<Global<float> *>(at)[e] = y[e];
+                            else reinterpret_cast<Global<T> *>(at)[e] = z[e];
+                        }
                 }
             }
             if constexpr (MODE == DOTS) {
                 // columns past the end have zero dots, rows that are not live zero outputs
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    f4v x = {0, 0, 0, 0};
-#pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct) x += __builtin_convertvector(dots[i][ct], f4v) * O[i][ct];
+                    const f4v x = __builtin_convertvector(dots[i], f4v) * O[i];
                     float dot = (x[0] + x[1]) + (x[2] + x[3]);
                     dot += __shfl_xor(dot, 16, 64);
                     dot += __shfl_xor(dot, 32, 64);
@@ -757,35 +724,36 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
         // S <- e^{total} S + sum over the chunk of weighted sources
         const float dec = sD.total;
 #pragma unroll
-        for (int t = 0; t < NKB; ++t)
-#pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) S[t][ct] *= dec;
+        for (int t = 0; t < NKB; ++t) S[t] *= dec;
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
-            Frag v0[NCT][NS], v1[NCT][NS];
+            Frag v0[NS], v1[NS];
+            const Frag x0 = TV::col(sV, 32 * m, wv, li, lq), x1 = TV::col(sV, 32 * m + 16, wv, li, lq);
             const f4v w0 = *reinterpret_cast<const f4v *>(&sD.src[32 * m + 4 * lq]);
             const f4v w1 = *reinterpret_cast<const f4v *>(&sD.src[32 * m + 16 + 4 * lq]);
 #pragma unroll
-            for (int ct = 0; ct < NCT; ++ct) {
-                const Frag x0 = TV::col(sV, 32 * m, wv + ct, li, lq);
-                const Frag x1 = TV::col(sV, 32 * m + 16, wv + ct, li, lq);
-                split(__builtin_convertvector(x0, f4v) * w0, v0[ct]);
-                split(__builtin_convertvector(x1, f4v) * w1, v1[ct]);
-            }
+            for (int t0 = 0; t0 < NKB; t0 += 4) {
+                Frag k0[4], k1[4];
 #pragma unroll
-            for (int t = 0; t < NKB; ++t) {
-                const Frag k0 = TK::col(sK, 32 * m, t, li, lq), k1 = TK::col(sK, 32 * m + 16, t, li, lq);
+                for (int t = 0; t < 4; ++t) {
+                    k0[t] = TK::col(sK, 32 * m, t0 + t, li, lq);
+                    k1[t] = TK::col(sK, 32 * m + 16, t0 + t, li, lq);
+                }
+                if (t0 == 0) {
+                    split(__builtin_convertvector(x0, f4v) * w0, v0);
+                    split(__builtin_convertvector(x1, f4v) * w1, v1);
+                }
 #pragma unroll
                 for (int s = 0; s < NS; ++s)
 #pragma unroll
-                    for (int ct = 0; ct < NCT; ++ct) S[t][ct] = mma2(k0, k1, v0[ct][s], v1[ct][s], S[t][ct]);
+                    for (int t = 0; t < 4; ++t) S[t0 + t] = mma2(k0[t], k1[t], v0[s], v1[s], S[t0 + t]);
             }
         }
         if constexpr (STATE_ONLY) seg_log2 += sD.log2_total;
         if (((n + 1) & (NW - 1)) == wv) chunk_decays(g, src_f, rev, sDecays[(n + 1) & 1]);
         lds_barrier();
         if constexpr (MODE == DOTS) {
-            if (tid < ck.rows) {
+            if (dots_on && tid < ck.rows) {
                 float x = 0.0f;
 #pragma unroll
                 for (int w = 0; w < NW; ++w) x += partial(w, tid);
@@ -797,22 +765,18 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
     float *fin = STATE_ONLY ? ro.local : ro.final;
     if (fin) {
         fin += static_cast<int64_t>(bh) * ro.st_bh + (STATE_ONLY ? seg * ro.st_seg : 0);
+        const int c = col0 + li;
+        float *p = fin + c * sc;
+        if (VEC && sk == 1) {
 #pragma unroll
-        for (int ct = 0; ct < NCT; ++ct) {
-            const int c = col0 + 16 * ct + li;
-            if (c >= cols) continue;
-            float *p = fin + c * sc;
-            if (VEC && sk == 1) {
+            for (int t = 0; t < NKB; ++t)
+                if (c < cols && 16 * t + 4 * lq < kcols) *reinterpret_cast<f4v *>(p + 16 * t + 4 * lq) = S[t];
+        } else {
 #pragma unroll
-                for (int t = 0; t < NKB; ++t)
-                    if (16 * t + 4 * lq < kcols) *reinterpret_cast<f4v *>(p + 16 * t + 4 * lq) = S[t][ct];
-            } else {
+            for (int t = 0; t < NKB; ++t)
 #pragma unroll
-                for (int t = 0; t < NKB; ++t)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (16 * t + 4 * lq + r < kcols) p[(16 * t + 4 * lq + r) * sk] = S[t][ct][r];
-            }
+                for (int r = 0; r < 4; ++r)
+                    if (c < cols && 16 * t + 4 * lq + r < kcols) p[(16 * t + 4 * lq + r) * sk] = S[t][r];
         }
     }
     if (STATE_ONLY && !rev && tid == 0) a.dec[static_cast<int64_t>(bh) * a.nSeg + seg] = __builtin_amdgcn_exp2f(seg_log2);
@@ -1371,12 +1335,17 @@ hipError_t launch_linattn_bwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
         rv.final = dS0;
     }
     // the dq and dk walks reduce over dv, the dv walk over dk
-    a.role[0] = rq, a.role[1] = rk;
-    a.nRoles = 2;
+    // Few walks go in one launch (16 sequences of 1024 steps, 64 wide, fp32: 69 us
+    // in two, 67 us in one); of many, dv's take the cheaper kernel.
+    const bool together = a.items <= 256 && (dk <= 64) == (dv <= 64);
+    a.role[0] = rq, a.role[1] = rk, a.role[2] = rv;
+    a.nRoles = together ? 3 : 2;
     if ((e = launch_walk<DOTS>(d.dtype, a, dv, dk, true, s)) != hipSuccess) return e;
-    a.role[0] = rv;
-    a.nRoles = 1;
-    if ((e = launch_walk<OUT>(d.dtype, a, dk, dv, rv.final != nullptr, s)) != hipSuccess) return e;
+    if (!together) {
+        a.role[0] = rv;
+        a.nRoles = 1;
+        if ((e = launch_walk<OUT>(d.dtype, a, dk, dv, rv.final != nullptr, s)) != hipSuccess) return e;
+    }
 
     DgArgs m{};
     m.x = x, m.y = y;
