@@ -530,8 +530,8 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
     const int64_t o_base = keep(static_cast<char *>(ro.out) + (b * T_ * H_ + h) * cols * o_size);
     const int64_t d_base = keep(static_cast<const T *>(ro.dot.p) + b * ro.dot.sb + (dots_on ? h / ro.dot.div : 0) * ro.dot.sh);
     const int64_t xdot = keep(ro.xdot + static_cast<int64_t>(bh) * T_);
-    // The rows of the next chunk travel while this one is worked on, and its decay
-    // sums are formed, by the waves in turn, while the others finish this one.
+    // The rows of the next chunk travel while this one is worked on; its decay sums
+    // are formed by the last wave, which has the fewest score tiles, meanwhile.
     float g = 0.0f;
     auto place = [&](int n) {
         Chunk ck = chunk_at(rev ? c_lo + chunks - 1 - n : c_lo + n, T_, len, rev);
@@ -550,9 +550,13 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
         v.load(ck);
         if constexpr (!STATE_ONLY) q.load(ck);
     };
-    if (wv < 2) load_g(wv);
+    const bool sums = wv == NW - 1;
+    if (sums) load_g(0);
     load(0);
-    if (wv == 0) chunk_decays(g, src_f, rev, sDecays[0]);
+    if (sums) {
+        chunk_decays(g, src_f, rev, sDecays[0]);
+        load_g(1);
+    }
 
     float seg_log2 = 0.0f;
     for (int n = 0; n < chunks; ++n) {
@@ -567,7 +571,10 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
         const Chunk ck = place(n);
 
         if constexpr (STATE_ONLY) load(n + 1);
-        if (((n + 2) & (NW - 1)) == wv) load_g(n + 2);
+        if (sums) {
+            chunk_decays(g, src_f, rev, sDecays[(n + 1) & 1]);
+            load_g(n + 2);
+        }
 
         if constexpr (!STATE_ONLY) {
             // scores: tile (i, j) with rows of q as columns, so that a lane holds
@@ -750,7 +757,6 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
             }
         }
         if constexpr (STATE_ONLY) seg_log2 += sD.log2_total;
-        if (((n + 1) & (NW - 1)) == wv) chunk_decays(g, src_f, rev, sDecays[(n + 1) & 1]);
         lds_barrier();
         if constexpr (MODE == DOTS) {
             if (dots_on && tid < ck.rows) {
