@@ -27,9 +27,19 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
-def _raw_stream(torch, stream, dev):
-    """The given stream, or the current one of device `dev`, as a pointer."""
-    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+def _raw_stream(torch, dev):
+    """The current stream of GPU `dev`, the current one, as a pointer."""
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"the tensors are on GPU {dev}, the current one is {torch.cuda.current_device()}")
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _on(stream, call, *args):
+    """call(*args) with `stream` current, so that what it allocates belongs to that stream: the allocator hands memory
+    that is freed to later work of the stream it came from, which has to be the one that the kernels run on."""
+    import torch
+    with torch.cuda.stream(stream):
+        return call(*args)
 
 
 def _dtype(torch, dtype):
@@ -136,6 +146,8 @@ def mgs_linattn_fwd(q, k, v, g, S0=None, lengths=None, scale=1.0, o=None, ST=Non
     projection do); query/key head h // (H / Hk) serves head h.  g: log decays, float32, (B,T,H) or (H,).
     S0 (B,H,dv,dk) float32 or None (zeros).  lengths (B,) int32 or None: later steps are not read, leave the
     state as it is and give zeros."""
+    if stream is not None:
+        return _on(stream, mgs_linattn_fwd, q, k, v, g, S0, lengths, scale, o, ST, ws, want_state)
     import torch
     dims, dev, per_head = _attn_inputs(torch, q, k, v, g, S0, lengths)
     B, T, H, Hk, dk, dv = dims
@@ -146,7 +158,7 @@ def mgs_linattn_fwd(q, k, v, g, S0=None, lengths=None, scale=1.0, o=None, ST=Non
                    *_NONE, *(_NONE if per_head else g.stride()))
     ws = _scratch(torch, ws, lambda: mgs_linattn_workspace_size(*dims, dtype=v.dtype), dev)
     check(load().mgs_linattn_fwd(d, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(S0), _ptr(lengths), _ptr(o), _ptr(ST),
-                                 _ptr(ws), ws.numel(), _raw_stream(torch, stream, dev)), "mgs_linattn_fwd")
+                                 _ptr(ws), ws.numel(), _raw_stream(torch, dev)), "mgs_linattn_fwd")
     return o, ST, ws
 
 
@@ -154,6 +166,8 @@ def mgs_linattn_bwd(q, k, v, g, do, S0=None, dST=None, lengths=None, scale=1.0, 
     """(dq, dk, dv, dg, dS0) for L = sum(do * o) + sum(dST * S_T); dg and, with decays per head, its sum over
     sequences and steps are float32, and so is dS0 (B,H,dv,dk).  do (B,T,H,dv) may be strided as v may.
     out: the five outputs, dense (dS0 may be None there)."""
+    if stream is not None:
+        return _on(stream, mgs_linattn_bwd, q, k, v, g, do, S0, dST, lengths, scale, out, ws)
     import torch
     dims, dev, per_head = _attn_inputs(torch, q, k, v, g, S0, lengths)
     B, T, H, Hk, dk, dv = dims
@@ -172,7 +186,7 @@ def mgs_linattn_bwd(q, k, v, g, do, S0=None, dST=None, lengths=None, scale=1.0, 
     ws = _scratch(torch, ws, lambda: mgs_linattn_workspace_size(*dims, dtype=v.dtype, backward=True), dev)
     check(load().mgs_linattn_bwd(d, _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(do), _ptr(S0), _ptr(dST), _ptr(lengths),
                                  _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(dg), _ptr(dS0), _ptr(ws), ws.numel(),
-                                 _raw_stream(torch, stream, dev)), "mgs_linattn_bwd")
+                                 _raw_stream(torch, dev)), "mgs_linattn_bwd")
     return dq, dk_, dv_, dg, dS0
 
 
@@ -181,6 +195,8 @@ def mgs_linattn_step(q, k, v, g, S, slots=None, scale=1.0, o=None, stream=None):
 
     q, k (B,Hk,dk), v (B,H,dv), g (B,H) or (H,).  slots (B,) int32: the state of sequence b is S[slots[b]]
     (None: S[b]); the slots of a call are distinct, and one outside S (-1) is idle: zeros out, no state touched."""
+    if stream is not None:
+        return _on(stream, mgs_linattn_step, q, k, v, g, S, slots, scale, o)
     import torch
     if v.dim() != 3 or q.dim() != 3 or S.dim() != 4:
         raise ValueError("q, k must be (B,Hk,dk), v (B,H,dv) and S (n_slots,H,dv,dk)")
@@ -202,7 +218,7 @@ def mgs_linattn_step(q, k, v, g, S, slots=None, scale=1.0, o=None, stream=None):
     d = _pack_desc(B, 1, H, Hk, dk, dv, _dtype(torch, dt), per_head, scale, qb, 0, qh, kb, 0, kh, vb, 0, vh, 0, 0, 0,
                    gb, 0, gh)
     check(load().mgs_linattn_step(d, q.data_ptr(), k.data_ptr(), v.data_ptr(), g.data_ptr(), S.data_ptr(), n_slots,
-                                  _ptr(slots), o.data_ptr(), _raw_stream(torch, stream, dev)), "mgs_linattn_step")
+                                  _ptr(slots), o.data_ptr(), _raw_stream(torch, dev)), "mgs_linattn_step")
     return o
 
 
@@ -242,6 +258,8 @@ def mgs_rmsnorm_fwd(x, w, residual=None, eps=1e-6, y=None, h=None, rstd=None, st
 
     x, residual (...,d), w (d,), float32 or bfloat16; rstd float32, one for each row.  Without a residual h is x
     itself, not a copy, unless a buffer is passed.  h may be the residual's (or x's) own dense tensor."""
+    if stream is not None:
+        return _on(stream, mgs_rmsnorm_fwd, x, w, residual, eps, y, h, rstd)
     import torch
     rows, d, xs, rs, dev, code = _norm_inputs(torch, x, w, residual)
     y = _like("y", y, x)
@@ -249,13 +267,15 @@ def mgs_rmsnorm_fwd(x, w, residual=None, eps=1e-6, y=None, h=None, rstd=None, st
     h_out = _like("h", h, x) if write_h else None
     rstd = _out(torch, "rstd", rstd, x.shape[:-1], torch.float32, dev)
     check(load().mgs_rmsnorm_fwd(x.data_ptr(), _ptr(residual), w.data_ptr(), y.data_ptr(), _ptr(h_out), rstd.data_ptr(),
-                                 rows, d, xs, rs, eps, code, _raw_stream(torch, stream, dev)), "mgs_rmsnorm_fwd")
+                                 rows, d, xs, rs, eps, code, _raw_stream(torch, dev)), "mgs_rmsnorm_fwd")
     return y, (h_out if write_h else x), rstd
 
 
 def mgs_rmsnorm_fwd_fp8(x, w, residual=None, eps=1e-6, group=0, y=None, scale=None, h=None, stream=None):
     """(y, scale, h): the norm with y in float8_e4m3fn and a float32 scale for each row (group = 0; scale (...,1)) or
     for each 128 columns (group = 128; scale (..., ceil(d / 128))); y * scale stands for the norm's output."""
+    if stream is not None:
+        return _on(stream, mgs_rmsnorm_fwd_fp8, x, w, residual, eps, group, y, scale, h)
     import torch
     rows, d, xs, rs, dev, code = _norm_inputs(torch, x, w, residual)
     y = _out(torch, "y", y, x.shape, torch.float8_e4m3fn, dev)
@@ -264,7 +284,7 @@ def mgs_rmsnorm_fwd_fp8(x, w, residual=None, eps=1e-6, group=0, y=None, scale=No
     write_h = h is not None or residual is not None or not x.is_contiguous()
     h_out = _like("h", h, x) if write_h else None
     check(load().mgs_rmsnorm_fwd_fp8(x.data_ptr(), _ptr(residual), w.data_ptr(), y.data_ptr(), scale.data_ptr(),
-                                     _ptr(h_out), rows, d, xs, rs, eps, group, code, _raw_stream(torch, stream, dev)),
+                                     _ptr(h_out), rows, d, xs, rs, eps, group, code, _raw_stream(torch, dev)),
           "mgs_rmsnorm_fwd_fp8")
     return y, scale, (h_out if write_h else x)
 
@@ -278,6 +298,8 @@ def mgs_rmsnorm_workspace_size(rows, d):
 def mgs_rmsnorm_bwd(dy, h, w, rstd, dh=None, dx=None, dw=None, ws=None, stream=None):
     """(dx, dw) for L = sum(dy * y) + sum(dh * h), from the forward's h and rstd; dx is the gradient of x and of the
     residual alike, dw (d,) float32.  dx may be dy's or dh's own tensor."""
+    if stream is not None:
+        return _on(stream, mgs_rmsnorm_bwd, dy, h, w, rstd, dh, dx, dw, ws)
     import torch
     d, dev, dt = h.shape[-1], _device("h", h), h.dtype
     code = _dtype(torch, dt)
@@ -293,7 +315,7 @@ def mgs_rmsnorm_bwd(dy, h, w, rstd, dh=None, dx=None, dw=None, ws=None, stream=N
     ws = _scratch(torch, ws, lambda: mgs_rmsnorm_workspace_size(rows, d), dev)
     check(load().mgs_rmsnorm_bwd(dy.data_ptr(), h.data_ptr(), w.data_ptr(), rstd.data_ptr(), _ptr(dh), dx.data_ptr(),
                                  dw.data_ptr(), rows, d, code, ws.data_ptr(), ws.numel(),
-                                 _raw_stream(torch, stream, dev)), "mgs_rmsnorm_bwd")
+                                 _raw_stream(torch, dev)), "mgs_rmsnorm_bwd")
     return dx, dw
 
 
@@ -314,6 +336,8 @@ def mgs_clip_norm(tensors, max_norm=None, out=None, norm=None, ws=None, stream=N
     tensors: contiguous, float32 or bfloat16 or both, any shapes.  out: tensors of the same shapes and types, or
     None to scale in place.  max_norm None: only the norm (second value None).  A norm that is not finite leaves
     the values as they are."""
+    if stream is not None:
+        return _on(stream, mgs_clip_norm, tensors, max_norm, out, norm, ws)
     import torch
     tensors = list(tensors)
     if not tensors:
@@ -349,5 +373,5 @@ def mgs_clip_norm(tensors, max_norm=None, out=None, norm=None, ws=None, stream=N
     check(load().mgs_clip_norm(len(counts), ins.buffer_info()[0], outp.buffer_info()[0] if outp is not None else None,
                                counts.buffer_info()[0], dtypes.buffer_info()[0],
                                0.0 if max_norm is None else max_norm, norm.data_ptr(), ws.data_ptr(), ws.numel(),
-                               _raw_stream(torch, stream, dev)), "mgs_clip_norm")
+                               _raw_stream(torch, dev)), "mgs_clip_norm")
     return norm, outs
