@@ -8,6 +8,11 @@
 // and sizes travel in its arguments, nothing is copied to the device).  Squares
 // are added in fp32 over the 8 elements of one access and in fp64 beyond, in
 // an order that depends on the sizes alone.
+// Measured, 393M bf16 elements in 150 tensors (0.8 GB): the squares 162 us (4.9
+// TB/s), adding up the partials 9 us, the scaling 277 us (1.6 GB, 5.8 TB/s: the
+// memory-side cache still holds part of what the first pass read; in that pass's
+// own order it took 70 us more).  40 tensors of up to 65536 fp32 elements: 5 and
+// 7 us, less than the host's work for the call.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -22,8 +27,9 @@ typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
 typedef float f8v __attribute__((ext_vector_type(8), aligned(16)));
 
 constexpr int kTile = static_cast<int>(kClipTile);
-// Up to this many partials every workgroup of the scaling adds them up itself;
-// beyond, one workgroup does it first, in a launch of its own.
+// Up to this many partials every workgroup of the scaling adds them up itself
+// (four loads a thread, shorter than a launch); beyond, one workgroup does it
+// first, in a launch of its own.
 constexpr int64_t kClipFew = 1024;
 
 struct ClipTable {

@@ -328,7 +328,7 @@ template <typename T, int DIM, int THREADS, bool VEC> struct Stage {
     }
 };
 
-// The chunk's decay sums in base 2, by wave 0, lane = row.  Forward G_r
+// The chunk's decay sums in base 2, by one wave, lane = row.  Forward G_r
 // includes row r's own decay, backward (rows in reverse order) it does not.
 // A decay below 2^-20000 clears the state as -inf does (the clamp keeps the
 // differences finite); NaN passes the comparison and propagates.
@@ -415,6 +415,16 @@ constexpr uint64_t kScoreTiles = 0xFEDCA98540ull;
 // The scores are formed once per workgroup and shared through LDS.  (With 32
 // columns a wave, half as many waves read LDS half as often, but their registers
 // leave two waves a SIMD, and waits and vector arithmetic then show.)
+//
+// What bounds it: nothing alone.  Measured on B=4, T=4096, 16 heads of 128 x 128,
+// bf16 (67 MB a tensor; a large copy runs at 4.7 TB/s): STATE 44 us (168 MB of k,
+// v and states, 3.8 TB/s), OUT 82 us (303 MB, 3.7 TB/s; 74 us, 4.1 TB/s, on one
+// sequence of 32768 steps x 8 heads), the two DOTS roles 230 us (722 MB, 3.1
+// TB/s; matrix cores busy 29% of the time, vector ALUs 47%).  A chunk is a chain
+// of LDS tile, products, splits into bf16 terms and two barriers; two workgroups
+// a CU fill each other's waits in part.  fp32, B=16, T=1024, one head of 64 x 64:
+// STATE 8, OUT 11, DOTS and dv in one launch 26 us, the time of 8 dependent
+// chunks (256 workgroups a role, one walk on a CU), not of their 4 MB a tensor.
 // MODE: STATE, the walk from a zero state without outputs; OUT, outputs rounded
 // to T; DOTS, outputs in T or fp32 (partials of shared heads), and, of the roles
 // that ask for them, the dots of their rows for dg.
@@ -529,6 +539,7 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
     const int o_step = rev ? -16 : 16;
     const int64_t o_base = keep(static_cast<char *>(ro.out) + (b * T_ * H_ + h) * cols * o_size);
     const int64_t d_base = keep(static_cast<const T *>(ro.dot.p) + b * ro.dot.sb + (dots_on ? h / ro.dot.div : 0) * ro.dot.sh);
+    const int finals = keep(ro.final ? 1 : 0);
     const int64_t xdot = keep(ro.xdot + static_cast<int64_t>(bh) * T_);
     // The rows of the next chunk travel while this one is worked on; its decay sums
     // are formed by the last wave, which has the fewest score tiles, meanwhile.
@@ -728,32 +739,35 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
             }
         }
 
-        // S <- e^{total} S + sum over the chunk of weighted sources
-        const float dec = sD.total;
+        // S <- e^{total} S + sum over the chunk of weighted sources (which nothing reads
+        // after the last chunk, unless the state leaves the kernel)
+        if (STATE_ONLY || n + 1 < chunks || finals) {
+            const float dec = sD.total;
 #pragma unroll
-        for (int t = 0; t < NKB; ++t) S[t] *= dec;
+            for (int t = 0; t < NKB; ++t) S[t] *= dec;
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            Frag v0[NS], v1[NS];
-            const Frag x0 = TV::col(sV, 32 * m, wv, li, lq), x1 = TV::col(sV, 32 * m + 16, wv, li, lq);
-            const f4v w0 = *reinterpret_cast<const f4v *>(&sD.src[32 * m + 4 * lq]);
-            const f4v w1 = *reinterpret_cast<const f4v *>(&sD.src[32 * m + 16 + 4 * lq]);
+            for (int m = 0; m < 2; ++m) {
+                Frag v0[NS], v1[NS];
+                const Frag x0 = TV::col(sV, 32 * m, wv, li, lq), x1 = TV::col(sV, 32 * m + 16, wv, li, lq);
+                const f4v w0 = *reinterpret_cast<const f4v *>(&sD.src[32 * m + 4 * lq]);
+                const f4v w1 = *reinterpret_cast<const f4v *>(&sD.src[32 * m + 16 + 4 * lq]);
 #pragma unroll
-            for (int t0 = 0; t0 < NKB; t0 += 4) {
-                Frag k0[4], k1[4];
+                for (int t0 = 0; t0 < NKB; t0 += 4) {
+                    Frag k0[4], k1[4];
 #pragma unroll
-                for (int t = 0; t < 4; ++t) {
-                    k0[t] = TK::col(sK, 32 * m, t0 + t, li, lq);
-                    k1[t] = TK::col(sK, 32 * m + 16, t0 + t, li, lq);
+                    for (int t = 0; t < 4; ++t) {
+                        k0[t] = TK::col(sK, 32 * m, t0 + t, li, lq);
+                        k1[t] = TK::col(sK, 32 * m + 16, t0 + t, li, lq);
+                    }
+                    if (t0 == 0) {
+                        split(__builtin_convertvector(x0, f4v) * w0, v0);
+                        split(__builtin_convertvector(x1, f4v) * w1, v1);
+                    }
+#pragma unroll
+                    for (int s = 0; s < NS; ++s)
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) S[t0 + t] = mma2(k0[t], k1[t], v0[s], v1[s], S[t0 + t]);
                 }
-                if (t0 == 0) {
-                    split(__builtin_convertvector(x0, f4v) * w0, v0);
-                    split(__builtin_convertvector(x1, f4v) * w1, v1);
-                }
-#pragma unroll
-                for (int s = 0; s < NS; ++s)
-#pragma unroll
-                    for (int t = 0; t < 4; ++t) S[t0 + t] = mma2(k0[t], k1[t], v0[s], v1[s], S[t0 + t]);
             }
         }
         if constexpr (STATE_ONLY) seg_log2 += sD.log2_total;
@@ -792,7 +806,9 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
 // Forward (blockIdx.y == 0): slot n of S gets the state entering segment n,
 // slot nSeg and ST the last one.  Backward: slot n of R gets the state entering
 // segment n from the future, dS0 the one left at the start.  One thread per
-// state element; 8 segments of loads in flight.
+// state element; 8 segments of loads in flight.  Bound by its traffic: 512
+// segments of 128 x 128 states, 70 MB, in 13 to 15 us (5 TB/s); both directions
+// 25 us.
 struct ChainArgs {
     float *S, *R;
     const float *dec, *S0, *dST;
@@ -841,7 +857,8 @@ __global__ void __launch_bounds__(256) chain_kernel(ChainArgs a)
 // --------------------------------------------------------------- dg and sums
 // dg of one (sequence, head, segment): the suffix sums of x - y from the
 // segment's end and <R, S> there, in double.  A step whose decay is zero has no
-// gradient (dg = a_t <D_t, S_{t-1}>).
+// gradient (dg = a_t <D_t, S_{t-1}>).  Bound by reading the states: 512 segments
+// of 128 x 128, 70 MB, in 19 us (3.7 TB/s).
 struct DgArgs {
     const float *x, *y, *S, *R;   // S: entering states, segment n's end is slot n + 1; R may be NULL
     const float *g;
@@ -966,7 +983,10 @@ __global__ void __launch_bounds__(256) group_sum_kernel(const float *p0, const f
 // -------------------------------------------------------------------- a step
 // One workgroup per (sequence, head, 16 R rows of the state): 16 lanes a row,
 // each 4 (dk <= 64) or 2 x 4 neighbouring elements of R rows.  The state is
-// read and written once; everything else is small.
+// read and written once; everything else is small.  Bound by HBM: 256 sequences
+// x 16 heads of 128 x 128, 541 MB, in 104 us (5.2 TB/s; R = 4 rows a thread in
+// flight, R = 1 took 155 us); one sequence x 16 heads of 64 x 64 in 3 us, less
+// than its launch.
 struct StepArgs {
     const void *q, *k, *v;
     const float *g;
