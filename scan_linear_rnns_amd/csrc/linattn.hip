@@ -405,8 +405,9 @@ __device__ __forceinline__ void drop_non_finite(typename Num<T>::Frag (&vf)[4], 
     }
 }
 
-// The ten 16 x 16 score tiles on or below the diagonal, tile = 4 i + j, one per nibble.
-constexpr uint64_t kScoreTiles = 0xFEDCA98540ull;
+// The ten 16 x 16 score tiles on or below the diagonal, tile = 4 i + j, one per
+// nibble, and the two above it that are read as zeros.
+constexpr uint64_t kScoreTiles = 0xB1FEDCA98540ull;
 
 // KD, VD: the reduction dimension and the output columns, padded.  Each of the
 // VD / 16 waves owns 16 output columns: of the state it keeps S^T tiles
@@ -422,9 +423,11 @@ constexpr uint64_t kScoreTiles = 0xFEDCA98540ull;
 // sequence of 32768 steps x 8 heads), the two DOTS roles 230 us (722 MB, 3.1
 // TB/s; matrix cores busy 29% of the time, vector ALUs 47%).  A chunk is a chain
 // of LDS tile, products, splits into bf16 terms and two barriers; two workgroups
-// a CU fill each other's waits in part.  fp32, B=16, T=1024, one head of 64 x 64:
-// STATE 8, OUT 11, DOTS and dv in one launch 26 us, the time of 8 dependent
-// chunks (256 workgroups a role, one walk on a CU), not of their 4 MB a tensor.
+// a CU fill each other's waits in part.  fp32, B=16, T=1024, one head of 64 x 64
+// (256 walks of one chunk a role): STATE 9, OUT 10, the three gradients in one
+// launch 19 us: the latency of a launch and of one chunk's loads, barriers and
+// products (an fp32 product of 64 x 64 x 64 keeps a CU's matrix cores 1 us), not
+// the 4 MB a tensor.
 // MODE: STATE, the walk from a zero state without outputs; OUT, outputs rounded
 // to T; DOTS, outputs in T or fp32 (partials of shared heads), and, of the roles
 // that ask for them, the dots of their rows for dg.
@@ -437,7 +440,7 @@ enum { STATE, OUT, DOTS };
 // waves a SIMD that the registers are cut for: as many as LDS lets in
 template <typename T> constexpr int walk_waves(int KD, int VD, int mode)
 {
-    if (sizeof(T) == 4) return mode == STATE && KD + VD <= 192 ? 3 : 2;
+    if (sizeof(T) == 4) return (mode == STATE && KD + VD <= 192) || KD + VD == 128 ? 3 : 2;
     return VD == 128 ? 4 : mode == STATE ? 4 : KD == 64 ? 3 : 2;
 }
 
@@ -453,12 +456,18 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
     constexpr int NKB = KD / 16;       // reduction blocks
     using TQ = Tile<T, KD, N::PADQ>;
     using TK = Tile<T, KD, N::PADK>;
-    using TV = Tile<T, VD, N::PADV>;
+    using TV = Tile<T, VD, sizeof(T) == 4 ? NW : N::PADV>;
     constexpr int LA = kC + 4;
-    __shared__ __align__(16) T sQ[STATE_ONLY ? 8 : TQ::SIZE];
-    __shared__ __align__(16) T sK[TK::SIZE];
+    __shared__ __align__(16) T sQ[STATE_ONLY ? 8 : TQ::SIZE - N::PADQ];
+    __shared__ __align__(16) T sK[TK::SIZE - N::PADK];
     __shared__ __align__(16) T sV[TV::SIZE];
-    __shared__ __align__(16) T sA[STATE_ONLY ? 1 : NO][STATE_ONLY ? 8 : kC * LA];
+    // fp32 scores take the place of q, which is done with by then, and the last rows
+    // of q and k have no padding: 42 blocks of 1280 bytes at 64 x 64, so three
+    // workgroups fit a CU (training B=16, T=1024, one head: 58.1 us, with two 62.2)
+    constexpr bool OVER = sizeof(T) == 4 && !STATE_ONLY;
+    static_assert(TQ::LD >= LA);
+    __shared__ __align__(16) T sA_own[STATE_ONLY || OVER ? 8 : NO * kC * LA];
+    T *const sA = OVER ? sQ : sA_own;
     __shared__ __align__(16) Decays sDecays[2];
 
     // the waves' partial dots of row r: in the 32 bytes after row r of the value tile
@@ -515,10 +524,8 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
         for (int t = 0; t < NKB; ++t)
             S[t] = f4v{0, 0, 0, 0};
     }
-    if constexpr (!STATE_ONLY) {   // the tiles above the diagonal stay zero
-#pragma unroll
-        for (int s = 0; s < NO; ++s)
-            for (int i = tid; i < kC * LA; i += kThreads) sA[s][i] = static_cast<T>(0.0f);
+    if constexpr (!STATE_ONLY && !OVER) {   // the tiles above the diagonal stay zero
+        for (int i = tid; i < NO * kC * LA; i += kThreads) sA[i] = static_cast<T>(0.0f);
     }
 
     Stage<T, KD, kThreads, VEC> q, k;
@@ -590,6 +597,7 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
         if constexpr (!STATE_ONLY) {
             // scores: tile (i, j) with rows of q as columns, so that a lane holds
             // 4 neighbouring sources of one row
+            [[maybe_unused]] f4v held[(12 + NW - 1) / NW];
 #pragma unroll
             for (int it = 0; it < (10 + NW - 1) / NW; ++it) {
                 const int slot = wv + NW * it;
@@ -611,10 +619,15 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
                         asm volatile("" : "+v"(e));   // (computed for every lane: a branch costs more)
                         w[r] = src + r <= row ? e : 0.0f;
                     }
-                    Frag ws[NO];
-                    split(w, ws);
+                    if constexpr (OVER) {
+                        held[it] = w;
+                    } else {
+                        Frag ws[NO];
+                        split(w, ws);
 #pragma unroll
-                    for (int s = 0; s < NO; ++s) *reinterpret_cast<Frag *>(&sA[s][row * LA + src]) = ws[s];
+                        for (int s = 0; s < NO; ++s)
+                            *reinterpret_cast<Frag *>(&sA[s * kC * LA + row * LA + src]) = ws[s];
+                    }
                 }
             }
             // the state's part of the output (which needs no one's scores), then the
@@ -643,6 +656,18 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
                 const float w = inter * __builtin_amdgcn_exp2f(sD.hi[16 * i + li]);
                 O[i] *= w;
             }
+            if constexpr (OVER) {
+                lds_barrier();
+#pragma unroll
+                for (int it = 0; it < (12 + NW - 1) / NW; ++it) {
+                    const int slot = wv + NW * it;
+                    if (slot < 12) {   // the last two are the zeros above the diagonal that are read
+                        const int tile = static_cast<int>((kScoreTiles >> (4 * slot)) & 15);
+                        const int row = 16 * (tile >> 2) + li, src = 16 * (tile & 3) + 4 * lq;
+                        *reinterpret_cast<f4v *>(&sA[row * LA + src]) = slot < 10 ? held[it] : f4v{0, 0, 0, 0};
+                    }
+                }
+            }
             lds_barrier();
             Frag vf[4];
 #pragma unroll
@@ -669,7 +694,7 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
                     Frag a0[4], a1[4];
 #pragma unroll
                     for (int i = 2 * m; i < 4; ++i) {
-                        const T *ar = &sA[s][(16 * i + li) * LA + 32 * m + 4 * lq];
+                        const T *ar = &sA[s * kC * LA + (16 * i + li) * LA + 32 * m + 4 * lq];
                         a0[i] = frag(ar);
                         a1[i] = frag(ar + 16);
                     }
