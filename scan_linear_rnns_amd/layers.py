@@ -349,7 +349,8 @@ def mgs_clip_norm(tensors, max_norm=None, out=None, norm=None, ws=None, stream=N
         return set(map(of.get_device, ts)) == {dev} and all(map(of.is_contiguous, ts))
 
     kinds = [t.dtype for t in tensors]
-    if not set(kinds) <= {torch.float32, torch.bfloat16} or not usable(tensors):
+    types = set(kinds)
+    if not types <= {torch.float32, torch.bfloat16} or not usable(tensors):
         for i, t in enumerate(tensors):
             _dtype(torch, t.dtype)
             _tensor(f"tensors[{i}]", t, t.shape, t.dtype, dev)
@@ -364,7 +365,10 @@ def mgs_clip_norm(tensors, max_norm=None, out=None, norm=None, ws=None, stream=N
                 _tensor(f"out[{i}]", o, t.shape, t.dtype, dev)
     elif out is not None:
         raise ValueError("out needs max_norm")
-    dtypes = array("i", [int(k is torch.bfloat16) for k in kinds])
+    if len(types) == 1:
+        dtypes = array("i", (_dtype(torch, kinds[0]),)) * len(kinds)
+    else:
+        dtypes = array("i", [k is torch.bfloat16 for k in kinds])
     norm = _out(torch, "norm", norm, (), torch.float32, dev)
     counts = array("q", map(of.numel, tensors))
     ws = _scratch(torch, ws, lambda: mgs_clip_norm_workspace_size(counts), dev)
