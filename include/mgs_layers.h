@@ -77,8 +77,9 @@ mgs_status mgs_linattn_fwd(const mgs_linattn_desc *desc, const void *q, const vo
  *     dq_t = scale S_t^T do_t,   dk_t = D_t^T v_t,   dv_t = D_t k_t,
  *     dg_t = exp(g_t) <D_t, S_{t-1}>,   dS0 = exp(g_1) D_1.
  * dq and dk_ are summed over the heads that share a query/key head; with
- * decay_per_head, dg is (H), summed over sequences and steps.  All sums run in
- * a fixed order.
+ * decay_per_head, dg is (H), summed over sequences and steps: zeros where there
+ * are none (T == 0, or B == 0, which needs no workspace).  All sums run in a
+ * fixed order.
  *   do_ : (B,T,H,dv), strides do_stride;  dST : (B,H,dv,dk) or NULL;
  *   dq, dk_ : (B,T,Hk,dk), dv_ : (B,T,H,dv), dense out;
  *   dg : fp32, (B,T,H) dense or (H), out;  dS0 : (B,H,dv,dk) out or NULL.

@@ -149,7 +149,7 @@ mgs_status mgs_linattn_bwd(const mgs_linattn_desc *desc, const void *q, const vo
     const size_t nqk = steps * d.Hk * d.dk * size, nv = steps * d.H * d.dv * size;
     const size_t ng = (d.decay_per_head ? static_cast<size_t>(d.H) : steps * d.H) * 4;
     if (nv > 0 && (!dq || !dk_ || !dv_)) return MGS_ERR_INVALID_VALUE;
-    if (ng > 0 && d.B > 0 && !dg) return MGS_ERR_INVALID_VALUE;
+    if (ng > 0 && !dg) return MGS_ERR_INVALID_VALUE;
     const void *f32[] = {S0, dST, lengths, dg, dS0}, *same[] = {dq, dk_, dv_};
     for (const void *p : f32)
         if (!aligned_to(p, 4)) return MGS_ERR_INVALID_VALUE;
@@ -160,10 +160,11 @@ mgs_status mgs_linattn_bwd(const mgs_linattn_desc *desc, const void *q, const vo
     in[n++] = Range{lengths, static_cast<size_t>(d.B) * 4};
     const Range out[] = {{dq, nqk}, {dk_, nqk}, {dv_, nv}, {dg, ng}, {dS0, states}};
     if (any_alias(in, n, out, 5)) return MGS_ERR_INVALID_VALUE;
-    if (d.B == 0 || d.H == 0) return MGS_OK;
+    if (d.H == 0 || (d.B == 0 && !d.decay_per_head)) return MGS_OK;
     const mgs::AttnGeom geo = mgs::attn_geometry(d, true);
     if (!attn_grids_fit(geo, d)) return MGS_ERR_UNSUPPORTED;
-    if (mgs_status st = check_workspace(workspace, workspace_bytes, geo.bytes)) return st;
+    if (d.B > 0)   // (of no sequences only dg is left, (H) zeros: no workspace)
+        if (mgs_status st = check_workspace(workspace, workspace_bytes, geo.bytes)) return st;
     return hip_status(mgs::launch_linattn_bwd(geo, d, q, k, v, g, do_, S0, dST, lengths, dq, dk_, dv_, dg, dS0,
                                               workspace, as_stream(stream)));
 }

@@ -1324,7 +1324,7 @@ hipError_t launch_linattn_bwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
 {
     const int dk = static_cast<int>(d.dk), dv = static_cast<int>(d.dv), E = dk * dv, H = static_cast<int>(d.H);
     hipError_t e;
-    if (geo.nC == 0) {
+    if (geo.nC == 0 || geo.BH == 0) {   // nothing to walk: sums over no steps, gradients that pass through
         if (d.decay_per_head && (e = copy_state(nullptr, dg, d.H, s)) != hipSuccess) return e;
         return copy_state(dST, dS0, geo.BH * E, s);
     }

@@ -167,3 +167,14 @@ def test_clip_norm_refusals(lib):
     assert lib.mgs_clip_norm_workspace_size(2, (I64 * 2)(5, 1 << 20), ctypes.byref(out)) == OK and out.value > 256
     assert lib.mgs_clip_norm_workspace_size(1, None, ctypes.byref(out)) == INVALID
     assert lib.mgs_clip_norm_workspace_size(0, None, ctypes.byref(out)) == OK
+
+
+def test_linattn_bwd_of_no_sequences_needs_the_decay_gradient(lib):
+    """With decays per head dg is (H) however many sequences there are, so it is required for B = 0 too."""
+    names = ("q", "k", "v", "g", "do", "S0", "dST", "lengths", "dq", "dk", "dv", "dg", "dS0")
+    none = {n: None for n in names}
+    call = lambda d, a: lib.mgs_linattn_bwd(ctypes.byref(d), *(a[n] for n in names), None, 0, None)  # noqa: E731
+    for T in (0, 100):
+        assert call(desc(B=0, T=T, per_head=1), {**none, "g": fake(3)}) == INVALID
+        assert call(desc(B=0, T=T, per_head=0), none) == OK
+    assert call(desc(B=0, H=0, Hk=0, per_head=1), none) == OK
