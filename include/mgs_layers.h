@@ -140,6 +140,8 @@ mgs_status mgs_rmsnorm_workspace_size(int64_t rows, int64_t d, size_t *bytes);
  *     dw = sum over rows of dy h rstd, in a fixed order.
  *   dy, h, dh : (rows,d) dense; dh may be NULL;  dx : (rows,d) dense out, may
  *   be dy's or dh's own buffer;  dw : (d) fp32 out.
+ * w and dw have d elements whatever rows is: both are required for rows == 0
+ * too, which writes zeros to dw.
  */
 mgs_status mgs_rmsnorm_bwd(const void *dy, const void *h, const void *w, const float *rstd, const void *dh,
                            void *dx, float *dw, int64_t rows, int64_t d, int dtype, void *workspace,

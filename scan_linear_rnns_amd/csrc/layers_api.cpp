@@ -271,8 +271,8 @@ mgs_status mgs_rmsnorm_bwd(const void *dy, const void *h, const void *w, const f
 {
     if (mgs_status st = check_norm(rows, d, dtype)) return st;
     const size_t size = size_of(dtype), n = static_cast<size_t>(rows) * d * size;
-    if (n > 0 && (!dy || !h || !w || !rstd || !dx)) return MGS_ERR_INVALID_VALUE;
-    if (!dw) return MGS_ERR_INVALID_VALUE;
+    if (n > 0 && (!dy || !h || !rstd || !dx)) return MGS_ERR_INVALID_VALUE;
+    if (!w || !dw) return MGS_ERR_INVALID_VALUE;   // (d), never empty: read and written for rows == 0 too
     const void *same[] = {dy, h, w, dh, dx};
     for (const void *p : same)
         if (!aligned_to(p, size)) return MGS_ERR_INVALID_VALUE;

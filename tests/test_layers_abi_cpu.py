@@ -178,3 +178,12 @@ def test_linattn_bwd_of_no_sequences_needs_the_decay_gradient(lib):
         assert call(desc(B=0, T=T, per_head=1), {**none, "g": fake(3)}) == INVALID
         assert call(desc(B=0, T=T, per_head=0), none) == OK
     assert call(desc(B=0, H=0, Hk=0, per_head=1), none) == OK
+
+
+def test_rmsnorm_bwd_of_no_rows_needs_the_weights(lib):
+    """w and dw are (d), not empty with the rows: a launch would read the one and write the other."""
+    def bwd(w=fake(2), dw=fake(6), ws=fake(9)):
+        return lib.mgs_rmsnorm_bwd(None, None, w, None, None, None, dw, 0, 64, 0, ws, 1 << 20, None)
+
+    assert bwd(w=None) == INVALID and bwd(dw=None) == INVALID
+    assert bwd(ws=None) == WORKSPACE
