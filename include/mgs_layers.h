@@ -80,6 +80,10 @@ mgs_status mgs_linattn_fwd(const mgs_linattn_desc *desc, const void *q, const vo
  * decay_per_head, dg is (H), summed over sequences and steps: zeros where there
  * are none (T == 0, or B == 0, which needs no workspace).  All sums run in a
  * fixed order.
+ * dg is formed from sums over later steps, which end at the next cleared state
+ * (exp(g) == 0 in fp32, where dg is zero): no step after it, whatever it holds,
+ * touches dg before it.  Up to there a non-finite v or k makes dg of up to 512
+ * steps before it non-finite too.
  *   do_ : (B,T,H,dv), strides do_stride;  dST : (B,H,dv,dk) or NULL;
  *   dq, dk_ : (B,T,Hk,dk), dv_ : (B,T,H,dv), dense out;
  *   dg : fp32, (B,T,H) dense or (H), out;  dS0 : (B,H,dv,dk) out or NULL.

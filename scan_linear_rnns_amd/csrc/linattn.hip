@@ -25,8 +25,10 @@
 // The gradient of g: with x_t = q_t . dq_t and y_t = k_t . dk_t, scaling all
 // decays from step t on shows
 //     dg_t = sum_{s=t}^{e} (x_s - y_s) + <R_e, S_e>
-// for any e >= t.  e is the end of t's segment (at most 512 steps): rounding
-// in the sum grows with its length.
+// for any e >= t.  e is the step ahead of the next one whose decay is zero, where
+// <R_e, S_e> = dg_{e+1} = 0, or else the end of t's segment (at most 512 steps):
+// rounding in the sum grows with its length, and nothing of what follows a
+// cleared state reaches the steps before it.
 //
 // MFMA layout: lane l supplies row (or column) l % 16 of an operand; its
 // elements of a 16-wide reduction block are 4 (l / 16) .. + 3, and register r
@@ -882,8 +884,10 @@ __global__ void __launch_bounds__(256) chain_kernel(ChainArgs a)
 // --------------------------------------------------------------- dg and sums
 // dg of one (sequence, head, segment): the suffix sums of x - y from the
 // segment's end and <R, S> there, in double.  A step whose decay is zero has no
-// gradient (dg = a_t <D_t, S_{t-1}>).  Bound by reading the states: 512 segments
-// of 128 x 128, 70 MB, in 19 us (3.7 TB/s).
+// gradient (dg = a_t <D_t, S_{t-1}>), and the sums of the steps before it start
+// anew, from zero: a segmented scan, the flags of 64 steps as one lane mask.
+// Bound by reading the states: 512 segments of 128 x 128, 70 MB, in 19 us (3.7
+// TB/s).
 struct DgArgs {
     const float *x, *y, *S, *R;   // S: entering states, segment n's end is slot n + 1; R may be NULL
     const float *g;
@@ -907,6 +911,7 @@ __device__ __forceinline__ double block_sum(double v, double *lds)
 __global__ void __launch_bounds__(256) dg_kernel(DgArgs a)
 {
     __shared__ double red[4];
+    __shared__ int restarts[4];
     const int tid = threadIdx.x, lane = tid & 63;
     const int64_t item = blockIdx.x;
     const int seg = static_cast<int>(item % a.nSeg);
@@ -946,30 +951,40 @@ __global__ void __launch_bounds__(256) dg_kernel(DgArgs a)
     }
     flux = block_sum(flux, red);
 
-    // 256 steps at a time, the latest first; thread i holds step hi - 1 - i
+    // 256 steps at a time, the latest first; thread i holds step hi - 1 - i.  flux is
+    // the sum carried in from the later steps; a clearing step (and what is carried
+    // to it) counts nothing for the steps before it.
     double sum = 0.0;
     for (int hi = t_hi; hi > t_lo; hi -= 256) {
         const int t = hi - 1 - tid;
+        const bool live = t >= t_lo && t < len;
+        const bool clears = live && a.g[b * a.gb + t * a.gt + h * a.gh] < -104.0f;
         double v = 0.0;
-        if (t >= t_lo) v = static_cast<double>(a.x[bh * a.T + t]) - static_cast<double>(a.y[bh * a.T + t]);
+        if (live && !clears) v = static_cast<double>(a.x[bh * a.T + t]) - static_cast<double>(a.y[bh * a.T + t]);
+        // lanes up to this one that clear; the sum starts after the last of them
+        const uint64_t upto = __ballot(clears) & (~uint64_t(0) >> (63 - lane));
+        const int from = upto ? 63 - __builtin_clzll(upto) : -1;
 #pragma unroll
         for (int off = 1; off < 64; off <<= 1) {
             const double u = __shfl_up(v, off, 64);
-            if (lane >= off) v += u;
+            if (lane - off >= max(from, 0)) v += u;
         }
         __syncthreads();
-        if (lane == 63) red[tid >> 6] = v;
+        if (lane == 63) {
+            red[tid >> 6] = v;
+            restarts[tid >> 6] = from >= 0;
+        }
         __syncthreads();
-        for (int w = 0; w < (tid >> 6); ++w) v += red[w];
-        const double all = (red[0] + red[1]) + (red[2] + red[3]);
-        double val = v + flux;
+        double mine = flux;   // carried in to this wave's first step
+        for (int w = 0; w < 4; ++w) {
+            if (w == (tid >> 6)) mine = flux;
+            flux = restarts[w] ? red[w] : flux + red[w];
+        }
+        const double val = live && !clears ? (from >= 0 ? v : v + mine) : 0.0;
         if (t >= t_lo) {
-            if (t >= len) val = 0.0;
-            else if (a.g[b * a.gb + t * a.gt + h * a.gh] < -104.0f) val = 0.0;
             if (!a.per_head) a.dg[(b * a.T + t) * a.H + h] = static_cast<float>(val);
             else sum += val;
         }
-        flux += all;
     }
     if (a.per_head) {
         sum = block_sum(sum, red);

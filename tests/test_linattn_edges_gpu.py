@@ -3,7 +3,7 @@ states, variants that only some calls reach.  Tolerances as in test_linattn_gpu.
 import pytest
 import torch
 
-from tests.test_linattn_gpu import make, run
+from tests.test_linattn_gpu import check, make, run
 from tests.test_parity_gpu import say
 
 pytestmark = pytest.mark.gpu
@@ -21,3 +21,52 @@ def test_no_sequences_give_zero_decay_gradients(gpu, T):
     got = mgs.mgs_linattn_bwd(*(a[n] for n in ("q", "k", "v", "g", "do")), out=outs)
     assert got[3] is outs[3] and torch.equal(got[3], torch.zeros(3, device=gpu))
     assert run(a, 1.0)["dg"].count_nonzero() == 0
+
+
+def packed(gpu, T, starts, dtype, seed):
+    """One sequence of T steps holding documents that begin at `starts` (0 first) with a cleared state."""
+    a = make(gpu, 2, T, 2, 1, 64, 64, dtype, S0=True, seed=seed)
+    a["g"][:, starts[1:]] = float("-inf")
+    return a
+
+
+def document(a, t0, t1):
+    """Its inputs alone: the state it is entered with counts for the first, the last one's gradient for the last."""
+    T = a["q"].shape[1]
+    cut = {n: a[n][:, t0:t1] for n in ("q", "k", "v", "g", "do")}
+    return dict(cut, S0=a["S0"] if t0 == 0 else None, dST=a["dST"] if t1 == T else None, lengths=None)
+
+
+PACKS = [(200, [0, 1]), (200, [0, 63, 64, 65, 128]), (600, [0, 100, 255, 256, 257, 511]), (1100, [0, 300, 512, 900]),
+         (700, [0, 512]), (600, [0, 5, 40, 41, 42, 590])]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,starts", PACKS)
+def test_cleared_states_part_the_gradients_of_documents(gpu, T, starts, dtype):
+    """Across a cleared state nothing reaches the documents before it, rounding errors neither: with each document's
+    gradients 10^3 times the one's before it, every one is as good as alone.  (A document may lie across one more
+    chunk than it would alone: one of the bound's 240 additions.)"""
+    say(f"linattn packed T={T} {starts} {dtype}")
+    a = packed(gpu, T, starts, dtype, T + len(starts))
+    ends = starts[1:] + [T]
+    for i, (t0, t1) in enumerate(zip(starts, ends)):
+        a["do"][:, t0:t1] *= 10.0 ** (3 * i)
+    a["dST"] *= 10.0 ** (3 * len(starts) - 3)
+    got = run(a, 0.125)
+    for t0, t1 in zip(starts, ends):
+        check({n: got[n][:, t0:t1] for n in ("o", "dq", "dk", "dv", "dg")}, document(a, t0, t1), 0.125, f"{t0}..{t1}")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,starts", PACKS)
+def test_non_finite_values_stay_out_of_earlier_documents(gpu, T, starts, dtype):
+    """A NaN value in the last document's second half (or only step) reaches no output of the documents before it."""
+    say(f"linattn packed with NaN T={T} {starts} {dtype}")
+    a = packed(gpu, T, starts, dtype, 7 * T + len(starts))
+    a["v"][:, (starts[-1] + T) // 2, 1, 5] = float("nan")
+    got = run(a, 0.125)
+    assert torch.isnan(got["o"][:, T - 1, 1, 5]).all() and torch.isnan(got["ST"][:, 1, 5]).all()
+    for t0, t1 in zip(starts[:-1], starts[1:]):
+        part = {n: got[n][:, t0:t1] for n in ("o", "dq", "dk", "dv", "dg")}
+        check(part, document(a, t0, t1), 0.125, f"{t0}..{t1}")
