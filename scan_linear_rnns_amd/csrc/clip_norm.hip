@@ -6,8 +6,8 @@
 // then the scaling.  Both are bound by HBM; what costs beside that is the
 // number of launches, so a launch covers up to 128 tensors (their addresses
 // and sizes travel in its arguments, nothing is copied to the device).  Squares
-// are added in fp32 over the 8 elements of one access and in fp64 beyond, in
-// an order that depends on the sizes alone.
+// are formed and added in fp64 (in fp32 they would overflow from elements of
+// 2^64 on and vanish below 2^-75), in an order that depends on the sizes alone.
 // Measured, 393M bf16 elements in 150 tensors (0.8 GB): the squares 162 us (4.9
 // TB/s), adding up the partials 9 us, the scaling 277 us (1.6 GB, 5.8 TB/s: the
 // memory-side cache still holds part of what the first pass read; in that pass's
@@ -68,12 +68,14 @@ template <int W> __device__ __forceinline__ double block_sum(double v, double *l
 __device__ __forceinline__ f8v widen(f8v v) { return v; }
 __device__ __forceinline__ f8v widen(bf8v v) { return __builtin_convertvector(v, f8v); }
 
+__device__ __forceinline__ double square(float x) { return static_cast<double>(x) * static_cast<double>(x); }
+
 __device__ __forceinline__ double square8(f8v x)
 {
-    float s = 0.0f;
+    double s = 0.0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s = __builtin_fmaf(x[e], x[e], s);
-    return static_cast<double>(s);
+    for (int e = 0; e < 8; ++e) s += square(x[e]);
+    return s;
 }
 
 // n elements of a tile: whole accesses of 8, those of a full tile all in flight;
@@ -94,10 +96,7 @@ template <typename T, typename V> __device__ __forceinline__ double tile_squares
         for (int i = threadIdx.x; i < done / 8; i += 256) sum += square8(widen(v[i]));
     }
 #pragma unroll 8
-    for (int i = done + threadIdx.x; i < n; i += 256) {
-        const float x = static_cast<float>(p[i]);
-        sum += static_cast<double>(x * x);
-    }
+    for (int i = done + threadIdx.x; i < n; i += 256) sum += square(static_cast<float>(p[i]));
     return sum;
 }
 
@@ -113,13 +112,16 @@ __global__ void __launch_bounds__(256) squares_kernel(ClipTable t, double *part)
     if (threadIdx.x == 0) part[t.base + blockIdx.x] = s;
 }
 
-// the norm from n partials, in a fixed order, by a workgroup of W waves
+// The norm from n partials, in a fixed order, by a workgroup of W waves.  From
+// 2^126 on its reciprocal, and so a coefficient, is no normal fp32 number: such a
+// norm counts as not finite.
 template <int W> __device__ __forceinline__ float norm_of(const double *part, int64_t n, double *lds)
 {
     double s = 0.0;
 #pragma unroll 8
     for (int64_t i = threadIdx.x; i < n; i += 64 * W) s += part[i];
-    return static_cast<float>(sqrt(block_sum<W>(s, lds)));
+    const double norm = sqrt(block_sum<W>(s, lds));
+    return static_cast<float>(norm < 0x1p126 ? norm : norm * __builtin_inf());
 }
 
 __global__ void __launch_bounds__(1024) norm_kernel(const double *part, int64_t n, float *norm)
