@@ -20,7 +20,10 @@
  *   - pointers are aligned to their element.  Inputs and outputs whose
  *     addresses and strides are multiples of 16 bytes take wide accesses, any
  *     others the same kernels with narrow ones;
- *   - a tensor may pass 2^31 elements (the limit is 2^40).
+ *   - a tensor may pass 2^31 elements (the limit is 2^40, and 2^31 - 65 for each
+ *     size).  Grids past what one launch takes (2^32 threads) go in several; with
+ *     up to 2^31 / 3 segments of sequences and heads in a whole-sequence call, and
+ *     2^28 sequences times heads in a step, beyond which MGS_ERR_UNSUPPORTED.
  * The workspaces here carry nothing from one call to the next and need not be
  * zero-filled; calls that share one must not run concurrently.
  */

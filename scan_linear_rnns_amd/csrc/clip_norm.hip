@@ -38,8 +38,8 @@ struct ClipTable {
     int64_t size[kClipTensors];
     int first[kClipTensors];   // first tile of each tensor, in this launch
     uint8_t bf16[kClipTensors], vec[kClipTensors];
-    int n;
-    int64_t base;              // this launch's first tile among all
+    int n, at;                 // at: the launch's first tile among the table's
+    int64_t base;              // the table's first tile among all
 };
 
 // The tensor that holds a tile: every lane looks at two first tiles (which are
@@ -103,13 +103,13 @@ template <typename T, typename V> __device__ __forceinline__ double tile_squares
 __global__ void __launch_bounds__(256) squares_kernel(ClipTable t, double *part)
 {
     __shared__ double lds[4];
-    const int i = tensor_of(t, blockIdx.x);
-    const int64_t at = static_cast<int64_t>(static_cast<int>(blockIdx.x) - t.first[i]) * kTile;
+    const int tile = t.at + static_cast<int>(blockIdx.x), i = tensor_of(t, tile);
+    const int64_t at = static_cast<int64_t>(tile - t.first[i]) * kTile;
     const int n = static_cast<int>(min(static_cast<int64_t>(kTile), t.size[i] - at));
     double s = t.bf16[i] ? tile_squares<__bf16, bf8v>(static_cast<const __bf16 *>(t.in[i]) + at, n, t.vec[i])
                          : tile_squares<float, f8v>(static_cast<const float *>(t.in[i]) + at, n, t.vec[i]);
     s = block_sum<4>(s, lds);
-    if (threadIdx.x == 0) part[t.base + blockIdx.x] = s;
+    if (threadIdx.x == 0) part[t.base + tile] = s;
 }
 
 // The norm from n partials, in a fixed order, by a workgroup of W waves.  From
@@ -164,16 +164,16 @@ __global__ void __launch_bounds__(256) scale_kernel(ClipTable t, const double *p
     float v;
     if (few) {
         v = norm_of<4>(part, n_part, lds);
-        if (t.base == 0 && blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
+        if (t.base + t.at + blockIdx.x == 0 && threadIdx.x == 0) *norm = v;
     } else {
         v = *norm;
     }
     float c = max_norm / (v + 1e-6f);
     if (!(c < 1.0f) || !isfinite(v)) c = 1.0f;
-    const int i = tensor_of(t, blockIdx.x);
+    const int tile = t.at + static_cast<int>(blockIdx.x), i = tensor_of(t, tile);
     if (c == 1.0f && t.in[i] == t.out[i]) return;
     const int64_t last = (t.size[i] - 1) / kTile;
-    const int64_t at = (last - (static_cast<int>(blockIdx.x) - t.first[i])) * kTile;
+    const int64_t at = (last - (tile - t.first[i])) * kTile;
     const int n = static_cast<int>(min(static_cast<int64_t>(kTile), t.size[i] - at));
     if (t.bf16[i])
         tile_scale<__bf16, bf8v>(static_cast<const __bf16 *>(t.in[i]) + at, static_cast<__bf16 *>(t.out[i]) + at, n, c, t.vec[i]);
@@ -181,14 +181,21 @@ __global__ void __launch_bounds__(256) scale_kernel(ClipTable t, const double *p
         tile_scale<float, f8v>(static_cast<const float *>(t.in[i]) + at, static_cast<float *>(t.out[i]) + at, n, c, t.vec[i]);
 }
 
-// Calls f(table, tiles) for each group of up to kClipTensors non-empty tensors,
-// from the first on, or from the last back.
+// Launches f(table, workgroups) for each group of up to kClipTensors non-empty
+// tensors, from the first on, or from the last back.
 template <typename F>
 hipError_t each_launch(int64_t n, const void *const *in, void *const *out, const int64_t *sizes, const int *dtypes,
                        bool back, F f)
 {
     ClipTable t{};
     int64_t base = 0, tiles = 0;
+    auto flush = [&] {
+        t.base = base;
+        return launch_sliced(tiles, 256, [&](int64_t first, unsigned blocks) {
+            t.at = static_cast<int>(first);
+            f(t, blocks);
+        });
+    };
     for (int64_t j = 0; j < n; ++j) {
         const int64_t i = back ? n - 1 - j : j;
         if (sizes[i] == 0) continue;
@@ -201,17 +208,14 @@ hipError_t each_launch(int64_t n, const void *const *in, void *const *out, const
         ++t.n;
         tiles += (sizes[i] + kTile - 1) / kTile;
         if (t.n == kClipTensors) {
-            t.base = base;
-            const hipError_t e = f(t, static_cast<unsigned>(tiles));
+            const hipError_t e = flush();
             if (e != hipSuccess) return e;
             base += tiles;
             tiles = 0;
             t.n = 0;
         }
     }
-    if (t.n == 0) return hipSuccess;
-    t.base = base;
-    return f(t, static_cast<unsigned>(tiles));
+    return flush();
 }
 
 }  // namespace
@@ -229,7 +233,6 @@ hipError_t launch_clip_norm(int64_t n, const void *const *in, void *const *out, 
     double *part = static_cast<double *>(ws);
     hipError_t e = each_launch(n, in, nullptr, sizes, dtypes, false, [&](const ClipTable &t, unsigned grid) {
         hipLaunchKernelGGL(squares_kernel, dim3(grid), dim3(256), 0, s, t, part);
-        return hipGetLastError();
     });
     if (e != hipSuccess) return e;
     const int few = out && tiles > 0 && tiles <= kClipFew;
@@ -240,7 +243,6 @@ hipError_t launch_clip_norm(int64_t n, const void *const *in, void *const *out, 
     if (!out) return hipSuccess;
     return each_launch(n, in, out, sizes, dtypes, true, [&](const ClipTable &t, unsigned grid) {
         hipLaunchKernelGGL(scale_kernel, dim3(grid), dim3(256), 0, s, t, part, tiles, max_norm, norm, few);
-        return hipGetLastError();
     });
 }
 

@@ -11,6 +11,20 @@
 
 namespace mgs {
 
+// A HIP launch has fewer than 2^32 threads along a dimension.  f(first, blocks)
+// launches workgroups first .. first + blocks - 1 of `threads` threads; larger
+// grids go in several launches.
+template <typename F> hipError_t launch_sliced(int64_t blocks, int threads, F f)
+{
+    const int64_t most = ((int64_t(1) << 32) - 1) / threads / 8 * 8;   // (a multiple of the XCDs)
+    for (int64_t first = 0; first < blocks; first += most) {
+        f(first, static_cast<unsigned>(blocks - first < most ? blocks - first : most));
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
+}
+
 // --------------------------------------------------------- linear attention
 constexpr int kAttnChunk = 64;     // steps per chunk
 constexpr int kAttnMaxDim = 128;   // largest dk, dv

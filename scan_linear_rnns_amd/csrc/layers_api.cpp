@@ -22,7 +22,7 @@ using mgs::Range;
 
 constexpr int64_t kMaxElems = int64_t(1) << 40;   // of one tensor
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1 - 64;
-constexpr int64_t kMaxGrid = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxGroups = (int64_t(1) << 31) - 1;   // workgroups numbered in 32 bits
 
 int64_t bounded(std::initializer_list<int64_t> dims) { return mgs::bounded_product(dims, kMaxElems, kMaxDim); }
 
@@ -84,13 +84,12 @@ int attn_inputs(const mgs_linattn_desc &d, int64_t T, const void *q, const void 
     return n;
 }
 
-// Blocks of every launch fit one grid dimension
-bool attn_grids_fit(const mgs::AttnGeom &g, const mgs_linattn_desc &d)
+// Workgroups of the walks, up to three a segment of a sequence and head, are
+// counted in 32 bits (the other kernels' in 64)
+bool attn_grids_fit(const mgs::AttnGeom &g)
 {
-    const int64_t items = mgs::bounded_product({g.BH, g.nSeg}, kMaxGrid, kMaxGrid);
-    if (items < 0 || items > kMaxGrid / 3 - 8) return false;
-    if (g.BH * d.dk * d.dv / 256 + 1 > kMaxGrid) return false;
-    return d.B * d.T * d.Hk * d.dk / 256 + 1 <= kMaxGrid;
+    const int64_t items = mgs::bounded_product({g.BH, g.nSeg}, kMaxGroups, kMaxGroups);
+    return items >= 0 && items <= kMaxGroups / 3 - 8;
 }
 
 }  // namespace
@@ -102,7 +101,7 @@ mgs_status mgs_linattn_workspace_size(const mgs_linattn_desc *desc, int backward
     if (!bytes) return MGS_ERR_INVALID_VALUE;
     if (mgs_status st = check_attn(desc)) return st;
     const mgs::AttnGeom f = mgs::attn_geometry(*desc, false), b = mgs::attn_geometry(*desc, true);
-    if (!attn_grids_fit(f, *desc) || (backward && !attn_grids_fit(b, *desc))) return MGS_ERR_UNSUPPORTED;
+    if (!attn_grids_fit(f) || (backward && !attn_grids_fit(b))) return MGS_ERR_UNSUPPORTED;
     *bytes = backward && b.bytes > f.bytes ? b.bytes : f.bytes;
     return MGS_OK;
 }
@@ -127,7 +126,7 @@ mgs_status mgs_linattn_fwd(const mgs_linattn_desc *desc, const void *q, const vo
     if (any_alias(in, n, out, 2)) return MGS_ERR_INVALID_VALUE;
     if (d.B == 0 || d.H == 0 || (d.T == 0 && !ST)) return MGS_OK;
     const mgs::AttnGeom geo = mgs::attn_geometry(d, false);
-    if (!attn_grids_fit(geo, d)) return MGS_ERR_UNSUPPORTED;
+    if (!attn_grids_fit(geo)) return MGS_ERR_UNSUPPORTED;
     if (mgs_status st = check_workspace(workspace, workspace_bytes, geo.bytes)) return st;
     return hip_status(mgs::launch_linattn_fwd(geo, d, q, k, v, g, S0, lengths, o, ST, workspace, as_stream(stream)));
 }
@@ -162,7 +161,7 @@ mgs_status mgs_linattn_bwd(const mgs_linattn_desc *desc, const void *q, const vo
     if (any_alias(in, n, out, 5)) return MGS_ERR_INVALID_VALUE;
     if (d.H == 0 || (d.B == 0 && !d.decay_per_head)) return MGS_OK;
     const mgs::AttnGeom geo = mgs::attn_geometry(d, true);
-    if (!attn_grids_fit(geo, d)) return MGS_ERR_UNSUPPORTED;
+    if (!attn_grids_fit(geo)) return MGS_ERR_UNSUPPORTED;
     if (d.B > 0)   // (of no sequences only dg is left, (H) zeros: no workspace)
         if (mgs_status st = check_workspace(workspace, workspace_bytes, geo.bytes)) return st;
     return hip_status(mgs::launch_linattn_bwd(geo, d, q, k, v, g, do_, S0, dST, lengths, dq, dk_, dv_, dg, dS0,
@@ -193,7 +192,7 @@ mgs_status mgs_linattn_step(const mgs_linattn_desc *desc, const void *q, const v
     const Range out[] = {{o, rows}, {S, static_cast<size_t>(cells) * 4}};
     if (any_alias(in, n, out, 2)) return MGS_ERR_INVALID_VALUE;
     if (rows == 0) return MGS_OK;
-    if (d.B * d.H > kMaxGrid / 8) return MGS_ERR_UNSUPPORTED;
+    if (d.B * d.H > kMaxGroups / 8) return MGS_ERR_UNSUPPORTED;
     return hip_status(mgs::launch_linattn_step(d, q, k, v, g, S, n_slots, slots, o, as_stream(stream)));
 }
 
@@ -230,7 +229,6 @@ static mgs_status norm_fwd(const void *x, const void *residual, const void *w, v
     const Range out[] = {{y, y_bytes}, {scale, scale_bytes}, {h, n * size}, {rstd, static_cast<size_t>(rows) * 4}};
     if (any_alias(in, 3, out, 4)) return MGS_ERR_INVALID_VALUE;
     if (n == 0) return MGS_OK;
-    if (rows > kMaxGrid) return MGS_ERR_UNSUPPORTED;
     return hip_status(mgs::launch_rmsnorm_fwd(x, residual, w, y, scale, h, rstd, rows, d, x_stride, r_stride, eps,
                                               group, fp8, dtype, as_stream(stream)));
 }

@@ -191,6 +191,7 @@ struct WalkArgs {
     const int32_t *lengths;
     float *dec;              // state-only pass: decay over each segment (bh, seg), by the forward role
     uint32_t items;          // (b, h, segment) triples
+    uint32_t first;          // this launch's first workgroup
     int nRoles, T, H, nC, nSeg, segLen, vec;
 };
 
@@ -479,8 +480,8 @@ __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kern
     int li = lane & 15, lq = lane >> 4;
     // the roles of 8 neighbouring items run side by side, an item's on one XCD:
     // they read the same rows
-    const uint32_t rest = blockIdx.x >> 3;
-    const uint32_t item = (rest / a.nRoles) * 8 + (blockIdx.x & 7);
+    const uint32_t group = a.first + blockIdx.x, rest = group >> 3;
+    const uint32_t item = (rest / a.nRoles) * 8 + (group & 7);
     if (item >= a.items) return;
     const Role &ro = a.role[rest % a.nRoles];
     const int seg = static_cast<int>(item % a.nSeg);
@@ -840,13 +841,13 @@ struct ChainArgs {
     float *S, *R;
     const float *dec, *S0, *dST;
     float *ST, *dS0;
-    int64_t BH;
+    int64_t BH, first;       // first: this launch's first workgroup
     int nSeg, E;             // E = dv dk
 };
 
 __global__ void __launch_bounds__(256) chain_kernel(ChainArgs a)
 {
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t at = (a.first + blockIdx.x) * 256 + threadIdx.x;
     if (at >= a.BH * a.E) return;
     const int64_t bh = at / a.E;
     const int e = static_cast<int>(at - bh * a.E);
@@ -895,6 +896,7 @@ struct DgArgs {
     const int32_t *lengths;
     float *dg;                    // (B,T,H), or per-head partials (B,H,nSeg)
     int64_t s_bh, s_seg, r_bh, r_seg;   // strides of S (from slot 1 on) and R
+    int64_t first;                // this launch's first workgroup
     int T, H, nSeg, segLen, E, per_head, vec;   // vec: E is a multiple of 8, S and R are 16-byte aligned
 };
 
@@ -913,7 +915,7 @@ __global__ void __launch_bounds__(256) dg_kernel(DgArgs a)
     __shared__ double red[4];
     __shared__ int restarts[4];
     const int tid = threadIdx.x, lane = tid & 63;
-    const int64_t item = blockIdx.x;
+    const int64_t item = a.first + blockIdx.x;
     const int seg = static_cast<int>(item % a.nSeg);
     const int64_t bh = item / a.nSeg, b = bh / a.H;
     const int h = static_cast<int>(bh - b * a.H);
@@ -993,10 +995,11 @@ __global__ void __launch_bounds__(256) dg_kernel(DgArgs a)
 }
 
 // dg of a decay per head: the partials of all sequences and segments, in order
-__global__ void __launch_bounds__(256) dg_head_kernel(const float *part, float *dg, int64_t B, int H, int nSeg)
+__global__ void __launch_bounds__(256) dg_head_kernel(const float *part, float *dg, int64_t B, int H, int nSeg,
+                                                      int first)
 {
     __shared__ double red[4];
-    const int h = blockIdx.x;
+    const int h = first + static_cast<int>(blockIdx.x);
     double s = 0.0;
     for (int64_t i = threadIdx.x; i < B * nSeg; i += 256) s += part[((i / nSeg) * H + h) * nSeg + i % nSeg];
     s = block_sum(s, red);
@@ -1006,9 +1009,9 @@ __global__ void __launch_bounds__(256) dg_head_kernel(const float *part, float *
 // dq, dk of a query/key head: its value heads' fp32 partials (B T,H,d) summed in order
 template <typename T>
 __global__ void __launch_bounds__(256) group_sum_kernel(const float *p0, const float *p1, T *o0, T *o1, int64_t n, int H,
-                                                        int Hk, int d)
+                                                        int Hk, int d, int64_t first)
 {
-    const int64_t at = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;   // of (B T,Hk,d)
+    const int64_t at = (first + blockIdx.x) * 256 + threadIdx.x;   // of (B T,Hk,d)
     if (at >= n) return;
     const float *p = blockIdx.y ? p1 : p0;
     const int per = H / Hk;
@@ -1035,6 +1038,7 @@ struct StepArgs {
     const int32_t *slots;
     int64_t qb, qh, kb, kh, vb, vh, gb, gh;
     int64_t n_slots;
+    uint32_t first;          // this launch's first workgroup
     int H, div, dk, dv, tiles, vec;
     float scale;
 };
@@ -1044,8 +1048,8 @@ __global__ void __launch_bounds__(256) step_kernel(StepArgs a)
 {
     using Frag = typename Num<T>::Frag;
     const int li = threadIdx.x & 15, row = threadIdx.x >> 4;
-    const uint32_t bh = blockIdx.x / a.tiles;
-    const int r0 = static_cast<int>(blockIdx.x - bh * a.tiles) * (16 * R) + row;
+    const uint32_t group = a.first + blockIdx.x, bh = group / a.tiles;
+    const int r0 = static_cast<int>(group - bh * a.tiles) * (16 * R) + row;
     const int64_t b = bh / a.H;
     const int h = static_cast<int>(bh % a.H);
     const int64_t slot = a.slots ? a.slots[b] : b;
@@ -1136,20 +1140,19 @@ bool wide(const void *p, const int64_t *st, int n, size_t size)
     return n < 3 || st[1] < (int64_t(1) << 21);
 }
 
-unsigned walk_grid(int64_t items, int roles)
-{
-    return static_cast<unsigned>((items + 7) / 8 * 8 * roles);
-}
-
 template <typename T, int MODE, int TERMS, bool VEC>
-hipError_t launch_walk(const WalkArgs &a, int kdim, int vdim, hipStream_t s)
+hipError_t launch_walk(WalkArgs a, int kdim, int vdim, hipStream_t s)
 {
-    const dim3 grid(walk_grid(a.items, a.nRoles)), block(vdim <= 64 ? 256 : 512);
-    if (kdim <= 64 && vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 64, MODE, TERMS, VEC>), grid, block, 0, s, a);
-    else if (kdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 128, MODE, TERMS, VEC>), grid, block, 0, s, a);
-    else if (vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 128, 64, MODE, TERMS, VEC>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((walk_kernel<T, 128, 128, MODE, TERMS, VEC>), grid, block, 0, s, a);
-    return hipGetLastError();
+    const int threads = vdim <= 64 ? 256 : 512;
+    const int64_t groups = (static_cast<int64_t>(a.items) + 7) / 8 * 8 * a.nRoles;
+    return launch_sliced(groups, threads, [&](int64_t first, unsigned blocks) {
+        const dim3 grid(blocks), block(threads);
+        a.first = static_cast<uint32_t>(first);
+        if (kdim <= 64 && vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 64, MODE, TERMS, VEC>), grid, block, 0, s, a);
+        else if (kdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 128, MODE, TERMS, VEC>), grid, block, 0, s, a);
+        else if (vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 128, 64, MODE, TERMS, VEC>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((walk_kernel<T, 128, 128, MODE, TERMS, VEC>), grid, block, 0, s, a);
+    });
 }
 
 // exact: whether a state that leaves the kernel, or dg, comes of the walk's state
@@ -1166,12 +1169,14 @@ hipError_t launch_walk(int dtype, const WalkArgs &a, int kdim, int vdim, bool ex
                  : launch_walk<float, MODE, 3, false>(a, kdim, vdim, s);
 }
 
-template <typename T, int NV, int R> hipError_t launch_step(const StepArgs &a, int64_t heads, hipStream_t s)
+template <typename T, int NV, int R> hipError_t launch_step(StepArgs a, int64_t heads, hipStream_t s)
 {
-    const dim3 grid(static_cast<unsigned>(heads * a.tiles)), block(256);
-    if (a.vec) hipLaunchKernelGGL((step_kernel<T, NV, R, true>), grid, block, 0, s, a);
-    else hipLaunchKernelGGL((step_kernel<T, NV, R, false>), grid, block, 0, s, a);
-    return hipGetLastError();
+    return launch_sliced(heads * a.tiles, 256, [&](int64_t first, unsigned blocks) {
+        const dim3 grid(blocks), block(256);
+        a.first = static_cast<uint32_t>(first);
+        if (a.vec) hipLaunchKernelGGL((step_kernel<T, NV, R, true>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((step_kernel<T, NV, R, false>), grid, block, 0, s, a);
+    });
 }
 
 template <typename T> hipError_t launch_step(const StepArgs &a, int64_t heads, int rows, hipStream_t s)
@@ -1258,18 +1263,19 @@ WalkArgs walk_args(const AttnGeom &geo, const mgs_linattn_desc &d, const float *
     return a;
 }
 
-hipError_t launch_chain(const AttnGeom &geo, const ChainArgs &c, int directions, hipStream_t s)
+hipError_t launch_chain(const AttnGeom &geo, ChainArgs c, int directions, hipStream_t s)
 {
-    const int64_t n = geo.BH * c.E;
-    hipLaunchKernelGGL(chain_kernel, dim3(static_cast<unsigned>((n + 255) / 256), directions), dim3(256), 0, s, c);
-    return hipGetLastError();
+    return launch_sliced((geo.BH * c.E + 255) / 256, 256, [&](int64_t first, unsigned blocks) {
+        c.first = first;
+        hipLaunchKernelGGL(chain_kernel, dim3(blocks, directions), dim3(256), 0, s, c);
+    });
 }
 
 hipError_t copy_state(const float *from, float *to, int64_t n, hipStream_t s);
 
-__global__ void __launch_bounds__(256) copy_state_kernel(const float *from, float *to, int64_t n)
+__global__ void __launch_bounds__(256) copy_state_kernel(const float *from, float *to, int64_t n, int64_t first)
 {
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t i = (first + blockIdx.x) * 256 + threadIdx.x;
     if (i < n) to[i] = from ? from[i] : 0.0f;
 }
 
@@ -1277,8 +1283,9 @@ __global__ void __launch_bounds__(256) copy_state_kernel(const float *from, floa
 hipError_t copy_state(const float *from, float *to, int64_t n, hipStream_t s)
 {
     if (!to || n == 0) return hipSuccess;
-    hipLaunchKernelGGL(copy_state_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), dim3(256), 0, s, from, to, n);
-    return hipGetLastError();
+    return launch_sliced((n + 255) / 256, 256, [&](int64_t first, unsigned blocks) {
+        hipLaunchKernelGGL(copy_state_kernel, dim3(blocks), dim3(256), 0, s, from, to, n, first);
+    });
 }
 
 }  // namespace
@@ -1424,23 +1431,30 @@ hipError_t launch_linattn_bwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
     m.T = a.T, m.H = H, m.nSeg = geo.nSeg, m.segLen = geo.segLen, m.E = E;
     m.per_head = d.decay_per_head != 0;
     m.vec = E % 8 == 0 && wide(dST, nullptr, 0, 4);
-    hipLaunchKernelGGL(dg_kernel, dim3(static_cast<unsigned>(a.items)), dim3(256), 0, s, m);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
+    e = launch_sliced(a.items, 256, [&](int64_t first, unsigned blocks) {
+        m.first = first;
+        hipLaunchKernelGGL(dg_kernel, dim3(blocks), dim3(256), 0, s, m);
+    });
+    if (e != hipSuccess) return e;
     if (d.decay_per_head) {
-        hipLaunchKernelGGL(dg_head_kernel, dim3(H), dim3(256), 0, s, m.dg, dg, d.B, H, geo.nSeg);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
+        e = launch_sliced(H, 256, [&](int64_t first, unsigned blocks) {
+            hipLaunchKernelGGL(dg_head_kernel, dim3(blocks), dim3(256), 0, s, m.dg, dg, d.B, H, geo.nSeg,
+                               static_cast<int>(first));
+        });
+        if (e != hipSuccess) return e;
     }
     if (geo.grouped) {
         const int64_t n = d.B * d.T * d.Hk * d.dk;
-        const dim3 grid(static_cast<unsigned>((n + 255) / 256), 2);
         const int Hk = static_cast<int>(d.Hk);
-        if (d.dtype == MGS_BF16)
-            hipLaunchKernelGGL(group_sum_kernel<__bf16>, grid, dim3(256), 0, s, at(geo.off_dq), at(geo.off_dk),
-                               static_cast<__bf16 *>(dq), static_cast<__bf16 *>(dk_), n, H, Hk, dk);
-        else
-            hipLaunchKernelGGL(group_sum_kernel<float>, grid, dim3(256), 0, s, at(geo.off_dq), at(geo.off_dk),
-                               static_cast<float *>(dq), static_cast<float *>(dk_), n, H, Hk, dk);
-        e = hipGetLastError();
+        e = launch_sliced((n + 255) / 256, 256, [&](int64_t first, unsigned blocks) {
+            const dim3 grid(blocks, 2);
+            if (d.dtype == MGS_BF16)
+                hipLaunchKernelGGL(group_sum_kernel<__bf16>, grid, dim3(256), 0, s, at(geo.off_dq), at(geo.off_dk),
+                                   static_cast<__bf16 *>(dq), static_cast<__bf16 *>(dk_), n, H, Hk, dk, first);
+            else
+                hipLaunchKernelGGL(group_sum_kernel<float>, grid, dim3(256), 0, s, at(geo.off_dq), at(geo.off_dk),
+                                   static_cast<float *>(dq), static_cast<float *>(dk_), n, H, Hk, dk, first);
+        });
     }
     return e;
 }

@@ -106,6 +106,7 @@ struct NormArgs {
     void *y, *h;
     float *scale, *rstd;
     int64_t rows, xs, rs;
+    int64_t first;   // this launch's first workgroup
     int d, group;
     float eps;
     int vec;
@@ -119,7 +120,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_fwd_kernel(NormArg
     constexpr int RPW = TPR < 256 ? 256 / TPR : 1;   // rows per workgroup
     __shared__ float lds[16];
     const int t = threadIdx.x % TPR;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * RPW + threadIdx.x / TPR;
+    const int64_t row = (a.first + blockIdx.x) * RPW + threadIdx.x / TPR;
     if (row >= a.rows) return;   // whole waves; with TPR > 64 whole workgroups
     const bool vec = a.vec != 0;
     const T *x = static_cast<const T *>(a.x) + row * a.xs;
@@ -371,14 +372,15 @@ template <typename F> hipError_t by_width(int64_t d, F f)
 
 int rows_per_group(int64_t d) { return d <= 1024 ? 4 : 1; }
 
-template <typename T, int OUT> hipError_t launch_fwd(const NormArgs &a, hipStream_t s)
+template <typename T, int OUT> hipError_t launch_fwd(NormArgs a, hipStream_t s)
 {
     return by_width(a.d, [&](auto tpr, auto iter) {
         constexpr int TPR = decltype(tpr)::value, ITER = decltype(iter)::value;
-        const int rpw = rows_per_group(a.d);
-        hipLaunchKernelGGL((norm_fwd_kernel<T, TPR, ITER, OUT>), dim3(static_cast<unsigned>((a.rows + rpw - 1) / rpw)),
-                           dim3(TPR < 256 ? 256 : TPR), 0, s, a);
-        return hipGetLastError();
+        const int rpw = rows_per_group(a.d), threads = TPR < 256 ? 256 : TPR;
+        return launch_sliced((a.rows + rpw - 1) / rpw, threads, [&](int64_t first, unsigned blocks) {
+            a.first = first;
+            hipLaunchKernelGGL((norm_fwd_kernel<T, TPR, ITER, OUT>), dim3(blocks), dim3(threads), 0, s, a);
+        });
     });
 }
 
