@@ -131,7 +131,8 @@ mgs_status mgs_rmsnorm_fwd(const void *x, const void *residual, const void *w, v
  * row (group == 0) or for each `group` columns of a row (group == 128; the last
  * group of a row may be narrower):
  *     scale = max(max |y| over the group, 1e-30) / 448,   y8 = round(y / scale),
- * rounded to nearest, ties to even, from the fp32 y.
+ * rounded to nearest, ties to even, from the fp32 quotient of the fp32 y and
+ * scale.
  *   y8 : (rows,d) bytes out;  scale : (rows, group ? ceil(d / group) : 1) fp32 out.
  */
 mgs_status mgs_rmsnorm_fwd_fp8(const void *x, const void *residual, const void *w, void *y8, float *scale,

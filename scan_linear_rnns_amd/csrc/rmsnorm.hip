@@ -192,10 +192,10 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_fwd_kernel(NormArg
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             const int c = (i * TPR + t) * 8;
-            // y / scale as y times 448 / max: one division a thread and turn; two ulps
-            // of fp32 ahead of a rounding to 4 bits
-            const float amax = fmaxf(m[i], kAmaxFloor), scale = amax / kE4m3Max, inv = kE4m3Max / amax;
-            const f8v q = h[i] * inv;
+            // (divided, not multiplied by 448 / max: with bf16 inputs quotients do fall on
+            // ties of the 8-bit type, and an ulp would send them to either side)
+            const float scale = fmaxf(m[i], kAmaxFloor) / kE4m3Max;
+            const f8v q = h[i] / scale;
             uint32_t lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], 0, false);
             lo = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], lo, true);
             uint32_t hi = __builtin_amdgcn_cvt_pk_fp8_f32(q[4], q[5], 0, false);
