@@ -434,10 +434,12 @@ constexpr uint64_t kScoreTiles = 0xB1FEDCA98540ull;
 // MODE: STATE, the walk from a zero state without outputs; OUT, outputs rounded
 // to T; DOTS, outputs in T or fp32 (partials of shared heads), and, of the roles
 // that ask for them, the dots of their rows for dg.
-// TERMS: how many bf16 terms the weighted values of the state's update take: 3
-// where the state itself, or dg, comes of it; 2 (16 bits) where only outputs
-// rounded to bf16 do.  Likewise states and scores on their way into an output: 2
-// in OUT, 3 in DOTS.
+// bf16 terms: the weighted values of the state's update take three, so a state is
+// fp32 whether it leaves the kernel or not, and what else a call asks for does not
+// change its outputs (two where only outputs come of it would save 2 to 3%).
+// States and scores on their way into an output take three in DOTS, whose outputs
+// make dg, and two in OUT, whose outputs are rounded to bf16: 2^-17 of each term
+// ahead of 2^-9 of the sum (three: prompts and training 3 to 6% longer).
 enum { STATE, OUT, DOTS };
 
 // waves a SIMD that the registers are cut for: as many as LDS lets in
@@ -447,13 +449,13 @@ template <typename T> constexpr int walk_waves(int KD, int VD, int mode)
     return VD == 128 ? 4 : mode == STATE ? 4 : KD == 64 ? 3 : 2;
 }
 
-template <typename T, int KD, int VD, int MODE, int TERMS, bool VEC>
+template <typename T, int KD, int VD, int MODE, bool VEC>
 __global__ void __launch_bounds__(4 * VD, walk_waves<T>(KD, VD, MODE)) walk_kernel(WalkArgs a)
 {
     using N = Num<T>;
     using Frag = typename N::Frag;
     constexpr bool STATE_ONLY = MODE == STATE;
-    constexpr int NS = N::NS == 3 ? TERMS : 1;                // terms of the weighted values
+    constexpr int NS = N::NS;                                 // terms of the weighted values
     constexpr int NO = N::NS == 3 && MODE != DOTS ? 2 : N::NS;   // of states and scores
     constexpr int kThreads = 4 * VD, NW = VD / 16;
     constexpr int NKB = KD / 16;       // reduction blocks
@@ -1140,7 +1142,7 @@ bool wide(const void *p, const int64_t *st, int n, size_t size)
     return n < 3 || st[1] < (int64_t(1) << 21);
 }
 
-template <typename T, int MODE, int TERMS, bool VEC>
+template <typename T, int MODE, bool VEC>
 hipError_t launch_walk(WalkArgs a, int kdim, int vdim, hipStream_t s)
 {
     const int threads = vdim <= 64 ? 256 : 512;
@@ -1148,25 +1150,18 @@ hipError_t launch_walk(WalkArgs a, int kdim, int vdim, hipStream_t s)
     return launch_sliced(groups, threads, [&](int64_t first, unsigned blocks) {
         const dim3 grid(blocks), block(threads);
         a.first = static_cast<uint32_t>(first);
-        if (kdim <= 64 && vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 64, MODE, TERMS, VEC>), grid, block, 0, s, a);
-        else if (kdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 128, MODE, TERMS, VEC>), grid, block, 0, s, a);
-        else if (vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 128, 64, MODE, TERMS, VEC>), grid, block, 0, s, a);
-        else hipLaunchKernelGGL((walk_kernel<T, 128, 128, MODE, TERMS, VEC>), grid, block, 0, s, a);
+        if (kdim <= 64 && vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 64, MODE, VEC>), grid, block, 0, s, a);
+        else if (kdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 64, 128, MODE, VEC>), grid, block, 0, s, a);
+        else if (vdim <= 64) hipLaunchKernelGGL((walk_kernel<T, 128, 64, MODE, VEC>), grid, block, 0, s, a);
+        else hipLaunchKernelGGL((walk_kernel<T, 128, 128, MODE, VEC>), grid, block, 0, s, a);
     });
 }
 
-// exact: whether a state that leaves the kernel, or dg, comes of the walk's state
-template <int MODE>
-hipError_t launch_walk(int dtype, const WalkArgs &a, int kdim, int vdim, bool exact, hipStream_t s)
+template <int MODE> hipError_t launch_walk(int dtype, const WalkArgs &a, int kdim, int vdim, hipStream_t s)
 {
-    if (dtype == MGS_BF16) {
-        if (!a.vec) return launch_walk<__bf16, MODE, 3, false>(a, kdim, vdim, s);
-        if constexpr (MODE != DOTS)
-            if (!exact) return launch_walk<__bf16, MODE, 2, true>(a, kdim, vdim, s);
-        return launch_walk<__bf16, MODE, 3, true>(a, kdim, vdim, s);
-    }
-    return a.vec ? launch_walk<float, MODE, 3, true>(a, kdim, vdim, s)
-                 : launch_walk<float, MODE, 3, false>(a, kdim, vdim, s);
+    if (dtype == MGS_BF16)
+        return a.vec ? launch_walk<__bf16, MODE, true>(a, kdim, vdim, s) : launch_walk<__bf16, MODE, false>(a, kdim, vdim, s);
+    return a.vec ? launch_walk<float, MODE, true>(a, kdim, vdim, s) : launch_walk<float, MODE, false>(a, kdim, vdim, s);
 }
 
 template <typename T, int NV, int R> hipError_t launch_step(StepArgs a, int64_t heads, hipStream_t s)
@@ -1315,7 +1310,7 @@ hipError_t launch_linattn_fwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
         r.state = S0;
         r.final = ST;
         r.st_bh = E;
-        return launch_walk<OUT>(d.dtype, a, dk, dv, ST != nullptr, s);
+        return launch_walk<OUT>(d.dtype, a, dk, dv, s);
     }
     char *w = static_cast<char *>(ws);
     float *S = reinterpret_cast<float *>(w + geo.off_S);
@@ -1323,7 +1318,7 @@ hipError_t launch_linattn_fwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
     r.st_seg = E;
     r.local = S;
     a.dec = reinterpret_cast<float *>(w + geo.off_dec);
-    hipError_t e = launch_walk<STATE>(d.dtype, a, dk, dv, ST != nullptr, s);
+    hipError_t e = launch_walk<STATE>(d.dtype, a, dk, dv, s);
     if (e != hipSuccess) return e;
     ChainArgs c{};
     c.S = S;
@@ -1336,7 +1331,7 @@ hipError_t launch_linattn_fwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
     e = launch_chain(geo, c, 1, s);
     if (e != hipSuccess) return e;
     r.state = S;
-    return launch_walk<OUT>(d.dtype, a, dk, dv, false, s);
+    return launch_walk<OUT>(d.dtype, a, dk, dv, s);
 }
 
 hipError_t launch_linattn_bwd(const AttnGeom &geo, const mgs_linattn_desc &d, const void *q, const void *k,
@@ -1394,7 +1389,7 @@ hipError_t launch_linattn_bwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
         l.role[0].local = S, l.role[0].st_bh = S_bh, l.role[0].st_seg = E;
         l.role[1] = rv;
         l.role[1].local = R;
-        if ((e = launch_walk<STATE>(d.dtype, l, dk, dv, true, s)) != hipSuccess) return e;
+        if ((e = launch_walk<STATE>(d.dtype, l, dk, dv, s)) != hipSuccess) return e;
         ChainArgs c{};
         c.S = S, c.R = R, c.dec = l.dec, c.S0 = S0, c.dST = dST, c.dS0 = dS0;
         c.BH = geo.BH, c.nSeg = geo.nSeg, c.E = E;
@@ -1413,11 +1408,11 @@ hipError_t launch_linattn_bwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
     const bool together = a.items <= 256 && (dk <= 64) == (dv <= 64);
     a.role[0] = rq, a.role[1] = rk, a.role[2] = rv;
     a.nRoles = together ? 3 : 2;
-    if ((e = launch_walk<DOTS>(d.dtype, a, dv, dk, true, s)) != hipSuccess) return e;
+    if ((e = launch_walk<DOTS>(d.dtype, a, dv, dk, s)) != hipSuccess) return e;
     if (!together) {
         a.role[0] = rv;
         a.nRoles = 1;
-        if ((e = launch_walk<OUT>(d.dtype, a, dk, dv, rv.final != nullptr, s)) != hipSuccess) return e;
+        if ((e = launch_walk<OUT>(d.dtype, a, dk, dv, s)) != hipSuccess) return e;
     }
 
     DgArgs m{};

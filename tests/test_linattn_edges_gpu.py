@@ -70,3 +70,28 @@ def test_non_finite_values_stay_out_of_earlier_documents(gpu, T, starts, dtype):
     for t0, t1 in zip(starts[:-1], starts[1:]):
         part = {n: got[n][:, t0:t1] for n in ("o", "dq", "dk", "dv", "dg")}
         check(part, document(a, t0, t1), 0.125, f"{t0}..{t1}")
+
+
+@pytest.mark.parametrize("B,T,H,d", [(1, 2100, 2, 64), (2, 700, 2, 128), (64, 140, 8, 64), (64, 140, 8, 128), (3, 50, 2, 64)],
+                         ids=["segments 64", "segments 128", "one piece 64", "one piece 128", "one chunk"])
+def test_outputs_do_not_depend_on_what_else_is_asked_for(gpu, B, T, H, d):
+    """o with and without the final state, the gradients with and without dS0, aligned rows or not: the same bits."""
+    import scan_linear_rnns_amd as mgs
+    say(f"linattn outputs asked for B={B} T={T} H={H} d={d}")
+    a = make(gpu, B, T, H, H, d, d, "bf16", seed=T + d)
+    ins = [a[n] for n in ("q", "k", "v", "g")]
+    o, ST, _ = mgs.mgs_linattn_fwd(*ins, scale=0.1)
+    assert torch.equal(mgs.mgs_linattn_fwd(*ins, scale=0.1, want_state=False)[0], o)
+    full = mgs.mgs_linattn_bwd(*ins, a["do"], scale=0.1)
+    part = [torch.empty_like(t) for t in full[:4]]
+    mgs.mgs_linattn_bwd(*ins, a["do"], scale=0.1, out=(*part, None))
+    for n, x, y in zip(("dq", "dk", "dv", "dg"), full, part):
+        assert torch.equal(x, y), n
+    c = dict(a)
+    for n in ("q", "k", "v", "do"):
+        pad = torch.empty(*a[n].shape[:3], d + 3, dtype=a[n].dtype, device=gpu)
+        pad[..., 1:-2] = a[n]
+        c[n] = pad[..., 1:-2]
+    got = run(c, 0.1)
+    for n, y in zip(("o", "ST", "dq", "dk", "dv", "dg", "dS0"), (o, ST, *full)):
+        assert torch.equal(got[n], y), n
