@@ -50,6 +50,7 @@ namespace {
 
 constexpr int kC = kAttnChunk;
 constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLog2eTail = static_cast<float>(1.44269504088896340736 - static_cast<double>(kLog2e));
 
 typedef float f4v __attribute__((ext_vector_type(4)));
 typedef float f8v __attribute__((ext_vector_type(8), aligned(16)));
@@ -1102,7 +1103,11 @@ __global__ void __launch_bounds__(256) step_kernel(StepArgs a)
                 }
         }
     }
-    const float dec = __builtin_amdgcn_exp2f(a.g[b * a.gb + h * a.gh] * kLog2e);
+    // e^g with the product's rounding made up for (of an exponent of 100 it is 2^-18)
+    const float g = a.g[b * a.gb + h * a.gh], e = g * kLog2e;
+    const float tail = __builtin_fmaf(g, kLog2eTail, __builtin_fmaf(g, kLog2e, -e));
+    const float near = __builtin_amdgcn_exp2f(e);
+    const float dec = fabsf(e) < 1000.0f ? __builtin_fmaf(near, tail * 0.693147180559945309417f, near) : near;
 #pragma unroll
     for (int j = 0; j < R; ++j) {
         const int r = r0 + 16 * j;

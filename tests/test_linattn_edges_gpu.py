@@ -95,3 +95,34 @@ def test_outputs_do_not_depend_on_what_else_is_asked_for(gpu, B, T, H, d):
     got = run(c, 0.1)
     for n, y in zip(("o", "ST", "dq", "dk", "dv", "dg", "dS0"), (o, ST, *full)):
         assert torch.equal(got[n], y), n
+
+
+@pytest.mark.parametrize("per_head", [False, True], ids=["decay per step", "decay per head"])
+def test_step_decay_is_an_exponential_of_fp32(gpu, per_head):
+    """With k = 0 the state is only scaled, by e^g: the exponential is good to 2^-23 (an ulp), its correction and the
+    product are rounded, 2^-24 each.  Cleared states, overflow and NaN are exact."""
+    import scan_linear_rnns_amd as mgs
+    say("linattn step decays")
+    B, H, d = 4, 64, 64
+    gen = torch.Generator().manual_seed(41)
+    S = torch.randn(B, H, d, d, generator=gen).to(gpu)
+    k = torch.zeros(B, 1, d, device=gpu)
+    v = torch.randn(B, H, d, generator=gen).to(gpu)
+    g = -torch.logspace(-4, 1.9, H).repeat(B, 1).to(gpu)      # to -79.4
+    g = g * (1 + 0.1 * torch.rand(B, H, generator=gen)).to(gpu)
+    if per_head:
+        g = g[0].contiguous()
+    want = torch.exp(g.double()).expand(B, H)[..., None, None] * S.double()
+    mgs.mgs_linattn_step(k, k, v, g, S)
+    assert bool(((S.double() - want).abs() <= 4.01 * 2.0 ** -24 * want.abs() + 2.0 ** -149).all())
+    before = S.clone()
+    edge = torch.tensor([float("-inf"), -3.0e38, 0.0, -1200.0, 89.0, float("inf"), float("nan"), -0.0], device=gpu)
+    g = edge.repeat(8).expand(B, H) if not per_head else edge.repeat(8)
+    mgs.mgs_linattn_step(k, k, v, g, S)
+    S, before = S.view(B, 8, 8, d, d), before.view(B, 8, 8, d, d)
+    for i in (0, 1, 3):
+        assert S[:, :, i].count_nonzero() == 0
+    for i in (2, 7):
+        assert torch.equal(S[:, :, i], before[:, :, i])
+    assert torch.isnan(S[:, :, 6]).all()
+    assert not torch.isfinite(S[:, :, 5]).any()
