@@ -1107,7 +1107,7 @@ __global__ void __launch_bounds__(256) step_kernel(StepArgs a)
     const float g = a.g[b * a.gb + h * a.gh], e = g * kLog2e;
     const float tail = __builtin_fmaf(g, kLog2eTail, __builtin_fmaf(g, kLog2e, -e));
     const float near = __builtin_amdgcn_exp2f(e);
-    const float dec = fabsf(e) < 1000.0f ? __builtin_fmaf(near, tail * 0.693147180559945309417f, near) : near;
+    const float dec = near > 0.0f && near < __builtin_inff() ? __builtin_fmaf(near, tail * 0.693147180559945309417f, near) : near;
 #pragma unroll
     for (int j = 0; j < R; ++j) {
         const int r = r0 + 16 * j;

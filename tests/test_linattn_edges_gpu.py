@@ -126,3 +126,17 @@ def test_step_decay_is_an_exponential_of_fp32(gpu, per_head):
         assert torch.equal(S[:, :, i], before[:, :, i])
     assert torch.isnan(S[:, :, 6]).all()
     assert not torch.isfinite(S[:, :, 5]).any()
+
+
+def test_step_growth_past_fp32_is_infinite(gpu):
+    """Where e^g overflows, a state becomes an infinity of its sign, whatever the exponent's tail is (zero for some)."""
+    import scan_linear_rnns_amd as mgs
+    say("linattn step growth")
+    H, d = 512, 16
+    S = torch.randn(1, H, d, d, generator=torch.Generator().manual_seed(43)).to(gpu)
+    z = torch.zeros(1, 1, d, device=gpu)
+    g = torch.linspace(88.75, 400.0, H, device=gpu)[None]
+    g[0, 0], g[0, 1] = 1e30, float("inf")
+    want = S.sign() * float("inf")
+    mgs.mgs_linattn_step(z, z, torch.zeros(1, H, d, device=gpu), g, S)
+    assert torch.equal(S, want)
