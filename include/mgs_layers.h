@@ -161,7 +161,8 @@ mgs_status mgs_rmsnorm_bwd(const void *dy, const void *h, const void *w, const f
  *     norm = sqrt(sum of squares over all of them),
  *     out_i = in_i c,   c = min(1, max_norm / (norm + 1e-6)).
  * in, out, sizes and dtypes are host arrays, read during the call; out[i] may
- * equal in[i] (in place), and no other overlaps are allowed.  Squares and their
+ * equal in[i] (in place), and no output may overlap anything else (so a tensor
+ * that is listed twice cannot be scaled in place).  Squares and their
  * sum are fp64, in a fixed order; norm is rounded to fp32 once.  Where the norm
  * is not finite (an element is not, or it would be 2^126 or more, where 1 / norm
  * is no normal fp32 number) the tensors are passed through unscaled and norm

@@ -5,9 +5,12 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstddef>
 #include <cstdint>
+#include <memory>
+#include <new>
 
 #include "api_common.hpp"
 #include "layers.hpp"
@@ -301,6 +304,36 @@ static mgs_status check_clip(int64_t n, const int64_t *sizes)
     return MGS_OK;
 }
 
+// Every output must be disjoint from every other output and from every input but
+// its own: all of them in the order of their addresses, each against the furthest
+// end before it.
+static mgs_status check_clip_overlaps(int64_t n, const void *const *in, void *const *out, const int64_t *sizes,
+                                      const int *dtypes)
+{
+    struct Span {
+        uintptr_t begin, end;
+        bool out;
+    };
+    std::unique_ptr<Span[]> all(new (std::nothrow) Span[2 * static_cast<size_t>(n)]);
+    if (!all) return hip_status(hipErrorOutOfMemory);
+    int64_t m = 0;
+    for (int64_t i = 0; i < n; ++i) {
+        const size_t bytes = static_cast<size_t>(sizes[i]) * size_of(dtypes[i]);
+        if (bytes == 0) continue;
+        const uintptr_t o = reinterpret_cast<uintptr_t>(out[i]), x = reinterpret_cast<uintptr_t>(in[i]);
+        all[m++] = Span{o, o + bytes, true};
+        if (x != o) all[m++] = Span{x, x + bytes, false};
+    }
+    std::sort(all.get(), all.get() + m, [](const Span &a, const Span &b) { return a.begin < b.begin; });
+    uintptr_t end[2] = {0, 0};   // of the inputs and the outputs so far
+    for (int64_t i = 0; i < m; ++i) {
+        const Span &s = all[i];
+        if (s.begin < end[1] || (s.out && s.begin < end[0])) return MGS_ERR_INVALID_VALUE;
+        end[s.out] = std::max(end[s.out], s.end);
+    }
+    return MGS_OK;
+}
+
 static size_t clip_bytes(int64_t tiles) { return 256 + static_cast<size_t>(tiles) * sizeof(double); }
 
 mgs_status mgs_clip_norm_workspace_size(int64_t n, const int64_t *sizes, size_t *bytes)
@@ -325,8 +358,10 @@ mgs_status mgs_clip_norm(int64_t n, const void *const *in, void *const *out, con
         const size_t size = size_of(dtypes[i]);
         if (!aligned_to(in[i], size) || (out && !aligned_to(out[i], size))) return MGS_ERR_INVALID_VALUE;
         const Range a{in[i], sizes[i] * size}, b{out ? out[i] : nullptr, sizes[i] * size}, s{norm, 4};
-        if (overlaps(a, s) || overlaps(b, s) || (b.p != a.p && overlaps(a, b))) return MGS_ERR_INVALID_VALUE;
+        if (overlaps(a, s) || overlaps(b, s)) return MGS_ERR_INVALID_VALUE;
     }
+    if (out && n > 0)
+        if (mgs_status st = check_clip_overlaps(n, in, out, sizes, dtypes)) return st;
     const int64_t tiles = mgs::clip_tiles(n, sizes);
     if (mgs_status st = check_workspace(workspace, workspace_bytes, clip_bytes(tiles))) return st;
     return hip_status(mgs::launch_clip_norm(n, in, out, sizes, dtypes, max_norm, norm, workspace, tiles,

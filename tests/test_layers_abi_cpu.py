@@ -187,3 +187,25 @@ def test_rmsnorm_bwd_of_no_rows_needs_the_weights(lib):
 
     assert bwd(w=None) == INVALID and bwd(dw=None) == INVALID
     assert bwd(ws=None) == WORKSPACE
+
+
+def test_clip_norm_outputs_over_other_tensors(lib):
+    """Two workgroups would read and write the same memory: a tensor listed twice and scaled in place, an output over
+    another's input or output, wherever they stand in the list.  Inputs may overlap each other."""
+    def call(spans, nbytes=0):
+        """spans: (in, out) addresses in bytes past a base, 10 fp32 elements each; WORKSPACE says the checks passed."""
+        n = len(spans)
+        p = lambda t: (ctypes.c_void_p * n)(*[fake(0, x).value for x in t])  # noqa: E731
+        return lib.mgs_clip_norm(n, p([i for i, _ in spans]), p([o for _, o in spans]), (I64 * n)(*[10] * n),
+                                 (ctypes.c_int * n)(*[0] * n), 1.0, fake(8), fake(9), nbytes, None)
+
+    far = [(4000 + 80 * i, 8000 + 80 * i) for i in range(20)]
+    for rest in ([], far):
+        assert call(rest + [(0, 0), (0, 0)]) == INVALID                  # the same tensor twice, in place
+        assert call([(0, 0)] + rest + [(20, 20)]) == INVALID             # views that share elements
+        assert call([(0, 400)] + rest + [(800, 400)]) == INVALID         # two outputs on one buffer
+        assert call([(0, 400)] + rest + [(400, 800)]) == INVALID         # an output over a later input
+        assert call([(400, 800)] + rest + [(0, 436)]) == INVALID   # over an earlier one, by a word
+        assert call([(400, 400)] + rest + [(0, 364)]) == INVALID
+        assert call([(0, 400)] + rest + [(0, 800), (20, 1200)]) == WORKSPACE        # inputs alone may
+        assert call([(0, 0)] + rest + [(40, 40), (80, 120)]) == WORKSPACE           # neighbours
