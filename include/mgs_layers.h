@@ -47,7 +47,7 @@ enum { MGS_F32 = 0, MGS_BF16 = 1 };
  *          query/key head h / (H / Hk), so Hk divides H;
  *   v    : (B,T,H,dv), strides v_stride;
  *   g    : log decays, fp32: (B,T,H) with strides g_stride, or (H) dense where
- *          decay_per_head != 0.  -inf clears the state exactly; NaN and +inf
+ *          decay_per_head != 0.  -inf clears a finite state exactly; NaN and +inf
  *          propagate.
  *   lengths : (B) int32 or NULL: steps t > lengths[b] are not read (whatever
  *          they hold); they leave the state as it is and get zeros in every
@@ -55,6 +55,9 @@ enum { MGS_F32 = 0, MGS_BF16 = 1 };
  *   S0, ST : (B,H,dv,dk) fp32, dense; ST (the state after the last step) may
  *          be NULL.
  *   o    : (B,T,H,dv), dense.
+ * An element of v that is not finite makes its column of o, and its row of the
+ * state, not finite from its step on (NaN also where the sum would be infinite);
+ * it touches no earlier step and no other column.
  * Envelope: 1 <= dk, dv <= 128.
  */
 typedef struct {

@@ -1,9 +1,10 @@
 """GPU tests of linear attention (mgs_linattn_fwd, _bwd, _step) at edges of its definition: empty batches, cleared
 states, variants that only some calls reach.  Tolerances as in test_linattn_gpu.py where nothing else is said."""
+import numpy as np
 import pytest
 import torch
 
-from tests.test_linattn_gpu import check, make, run
+from tests.test_linattn_gpu import check, make, n64, reference, run
 from tests.test_parity_gpu import say
 
 pytestmark = pytest.mark.gpu
@@ -140,3 +141,83 @@ def test_step_growth_past_fp32_is_infinite(gpu):
     want = S.sign() * float("inf")
     mgs.mgs_linattn_step(z, z, torch.zeros(1, H, d, device=gpu), g, S)
     assert torch.equal(S, want)
+
+
+def check_cut(got, a, scale, who=""):
+    """check() where an output in bf16 comes of two bf16 terms: each state and score on its way there is cut to within
+    2^-18 of itself (8 bits and 8 of the rest), so the bound of test_linattn_gpu.py grows by 2^-18 of the sum of
+    absolute terms.  Everything that is not rounded to bf16 has to meet the bound as it is."""
+    want, size = reference(a, scale)
+    T, dk, dv = a["q"].shape[1], a["q"].shape[3], a["v"].shape[3]
+    gamma = (dk + dv + 64 + -(-T // 64) + 48) * 2.0 ** -24
+    for name, t in got.items():
+        x = n64(t)
+        tol = gamma * size[name]
+        if t.dtype == torch.bfloat16:
+            tol = tol + 2.0 ** -18 * size[name] + 2.0 ** -8 * np.abs(want[name])
+        assert x.shape == want[name].shape, (who, name)
+        bad = ~(np.abs(x - want[name]) <= tol)
+        assert not bad.any(), (who, name, int(bad.sum()), float(np.abs(x - want[name])[bad].max()))
+
+
+@pytest.mark.parametrize("B,T,H,d", [(1, 1300, 2, 64), (1, 600, 2, 128), (260, 70, 2, 64), (2, 100, 2, 128)],
+                         ids=["segments 64", "segments 128", "one piece 64", "few chunks 128"])
+def test_output_alone(gpu, B, T, H, d):
+    """The forward of a training step: no final state is asked for."""
+    import scan_linear_rnns_amd as mgs
+    say(f"linattn output alone B={B} T={T} H={H} d={d}")
+    a = make(gpu, B, T, H, H, d, d, "bf16", seed=T, back=False)
+    o, ST, _ = mgs.mgs_linattn_fwd(*(a[n] for n in ("q", "k", "v", "g")), scale=d ** -0.5, want_state=False)
+    assert ST is None
+    check_cut(dict(o=o), a, d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("S0", [True, False], ids=["states", "no states"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_gradients_of_many_walks(gpu, d, S0, dtype):
+    """Over 256 (sequence, head, segment) triples: dv's walk is a launch of its own, in reverse, with and without the
+    states' gradients."""
+    import scan_linear_rnns_amd as mgs
+    B, T, H = 33, 70, 8
+    say(f"linattn many walks d={d} states={S0} {dtype}")
+    a = make(gpu, B, T, H, H, d, d, dtype, S0=S0, seed=d)
+    ins = [a[n] for n in ("q", "k", "v", "g")]
+    outs = [torch.empty_like(a[n]) for n in ("q", "k", "v")] + [torch.empty_like(a["g"])]
+    dS0 = torch.empty(B, H, d, d, device=gpu) if S0 else None
+    mgs.mgs_linattn_bwd(*ins, a["do"], S0=a["S0"], dST=a["dST"], scale=d ** -0.5, out=(*outs, dS0))
+    got = dict(zip(("dq", "dk", "dv", "dg"), outs))
+    if S0:
+        got["dS0"] = dS0
+    check_cut(got, a, d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("B,H,Hk,dk,dv", [(2, 4, 2, 64, 64), (3, 2, 1, 33, 17), (70, 8, 8, 64, 128)])
+def test_step_with_a_decay_per_head(gpu, B, H, Hk, dk, dv, dtype):
+    import scan_linear_rnns_amd as mgs
+    say(f"linattn step, decay per head B={B} H={H} dk={dk} dv={dv} {dtype}")
+    a = make(gpu, B, 1, H, Hk, dk, dv, dtype, decay="head", S0=True, seed=B, back=False)
+    want, size = reference(a, 0.3)
+    S = a["S0"].clone()
+    o = mgs.mgs_linattn_step(a["q"][:, 0], a["k"][:, 0], a["v"][:, 0], a["g"], S, scale=0.3)
+    gamma = (dk + 48) * 2.0 ** -24
+    assert (np.abs(n64(S) - want["ST"]) <= gamma * size["ST"]).all()
+    last = 2.0 ** -8 * np.abs(want["o"][:, 0]) if dtype == "bf16" else 0.0
+    assert (np.abs(n64(o) - want["o"][:, 0]) <= gamma * size["o"][:, 0] + last).all()
+
+
+def test_infinite_values_are_not_finite_from_their_step_on(gpu):
+    """An infinity in v makes its column's outputs and state not finite from its step on (NaN or infinite), and
+    touches no earlier step and no other column."""
+    say("linattn infinite values")
+    for dtype in ("f32", "bf16"):
+        for value in (float("inf"), float("-inf")):
+            a = make(gpu, 1, 200, 1, 1, 64, 64, dtype, back=False, seed=47)
+            a["v"][0, 70, 0, 3] = value
+            got = run(a, 1.0)
+            o = got["o"].float()
+            assert torch.isfinite(o[0, :70]).all() and not torch.isfinite(o[0, 70:, 0, 3]).any()
+            other = torch.arange(64, device=gpu) != 3
+            assert torch.isfinite(o[..., other]).all() and torch.isfinite(got["ST"][:, :, other]).all()
+            assert not torch.isfinite(got["ST"][0, 0, 3]).any()
