@@ -8,8 +8,8 @@
 // and sizes travel in its arguments, nothing is copied to the device).  Squares
 // are formed and added in fp64 (in fp32 they would overflow from elements of
 // 2^64 on and vanish below 2^-75), in an order that depends on the sizes alone.
-// Measured, 393M bf16 elements in 150 tensors (0.8 GB): the squares 162 us (4.9
-// TB/s), adding up the partials 9 us, the scaling 277 us (1.6 GB, 5.8 TB/s: the
+// Measured, 393M bf16 elements in 150 tensors (0.8 GB): the squares 161 us (4.9
+// TB/s), adding up the partials 8 us, the scaling 276 us (1.6 GB, 5.8 TB/s: the
 // memory-side cache still holds part of what the first pass read; in that pass's
 // own order it took 70 us more).  40 tensors of up to 65536 fp32 elements: 5 and
 // 7 us, less than the host's work for the call.

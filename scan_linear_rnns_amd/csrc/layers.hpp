@@ -55,7 +55,7 @@ hipError_t launch_linattn_step(const mgs_linattn_desc &d, const void *q, const v
                                hipStream_t s);
 
 // --------------------------------------------------------------------- norm
-constexpr int64_t kNormMaxDim = 65536;   // a row is held in one workgroup's registers
+constexpr int64_t kNormMaxDim = 65536;   // a row is held by one workgroup (in registers up to 8192 columns)
 
 struct NormBwdGeom {
     int blocks;        // workgroups, each walking rows blockIdx, blockIdx + blocks, ...

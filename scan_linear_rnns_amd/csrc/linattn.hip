@@ -7,8 +7,8 @@
 //     S  <- e^{G_C} S + sum_j e^{G_C - G_j} v_j k_j^T:
 // matrix products over the chunk.  All exponents are differences of sums of
 // the same chunk, kept in base 2 as two floats (a double rounded to head and
-// tail), so a decay is good to an ulp wherever it counts however long the
-// chunk's sums grow, and e^{-inf} (a cleared state) is an exact zero.
+// tail), so a difference is good to 2^-24 of itself however large the sums that it
+// comes of, and e^{-inf} (a cleared state) is an exact zero.
 //
 // The three gradients are the same walk with other operands.  With do in the
 // query's place, v in the key's and k in the value's, the walk's output is dq
@@ -422,16 +422,18 @@ constexpr uint64_t kScoreTiles = 0xB1FEDCA98540ull;
 // leave two waves a SIMD, and waits and vector arithmetic then show.)
 //
 // What bounds it: nothing alone.  Measured on B=4, T=4096, 16 heads of 128 x 128,
-// bf16 (67 MB a tensor; a large copy runs at 4.7 TB/s): STATE 44 us (168 MB of k,
-// v and states, 3.8 TB/s), OUT 82 us (303 MB, 3.7 TB/s; 74 us, 4.1 TB/s, on one
-// sequence of 32768 steps x 8 heads), the two DOTS roles 230 us (722 MB, 3.1
-// TB/s; matrix cores busy 29% of the time, vector ALUs 47%).  A chunk is a chain
+// bf16 (67 MB a tensor; a large copy runs at 4.7 TB/s): STATE 47 us (169 MB of k,
+// v and states, 3.6 TB/s), OUT 88 us (306 MB, 3.5 TB/s; 75 us, 4.1 TB/s, on one
+// sequence of 32768 steps x 8 heads), the two DOTS roles 233 us (726 MB, 3.1
+// TB/s; matrix cores busy 27% of the time, vector ALUs 46%).  A chunk is a chain
 // of LDS tile, products, splits into bf16 terms and two barriers; two workgroups
-// a CU fill each other's waits in part.  fp32, B=16, T=1024, one head of 64 x 64
-// (256 walks of one chunk a role): STATE 9, OUT 10, the three gradients in one
-// launch 19 us: the latency of a launch and of one chunk's loads, barriers and
-// products (an fp32 product of 64 x 64 x 64 keeps a CU's matrix cores 1 us), not
-// the 4 MB a tensor.
+// a CU fill each other's waits in part.  (At 128 x 128 in bf16 2 to 4 vector
+// registers spill in OUT and DOTS.)  fp32, B=16, T=1024, one head of 64 x 64 (256
+// walks of one chunk a role): STATE 8, OUT 10, the three gradients in one launch
+// 19 us: the latency of a launch and of one chunk's loads, barriers and products
+// (an fp32 product of 64 x 64 x 64 keeps a CU's matrix cores 1 us), not the 4 MB a
+// tensor.  A chunk past a sequence's length reads nothing, but is walked as any
+// other.
 // MODE: STATE, the walk from a zero state without outputs; OUT, outputs rounded
 // to T; DOTS, outputs in T or fp32 (partials of shared heads), and, of the roles
 // that ask for them, the dots of their rows for dg.
@@ -439,11 +441,12 @@ constexpr uint64_t kScoreTiles = 0xB1FEDCA98540ull;
 // fp32 whether it leaves the kernel or not, and what else a call asks for does not
 // change its outputs (two where only outputs come of it would save 2 to 3%).
 // States and scores on their way into an output take three in DOTS, whose outputs
-// make dg, and two in OUT, whose outputs are rounded to bf16: 2^-17 of each term
+// make dg, and two in OUT, whose outputs are rounded to bf16: 2^-18 of each term
 // ahead of 2^-9 of the sum (three: prompts and training 3 to 6% longer).
 enum { STATE, OUT, DOTS };
 
-// waves a SIMD that the registers are cut for: as many as LDS lets in
+// Waves a SIMD that the registers are cut for: as many as LDS lets in, or one more
+// (bf16 64 x 64 with dots gets two, fp32 of 128 by 64 one).
 template <typename T> constexpr int walk_waves(int KD, int VD, int mode)
 {
     if (sizeof(T) == 4) return (mode == STATE && KD + VD <= 192) || KD + VD == 128 ? 3 : 2;
@@ -1030,9 +1033,8 @@ __global__ void __launch_bounds__(256) group_sum_kernel(const float *p0, const f
 // One workgroup per (sequence, head, 16 R rows of the state): 16 lanes a row,
 // each 4 (dk <= 64) or 2 x 4 neighbouring elements of R rows.  The state is
 // read and written once; everything else is small.  Bound by HBM: 256 sequences
-// x 16 heads of 128 x 128, 541 MB, in 104 us (5.2 TB/s; R = 4 rows a thread in
-// flight, R = 1 took 155 us); one sequence x 16 heads of 64 x 64 in 3 us, less
-// than its launch.
+// x 16 heads of 128 x 128, 541 MB, in 104 us (5.2 TB/s); one sequence x 16 heads
+// of 64 x 64 in 3 us, less than its launch.
 struct StepArgs {
     const void *q, *k, *v;
     const float *g;
@@ -1189,12 +1191,15 @@ size_t align_up(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 
-// Segments: a walk takes one workgroup through its chunks in order, and the chip
-// holds 512 such workgroups of 8 waves, or twice as many of 4 (up to 64 columns),
-// so a long sequence of few heads is cut until there are that many (512 of either
-// kind are left whole: cutting costs two more launches and reads k and v twice).
-// Half or twice as many cost up to 15% (prompts of 8 x 1999 steps x 16 heads: 93,
-// 82, 94 us).
+// Segments: a walk takes one workgroup through its chunks in order, and of those
+// with outputs LDS lets 512 of 8 waves (fp32: 256) or 768 of 4 (64 x 64; bf16 with
+// dots: 512) on the chip.  A long sequence of few heads is cut until there are 512
+// walks, or 1024 of 64 x 64 (512 of either kind are left whole: cutting costs two
+// more launches and reads k and v twice).  No one target is best: half of it, it
+// and twice it take 95, 85, 95 us for ragged prompts of 8 x 1999 steps x 16 heads
+// of 64 x 128, but 126, 132, 152 for one of 32768 steps x 8 heads of 128 x 128, and
+// for 4 x 4096 steps x 8 heads 39, 42, 55 (bf16, 64 x 64), 68, 75, 96 (128 x 128), 67,
+// 69, 78 and 168, 176, 200 (the same in fp32).
 // The backward also bounds a segment to 8 chunks, which bounds the rounding of
 // dg's sums.
 AttnGeom attn_geometry(const mgs_linattn_desc &d, bool backward)
@@ -1408,8 +1413,11 @@ hipError_t launch_linattn_bwd(const AttnGeom &geo, const mgs_linattn_desc &d, co
         rv.final = dS0;
     }
     // the dq and dk walks reduce over dv, the dv walk over dk
-    // Few walks go in one launch (16 sequences of 1024 steps, 64 wide, fp32: 69 us
-    // in two, 67 us in one); of many, dv's take the cheaper kernel.
+    // Few walks go in one launch: of one chunk, fp32 64 x 64, 64 walks a role 15 us
+    // against 24 in two, 256: 22 against 29; bf16 128 x 128, 17 against 25 and 32
+    // against 31.  Of many, dv's take the kernel without dots, which makes little
+    // difference: 4 x 4096 x 16 heads in bf16, 128 x 128: 393 us so and 383 in one
+    // (510 and 511 with the forward); 64 x 64: 171 and 174.
     const bool together = a.items <= 256 && (dk <= 64) == (dv <= 64);
     a.role[0] = rq, a.role[1] = rk, a.role[2] = rv;
     a.nRoles = together ? 3 : 2;
@@ -1471,8 +1479,10 @@ hipError_t launch_linattn_step(const mgs_linattn_desc &d, const void *q, const v
     a.gh = d.decay_per_head ? 1 : d.g_stride[2];
     a.H = static_cast<int>(d.H), a.div = static_cast<int>(d.H / d.Hk);
     a.dk = static_cast<int>(d.dk), a.dv = static_cast<int>(d.dv);
-    // 4 rows a thread keep more of the state in flight, 1 spreads a small batch
-    // over more of the chip
+    // 4 rows a thread keep more of the state in flight, 1 spreads a small batch over
+    // more of the chip.  By row tiles of 16, one row and four: 128 x 128, 512: 3.8
+    // and 4.8 us, 2048: 7.2 and 7.3, 4096: 14.0 and 12.4, 16384: 48.9 and 48.9, 32768:
+    // 97 and 103; 64 x 64, 1024: 3.9 and 5.8, 4096: 8.9 and 8.2, 8192: 15.7 and 13.4.
     const int rows = d.B * d.H * ((a.dv + 15) / 16) >= 4096 ? 4 : 1;
     a.tiles = (a.dv + 16 * rows - 1) / (16 * rows);
     const size_t size = d.dtype == MGS_BF16 ? 2 : 4;

@@ -10,9 +10,13 @@
 // to memory in a wider type.  TPR threads share a row: a wave for short rows
 // (no barrier), a workgroup for long ones.
 // Measured (a large copy runs at 4.7 TB/s): forward 16384 x 4096 bf16 88 us
-// (537 MB, 6.1 TB/s), 8-bit forward 8191 x 5000 with a scale for each 128 columns
-// 60 us (288 MB, 4.8 TB/s), gradient of 16384 x 4096 bf16 111 us (545 MB, 4.9
+// (538 MB, 6.1 TB/s), 8-bit forward 8191 x 5000 with a scale for each 128 columns
+// 61 us (291 MB, 4.8 TB/s), gradient of 16384 x 4096 bf16 110 us (546 MB, 5.0
 // TB/s) and 5 us for dw.  4095 x 1000 fp32: 13, 13 and 4 us.
+// Wide rows do not fit the registers of 1024 threads: the forward spills above
+// 16384 columns (2048 x 32768 bf16: 281 us, 1.9 TB/s), the gradient, which holds two
+// rows, above 8192 (4096 x 16384 bf16: 248 us, 2.2 TB/s) and heavily above 16384
+// (2048 x 32768 bf16: 2.1 ms, 0.25 TB/s).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
