@@ -221,3 +221,26 @@ def test_infinite_values_are_not_finite_from_their_step_on(gpu):
             other = torch.arange(64, device=gpu) != 3
             assert torch.isfinite(o[..., other]).all() and torch.isfinite(got["ST"][:, :, other]).all()
             assert not torch.isfinite(got["ST"][0, 0, 3]).any()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,at", [(200, 70), (1100, 600), (150, 149), (640, 0), (640, 511), (640, 512)])
+@pytest.mark.parametrize("name", ["q", "k", "v", "do"])
+def test_non_finite_values_stay_on_their_side(gpu, name, T, at, dtype):
+    """A value that is not finite at one step reaches only the outputs whose sums hold it: with q and do their own
+    step's o and dq and the earlier steps' dk and dv, with k and v the later steps' o and dq and their own dv and dk;
+    and nothing of another head."""
+    say(f"linattn non-finite {name} T={T} at={at} {dtype}")
+    t = torch.arange(T, device=gpu)
+    later, earlier, own, none = t >= at, t <= at, t == at, t < 0
+    may = {"q": dict(o=own, dq=none, dk=earlier, dv=earlier), "do": dict(o=none, dq=own, dk=earlier, dv=earlier),
+           "k": dict(o=later, dq=later, dk=none, dv=own), "v": dict(o=later, dq=later, dk=own, dv=none)}[name]
+    for value in (float("nan"), float("inf")):
+        a = make(gpu, 1, T, 2, 2, 64, 64, dtype, S0=True, seed=at)
+        a[name][0, at, 0, 5] = value
+        got = run(a, 0.1)
+        for n, steps in may.items():
+            x = got[n].float()
+            assert torch.isfinite(x[:, :, 1]).all(), n
+            assert bool((torch.isfinite(x[0, :, 0]).all(-1) | steps).all()), n
+        assert torch.isfinite(got["dg"][:, :, 1]).all()
