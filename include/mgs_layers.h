@@ -54,7 +54,8 @@ enum { MGS_F32 = 0, MGS_BF16 = 1 };
  *          output.  Values past T mean T, values below 0 mean 0.
  *   S0, ST : (B,H,dv,dk) fp32, dense; ST (the state after the last step) may
  *          be NULL.
- *   o    : (B,T,H,dv), dense.
+ *   o    : (B,T,H,dv), dense.  States are fp32; a bf16 o is rounded from a sum
+ *          whose terms are good to 2^-18.
  * An element of v that is not finite makes its column of o, and its row of the
  * state, not finite from its step on (NaN also where the sum would be infinite);
  * it touches no earlier step and no other column.

@@ -209,3 +209,18 @@ def test_clip_norm_outputs_over_other_tensors(lib):
         assert call([(400, 400)] + rest + [(0, 364)]) == INVALID
         assert call([(0, 400)] + rest + [(0, 800), (20, 1200)]) == WORKSPACE        # inputs alone may
         assert call([(0, 0)] + rest + [(40, 40), (80, 120)]) == WORKSPACE           # neighbours
+
+
+def test_limits_of_the_grids(lib):
+    """Workgroups of the walks and of the step are numbered in 32 bits: up to 2^31 / 3 segments, 2^28 heads of a step."""
+    one = dict(T=1, H=1, Hk=1, dk=1, dv=1)
+    for backward in (0, 1):
+        assert size(lib, desc(B=(1 << 31) // 3 - 9, **one), backward)[0] == OK
+        assert size(lib, desc(B=(1 << 31) // 3, **one), backward)[0] == UNSUPPORTED
+    big = desc(B=1 << 28, **one)
+    assert lib.mgs_linattn_step(ctypes.byref(big), fake(0), fake(1), fake(2), fake(3), fake(4), 1 << 28, None, fake(6),
+                                None) == UNSUPPORTED
+    assert lib.mgs_linattn_fwd(ctypes.byref(desc(B=(1 << 31) // 3, **one)), fake(0), fake(8), fake(16), fake(24), None,
+                               None, fake(32), None, fake(64), 1 << 62, None) == UNSUPPORTED
+    out = ctypes.c_size_t(0)
+    assert lib.mgs_rmsnorm_workspace_size(1 << 30, 64, ctypes.byref(out)) == OK
