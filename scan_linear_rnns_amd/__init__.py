@@ -18,6 +18,10 @@ Layer operators (layers.py; include/mgs_layers.h for the definitions):
   * mgs_linattn_fwd / mgs_linattn_bwd / mgs_linattn_step    linear attention with a decay per head
   * mgs_rmsnorm_fwd / mgs_rmsnorm_fwd_fp8 / mgs_rmsnorm_bwd root-mean-square norm with the residual's addition
   * mgs_clip_norm                                       global gradient norm, and clipping by it
+From a token to the next one (tokens.py; include/mgs_tokens.h for the definitions):
+  * mgs_embed_fwd / mgs_embed_bwd                       embedding lookup with scaling, and the table's gradient
+  * mgs_gated_fwd / mgs_gated_bwd / mgs_gated_step      gated linear recurrence with learnt decays
+  * mgs_sample                                          sampling with temperature, top-k, top-p and min-p
 """
 from __future__ import annotations
 
@@ -25,8 +29,10 @@ import ctypes
 
 from . import _lib
 from . import layers
+from . import tokens
 from ._lib import MgsError, check, declared_functions, load, status_string  # noqa: F401
 from .layers import *  # noqa: F401,F403
+from .tokens import *  # noqa: F401,F403
 
 __all__ = [
     "MgsError", "load", "workspace", "mgs_workspace_check", "mgs_workspace_set_waits",
@@ -37,7 +43,7 @@ __all__ = [
     "mgs_givens_scan_workspace_size", "mgs_givens_scan_fwd", "mgs_givens_scan_bwd",
     "mgs_block_matrix_scan_workspace_size", "mgs_block_matrix_scan_fwd", "mgs_block_matrix_scan_bwd",
     "mgs_delta_workspace_size", "mgs_delta_fwd",
-] + layers.__all__
+] + layers.__all__ + tokens.__all__
 
 
 def _ptr(t):

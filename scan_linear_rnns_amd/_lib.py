@@ -14,6 +14,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("MGS_LIBRARY", os.path.join(HERE, "libmgs.so"))
 HEADER = os.path.join(os.path.dirname(HERE), "include", "mgs.h")
 LAYERS_HEADER = os.path.join(os.path.dirname(HERE), "include", "mgs_layers.h")
+TOKENS_HEADER = os.path.join(os.path.dirname(HERE), "include", "mgs_tokens.h")
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -27,6 +28,18 @@ class LinattnDesc(ctypes.Structure):
     _fields_ = [(n, _I64) for n in ("B", "T", "H", "Hk", "dk", "dv")] + [
         ("dtype", _INT), ("decay_per_head", _INT), ("scale", _F32)] + [
         (n, _I64 * 3) for n in ("q_stride", "k_stride", "v_stride", "do_stride", "g_stride")]
+
+
+class GatedDesc(ctypes.Structure):
+    """mgs_gated_desc of include/mgs_tokens.h."""
+    _fields_ = [(n, _I64) for n in ("B", "T", "D")] + [("dtype", _INT), ("rate", _F32)] + [
+        (n, _I64 * 2) for n in ("x_stride", "r_stride", "i_stride", "dy_stride")]
+
+
+class SampleDesc(ctypes.Structure):
+    """mgs_sample_desc of include/mgs_tokens.h."""
+    _fields_ = [(n, _I64) for n in ("B", "vocab", "logits_stride")] + [("dtype", _INT), ("top_k", _INT)] + [
+        (n, _F32) for n in ("temperature", "top_p", "min_p")]
 
 
 SIGNATURES = {
@@ -68,6 +81,16 @@ SIGNATURES = {
     "mgs_rmsnorm_bwd": ([_P] * 7 + [_I64, _I64, _INT, _P, _SZ, _P], _INT),
     "mgs_clip_norm_workspace_size": ([_I64, _P, ctypes.POINTER(_SZ)], _INT),
     "mgs_clip_norm": ([_I64, _P, _P, _P, _P, _F32, _P, _P, _SZ, _P], _INT),
+    # include/mgs_tokens.h
+    "mgs_embed_fwd": ([_P, _INT, _P, _P] + [_I64] * 4 + [_F32, _INT, _P], _INT),
+    "mgs_embed_workspace_size": ([_I64, _I64, _I64, ctypes.POINTER(_SZ)], _INT),
+    "mgs_embed_bwd": ([_P, _INT, _P, _P] + [_I64] * 4 + [_F32, _INT, _INT, _INT, _P, _SZ, _P], _INT),
+    "mgs_gated_workspace_size": ([_P, _INT, ctypes.POINTER(_SZ)], _INT),
+    "mgs_gated_fwd": ([_P] + [_P] * 10 + [_P, _SZ, _P], _INT),
+    "mgs_gated_bwd": ([_P] + [_P] * 14 + [_P, _SZ, _P], _INT),
+    "mgs_gated_step": ([_P] + [_P] * 5 + [_I64, _P, _P, _P], _INT),
+    "mgs_sample_workspace_size": ([_P, ctypes.POINTER(_SZ)], _INT),
+    "mgs_sample": ([_P] + [_P] * 8 + [_P, _SZ, _P], _INT),
 }
 
 _lib = None

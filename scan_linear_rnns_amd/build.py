@@ -27,7 +27,11 @@ SOURCES = [("mgs_api.cpp", "mgs_api", ()),
            ("layers_api.cpp", "layers_api", ()),
            ("linattn.hip", "linattn", ()),
            ("rmsnorm.hip", "rmsnorm", ()),
-           ("clip_norm.hip", "clip_norm", ())] + [
+           ("clip_norm.hip", "clip_norm", ()),
+           ("tokens_api.cpp", "tokens_api", ()),
+           ("embed.hip", "embed", ()),
+           ("gated.hip", "gated", ()),
+           ("sample.hip", "sample", ())] + [
           ("block_scan_k.hip", f"block_scan_k{k}", (f"-DMGS_ROWS_K={k}",)) for k in (1, 2, 4, 16)]
 JOBS = int(os.environ.get("MGS_BUILD_JOBS", "8"))
 ARCH = os.environ.get("MGS_OFFLOAD_ARCH", "gfx950")

@@ -1,0 +1,390 @@
+// embed.hip -- the embedding lookup with scaling, and the table's gradient by
+// sorted ids (gfx950).
+//
+//     y_n = scale W[id_n],      dW_v = scale sum over n with id_n = v of dy_n
+//
+// Gradient: three kernels.  The first sorts the places n by their ids: each
+// workgroup serves a range of ids, reads all of them (they stay in L2) and places the
+// ones in its range by counting, without a word to any other workgroup; it also writes
+// the zeros of the rows that no id points to, most of the traffic of a large table,
+// meanwhile.  The second walks the sorted places in chunks of equal length, so that
+// an id that makes up half of a text costs no workgroup more than the others, adds
+// the rows up in fp32 and writes each sum that lies inside a chunk; the third joins
+// the sums that cross chunks.  All orders are fixed by the ids.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+
+#include "device.hpp"
+#include "launch.hpp"
+#include "layers.hpp"
+#include "tokens.hpp"
+
+namespace mgs {
+namespace {
+
+constexpr int kChunk = 32;        // sorted places of a workgroup
+constexpr int kSortWaves = 16;
+constexpr int kMaxRange = 512;    // ids of a sorting workgroup
+constexpr int64_t kMinRange = 64;
+
+typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
+typedef float f8v __attribute__((ext_vector_type(8), aligned(16)));
+
+template <typename T> struct Raw;
+template <> struct Raw<float> { using V = f8v; };
+template <> struct Raw<__bf16> { using V = bf8v; };
+
+__device__ __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// elements c .. c + 7 of a row of d, zeros past its end
+template <typename T> __device__ __forceinline__ f8v load8(const T *row, int64_t c, int64_t d, bool vec)
+{
+    f8v v = {0, 0, 0, 0, 0, 0, 0, 0};
+    if (vec) {
+        if (c < d) v = __builtin_convertvector(*reinterpret_cast<const typename Raw<T>::V *>(row + c), f8v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < d) v[i] = static_cast<float>(row[c + i]);
+    }
+    return v;
+}
+
+template <typename T> __device__ __forceinline__ void store8(T *row, int64_t c, int64_t d, bool vec, f8v v)
+{
+    const typename Raw<T>::V o = __builtin_convertvector(v, typename Raw<T>::V);
+    if (vec) {
+        if (c < d) *reinterpret_cast<typename Raw<T>::V *>(row + c) = o;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i < d) row[c + i] = o[i];
+    }
+}
+
+__device__ __forceinline__ int64_t id_at(const void *ids, bool wide, int64_t n)
+{
+    return wide ? static_cast<const int64_t *>(ids)[n] : static_cast<const int32_t *>(ids)[n];
+}
+
+// ------------------------------------------------------------------ lookup
+struct LookupArgs {
+    const void *ids, *W;
+    void *y;
+    int64_t first, n, vocab, d, ws;
+    int slabs;         // pieces of 8 columns of a row, rounded up to a power of two, at most 256
+    float scale;
+    bool wide_ids, vec;
+};
+
+// `slabs` threads share a row
+template <typename T> __global__ void __launch_bounds__(256) lookup_kernel(LookupArgs a)
+{
+    const int sub = threadIdx.x / a.slabs, t = threadIdx.x % a.slabs;
+    const int64_t n = (a.first + blockIdx.x) * (256 / a.slabs) + sub;
+    if (n >= a.n) return;
+    const int64_t id = id_at(a.ids, a.wide_ids, n);
+    const bool in = id >= 0 && id < a.vocab;
+    const T *row = static_cast<const T *>(a.W) + (in ? id : 0) * a.ws;
+    T *y = static_cast<T *>(a.y) + n * a.d;
+    for (int64_t c = 8 * t; c < a.d; c += 8 * a.slabs) {
+        f8v v = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (in) v = a.scale * load8(row, c, a.d, a.vec);
+        store8(y, c, a.d, a.vec, v);
+    }
+}
+
+// -------------------------------------------------------------------- sort
+struct SortArgs {
+    const void *ids;
+    int64_t n, vocab, d;
+    int range;
+    bool wide_ids, clear;
+    int64_t *count;     // ids inside the table
+    int32_t *first;     // of each id, and one past the last
+    int32_t *row, *id;  // sorted
+    char *dW;
+    int64_t row_bytes;
+};
+
+// Each wave takes an equal share of the places and counts its ids of the range in a
+// row of its own, so the second pass places them in order without a barrier.
+__global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
+{
+    __shared__ int32_t at[kSortWaves * kMaxRange];   // [wave][local id]: counts, then next places
+    __shared__ int64_t below[kSortWaves];
+    __shared__ int32_t scan[kSortWaves];
+    const int lane = threadIdx.x & 63, wv = wave();
+    const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.range;
+    const int ids = static_cast<int>(a.vocab - lo < a.range ? a.vocab - lo : a.range);
+    for (int i = threadIdx.x; i < kSortWaves * a.range; i += 64 * kSortWaves) at[i] = 0;
+    __syncthreads();
+    const int64_t share = (a.n + kSortWaves - 1) / kSortWaves;
+    const int64_t n0 = wv * share, n1 = n0 + share < a.n ? n0 + share : a.n;
+    volatile int32_t *mine = at + wv * a.range;   // (its wave's lanes share it without barriers)
+    int64_t smaller = 0;
+    for (int64_t n = n0 + lane; n < n1; n += 64) {
+        const int64_t id = id_at(a.ids, a.wide_ids, n);
+        if (id >= 0 && id < lo) ++smaller;
+        if (id >= lo && id < lo + ids) atomicAdd(&at[wv * a.range + (id - lo)], 1);
+    }
+    for (int off = 32; off; off >>= 1) smaller += __shfl_xor(smaller, off, 64);
+    if (lane == 0) below[wv] = smaller;
+    __syncthreads();
+    int64_t base = 0;
+    for (int w = 0; w < kSortWaves; ++w) base += below[w];
+    // exclusive sums over (id, wave): a thread takes neighbouring ids
+    const int per = (a.range + 64 * kSortWaves - 1) / (64 * kSortWaves);
+    const int i0 = threadIdx.x * per, i1 = i0 + per < ids ? i0 + per : ids;
+    int32_t sum = 0;
+    for (int i = i0; i < i1; ++i)
+        for (int w = 0; w < kSortWaves; ++w) sum += at[w * a.range + i];
+    int32_t before = sum;   // of the threads up to this one
+    for (int off = 1; off < 64; off <<= 1) {
+        const int32_t u = __shfl_up(before, off, 64);
+        if (lane >= off) before += u;
+    }
+    if (lane == 63) scan[wv] = before;
+    before -= sum;
+    __syncthreads();
+    for (int w = 0; w < wv; ++w) before += scan[w];
+    int32_t next = static_cast<int32_t>(base) + before;
+    for (int i = i0; i < i1; ++i) {
+        a.first[lo + i] = next;
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int32_t c = at[w * a.range + i];
+            at[w * a.range + i] = next;
+            next += c;
+        }
+        if (lo + i == a.vocab - 1) {
+            a.first[a.vocab] = next;
+            *a.count = next;
+        }
+    }
+    __syncthreads();
+    for (int64_t n = n0 + lane; n - lane < n1; n += 64) {
+        const int64_t id = n < n1 ? id_at(a.ids, a.wide_ids, n) : -1;
+        int local = id >= lo && id < lo + ids ? static_cast<int>(id - lo) : -1;
+        // one round for each id among the lanes: its lanes in order
+        for (uint64_t left = __ballot(local >= 0); left;) {
+            const int now = __builtin_amdgcn_readlane(local, __builtin_ctzll(left));
+            const uint64_t same = __ballot(local == now);
+            const int32_t start = mine[now];
+            if (local == now) {
+                const int32_t place = start + __popcll(same & ((1ull << lane) - 1));
+                a.row[place] = static_cast<int32_t>(n);
+                a.id[place] = static_cast<int32_t>(id);
+            }
+            if (lane == 0) mine[now] = start + __popcll(same);
+            left &= ~same;
+        }
+    }
+    if (!a.clear) return;
+    __syncthreads();
+    // rows of no id: the last wave's next place is still the first one
+    for (int i = wv; i < ids; i += kSortWaves) {
+        if (at[(kSortWaves - 1) * a.range + i] != a.first[lo + i]) continue;
+        char *row = a.dW + (lo + i) * a.row_bytes;
+        const int64_t head = (16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15;
+        const int64_t wide = head < a.row_bytes ? (a.row_bytes - head) / 16 : 0;
+        for (int64_t o = lane; o < wide; o += 64) {
+            const f32x4 z = {0, 0, 0, 0};
+            __builtin_nontemporal_store(z, reinterpret_cast<f32x4 *>(row + head) + o);
+        }
+        if (head == 0 && 16 * wide == a.row_bytes) continue;
+        // the ends, in halves: an element is two or four bytes
+        for (int64_t o = 2 * lane; o < a.row_bytes; o += 128)
+            if (o < head || o >= head + 16 * wide) *reinterpret_cast<uint16_t *>(row + o) = 0;
+    }
+}
+
+// -------------------------------------------------------------------- sums
+struct SumArgs {
+    const int64_t *count;
+    const int32_t *first, *row, *id;
+    float *part;       // [chunk][2][d]: of the run that enters the chunk, of the one that leaves it
+    const void *dy;
+    void *dW;
+    int64_t block, d, gs;
+    int slabs;
+    float scale;
+    bool add, vec_in, vec_out;
+};
+
+template <typename D> __device__ __forceinline__ void put(const SumArgs &a, int64_t id, int64_t c, f8v sum)
+{
+    D *o = static_cast<D *>(a.dW) + id * a.d;
+    sum *= a.scale;
+    if (a.add) sum += load8(o, c, a.d, a.vec_out);
+    store8(o, c, a.d, a.vec_out, sum);
+}
+
+__device__ __forceinline__ f8v *partial(const SumArgs &a, int64_t chunk, int which, int64_t c)
+{
+    const int64_t width = (a.d + 7) / 8 * 8;
+    return reinterpret_cast<f8v *>(a.part + (chunk * 2 + which) * width + c);
+}
+
+// `slabs` threads walk a chunk, 8 columns each
+template <typename T, typename D> __global__ void __launch_bounds__(256) sum_kernel(SumArgs a)
+{
+    const int sub = threadIdx.x / a.slabs, t = threadIdx.x % a.slabs;
+    const int64_t chunk = (a.block + blockIdx.x) * (256 / a.slabs) + sub, total = *a.count;
+    const int64_t k0 = chunk * kChunk, k1 = k0 + kChunk < total ? k0 + kChunk : total;
+    if (k0 >= k1) return;
+    for (int64_t c = 8 * (t + static_cast<int64_t>(blockIdx.y) * a.slabs); c < a.d;
+         c += 8 * static_cast<int64_t>(a.slabs) * gridDim.y) {
+        f8v sum = {0, 0, 0, 0, 0, 0, 0, 0};
+        bool entered = k0 > 0 && a.id[k0 - 1] == a.id[k0];
+        for (int64_t k = k0; k < k1; ++k) {
+            const int32_t id = a.id[k];
+            sum += load8(static_cast<const T *>(a.dy) + a.row[k] * a.gs, c, a.d, a.vec_in);
+            const bool ends = k + 1 == total || a.id[k + 1] != id;
+            if (!ends && k + 1 < k1) continue;
+            if (entered)
+                *partial(a, chunk, 0, c) = sum;
+            else if (ends)
+                put<D>(a, id, c, sum);
+            else
+                *partial(a, chunk, 1, c) = sum;
+            entered = false;
+            sum = f8v{0, 0, 0, 0, 0, 0, 0, 0};
+        }
+    }
+}
+
+// Runs that leave the chunk they start in: its partial sum, and those of the chunks
+// that they enter, shared among four waves and added in order
+template <typename D> __global__ void __launch_bounds__(256) join_kernel(SumArgs a)
+{
+    __shared__ f8v s[4][64];
+    const int64_t chunk = a.block + blockIdx.x, total = *a.count;
+    const int64_t k0 = chunk * kChunk, k1 = k0 + kChunk;
+    if (k1 >= total) return;
+    const int32_t id = a.id[k1 - 1];
+    if (a.id[k1] != id || a.first[id] < k0) return;
+    const int64_t last = (a.first[id + 1] - 1) / kChunk, many = last - chunk;   // chunks that it enters
+    const int lane = threadIdx.x & 63, wv = wave();
+    const int64_t share = (many + 3) / 4;
+    const int64_t q0 = chunk + 1 + wv * share, q1 = q0 + share < last + 1 ? q0 + share : last + 1;
+    for (int64_t c0 = 512 * static_cast<int64_t>(blockIdx.y); c0 < a.d; c0 += 512 * static_cast<int64_t>(gridDim.y)) {
+        const int64_t c = c0 + 8 * lane;
+        f8v sum = {0, 0, 0, 0, 0, 0, 0, 0};
+        if (c < a.d) {
+            if (wv == 0) sum = *partial(a, chunk, 1, c);
+            for (int64_t q = q0; q < q1; ++q) sum += *partial(a, q, 0, c);
+        }
+        s[wv][lane] = sum;
+        __syncthreads();
+        if (wv == 0 && c < a.d) put<D>(a, id, c, ((sum + s[1][lane]) + s[2][lane]) + s[3][lane]);
+        __syncthreads();
+    }
+}
+
+int slabs_of(int64_t d)
+{
+    int s = 1;
+    while (s < 256 && s * 8 < d) s *= 2;
+    return s;
+}
+
+// whether rows of d elements, `stride` apart, can be moved eight elements at once
+bool whole8(const void *p, int64_t d, int64_t stride, int size)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && d % 8 == 0 && (stride * size) % 16 == 0;
+}
+
+template <typename T, typename D>
+hipError_t sums(SumArgs a, const EmbedGeom &g, hipStream_t s)
+{
+    const unsigned cols = static_cast<unsigned>(std::min<int64_t>((a.d + 8 * a.slabs - 1) / (8 * a.slabs), 64));
+    const int per = 256 / a.slabs;
+    hipError_t e = launch_sliced((g.chunks + per - 1) / per, 256, [&](int64_t first, unsigned blocks) {
+        a.block = first;
+        sum_kernel<T, D><<<dim3(blocks, cols), dim3(256), 0, s>>>(a);
+    });
+    if (e != hipSuccess || g.chunks < 2) return e;
+    return launch_sliced(g.chunks - 1, 256, [&](int64_t first, unsigned blocks) {
+        a.block = first;
+        join_kernel<D><<<dim3(blocks, static_cast<unsigned>(std::min<int64_t>((a.d + 511) / 512, 64))), dim3(256), 0, s>>>(a);
+    });
+}
+
+}  // namespace
+
+EmbedGeom embed_geometry(int64_t n, int64_t vocab, int64_t d)
+{
+    EmbedGeom g{};
+    int64_t range = kMinRange;   // about a workgroup for each of the 256 CUs
+    while (range < kMaxRange && range * 256 < vocab) range *= 2;
+    g.range = static_cast<int>(range);
+    g.ranges = (vocab + range - 1) / range;
+    g.chunks = (n + kChunk - 1) / kChunk;
+    size_t off = 256;
+    g.off_first = off; off = align256(off + (static_cast<size_t>(vocab) + 1) * 4);
+    g.off_row = off;   off = align256(off + static_cast<size_t>(n) * 4);
+    g.off_id = off;    off = align256(off + static_cast<size_t>(n) * 4);
+    g.off_part = off;  off = align256(off + static_cast<size_t>(g.chunks) * 2 * ((d + 7) / 8 * 8) * 4);
+    g.bytes = off;
+    return g;
+}
+
+hipError_t launch_embed_fwd(const void *ids, bool wide_ids, const void *W, void *y, int64_t n, int64_t vocab,
+                            int64_t d, int64_t w_stride, float scale, int dtype, hipStream_t s)
+{
+    const int size = dtype == MGS_BF16 ? 2 : 4;
+    LookupArgs a{ids, W, y, 0, n, vocab, d, w_stride, slabs_of(d), scale, wide_ids,
+                 whole8(W, d, w_stride, size) && whole8(y, d, d, size)};
+    const int per = 256 / a.slabs;
+    return launch_sliced((n + per - 1) / per, 256, [&](int64_t first, unsigned blocks) {
+        a.first = first;
+        if (dtype == MGS_BF16) lookup_kernel<__bf16><<<dim3(blocks), dim3(256), 0, s>>>(a);
+        else lookup_kernel<float><<<dim3(blocks), dim3(256), 0, s>>>(a);
+    });
+}
+
+hipError_t launch_embed_bwd(const EmbedGeom &g, const void *ids, bool wide_ids, const void *dy, void *dW, int64_t n,
+                            int64_t vocab, int64_t d, int64_t dy_stride, float scale, bool accumulate, int dtype,
+                            int dw_dtype, void *ws, hipStream_t s)
+{
+    char *w = static_cast<char *>(ws);
+    const int out = dw_dtype == MGS_BF16 ? 2 : 4, size = dtype == MGS_BF16 ? 2 : 4;
+    SortArgs a{};
+    a.ids = ids;
+    a.n = n;
+    a.vocab = vocab;
+    a.d = d;
+    a.range = g.range;
+    a.wide_ids = wide_ids;
+    a.clear = !accumulate;
+    a.count = reinterpret_cast<int64_t *>(w);
+    a.first = reinterpret_cast<int32_t *>(w + g.off_first);
+    a.row = reinterpret_cast<int32_t *>(w + g.off_row);
+    a.id = reinterpret_cast<int32_t *>(w + g.off_id);
+    a.dW = static_cast<char *>(dW);
+    a.row_bytes = d * out;
+    sort_kernel<<<dim3(static_cast<unsigned>(g.ranges)), dim3(64 * kSortWaves), 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || n == 0) return e;
+    SumArgs b{};
+    b.count = a.count;
+    b.first = a.first;
+    b.row = a.row;
+    b.id = a.id;
+    b.part = reinterpret_cast<float *>(w + g.off_part);
+    b.dy = dy;
+    b.dW = dW;
+    b.d = d;
+    b.gs = dy_stride;
+    b.slabs = slabs_of(d);
+    b.scale = scale;
+    b.add = accumulate;
+    b.vec_in = whole8(dy, d, dy_stride, size);
+    b.vec_out = whole8(dW, d, d, out);
+    if (dtype == MGS_BF16)
+        return dw_dtype == MGS_BF16 ? sums<__bf16, __bf16>(b, g, s) : sums<__bf16, float>(b, g, s);
+    return dw_dtype == MGS_BF16 ? sums<float, __bf16>(b, g, s) : sums<float, float>(b, g, s);
+}
+
+}  // namespace mgs
