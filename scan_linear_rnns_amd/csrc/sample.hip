@@ -1,12 +1,29 @@
 // sample.hip -- sampling of the next token with temperature, top-k, top-p and
 // min-p (gfx950).
 //
-// All three filters keep a prefix of the order by (logit descending, index
-// ascending), so what is kept is a threshold: everything above a value, and of its
-// equals the first few by index.
+// The filters keep a prefix of the order by (logit descending, index ascending), so
+// what is kept is an edge: everything above its value, and its equals up to an index.
+// A row goes through
+//   1. its largest logit;
+//   2. a histogram over (largest - x) / temperature in steps of 1/64: of the counts
+//      for top-k, of the weights, as multiples of 2^-43, for top-p (integers: their sums
+//      do not depend on the order of the atomics);
+//   3. the few that lie in the bin where the filter ends (for top-k, all up to there),
+//      gathered and sorted, and the sums of the weights ahead of that bin, a sum for
+//      each wave's share of the row;
+//   4. the edge, from the sorted ones; the share in which the running sum passes u
+//      times the total; the token in that share.
+// A row without top-k and top-p needs 1, the sums of 3, and 4.  Where a bin holds too
+// many to sort (equal logits by the thousand), its values are split again, one
+// histogram after another, by the row's workgroup alone.
+// Large batches take a workgroup a row for all of it; for small ones a row is cut into
+// slices, each step a launch.
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
+
 #include "device.hpp"
+#include "launch.hpp"
 #include "layers.hpp"
 #include "tokens.hpp"
 
@@ -14,6 +31,12 @@ namespace mgs {
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
+constexpr int kBins = 2048;         // of 1/64: weights below e^-32 are less than a step
+constexpr float kPerUnit = 64.0f;
+constexpr int kList = 4096;         // candidates that are sorted
+constexpr int kFixed = 43;          // a weight's bits behind the point: 2^20 of them fit 64 bits
+constexpr int kMaxSlices = 64;
+constexpr float kInf = __builtin_inff();
 
 struct SampleArgs {
     const void *logits;
@@ -21,12 +44,17 @@ struct SampleArgs {
     const int32_t *top_k;
     int64_t *token;
     float *logp;
-    int64_t vocab, stride;
-    int k0;
+    int64_t stride;
+    char *ws;
+    size_t slot;     // workspace bytes of a row
+    int vocab, slices, share, k0;
     float t0, p0, m0;
+    bool vec;
 };
 
-// Unsigned numbers in the order of the floats (NaN apart; -0 counts as 0)
+__device__ __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+
+// Unsigned numbers in the order of the floats (no NaN; -0 counts as 0), never 0
 __device__ __forceinline__ uint32_t key_of(float x)
 {
     const uint32_t b = __float_as_uint(x == 0.0f ? 0.0f : x);
@@ -38,28 +66,130 @@ __device__ __forceinline__ float of_key(uint32_t k)
     return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
 }
 
-__device__ __forceinline__ double weight(float x, float top, double inv)
+// ---------------------------------------------------------- a row's settings
+enum { DONE = 0, GREEDY = 1, PLAIN = 2, TOP_K = 3, TOP_P = 4 };
+
+struct Row {
+    int kind;
+    int top_k;           // 0: off
+    float top;           // the largest logit
+    float inv;           // 1 / temperature
+    double scale;        // log2 e / temperature
+    double top_p, min_p;
+    float u;
+};
+
+__device__ __forceinline__ Row settings(const SampleArgs &a, int64_t b, float top)
 {
-    if (x == top) return 1.0;
-    if (x == -__builtin_inff() || top == __builtin_inff()) return 0.0;
-    return exp((static_cast<double>(x) - static_cast<double>(top)) * inv);
+    Row r;
+    float tau = a.temperature ? a.temperature[b] : a.t0, p = a.top_p ? a.top_p[b] : a.p0;
+    float m = a.min_p ? a.min_p[b] : a.m0;
+    const int k = a.top_k ? a.top_k[b] : a.k0;
+    const float u = a.u[b];
+    r.u = u > 0.0f ? (u < 1.0f ? u : 0.99999994f) : 0.0f;
+    r.top = top;
+    r.inv = 1.0f / tau;
+    r.scale = 1.4426950408889634 / static_cast<double>(tau);
+    r.top_k = k > 0 && k < a.vocab ? k : 0;
+    r.top_p = p < 1.0f ? (p > 0.0f ? p : 0.0f) : 1.0;
+    r.min_p = m > 0.0f ? (m < 1.0f ? m : 1.0f) : 0.0f;
+    r.kind = !(top > -kInf) ? DONE : !(tau > 0.0f) ? GREEDY : r.top_k ? TOP_K : r.top_p < 1.0 ? TOP_P : PLAIN;
+    return r;
 }
 
-template <typename V> __device__ __forceinline__ V block_sum(V v, V *lds)
+// ------------------------------------------------------------------ weights
+// 2^(j/64), j = 0..63, for the function below
+__device__ __forceinline__ void fill_roots(double *roots)
+{
+    if (threadIdx.x < 64) roots[threadIdx.x] = exp2(static_cast<double>(threadIdx.x) / 64.0);
+}
+
+// e^((x - top) / temperature) in fp64: y = n + j/64 + s, |s| <= 1/128, 2^s by its
+// series to s^6 (the next term is below 2^-60 of it).  x <= top.
+__device__ __forceinline__ double weight(float x, const Row &r, const double *roots)
+{
+    constexpr double kShift = 1.5 * 70368744177664.0;   // 2^46: adding it rounds to 1/64
+    const double y = (static_cast<double>(x) - static_cast<double>(r.top)) * r.scale;
+    const double z = y + kShift, s = y - (z - kShift);
+    const int k = static_cast<int>(__double2loint(z));
+    double q = 1.5403530393381608e-4;
+    q = __builtin_fma(q, s, 1.3333558146428443e-3);
+    q = __builtin_fma(q, s, 9.6181291076284772e-3);
+    q = __builtin_fma(q, s, 5.5504108664821580e-2);
+    q = __builtin_fma(q, s, 2.4022650695910071e-1);
+    q = __builtin_fma(q, s, 6.9314718055994531e-1);
+    const double root = roots[k & 63];
+    const double w = ldexp(__builtin_fma(q * s, root, root), k >> 6);
+    return x == r.top ? 1.0 : !(y > -1100.0) ? 0.0 : w;   // (y is -inf or NaN next to infinities)
+}
+
+// w <= 1 as a multiple of 2^-43
+__device__ __forceinline__ uint64_t fixed(double w)
+{
+    constexpr double kOne = 768.0;   // 1.5 * 2^(52 - 43)
+    return __double_as_longlong(w + kOne) - __double_as_longlong(kOne);
+}
+
+__device__ __forceinline__ double unfixed(uint64_t q) { return static_cast<double>(q) * 0x1p-43; }
+
+// The bin of x, kBins and more past the last one (-inf too); falls with x
+__device__ __forceinline__ int bin_of(float x, const Row &r)
+{
+    const float t = (r.top - x) * r.inv * kPerUnit;
+    return x == r.top ? 0 : t < static_cast<float>(kBins) && x > -kInf ? static_cast<int>(t) : kBins;
+}
+
+// ------------------------------------------------------------ walking a row
+template <typename T> struct Wide;
+template <> struct Wide<float> {
+    typedef float V __attribute__((ext_vector_type(4)));
+    static constexpr int N = 4;
+};
+template <> struct Wide<__bf16> {
+    typedef __bf16 V __attribute__((ext_vector_type(8)));
+    static constexpr int N = 8;
+};
+
+// f(value, index) for the places lo..hi-1, hi <= V, of a row, spread over a wave's
+// lanes; lo is a multiple of what it reads at once.  -inf stands for places past hi.
+template <typename T, typename F> __device__ __forceinline__ void walk(const T *x, int lo, int hi, bool vec, F f)
+{
+    constexpr int N = Wide<T>::N, U = 4;
+    const int lane = threadIdx.x & 63;
+    for (int base = lo; base < hi; base += 64 * N * U) {
+        float v[U][N];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const int i = base + (j * 64 + lane) * N;
+            if (vec && i + N <= hi) {
+                const typename Wide<T>::V w = *reinterpret_cast<const typename Wide<T>::V *>(x + i);
+#pragma unroll
+                for (int e = 0; e < N; ++e) v[j][e] = static_cast<float>(w[e]);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e) v[j][e] = i + e < hi ? static_cast<float>(x[i + e]) : -kInf;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if (base + j * 64 * N >= hi) break;
+#pragma unroll
+            for (int e = 0; e < N; ++e) f(v[j][e], base + (j * 64 + lane) * N + e);
+        }
+    }
+}
+
+// ------------------------------------------------------------ workgroup sums
+template <typename V> __device__ __forceinline__ V wave_sum(V v)
 {
     for (int off = 32; off; off >>= 1) v += __shfl_xor(v, off, 64);
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = lds[0];
-    for (int w = 1; w < kWaves; ++w) v += lds[w];
     return v;
 }
 
-// sum over the threads before this one
-template <typename V> __device__ __forceinline__ V block_before(V v, V *lds)
+// The sum over the threads before this one, and over all of them
+template <typename V> __device__ __forceinline__ V scan_block(V v, V *lds, V &all)
 {
-    const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
+    const int lane = threadIdx.x & 63, wv = wave();
     V up = v;
     for (int off = 1; off < 64; off <<= 1) {
         const V o = __shfl_up(up, off, 64);
@@ -68,172 +198,805 @@ template <typename V> __device__ __forceinline__ V block_before(V v, V *lds)
     __syncthreads();
     if (lane == 63) lds[wv] = up;
     __syncthreads();
-    V sum = 0;
-    for (int w = 0; w < wv; ++w) sum += lds[w];
+    V before = 0;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w < wv) before += lds[w];
+        all += lds[w];
+    }
     const V prev = __shfl_up(up, 1, 64);
-    return lane ? sum + prev : sum;
+    return lane ? before + prev : before;
 }
 
-// A workgroup for each row
-template <typename T> __global__ void __launch_bounds__(kThreads) sample_kernel(SampleArgs a)
+__device__ __forceinline__ void sort_list(uint64_t *list, int n)   // n: a power of two
 {
-    __shared__ double sd[kWaves];
-    __shared__ uint64_t su[kWaves];
-    __shared__ int found;
-    const int64_t b = blockIdx.x;
-    const T *x = static_cast<const T *>(a.logits) + b * a.stride;
-    const int V = static_cast<int>(a.vocab), tid = threadIdx.x;
-    float tau = a.temperature ? a.temperature[b] : a.t0, top_p = a.top_p ? a.top_p[b] : a.p0;
-    float min_p = a.min_p ? a.min_p[b] : a.m0, u = a.u[b];
-    const int top_k = a.top_k ? a.top_k[b] : a.k0;
-    if (!(tau > 0.0f)) tau = 0.0f;
-    min_p = min_p > 0.0f ? (min_p < 1.0f ? min_p : 1.0f) : 0.0f;
-    u = u > 0.0f ? (u < 1.0f ? u : 0.99999994f) : 0.0f;
+    for (int size = 2; size <= n; size *= 2)
+        for (int step = size / 2; step; step /= 2) {
+            __syncthreads();
+            for (int p = threadIdx.x; p < n / 2; p += kThreads) {
+                const int i = (p / step) * 2 * step + p % step, j = i + step;
+                const uint64_t x = list[i], y = list[j];
+                if ((x > y) == ((i & size) == 0)) {
+                    list[i] = y;
+                    list[j] = x;
+                }
+            }
+        }
+    __syncthreads();
+}
 
-    // the largest, its first place; whether there is a NaN
-    uint64_t best = 0;   // (key, places from the end)
+// ------------------------------------------------------------- steps 1 to 3
+struct Shared {
+    uint64_t mass[kBins];
+    uint32_t count[kBins];   // (right behind mass: see finish)
+    uint64_t list[kList];
+    double sub[kMaxSlices * kWaves];
+    double roots[64];
+    double wd[kWaves];
+    uint64_t wu[kWaves];
+    float top[kWaves];
+    uint32_t n;
+    int bin, at, last;
+    uint64_t ahead;
+    double w_at;
+};
+
+// Workspace of a row that is cut into slices
+struct Slot {
+    float *top;        // of each slice; NaN where the slice has one
+    uint32_t *n;       // candidates
+    uint32_t *count;
+    uint64_t *mass, *list;
+    double *sub;
+};
+
+constexpr size_t kSlotMass = 512, kSlotCount = kSlotMass + 8 * kBins, kSlotList = kSlotCount + 4 * kBins,
+                 kSlotSub = kSlotList + 8 * kList;
+
+__device__ __forceinline__ Slot slot_of(const SampleArgs &a, int64_t b)
+{
+    char *w = a.ws + b * a.slot;
+    return Slot{reinterpret_cast<float *>(w), reinterpret_cast<uint32_t *>(w + 256),
+                reinterpret_cast<uint32_t *>(w + kSlotCount), reinterpret_cast<uint64_t *>(w + kSlotMass),
+                reinterpret_cast<uint64_t *>(w + kSlotList), reinterpret_cast<double *>(w + kSlotSub)};
+}
+
+// 1: the largest of a slice, NaN if it holds one, known to every thread
+template <typename T>
+__device__ __forceinline__ float slice_top(const SampleArgs &a, const T *x, int lo, int hi, Shared &sh)
+{
+    float top = -kInf;
     bool nan = false;
-    for (int i = tid; i < V; i += kThreads) {
-        const float v = static_cast<float>(x[i]);
+    walk(x, lo, hi, a.vec, [&](float v, int) {
+        top = fmaxf(top, v);
         nan |= v != v;
-        const uint64_t c = (static_cast<uint64_t>(key_of(v)) << 32) | static_cast<uint32_t>(~i);
-        best = c > best ? c : best;
-    }
+    });
+    if (nan) top = __builtin_nanf("");
     for (int off = 32; off; off >>= 1) {
-        const uint64_t o = __shfl_xor(best, off, 64);
-        best = o > best ? o : best;
+        const float o = __shfl_xor(top, off, 64);
+        top = top != top || o != o ? __builtin_nanf("") : fmaxf(top, o);
     }
-    if ((tid & 63) == 0) su[tid >> 6] = best;
-    nan = __syncthreads_or(nan);
-    for (int w = 0; w < kWaves; ++w) best = su[w] > best ? su[w] : best;
-    const uint32_t top_key = static_cast<uint32_t>(best >> 32);
-    const float top = of_key(top_key);
-    const float inf = __builtin_inff();
-    if (nan || top == -inf || V == 0) {
-        if (tid == 0) {
-            a.token[b] = -1;
-            if (a.logp) a.logp[b] = -inf;
-        }
-        return;
-    }
-    if (tau == 0.0f) {
-        if (tid == 0) {
-            a.token[b] = static_cast<int64_t>(~static_cast<uint32_t>(best));
-            if (a.logp) a.logp[b] = 0.0f;
-        }
-        return;
-    }
-    const double inv = 1.0 / static_cast<double>(tau);
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) sh.top[wave()] = top;
+    __syncthreads();
+    top = sh.top[0];
+    for (int w = 1; w < kWaves; ++w) top = top != top || sh.top[w] != sh.top[w] ? __builtin_nanf("") : fmaxf(top, sh.top[w]);
+    return top;
+}
 
-    // kept: keys above `edge`, and the first `ties` of its equals
-    uint32_t edge = 0;
-    int64_t ties = V;
+// 2: the histogram of a wave's share into LDS
+template <typename T>
+__device__ __forceinline__ void histogram(const SampleArgs &a, const Row &r, const T *x, int lo, int hi, Shared &sh)
+{
+    if (r.kind == TOP_K)
+        walk(x, lo, hi, a.vec, [&](float v, int) {
+            const int bin = bin_of(v, r);
+            if (bin < kBins) atomicAdd(&sh.count[bin], 1u);
+        });
+    else
+        walk(x, lo, hi, a.vec, [&](float v, int) {
+            const int bin = bin_of(v, r);
+            if (bin < kBins) {
+                atomicAdd(&sh.count[bin], 1u);
+                atomicAdd(reinterpret_cast<unsigned long long *>(&sh.mass[bin]), fixed(weight(v, r, sh.roots)));
+            }
+        });
+}
+
+// Whole workgroup: the bin in which the filter ends, from the row's histogram: the first
+// at whose end there are top_k, or top_p of the weight.  -> sh.bin, what is ahead of
+// it -> sh.ahead.  kBins where all are kept.
+__device__ __forceinline__ void end_bin(const Row &r, const uint32_t *count, const uint64_t *mass, Shared &sh)
+{
+    const int b = 2 * threadIdx.x;
+    uint64_t v0, v1, all;
+    if (r.kind == TOP_K) {
+        v0 = count[b];
+        v1 = count[b + 1];
+    } else {
+        v0 = mass[b];
+        v1 = mass[b + 1];
+    }
+    if (threadIdx.x == 0) sh.bin = kBins;
+    const uint64_t before = scan_block(v0 + v1, sh.wu, all);
+    const double want = r.kind == TOP_K ? static_cast<double>(r.top_k) : r.top_p * unfixed(all) * 0x1p43;
+    auto less = [&](uint64_t m) { return static_cast<double>(m) < want; };
+    // (the first bin is never empty: the largest is in it)
+    const bool e0 = (b == 0 || less(before)) && !less(before + v0);
+    const bool e1 = less(before + v0) && !less(before + v0 + v1);
+    if (e0 || e1) {
+        sh.bin = e0 ? b : b + 1;
+        sh.ahead = e0 ? before : before + v0;
+    }
     __syncthreads();
-    auto count_over = [&](uint32_t k) {   // keys above k
-        uint64_t n = 0;
-        for (int i = tid; i < V; i += kThreads) n += key_of(static_cast<float>(x[i])) > k;
-        return static_cast<int64_t>(block_sum(n, su));
-    };
-    auto mass_over = [&](uint32_t k, uint32_t floor, int64_t equal) {   // of keys above k, and `equal` of floor's
-        double m = 0.0;
-        for (int i = tid; i < V; i += kThreads) {
-            const float v = static_cast<float>(x[i]);
-            const uint32_t c = key_of(v);
-            if (c > k && c > floor) m += weight(v, top, inv);
+}
+
+// 3: candidates into the list (`n` and `list` in LDS or the workspace), and the sum of
+// the weights ahead of them in this wave's share (top-p; of all of it without filters).
+// More than kList candidates are counted but not kept.
+template <typename T>
+__device__ __forceinline__ double gather(const SampleArgs &a, const Row &r, const T *x, int lo, int hi, int end, Shared &sh,
+                                         uint32_t *n, uint64_t *list)
+{
+    double sum = 0.0;
+    const int lane = threadIdx.x & 63;
+    walk(x, lo, hi, a.vec, [&](float v, int i) {
+        bool in = false, candidate = false;
+        if (r.kind == PLAIN) {
+            in = v > -kInf;
+        } else {
+            const int bin = bin_of(v, r);
+            if (r.kind == TOP_K) {
+                candidate = bin <= end && bin < kBins;
+            } else {
+                in = bin < end;
+                candidate = bin == end && bin < kBins;
+            }
         }
-        m = block_sum(m, sd);
-        if (floor > k) m += static_cast<double>(equal) * weight(of_key(floor), top, inv);
-        return m;
-    };
-    if (top_k > 0 && top_k < V) {
-        // the smallest key with fewer than top_k above it
-        uint32_t lo = 0, hi = 0xFFFFFFFFu;
-        while (lo < hi) {
-            const uint32_t mid = lo + (hi - lo) / 2;
-            if (count_over(mid) < top_k) hi = mid;
-            else lo = mid + 1;
+        if (in) {
+            const double w = weight(v, r, sh.roots);
+            sum += w >= r.min_p ? w : 0.0;
         }
-        edge = lo;
-        ties = top_k - count_over(lo);
-    }
-    if (top_p < 1.0f) {
-        int64_t equal = count_over(edge - 1) - count_over(edge);
-        if (edge == 0) equal = 0;
-        equal = equal < ties ? equal : ties;
-        const double want = static_cast<double>(top_p) * mass_over(0, edge, equal);
-        uint32_t lo = edge, hi = top_key;
-        while (lo < hi) {
-            const uint32_t mid = lo + (hi - lo) / 2;
-            if (mass_over(mid, edge, equal) < want) hi = mid;
-            else lo = mid + 1;
+        const uint64_t who = __ballot(candidate);
+        if (who) {
+            uint32_t at = 0;
+            if (lane == __builtin_ctzll(who)) at = atomicAdd(n, static_cast<uint32_t>(__popcll(who)));
+            at = __builtin_amdgcn_readlane(at, __builtin_ctzll(who)) + __popcll(who & ((1ull << lane) - 1));
+            if (candidate && at < kList) list[at] = (static_cast<uint64_t>(~key_of(v)) << 32) | static_cast<uint32_t>(i);
         }
-        // of the equals of lo, those with less than `want` ahead of them
-        const double ahead = mass_over(lo, edge, equal), w = weight(of_key(lo), top, inv);
-        const int64_t same = lo == edge ? equal : count_over(lo - 1) - count_over(lo);
-        int64_t n = 0, most = same;
-        while (n < most) {
-            const int64_t mid = (n + most) / 2;
-            if (ahead + static_cast<double>(mid) * w < want) n = mid + 1;
-            else most = mid;
-        }
-        edge = lo;
-        ties = lo == top_key && n == 0 ? 1 : n;
-    }
-    // kept weights of each thread's neighbouring places, equals of the edge counted from the first
-    const int per = (V + kThreads - 1) / kThreads;
-    const int i0 = tid * per, i1 = i0 + per < V ? i0 + per : V;
-    int64_t equals = 0;
-    for (int i = i0; i < i1; ++i) equals += key_of(static_cast<float>(x[i])) == edge;
-    int64_t seen = static_cast<int64_t>(block_before(static_cast<uint64_t>(equals), su));
-    auto kept = [&](int i, int64_t &rank) {
+    });
+    return wave_sum(sum);
+}
+
+// -------------------------------------------------------------------- step 4
+struct Edge {
+    uint32_t key;   // kept: keys above this one, and its equals
+    int limit;      // up to this index
+};
+
+__device__ __forceinline__ bool kept(float v, int i, const Edge &e)
+{
+    const uint32_t k = key_of(v);
+    return k > e.key || (k == e.key && i <= e.limit);
+}
+
+__device__ __forceinline__ void emit(const SampleArgs &a, int64_t b, int64_t token, float logp)
+{
+    a.token[b] = token;
+    if (a.logp) a.logp[b] = logp;
+}
+
+// The token of a row whose shares' kept weights are sh.sub[0..subs)
+template <typename T>
+__device__ __forceinline__ void pick(const SampleArgs &a, const Row &r, int64_t b, const T *x, int subs, const Edge &e,
+                                     Shared &sh)
+{
+    double all, total;
+    const double mine = threadIdx.x < static_cast<unsigned>(subs) ? sh.sub[threadIdx.x] : 0.0;
+    const double before = scan_block(mine, sh.wd, total);
+    const double target = static_cast<double>(r.u) * total;
+    if (threadIdx.x == 0) sh.at = subs;
+    __syncthreads();
+    if (mine > 0.0 && before + mine > target) atomicMin(&sh.at, static_cast<int>(threadIdx.x));
+    __syncthreads();
+    // (a target that rounding puts past the last share's end: the last one)
+    const int j = sh.at;
+    if (threadIdx.x == 0) sh.last = -1;
+    __syncthreads();
+    if (j == subs && mine > 0.0) atomicMax(&sh.last, static_cast<int>(threadIdx.x));
+    __syncthreads();
+    const int sub = j < subs ? j : sh.last;
+    if (threadIdx.x == static_cast<unsigned>(sub)) sh.w_at = before;
+    __syncthreads();
+    const double start = sh.w_at;
+    const int lo = sub * a.share, hi = lo + a.share < a.vocab ? lo + a.share : a.vocab;
+    // each thread takes neighbouring places
+    const int per = (a.share + kThreads - 1) / kThreads;
+    const int i0 = lo + static_cast<int>(threadIdx.x) * per, i1 = i0 + per < hi ? i0 + per : hi;
+    auto weight_at = [&](int i) {
         const float v = static_cast<float>(x[i]);
-        const uint32_t c = key_of(v);
-        if (c < edge || (c == edge && rank++ >= ties)) return 0.0;
-        const double w = weight(v, top, inv);
-        return w >= static_cast<double>(min_p) ? w : 0.0;
+        if (v == -kInf || !kept(v, i, e)) return 0.0;
+        const double w = weight(v, r, sh.roots);
+        return w >= r.min_p ? w : 0.0;
     };
-    double mine = 0.0;
-    int64_t rank = seen;
-    for (int i = i0; i < i1; ++i) mine += kept(i, rank);
-    const double before = block_before(mine, sd), total = block_sum(mine, sd);
-    const double target = static_cast<double>(u) * total;
-    if (tid == 0) found = V;
+    double own = 0.0;
+    for (int i = i0; i < i1; ++i) own += weight_at(i);
+    const double ahead = start + scan_block(own, sh.wd, all);
+    if (threadIdx.x == 0) {
+        sh.at = a.vocab;
+        sh.last = -1;
+    }
     __syncthreads();
-    int at = V;
-    double w_at = 0.0, run = before;
-    rank = seen;
-    if (before + mine > target)
+    int at = -1, last = -1;
+    double run = ahead, w_at = 0.0, w_last = 0.0;
+    if (own > 0.0)
         for (int i = i0; i < i1; ++i) {
-            const double w = kept(i, rank);
+            const double w = weight_at(i);
+            if (!(w > 0.0)) continue;
             run += w;
-            if (run > target && w > 0.0) {
+            last = i;
+            w_last = w;
+            if (run > target) {
                 at = i;
                 w_at = w;
                 break;
             }
         }
-    if (at < V) atomicMin(&found, at);
+    if (at >= 0) atomicMin(&sh.at, at);
+    if (last >= 0) atomicMax(&sh.last, last);
     __syncthreads();
-    if (at < V && at == found) {
-        a.token[b] = at;
-        if (a.logp) a.logp[b] = static_cast<float>(log(w_at / total));
+    const int found = sh.at;
+    if (at >= 0 && at == found) emit(a, b, at, static_cast<float>(log(w_at / total)));
+    if (found == a.vocab && last >= 0 && last == sh.last) emit(a, b, last, static_cast<float>(log(w_last / total)));
+}
+
+template <typename T>
+__device__ __forceinline__ void pick_first(const SampleArgs &a, const Row &r, int64_t b, const T *x, Shared &sh)
+{
+    if (threadIdx.x == 0) sh.at = a.vocab;
+    __syncthreads();
+    const int wv = wave();
+    const int per = (a.vocab + kWaves * 512 - 1) / (kWaves * 512) * 512;
+    const int lo = wv * per, hi = lo + per < a.vocab ? lo + per : a.vocab;
+    int first = a.vocab;
+    walk(x, lo, hi, a.vec, [&](float v, int i) {
+        if (v == r.top && i < first) first = i;
+    });
+    if (first < a.vocab) atomicMin(&sh.at, first);
+    __syncthreads();
+    if (threadIdx.x == 0) emit(a, b, sh.at, 0.0f);
+}
+
+// Sorted candidates' weights: the sum over the places before `i`, thread by thread; a
+// thread holds four neighbours
+struct Four {
+    double w[4], before;
+};
+
+__device__ __forceinline__ Four weights4(const Row &r, int n, Shared &sh, double &all, bool by_index)
+{
+    Four f;
+    double sum = 0.0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int i = 4 * threadIdx.x + e;
+        const uint64_t c = sh.list[i < n ? i : 0];
+        const uint32_t key = by_index ? ~static_cast<uint32_t>(c) : ~static_cast<uint32_t>(c >> 32);
+        f.w[e] = i < n ? weight(of_key(key), r, sh.roots) : 0.0;
+        sum += f.w[e];
     }
+    f.before = scan_block(sum, sh.wd, all);
+    return f;
+}
+
+__device__ __forceinline__ int pad_list(int n, Shared &sh)
+{
+    int size = 64;
+    while (size < n) size *= 2;
+    __syncthreads();
+    for (int i = n + threadIdx.x; i < size; i += kThreads) sh.list[i] = ~0ull;
+    return size;
+}
+
+// How many of the n sorted candidates stay: those with less than `want` of the weight
+// ahead of them, one at least
+__device__ __forceinline__ int cut(const Four &f, int n, double ahead, double want, Shared &sh)
+{
+    __syncthreads();
+    if (threadIdx.x == 0) sh.at = 0;
+    __syncthreads();
+    double run = ahead + f.before;
+    int most = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int i = 4 * threadIdx.x + e;
+        if (i < n && run < want) most = i + 1;
+        run += f.w[e];
+    }
+    if (most) atomicMax(&sh.at, most);
+    __syncthreads();
+    return sh.at;
+}
+
+// Top-k: the list holds all candidates, n of them; top-p, min-p and the draw are done on it
+__device__ __forceinline__ void finish_list(const SampleArgs &a, const Row &r, int64_t b, int n, Shared &sh)
+{
+    sort_list(sh.list, pad_list(n, sh));
+    n = n < r.top_k ? n : r.top_k;
+    double all;
+    Four f = weights4(r, n, sh, all, false);
+    if (r.top_p < 1.0) {
+        const int m = cut(f, n, 0.0, r.top_p * all, sh);
+        n = m > 1 ? m : 1;
+    }
+    __syncthreads();
+    // by index; what min-p drops goes to the end
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const int i = 4 * threadIdx.x + e;
+        if (i < n) {
+            const uint64_t c = sh.list[i];
+            sh.list[i] = f.w[e] >= r.min_p ? (c << 32) | (c >> 32) : ~0ull;
+        }
+    }
+    sort_list(sh.list, pad_list(n, sh));
+    f = weights4(r, n, sh, all, true);   // (the dropped ones' key is a NaN's: no weight)
+    const double target = static_cast<double>(r.u) * all;
+    if (threadIdx.x == 0) sh.at = n;
+    __syncthreads();
+    double run = f.before;
+    int at = -1, last = -1;
+    double w_at = 0.0, w_last = 0.0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        run += f.w[e];
+        if (f.w[e] > 0.0) {
+            last = 4 * threadIdx.x + e;
+            w_last = f.w[e];
+            if (at < 0 && run > target) {
+                at = last;
+                w_at = w_last;
+            }
+        }
+    }
+    if (threadIdx.x == 0) sh.last = -1;
+    __syncthreads();
+    if (at >= 0) atomicMin(&sh.at, at);
+    if (last >= 0) atomicMax(&sh.last, last);
+    __syncthreads();
+    const int found = sh.at;
+    if (at >= 0 && at == found) emit(a, b, static_cast<int64_t>(sh.list[at] >> 32), static_cast<float>(log(w_at / all)));
+    if (found == n && last >= 0 && last == sh.last)
+        emit(a, b, static_cast<int64_t>(sh.list[last] >> 32), static_cast<float>(log(w_last / all)));
+}
+
+// ---------------------------------------------- rows with too many candidates
+// The edge of a filter over what `before` keeps, by the row's workgroup alone: want
+// (a count, or a weight) is reached within the keys lo..hi, with `ahead` above hi.
+// The range is split by histograms until it is short enough to sort or one value.
+template <typename T, bool MASS>
+__device__ __forceinline__ Edge narrow(const SampleArgs &a, const Row &r, const T *x, uint32_t lo, uint32_t hi, double ahead,
+                                       double want, const Edge &before, Shared &sh)
+{
+    const int per = (a.vocab + kWaves * 512 - 1) / (kWaves * 512) * 512;
+    const int i0 = wave() * per, i1 = i0 + per < a.vocab ? i0 + per : a.vocab;
+    for (;;) {
+        // histogram of lo..hi, largest first
+        int shift = 0;
+        while (((hi - lo) >> shift) >= kBins) ++shift;
+        __syncthreads();
+        for (int i = threadIdx.x; i < kBins; i += kThreads) {
+            sh.count[i] = 0;
+            sh.mass[i] = 0;
+        }
+        __syncthreads();
+        walk(x, i0, i1, a.vec, [&](float v, int i) {
+            const uint32_t k = key_of(v);
+            if (v == -kInf || k < lo || k > hi || !kept(v, i, before)) return;
+            const int bin = (hi - k) >> shift;
+            atomicAdd(&sh.count[bin], 1u);
+            if constexpr (MASS)
+                atomicAdd(reinterpret_cast<unsigned long long *>(&sh.mass[bin]), fixed(weight(v, r, sh.roots)));
+        });
+        __syncthreads();
+        const int b = 2 * threadIdx.x;
+        const uint64_t v0 = MASS ? sh.mass[b] : sh.count[b], v1 = MASS ? sh.mass[b + 1] : sh.count[b + 1];
+        uint64_t all;
+        const uint64_t sum = scan_block(v0 + v1, sh.wu, all);
+        const double unit = MASS ? 0x1p-43 : 1.0;
+        auto less = [&](uint64_t m) { return ahead + static_cast<double>(m) * unit < want; };
+        if (threadIdx.x == 0) {
+            sh.bin = -1;
+            sh.last = -1;
+        }
+        __syncthreads();
+        // the last bin that is entered with less than `want` ahead, and is not empty
+        const uint32_t c0 = sh.count[b], c1 = sh.count[b + 1];
+        if (c1 && less(sum + v0)) atomicMax(&sh.bin, b + 1);
+        else if (c0 && less(sum)) atomicMax(&sh.bin, b);
+        __syncthreads();
+        const int bin = sh.bin;
+        if (bin < 0) {   // nothing may follow what is ahead: the largest alone
+            sh.n = 0;
+            __syncthreads();
+            return Edge{hi, -1};
+        }
+        if (b == (bin & ~1)) sh.ahead = bin & 1 ? sum + v0 : sum;
+        __syncthreads();
+        ahead += static_cast<double>(sh.ahead) * unit;
+        const uint32_t top = hi - (static_cast<uint32_t>(bin) << shift);
+        const uint32_t span = (1u << shift) - 1;
+        lo = top - lo > span ? top - span : lo;
+        hi = top;
+        const int n = sh.count[bin];
+        if (n <= kList) {
+            // few: sort them
+            __syncthreads();
+            if (threadIdx.x == 0) sh.n = 0;
+            __syncthreads();
+            walk(x, i0, i1, a.vec, [&](float v, int i) {
+                const uint32_t k = key_of(v);
+                if (v == -kInf || k < lo || k > hi || !kept(v, i, before)) return;
+                sh.list[atomicAdd(&sh.n, 1u)] = (static_cast<uint64_t>(~k) << 32) | static_cast<uint32_t>(i);
+            });
+            sort_list(sh.list, pad_list(n, sh));
+            int m;
+            if constexpr (MASS) {
+                double sum4;
+                m = cut(weights4(r, n, sh, sum4, false), n, ahead, want, sh);
+            } else {
+                m = static_cast<int>(want - ahead);
+                m = m < n ? m : n;
+            }
+            m = m > 1 ? m : 1;
+            const uint64_t c = sh.list[m - 1];
+            __syncthreads();
+            return Edge{~static_cast<uint32_t>(c >> 32), static_cast<int>(static_cast<uint32_t>(c))};
+        }
+        if (lo == hi) {
+            // one value: the first few of its places
+            int m = n;
+            if constexpr (MASS) {
+                const double w = weight(of_key(lo), r, sh.roots);
+                int low = 1;   // the smallest number that is not followed
+                while (low < m) {
+                    const int mid = low + (m - low) / 2;
+                    if (ahead + static_cast<double>(mid) * w < want) low = mid + 1;
+                    else m = mid;
+                }
+            } else {
+                m = want - ahead < n ? static_cast<int>(want - ahead) : n;
+            }
+            // the index of the m-th: counted by threads' neighbouring places
+            const int each = (a.vocab + kThreads - 1) / kThreads;
+            const int j0 = threadIdx.x * each, j1 = j0 + each < a.vocab ? j0 + each : a.vocab;
+            uint64_t own = 0, total;
+            auto same = [&](int i) {
+                const float v = static_cast<float>(x[i]);
+                return key_of(v) == lo && kept(v, i, before);
+            };
+            for (int i = j0; i < j1; ++i) own += same(i);
+            uint64_t seen = scan_block(own, sh.wu, total);
+            if (seen < static_cast<uint64_t>(m) && seen + own >= static_cast<uint64_t>(m))
+                for (int i = j0; i < j1; ++i)
+                    if (same(i) && ++seen == static_cast<uint64_t>(m)) sh.last = i;
+            __syncthreads();
+            const int limit = sh.last;
+            __syncthreads();
+            return Edge{lo, limit};
+        }
+    }
+}
+
+// Kept weights of all of a row, into the shares' sums
+template <typename T>
+__device__ __forceinline__ double kept_sums(const SampleArgs &a, const Row &r, const T *x, int subs, const Edge &e, Shared &sh)
+{
+    double mine = 0.0;
+    for (int s = wave(); s < subs; s += kWaves) {
+        double sum = 0.0;
+        const int lo = s * a.share, hi = lo + a.share < a.vocab ? lo + a.share : a.vocab;
+        walk(x, lo, hi, a.vec, [&](float v, int i) {
+            if (v == -kInf || !kept(v, i, e)) return;
+            const double w = weight(v, r, sh.roots);
+            sum += w >= r.min_p ? w : 0.0;
+        });
+        sum = wave_sum(sum);
+        mine += sum;
+        if ((threadIdx.x & 63) == 0) sh.sub[s] = sum;
+    }
+    __syncthreads();
+    double all;
+    scan_block((threadIdx.x & 63) == 0 ? mine : 0.0, sh.wd, all);
+    return all;
+}
+
+template <typename T>
+__device__ __forceinline__ void solve_alone(const SampleArgs &a, Row r, int64_t b, const T *x, int subs, Shared &sh)
+{
+    Edge e{0, a.vocab};
+    const uint32_t top = key_of(r.top);
+    const double min_p = r.min_p;
+    if (r.top_k) e = narrow<T, false>(a, r, x, 1, top, 0.0, static_cast<double>(r.top_k), e, sh);
+    if (r.top_p < 1.0) {
+        r.min_p = 0.0;
+        const double want = r.top_p * kept_sums(a, r, x, subs, e, sh);
+        const Edge f = narrow<T, true>(a, r, x, 1, top, 0.0, want, e, sh);
+        if (f.limit >= 0) {
+            e = f;
+        } else {   // want is nothing: the first of the largest
+            e = narrow<T, false>(a, r, x, top, top, 0.0, 1.0, e, sh);
+        }
+        r.min_p = min_p;
+    }
+    kept_sums(a, r, x, subs, e, sh);
+    __syncthreads();
+    pick(a, r, b, x, subs, e, sh);
+}
+
+// The last step of a row: thresholds and candidates are known (in LDS: sh.bin, sh.ahead,
+// sh.list with `n` found in all, sh.sub)
+template <typename T>
+__device__ __forceinline__ void finish(const SampleArgs &a, const Row &r, int64_t b, const T *x, int subs, int n,
+                                       double want, Shared &sh)
+{
+    if (r.kind == PLAIN) {
+        pick(a, r, b, x, subs, Edge{0, a.vocab}, sh);
+        return;
+    }
+    if (n > kList) {
+        solve_alone(a, r, b, x, subs, sh);
+        return;
+    }
+    if (r.kind == TOP_K) {
+        finish_list(a, r, b, n, sh);
+        return;
+    }
+    // top-p: the last of the sorted candidates that stays is the edge
+    sort_list(sh.list, pad_list(n, sh));
+    double all;
+    const Four f = weights4(r, n, sh, all, false);
+    const double ahead = unfixed(sh.ahead);
+    int m = cut(f, n, ahead, want, sh);
+    m = m > 1 ? m : 1;
+    const uint64_t c = sh.list[m - 1];
+    const Edge e{~static_cast<uint32_t>(c >> 32), static_cast<int>(static_cast<uint32_t>(c))};
+    __syncthreads();
+    // their weights into the sums of their shares, share by share in the candidates' order
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int i = 4 * threadIdx.x + k;
+        if (i < m) {
+            const uint64_t v = sh.list[i];
+            sh.list[i] = (v << 32) | (v >> 32);
+        }
+    }
+    sort_list(sh.list, pad_list(m, sh));
+    double *ws = reinterpret_cast<double *>(sh.mass);   // (the histogram has been read)
+    constexpr int kRoom = (sizeof(sh.mass) + sizeof(sh.count)) / sizeof(double);
+    auto weight_of = [&](int i) {
+        const double w = weight(of_key(~static_cast<uint32_t>(sh.list[i])), r, sh.roots);
+        return w >= r.min_p ? w : 0.0;
+    };
+    auto share_of = [&](int i) { return static_cast<int>(static_cast<uint32_t>(sh.list[i] >> 32) / a.share); };
+    for (int i = threadIdx.x; i < m && i < kRoom; i += kThreads) ws[i] = weight_of(i);
+    __syncthreads();
+    for (int i = threadIdx.x; i < m; i += kThreads) {
+        const int s = share_of(i);
+        if (i > 0 && share_of(i - 1) == s) continue;
+        double sum = sh.sub[s];   // the first of its share adds them up
+        for (int j = i; j < m && share_of(j) == s; ++j) sum += j < kRoom ? ws[j] : weight_of(j);
+        sh.sub[s] = sum;
+    }
+    __syncthreads();
+    pick(a, r, b, x, subs, e, sh);
+}
+
+__device__ __forceinline__ void clear_histogram(Shared &sh)
+{
+    for (int i = threadIdx.x; i < kBins; i += kThreads) {
+        sh.count[i] = 0;
+        sh.mass[i] = 0;
+    }
+    if (threadIdx.x == 0) sh.n = 0;
+}
+
+// top_p of the histogram's weight
+__device__ __forceinline__ double wanted(const Row &r, const uint64_t *mass, Shared &sh)
+{
+    uint64_t all;
+    scan_block(mass[2 * threadIdx.x] + mass[2 * threadIdx.x + 1], sh.wu, all);
+    return r.top_p * unfixed(all);
+}
+
+template <typename T> __global__ void __launch_bounds__(kThreads) sample_row_kernel(SampleArgs a)
+{
+    __shared__ Shared sh;
+    const int64_t b = blockIdx.x;
+    const T *x = static_cast<const T *>(a.logits) + b * a.stride;
+    const int lo = wave() * a.share < a.vocab ? wave() * a.share : a.vocab;
+    const int hi = lo + a.share < a.vocab ? lo + a.share : a.vocab;
+    fill_roots(sh.roots);
+    clear_histogram(sh);
+    const Row r = settings(a, b, slice_top(a, x, lo, hi, sh));
+    if (r.kind == DONE) {
+        if (threadIdx.x == 0) emit(a, b, -1, -kInf);
+        return;
+    }
+    if (r.kind == GREEDY) {
+        pick_first(a, r, b, x, sh);
+        return;
+    }
+    double want = 0.0;
+    if (r.kind != PLAIN) {
+        histogram(a, r, x, lo, hi, sh);
+        __syncthreads();
+        end_bin(r, sh.count, sh.mass, sh);
+        if (r.kind == TOP_P) want = wanted(r, sh.mass, sh);
+    }
+    const double sum = gather(a, r, x, lo, hi, sh.bin, sh, &sh.n, sh.list);
+    if ((threadIdx.x & 63) == 0) sh.sub[wave()] = sum;
+    __syncthreads();
+    finish(a, r, b, x, kWaves, static_cast<int>(sh.n), want, sh);
+}
+
+// ------------------------------------------------------ rows cut into slices
+// Workgroup: blockIdx.x / slices is the row
+struct Piece {
+    int64_t b;
+    int slice, lo, hi;   // this wave's share
+};
+
+__device__ __forceinline__ Piece piece(const SampleArgs &a)
+{
+    Piece p;
+    const int64_t row = blockIdx.x / a.slices;
+    p.b = row;
+    p.slice = static_cast<int>(blockIdx.x - row * a.slices);
+    const int64_t lo = static_cast<int64_t>(p.slice * kWaves + wave()) * a.share;
+    p.lo = static_cast<int>(lo < a.vocab ? lo : a.vocab);
+    p.hi = p.lo + a.share < a.vocab ? p.lo + a.share : a.vocab;
+    return p;
+}
+
+__device__ __forceinline__ float row_top(const SampleArgs &a, const Slot &s)
+{
+    float top = -kInf;
+    for (int i = 0; i < a.slices; ++i) top = top != top || s.top[i] != s.top[i] ? __builtin_nanf("") : fmaxf(top, s.top[i]);
+    return top;
+}
+
+template <typename T> __global__ void __launch_bounds__(kThreads) sample_top_kernel(SampleArgs a)
+{
+    __shared__ Shared sh;
+    const Piece p = piece(a);
+    const Slot s = slot_of(a, p.b);
+    const float top = slice_top(a, static_cast<const T *>(a.logits) + p.b * a.stride, p.lo, p.hi, sh);
+    if (threadIdx.x == 0) s.top[p.slice] = top;
+    for (int i = p.slice * kThreads + threadIdx.x; i < kBins; i += a.slices * kThreads) {
+        s.count[i] = 0;
+        s.mass[i] = 0;
+    }
+    if (p.slice == 0 && threadIdx.x == 0) *s.n = 0;
+}
+
+template <typename T> __global__ void __launch_bounds__(kThreads) sample_bins_kernel(SampleArgs a)
+{
+    __shared__ Shared sh;
+    const Piece p = piece(a);
+    const Slot s = slot_of(a, p.b);
+    const Row r = settings(a, p.b, row_top(a, s));
+    if (r.kind != TOP_K && r.kind != TOP_P) return;
+    fill_roots(sh.roots);
+    clear_histogram(sh);
+    __syncthreads();
+    histogram(a, r, static_cast<const T *>(a.logits) + p.b * a.stride, p.lo, p.hi, sh);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kBins; i += kThreads) {
+        if (!sh.count[i]) continue;
+        atomicAdd(&s.count[i], sh.count[i]);
+        if (r.kind == TOP_P) atomicAdd(reinterpret_cast<unsigned long long *>(&s.mass[i]), sh.mass[i]);
+    }
+}
+
+template <typename T> __global__ void __launch_bounds__(kThreads) sample_gather_kernel(SampleArgs a)
+{
+    __shared__ Shared sh;
+    const Piece p = piece(a);
+    const Slot s = slot_of(a, p.b);
+    const Row r = settings(a, p.b, row_top(a, s));
+    if (r.kind == DONE || r.kind == GREEDY) return;
+    fill_roots(sh.roots);
+    __syncthreads();
+    if (r.kind != PLAIN) end_bin(r, s.count, s.mass, sh);
+    const double sum = gather(a, r, static_cast<const T *>(a.logits) + p.b * a.stride, p.lo, p.hi, sh.bin, sh, s.n, s.list);
+    if ((threadIdx.x & 63) == 0) s.sub[p.slice * kWaves + wave()] = sum;
+}
+
+template <typename T> __global__ void __launch_bounds__(kThreads) sample_pick_kernel(SampleArgs a)
+{
+    __shared__ Shared sh;
+    const int64_t b = blockIdx.x;
+    const Slot s = slot_of(a, b);
+    const T *x = static_cast<const T *>(a.logits) + b * a.stride;
+    const Row r = settings(a, b, row_top(a, s));
+    if (r.kind == DONE) {
+        if (threadIdx.x == 0) emit(a, b, -1, -kInf);
+        return;
+    }
+    if (r.kind == GREEDY) {
+        pick_first(a, r, b, x, sh);
+        return;
+    }
+    fill_roots(sh.roots);
+    const int subs = a.slices * kWaves, n = static_cast<int>(*s.n);
+    for (int i = threadIdx.x; i < subs; i += kThreads) sh.sub[i] = s.sub[i];
+    double want = 0.0;
+    if (r.kind != PLAIN) {
+        for (int i = threadIdx.x; i < n && i < kList; i += kThreads) sh.list[i] = s.list[i];
+        __syncthreads();
+        end_bin(r, s.count, s.mass, sh);
+        if (r.kind == TOP_P) want = wanted(r, s.mass, sh);
+    }
+    __syncthreads();
+    finish(a, r, b, x, subs, n, want, sh);
+}
+
+struct SampleGeom {
+    int slices, share;
+    size_t slot;
+};
+
+SampleGeom sample_geometry(const mgs_sample_desc &d)
+{
+    SampleGeom g{};
+    const int64_t step = 64 * (d.dtype == MGS_BF16 ? 8 : 4);   // what a wave reads at once
+    const int64_t steps = (d.vocab + step - 1) / step;
+    // workgroups for every CU, no more than there are waves' steps
+    int64_t s = std::min<int64_t>((steps + kWaves - 1) / kWaves, d.B > 0 ? 512 / d.B : 1);
+    s = std::max<int64_t>(1, std::min<int64_t>(s, kMaxSlices));
+    g.slices = static_cast<int>(s);
+    g.share = static_cast<int>((steps + s * kWaves - 1) / (s * kWaves) * step);
+    g.slot = s > 1 ? align256(kSlotSub + sizeof(double) * kWaves * s) : 0;
+    return g;
+}
+
+template <typename T> hipError_t run(const SampleArgs &a, unsigned rows, hipStream_t s)
+{
+    if (a.slices == 1) {
+        sample_row_kernel<T><<<dim3(rows), dim3(kThreads), 0, s>>>(a);
+        return hipGetLastError();
+    }
+    const dim3 grid(rows * a.slices), block(kThreads);
+    const bool filters = a.top_k || a.top_p || (a.k0 > 0 && a.k0 < a.vocab) || a.p0 < 1.0f;
+    sample_top_kernel<T><<<grid, block, 0, s>>>(a);
+    if (filters) sample_bins_kernel<T><<<grid, block, 0, s>>>(a);
+    sample_gather_kernel<T><<<grid, block, 0, s>>>(a);
+    sample_pick_kernel<T><<<dim3(rows), block, 0, s>>>(a);
+    return hipGetLastError();
 }
 
 }  // namespace
 
-size_t sample_workspace(const mgs_sample_desc &) { return 256; }
+size_t sample_workspace(const mgs_sample_desc &d)
+{
+    const SampleGeom g = sample_geometry(d);
+    return 256 + g.slot * static_cast<size_t>(d.B);
+}
 
 hipError_t launch_sample(const mgs_sample_desc &d, const void *logits, const float *u, const float *temperature,
                          const int32_t *top_k, const float *top_p, const float *min_p, int64_t *token, float *logp,
-                         void *, hipStream_t s)
+                         void *ws, hipStream_t s)
 {
-    SampleArgs a{logits, u, temperature, top_p, min_p, top_k, token, logp, d.vocab, d.logits_stride, d.top_k,
-                 d.temperature, d.top_p, d.min_p};
-    const dim3 grid(static_cast<unsigned>(d.B)), block(kThreads);
-    if (d.dtype == MGS_BF16) sample_kernel<__bf16><<<grid, block, 0, s>>>(a);
-    else sample_kernel<float><<<grid, block, 0, s>>>(a);
-    return hipGetLastError();
+    const SampleGeom g = sample_geometry(d);
+    const int size = d.dtype == MGS_BF16 ? 2 : 4;
+    const bool vec = (reinterpret_cast<uintptr_t>(logits) & 15) == 0 && (d.B == 1 || (d.logits_stride * size) % 16 == 0);
+    const SampleArgs a{logits, u, temperature, top_p, min_p, top_k, token, logp, d.logits_stride,
+                       static_cast<char *>(ws), g.slot, static_cast<int>(d.vocab), g.slices, g.share, d.top_k,
+                       d.temperature, d.top_p, d.min_p, vec};
+    const unsigned rows = static_cast<unsigned>(d.B);
+    return d.dtype == MGS_BF16 ? run<__bf16>(a, rows, s) : run<float>(a, rows, s);
 }
 
 }  // namespace mgs
