@@ -32,6 +32,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kWaves = 8;                // per workgroup
 constexpr int kGroup = 128;              // channels of a workgroup
 constexpr int kFwdSteps = 16, kBwdSteps = 8;   // of a wave
+constexpr int kFwdOccupancy = 4, kBwdOccupancy = 4;   // waves of a SIMD
 constexpr int kUnit = 8;                 // tiles whose pairs a tile reads at most
 static_assert(kUnit <= kWaves, "each wave polls one tile");
 constexpr int kFwdTile = kWaves * kFwdSteps, kBwdTile = kWaves * kBwdSteps;
@@ -50,25 +51,64 @@ template <typename T> struct Two;
 template <> struct Two<float> { using V = f32x2; };
 template <> struct Two<__bf16> { using V = bf2v; };
 
-// Elements c and c + 1 of a row, where they exist (c < d)
-template <typename T, bool PAIRS> __device__ __forceinline__ f32x2 load2(const T *row, int c, int d)
-{
-    if constexpr (PAIRS) {
-        c = c < d ? c : d - 2;
-        return __builtin_convertvector(*reinterpret_cast<const typename Two<T>::V *>(row + c), f32x2);
-    } else {
-        return f32x2{static_cast<float>(row[c < d ? c : d - 1]), static_cast<float>(row[c + 1 < d ? c + 1 : d - 1])};
+// A lane's two channels, c and c + 1: byte offsets into a row of T, past the last
+// channel the last one's (that lane's results are not stored).
+template <typename T, bool PAIRS> struct Lane {
+    uint32_t at, next;
+    bool in, both;
+    __device__ __forceinline__ Lane(int c, int d) : in(c < d), both(c + 1 < d)
+    {
+        const int size = sizeof(T);
+        if constexpr (PAIRS) {
+            at = static_cast<uint32_t>((in ? c : d - 2) * size);
+            next = at + size;
+        } else {
+            at = static_cast<uint32_t>((in ? c : d - 1) * size);
+            next = static_cast<uint32_t>((both ? c + 1 : d - 1) * size);
+        }
     }
+    __device__ __forceinline__ typename Two<T>::V load(const char *row) const
+    {
+        if constexpr (PAIRS)
+            return *reinterpret_cast<const typename Two<T>::V *>(row + at);
+        else
+            return typename Two<T>::V{*reinterpret_cast<const T *>(row + at), *reinterpret_cast<const T *>(row + next)};
+    }
+    // (in a lane that is `in`)
+    __device__ __forceinline__ void store(char *row, f32x2 v) const
+    {
+        const typename Two<T>::V o = __builtin_convertvector(v, typename Two<T>::V);
+        if constexpr (PAIRS) {
+            __builtin_nontemporal_store(o, reinterpret_cast<typename Two<T>::V *>(row + at));
+        } else {
+            *reinterpret_cast<T *>(row + at) = o[0];
+            if (both) *reinterpret_cast<T *>(row + next) = o[1];
+        }
+    }
+};
+
+template <typename V> __device__ __forceinline__ f32x2 wide(V v) { return __builtin_convertvector(v, f32x2); }
+
+// Holds the compiler to computing v here: it would put off what is needed only behind
+// the barriers, and keep the operands, which are more
+__device__ __forceinline__ void settle(f32x2 &v)
+{
+    float x = v[0], y = v[1];
+    asm volatile("" : "+v"(x), "+v"(y));
+    v = f32x2{x, y};
 }
 
-template <typename T, bool PAIRS> __device__ __forceinline__ void store2(T *row, int c, int d, f32x2 v)
+// wide(v), later: hides that things of v have been computed before, which would be kept
+// all the while
+template <typename V> __device__ __forceinline__ f32x2 again(V v)
 {
-    const typename Two<T>::V o = __builtin_convertvector(v, typename Two<T>::V);
-    if constexpr (PAIRS) {
-        if (c < d) __builtin_nontemporal_store(o, reinterpret_cast<typename Two<T>::V *>(row + c));
+    if constexpr (sizeof(V) == 4) {
+        uint32_t u = __builtin_bit_cast(uint32_t, v);
+        asm volatile("" : "+v"(u));
+        return wide(__builtin_bit_cast(V, u));
     } else {
-        if (c < d) row[c] = o[0];
-        if (c + 1 < d) row[c + 1] = o[1];
+        asm volatile("" : "+v"(v));
+        return v;
     }
 }
 
@@ -98,42 +138,37 @@ template <typename T> __device__ __forceinline__ float exp_neg(float z)
 // 1 - s of s = 1 / (1 + e), without cancellation; e may be infinite
 __device__ __forceinline__ float shut(float e, float s) { return e > 0x1p100f ? 1.0f : e * s; }
 
-// a = e^l and beta^2 = 1 - a^2 for l <= 0.  Near 0 both come of p = 1 - e^l by its
-// series (six terms: below 2^-24 of p up to |l| = 1/4): 1 - a^2 = p (2 - p) keeps
-// p's relative accuracy, where 1 - a^2 of a rounded a would lose it.
+// a = 2^l and beta^2 = 1 - a^2 for l <= 0 (log2 a; -inf where a document starts).  1 - a loses what a rounds away
+// where a is near 1; below |l| = 1/16 (2^-20 of it) the series of 1 - 2^l takes its
+// place, four terms, off by 2^-23 at most.
 __device__ __forceinline__ void decay(float l, float &a, float &beta2)
 {
-    float s = __builtin_fmaf(l, 1.0f / 7.0f, 1.0f);
-    s = __builtin_fmaf(l * s, 1.0f / 6.0f, 1.0f);
-    s = __builtin_fmaf(l * s, 1.0f / 5.0f, 1.0f);
-    s = __builtin_fmaf(l * s, 1.0f / 4.0f, 1.0f);
-    s = __builtin_fmaf(l * s, 1.0f / 3.0f, 1.0f);
-    s = __builtin_fmaf(l * s, 1.0f / 2.0f, 1.0f);
-    const float near = -l * s;
-    const bool small = l > -0.25f;
-    const float e = ex2(l * kLog2e);
-    const float p = small ? near : 1.0f - e;
-    a = small ? 1.0f - near : e;
-    beta2 = p * (1.0f + a);
+    a = ex2(l);
+    float s = __builtin_fmaf(l, -9.618129107628477e-3f, -5.550410866482158e-2f);
+    s = __builtin_fmaf(l, s, -2.402265069591007e-1f);
+    s = __builtin_fmaf(l, s, -6.931471805599453e-1f);
+    const float p = l > -0.0625f ? l * s : 1.0f - a;
+    beta2 = __builtin_fmaf(p, a, p);
 }
 
-// -rate softplus(lam)
+// -rate softplus(lam), and that in base 2
 __device__ __forceinline__ float slope(float lam, float rate)
 {
     return -rate * (fmaxf(lam, 0.0f) + log1pf(expf(-fabsf(lam))));
 }
+__device__ __forceinline__ float slope2(float lam, float rate) { return slope(lam, rate) * kLog2e; }
 
 struct Gate {
     float a, b;   // h -> a h + b
 };
 
-template <typename T> __device__ __forceinline__ Gate gate(float x, float r, float i, float k, bool fresh)
+// k: slope2; start: -inf where a document starts, 0 elsewhere
+template <typename T> __device__ __forceinline__ Gate gate(float x, float r, float i, float k, float start)
 {
     const float rho = rcp(1.0f + exp_neg<T>(r)), iota = rcp(1.0f + exp_neg<T>(i));
     float a, beta2;
-    decay(k * rho, a, beta2);
-    const float beta = fresh ? 1.0f : __builtin_amdgcn_sqrtf(beta2);
-    return Gate{fresh ? -0.0f : a, beta * iota * x};
+    decay(__builtin_fmaf(k, rho, start), a, beta2);
+    return Gate{a, __builtin_amdgcn_sqrtf(beta2) * iota * x};
 }
 
 __device__ __forceinline__ bool clears(float A) { return __float_as_uint(A) == 0x80000000u; }
@@ -144,6 +179,19 @@ __device__ __forceinline__ float apply(float A, float H, float h)
 }
 // A of the first pair, then this one
 __device__ __forceinline__ float chain(float A1, float A2) { return clears(A2) ? A2 : A1 * A2; }
+// The pair (A, H), then (A2, H2)
+__device__ __forceinline__ void append(f32x2 &A, f32x2 &H, f32x2 A2, f32x2 H2)
+{
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        H[v] = apply(A2[v], H2[v], H[v]);
+        A[v] = chain(A[v], A2[v]);
+    }
+}
+__device__ __forceinline__ f32x2 apply2(f32x2 A, f32x2 H, f32x2 h)
+{
+    return f32x2{apply(A[0], H[0], h[0]), apply(A[1], H[1], h[1])};
+}
 
 // ------------------------------------------------------------- look-back
 // Tiles of one channel group pass on their pairs in units of kUnit tiles: the
@@ -161,8 +209,9 @@ struct Lookback {
 };
 
 struct Shared {
-    f32x2 A[kWaves][64], H[kWaves][64];      // the waves' pairs
+    f32x2 A[kWaves][64], H[kWaves][64];      // the waves' pairs; then those of all waves ahead of each
     f32x2 pA[kUnit][64], pH[kUnit][64];      // the unit's tiles' pairs; pH[0]: the value that enters the unit
+    float k[kGroup];                         // slope2
     uint32_t ticket[3];
 };
 
@@ -196,55 +245,49 @@ __device__ __forceinline__ f32x2 await2(const Lookback &l, const uint64_t *p, ui
     }
 }
 
-// Whole-workgroup: the value that enters tile j, from `first` at the first one.
-// sh.A, sh.H hold the waves' pairs in the order of the pass (barrier done, epoch_end
-// done).  Publishes what later tiles read.
-__device__ __forceinline__ f32x2 enter(const Lookback &l, Shared &sh, uint32_t j, int64_t group, f32x2 first)
+// Whole-workgroup: the value that enters wave `pass` of tile j, from `first` at the
+// first one.  sh.A, sh.H hold the waves' pairs in the order of the pass (barrier and, with
+// MULTI, epoch_end done).  Publishes what later tiles read.
+template <bool MULTI>
+__device__ __forceinline__ f32x2 enter(const Lookback &l, Shared &sh, uint32_t j, uint32_t group, int pass, f32x2 first)
 {
-    const int lane = threadIdx.x & 63, wv = wave();
+    const int lane = threadIdx.x & 63;
     const uint32_t tag = sh.ticket[0], want = sh.ticket[1], limit = sh.ticket[2];
     const uint32_t unit = j / kUnit, at = j % kUnit;
     const bool closes = at == kUnit - 1;
     f32x2 TA = {1.0f, 1.0f}, TH = {0.0f, 0.0f};
-    if (wv == 0) {
+    if (pass == 0) {
 #pragma unroll
         for (int w = 0; w < kWaves; ++w) {
             const f32x2 A = sh.A[w][lane], H = sh.H[w][lane];
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                TH[v] = apply(A[v], H[v], TH[v]);
-                TA[v] = chain(TA[v], A[v]);
-            }
+            sh.A[w][lane] = TA;
+            sh.H[w][lane] = TH;
+            append(TA, TH, A, H);
         }
-        if (!closes && j + 1 < l.tiles) {
+        if (MULTI && !closes && j + 1 < l.tiles) {
             uint64_t *p = agg_at(l, j, group) + 2 * lane;
             publish2(p, tag, TA, l.local);
             publish2(p + kGroup, tag, TH, l.local);
         }
     }
-    if (wv <= static_cast<int>(at)) {
-        if (wv == 0) {
+    if (MULTI && pass <= static_cast<int>(at)) {
+        if (pass == 0) {
             sh.pH[0][lane] = unit == 0 ? first : await2(l, incl_at(l, unit - 1, group) + 2 * lane, want, limit);
         } else {
-            const uint64_t *p = agg_at(l, static_cast<int64_t>(unit) * kUnit + wv - 1, group) + 2 * lane;
-            sh.pA[wv][lane] = await2(l, p, want, limit);
-            sh.pH[wv][lane] = await2(l, p + kGroup, want, limit);
+            const uint64_t *p = agg_at(l, static_cast<int64_t>(unit) * kUnit + pass - 1, group) + 2 * lane;
+            sh.pA[pass][lane] = await2(l, p, want, limit);
+            sh.pH[pass][lane] = await2(l, p + kGroup, want, limit);
         }
     }
     __syncthreads();
-    f32x2 c = sh.pH[0][lane];
-    for (uint32_t q = 1; q <= at; ++q) {
-        const f32x2 A = sh.pA[q][lane], H = sh.pH[q][lane];
-#pragma unroll
-        for (int v = 0; v < 2; ++v) c[v] = apply(A[v], H[v], c[v]);
+    f32x2 c = first;
+    if constexpr (MULTI) {
+        c = sh.pH[0][lane];
+        for (uint32_t q = 1; q <= at; ++q) c = apply2(sh.pA[q][lane], sh.pH[q][lane], c);
+        if (pass == 0 && closes && j + 1 < l.tiles)
+            publish2(incl_at(l, unit, group) + 2 * lane, tag, apply2(TA, TH, c), l.local);
     }
-    if (wv == 0 && closes && j + 1 < l.tiles) {
-        f32x2 out;
-#pragma unroll
-        for (int v = 0; v < 2; ++v) out[v] = apply(TA[v], TH[v], c[v]);
-        publish2(incl_at(l, unit, group) + 2 * lane, tag, out, l.local);
-    }
-    return c;
+    return apply2(sh.A[pass][lane], sh.H[pass][lane], c);
 }
 
 struct GatedArgs {
@@ -288,221 +331,372 @@ __device__ __forceinline__ Place place(const GatedArgs &a)
     return p;
 }
 
-// Which of the wave's N steps from t0 on start a document
-template <int N> __device__ __forceinline__ uint64_t resets(const GatedArgs &a, const Place &p, int64_t t0)
+// A wave's steps
+struct Steps {
+    int64_t t0;
+    int all, live;     // of its N: inside T, inside the length
+    uint32_t fresh;    // the ones that start a document
+};
+
+template <int N> __device__ __forceinline__ Steps steps(const GatedArgs &a, const Place &p, int64_t t0)
 {
-    if (!a.reset) return 0;
-    const int lane = threadIdx.x & 63;
-    const bool in = lane < N && t0 + lane < p.n;
-    return __ballot(in && a.reset[p.b * a.T + t0 + lane] != 0);
+    static_assert(N <= 32, "a bit for each");
+    Steps w;
+    w.t0 = t0;
+    w.all = static_cast<int>(a.T - t0 < 0 ? 0 : a.T - t0 < N ? a.T - t0 : N);
+    w.live = static_cast<int>(p.n - t0 < 0 ? 0 : p.n - t0 < N ? p.n - t0 : N);
+    w.fresh = 0;
+    if (a.reset) {
+        const int lane = threadIdx.x & 63;
+        const uint8_t *from = a.reset + p.b * a.T + t0;
+        w.fresh = static_cast<uint32_t>(__ballot(lane < w.live && from[lane < w.live ? lane : 0] != 0));
+    }
+    return w;
 }
 
-template <typename T, bool PAIRS, bool MULTI>
-__global__ void __launch_bounds__(64 * kWaves) gated_fwd_kernel(GatedArgs a)
+// Whether all N steps of a tile from t on are live and none starts a document: a
+// workgroup takes one of two bodies by this
+template <int N> __device__ __forceinline__ bool plain_tile(const GatedArgs &a, const Place &p, int64_t t)
 {
-    constexpr int C = kFwdSteps;
-    __shared__ Shared sh;
-    const int lane = threadIdx.x & 63, wv = wave();
-    const Place p = place(a);
-    const int64_t t0 = static_cast<int64_t>(p.j) * kFwdTile + wv * C;
-    const T *x = static_cast<const T *>(a.x) + p.b * a.xs[0];
-    const T *r = static_cast<const T *>(a.r) + p.b * a.rs[0];
-    const T *in = static_cast<const T *>(a.i) + p.b * a.is[0];
+    static_assert(N % 64 == 0, "whole words of a wave");
+    if (t + N > p.n) return false;
+    if (!a.reset) return true;
+    const uint8_t *from = a.reset + p.b * a.T + t + (threadIdx.x & 63);
+    int any = 0;
+#pragma unroll
+    for (int i = 0; i < N; i += 64) any |= from[i];
+    return __ballot(any != 0) == 0;
+}
 
-    // steps past the length read the last live row again (nothing, where there is none)
-    f32x2 rx[C], rr[C], ri[C];
-    if (t0 < p.n) {
+// The wave's N rows of a (B,T,...) tensor; past the last live one, that one again
+// (p.n > 0)
+template <typename T, int N, bool PLAIN, typename L>
+__device__ __forceinline__ void rows(const void *base, const int64_t *stride, const Place &p, const Steps &w, const L &lane,
+                                     typename Two<T>::V *out)
+{
+    const int64_t step = stride[1] * static_cast<int64_t>(sizeof(T));
+    const int64_t t = PLAIN || w.live > 0 ? w.t0 : p.n - 1;
+    const char *row = static_cast<const char *>(base) + p.b * stride[0] * static_cast<int64_t>(sizeof(T)) + t * step;
 #pragma unroll
-        for (int s = 0; s < C; ++s) {
-            const int64_t t = t0 + s < p.n ? t0 + s : p.n - 1;
-            rx[s] = load2<T, PAIRS>(x + t * a.xs[1], p.c, p.d);
-            rr[s] = load2<T, PAIRS>(r + t * a.rs[1], p.c, p.d);
-            ri[s] = load2<T, PAIRS>(in + t * a.is[1], p.c, p.d);
-        }
-    } else {
-#pragma unroll
-        for (int s = 0; s < C; ++s) rx[s] = rr[s] = ri[s] = f32x2{0.0f, 0.0f};
+    for (int s = 0; s < N; ++s) {
+        out[s] = lane.load(row);
+        row += PLAIN || s + 1 < w.live ? step : 0;
     }
+}
+
+// The wave's rows of a dense output: f(step) of the live ones, zeros of the others
+template <typename T, int N, bool PLAIN, typename L, typename F>
+__device__ __forceinline__ void put_rows(void *base, const GatedArgs &a, const Place &p, const Steps &w, const L &lane, F f)
+{
+    const int64_t step = a.D * static_cast<int64_t>(sizeof(T));
+    char *row = static_cast<char *>(base) + (p.b * a.T + w.t0) * step;
+    if (!lane.in) return;
+#pragma unroll
+    for (int s = 0; s < N; ++s) {
+        if constexpr (PLAIN)
+            lane.store(row, f(s));
+        else if (s < w.all)
+            lane.store(row, s < w.live ? f(s) : f32x2{0.0f, 0.0f});
+        row += step;
+    }
+}
+
+// The channels' slope2 into LDS (a logarithm and two exponentials each: once per
+// workgroup, not once per wave)
+__device__ __forceinline__ void fill_slopes(const GatedArgs &a, const Place &p, Shared &sh)
+{
+    if (threadIdx.x < kGroup) {
+        const int64_t c = p.c - 2 * static_cast<int64_t>(threadIdx.x & 63) + threadIdx.x;
+        sh.k[threadIdx.x] = slope2(a.lam[c < a.D ? c : a.D - 1], a.rate);
+    }
+}
+
+// A tile that lies past its sequence's length: hands on what enters it, `from` (or
+// zeros) at the first one, and returns it
+template <bool MULTI>
+__device__ __forceinline__ f32x2 pass_on(const GatedArgs &a, const Place &p, Shared &sh, int pass, const float *from)
+{
+    const int lane = threadIdx.x & 63;
     Launch ep{0, 0};
     if constexpr (MULTI) ep = epoch_begin(a.l.hd);
-    f32x2 k = load_f2(a.lam, p.c, p.d), first = {0.0f, 0.0f};
-    if (a.h0) first = load_f2(a.h0 + p.b * a.D, p.c, p.d);
-#pragma unroll
-    for (int v = 0; v < 2; ++v) k[v] = slope(k[v], a.rate);
-    const uint64_t fresh = resets<C>(a, p, t0);
-
-    f32x2 ga[C], gb[C], A = {1.0f, 1.0f}, H = {0.0f, 0.0f};
-#pragma unroll
-    for (int s = 0; s < C; ++s) {
-        const bool live = t0 + s < p.n;
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            const Gate g = gate<T>(rx[s][v], rr[s][v], ri[s][v], k[v], (fresh >> s) & 1);
-            ga[s][v] = live ? g.a : 1.0f;
-            gb[s][v] = live ? g.b : 0.0f;
-            H[v] = apply(ga[s][v], gb[s][v], H[v]);
-            A[v] = chain(A[v], ga[s][v]);
-        }
-    }
-    sh.A[wv][lane] = A;
-    sh.H[wv][lane] = H;
+    f32x2 first = {0.0f, 0.0f};
+    if (from) first = load_f2(from + p.b * a.D, p.c, p.d);
+    sh.A[pass][lane] = f32x2{1.0f, 1.0f};
+    sh.H[pass][lane] = f32x2{0.0f, 0.0f};
     if (MULTI && threadIdx.x == 0) epoch_end(a.l.hd, ep, a.l.tiles * a.l.groups, sh.ticket);
     __syncthreads();
-    f32x2 h = first;
-    if constexpr (MULTI) h = enter(a.l, sh, p.j, p.group, first);
-    for (int w = 0; w < wv; ++w) {
-        const f32x2 wA = sh.A[w][lane], wH = sh.H[w][lane];
+    return enter<MULTI>(a.l, sh, p.j, p.group, pass, first);
+}
+
+// The pair of a wave's steps.  Steps past the length become the identity, the decays of
+// those that start a document -0.
+template <int N, bool PLAIN> __device__ __forceinline__ void fold(const Steps &w, f32x2 *ga, f32x2 *gb, f32x2 &A, f32x2 &H)
+{
 #pragma unroll
-        for (int v = 0; v < 2; ++v) h[v] = apply(wA[v], wH[v], h[v]);
+    for (int s = 0; s < N; ++s) {
+        if constexpr (PLAIN) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                H[v] = __builtin_fmaf(ga[s][v], H[v], gb[s][v]);
+                A[v] *= ga[s][v];
+            }
+            continue;
+        }
+        const bool live = s < w.live, fresh = (w.fresh >> s) & 1;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            ga[s][v] = live ? (fresh ? -0.0f : ga[s][v]) : 1.0f;
+            gb[s][v] = live ? gb[s][v] : 0.0f;
+        }
+        append(A, H, ga[s], gb[s]);
     }
-    if (a.states && t0 % MGS_GATED_CHUNK == 0 && t0 < a.T)
-        store_f2(a.states + (p.b * a.chunks + t0 / MGS_GATED_CHUNK) * a.D, p.c, p.d, h);
-    T *y = static_cast<T *>(a.y) + p.b * a.T * a.D;
+}
+
+template <typename T, bool PAIRS, bool MULTI, bool PLAIN>
+__device__ __forceinline__ void fwd_tile(const GatedArgs &a, const Place &p, Shared &sh)
+{
+    constexpr int C = kFwdSteps;
+    const int lane = threadIdx.x & 63, wv = wave();
+    const Lane<T, PAIRS> two(p.c, p.d);
+    const Steps w = steps<C>(a, p, static_cast<int64_t>(p.j) * kFwdTile + wv * C);
+    f32x2 h, ga[C], gb[C];
+    if (!PLAIN && static_cast<int64_t>(p.j) * kFwdTile >= p.n) {   // no step of the tile is live
+        h = pass_on<MULTI>(a, p, sh, wv, a.h0);
 #pragma unroll
-    for (int s = 0; s < C; ++s) {
+        for (int s = 0; s < C; ++s) {
+            ga[s] = f32x2{1.0f, 1.0f};
+            gb[s] = f32x2{0.0f, 0.0f};
+        }
+    } else {
+        typename Two<T>::V rx[C], rr[C], ri[C];
+        rows<T, C, PLAIN>(a.x, a.xs, p, w, two, rx);
+        rows<T, C, PLAIN>(a.r, a.rs, p, w, two, rr);
+        rows<T, C, PLAIN>(a.i, a.is, p, w, two, ri);
+        Launch ep{0, 0};
+        if constexpr (MULTI) ep = epoch_begin(a.l.hd);
+        f32x2 first = {0.0f, 0.0f};
+        if (a.h0) first = load_f2(a.h0 + p.b * a.D, p.c, p.d);
+        fill_slopes(a, p, sh);
+        __syncthreads();
+        const f32x2 k = {sh.k[2 * lane], sh.k[2 * lane + 1]};
+        f32x2 A = {1.0f, 1.0f}, H = {0.0f, 0.0f};
 #pragma unroll
-        for (int v = 0; v < 2; ++v) h[v] = apply(ga[s][v], gb[s][v], h[v]);
-        if (t0 + s < a.T)
-            store2<T, PAIRS>(y + (t0 + s) * a.D, p.c, p.d, t0 + s < p.n ? h : f32x2{0.0f, 0.0f});
+        for (int s = 0; s < C; ++s) {
+            const f32x2 x = wide(rx[s]), r = wide(rr[s]), i = wide(ri[s]);
+            const float start = !PLAIN && (w.fresh >> s) & 1 ? -__builtin_inff() : 0.0f;
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const Gate g = gate<T>(x[v], r[v], i[v], k[v], start);
+                ga[s][v] = g.a;
+                gb[s][v] = g.b;
+            }
+            settle(ga[s]);
+            settle(gb[s]);
+        }
+        fold<C, PLAIN>(w, ga, gb, A, H);
+        sh.A[wv][lane] = A;
+        sh.H[wv][lane] = H;
+        if (MULTI && threadIdx.x == 0) epoch_end(a.l.hd, ep, a.l.tiles * a.l.groups, sh.ticket);
+        __syncthreads();
+        h = enter<MULTI>(a.l, sh, p.j, p.group, wv, first);
     }
+    if (a.states && w.t0 % MGS_GATED_CHUNK == 0 && (PLAIN || w.t0 < a.T))
+        store_f2(a.states + (p.b * a.chunks + w.t0 / MGS_GATED_CHUNK) * a.D, p.c, p.d, h);
+    put_rows<T, C, PLAIN>(a.y, a, p, w, two, [&](int s) {
+        if constexpr (PLAIN) {
+#pragma unroll
+            for (int v = 0; v < 2; ++v) h[v] = __builtin_fmaf(ga[s][v], h[v], gb[s][v]);
+        } else {
+            h = apply2(ga[s], gb[s], h);
+        }
+        return h;
+    });
+    // (steps past the length leave it as it is)
     if (a.hT && p.j + 1 == a.l.tiles && wv == kWaves - 1) store_f2(a.hT + p.b * a.D, p.c, p.d, h);
 }
 
 template <typename T, bool PAIRS, bool MULTI>
-__global__ void __launch_bounds__(64 * kWaves) gated_bwd_kernel(GatedArgs a)
+__global__ void __launch_bounds__(64 * kWaves, kFwdOccupancy) gated_fwd_kernel(GatedArgs a)
+{
+    __shared__ Shared sh;
+    const Place p = place(a);
+    if (plain_tile<kFwdTile>(a, p, static_cast<int64_t>(p.j) * kFwdTile))
+        fwd_tile<T, PAIRS, MULTI, true>(a, p, sh);
+    else
+        fwd_tile<T, PAIRS, MULTI, false>(a, p, sh);
+}
+
+// One step of the backward from its inputs
+struct Slopes {
+    float a, b;
+    float x, i;    // d b / d x, d b / d i
+    float l;       // -d b / d log a: iota x a^2 / beta
+};
+
+template <typename T> __device__ __forceinline__ Slopes slopes(float x, float r, float i, float k, float start)
+{
+    const float rho = rcp(1.0f + exp_neg<T>(r)), ei = exp_neg<T>(i), iota = rcp(1.0f + ei);
+    Slopes o;
+    float beta2;
+    decay(__builtin_fmaf(k, rho, start), o.a, beta2);
+    // 1 / beta; 1 - a^2 below the smallest normal number counts as 0
+    const float inv = beta2 < 0x1p-126f ? 0.0f : __builtin_amdgcn_rsqf(beta2), ix = iota * x;
+    o.x = beta2 * inv * iota;
+    o.b = o.x * x;
+    o.i = o.b * shut(ei, iota);
+    o.l = ix * (o.a * o.a) * inv;
+    return o;
+}
+
+// A tile's sums of dl rho, for dlam
+__device__ __forceinline__ void put_part(const GatedArgs &a, const Place &p, int64_t tile, uint32_t tag, f32x2 sum)
+{
+    uint64_t *o = a.part + (p.b * a.l.tiles + tile) * a.D;
+#pragma unroll
+    for (int v = 0; v < 2; ++v)
+        if (p.c + v < p.d) o[p.c + v] = (static_cast<uint64_t>(tag) << 32) | __float_as_uint(sum[v]);
+}
+
+struct BwdShared {
+    Shared s;
+    f32x2 F[2][kWaves][64];   // the waves' pairs of the forward; then (second) the state ahead of each
+    f32x2 sum[kWaves][64];
+};
+
+template <typename T, bool PAIRS, bool MULTI, bool PLAIN>
+__device__ __forceinline__ void bwd_tile(const GatedArgs &a, const Place &p, int64_t tile, BwdShared &sh)
 {
     constexpr int C = kBwdSteps;
-    __shared__ Shared sh;
-    __shared__ f32x2 sF[2][kWaves][64];   // the waves' pairs of the forward; later their sums of dl rho
     const int lane = threadIdx.x & 63;
     const int pass = wave(), wv = kWaves - 1 - pass;   // in the order of the pass, and of the steps
-    const Place p = place(a);
-    const int64_t tile = static_cast<int64_t>(a.l.tiles) - 1 - p.j;
-    const int64_t t0 = tile * kBwdTile + wv * C;
-    const T *x = static_cast<const T *>(a.x) + p.b * a.xs[0];
-    const T *r = static_cast<const T *>(a.r) + p.b * a.rs[0];
-    const T *in = static_cast<const T *>(a.i) + p.b * a.is[0];
-    const T *dy = static_cast<const T *>(a.dy) + p.b * a.gs[0];
-
-    f32x2 rx[C], rr[C], ri[C], g[C];
-    if (t0 < p.n) {
-#pragma unroll
-        for (int s = 0; s < C; ++s) {
-            const int64_t t = t0 + s < p.n ? t0 + s : p.n - 1;
-            rx[s] = load2<T, PAIRS>(x + t * a.xs[1], p.c, p.d);
-            rr[s] = load2<T, PAIRS>(r + t * a.rs[1], p.c, p.d);
-            ri[s] = load2<T, PAIRS>(in + t * a.is[1], p.c, p.d);
-            g[s] = load2<T, PAIRS>(dy + t * a.gs[1], p.c, p.d);
-        }
-    } else {
-#pragma unroll
-        for (int s = 0; s < C; ++s) rx[s] = rr[s] = ri[s] = g[s] = f32x2{0.0f, 0.0f};
+    const Lane<T, PAIRS> two(p.c, p.d);
+    const Steps w = steps<C>(a, p, tile * kBwdTile + wv * C);
+    if (!PLAIN && tile * kBwdTile >= p.n) {   // no step of the tile is live
+        const f32x2 K = pass_on<MULTI>(a, p, sh.s, pass, a.dhT);
+        for (void *o : {a.dx, a.dr, a.di})
+            put_rows<T, C, false>(o, a, p, w, two, [](int) { return f32x2{0.0f, 0.0f}; });
+        if (a.dh0 && tile == 0 && wv == 0) store_f2(a.dh0 + p.b * a.D, p.c, p.d, K);
+        if (wv == 0) put_part(a, p, tile, MULTI ? sh.s.ticket[0] : 0, f32x2{0.0f, 0.0f});
+        return;
     }
+    typename Two<T>::V rx[C], rr[C], ri[C], rg[C];
+    rows<T, C, PLAIN>(a.x, a.xs, p, w, two, rx);
+    rows<T, C, PLAIN>(a.r, a.rs, p, w, two, rr);
+    rows<T, C, PLAIN>(a.i, a.is, p, w, two, ri);
+    rows<T, C, PLAIN>(a.dy, a.gs, p, w, two, rg);
     Launch ep{0, 0};
     if constexpr (MULTI) ep = epoch_begin(a.l.hd);
-    f32x2 k = load_f2(a.lam, p.c, p.d), first = {0.0f, 0.0f}, h = {0.0f, 0.0f};
+    f32x2 first = {0.0f, 0.0f}, state = {0.0f, 0.0f};
     if (a.dhT) first = load_f2(a.dhT + p.b * a.D, p.c, p.d);
-    if (tile * kBwdTile < a.T)
-        h = load_f2(a.states + (p.b * a.chunks + tile * (kBwdTile / MGS_GATED_CHUNK)) * a.D, p.c, p.d);
-#pragma unroll
-    for (int v = 0; v < 2; ++v) k[v] = slope(k[v], a.rate);
-    const uint64_t fresh = resets<C>(a, p, t0);
+    if (pass == 1)
+        state = load_f2(a.states + (p.b * a.chunks + tile * (kBwdTile / MGS_GATED_CHUNK)) * a.D, p.c, p.d);
+    fill_slopes(a, p, sh.s);
+    __syncthreads();
+    const f32x2 k = {sh.s.k[2 * lane], sh.s.k[2 * lane + 1]};
 
-    // Per step: the decay, and what G multiplies: m1 -> dx, m2 -> di, and for dl rho
-    // first iota x a^2 / beta, then (a h_{t-1} - that) rho
-    f32x2 ga[C], gb[C], m1[C], m2[C], w[C], rho[C], late[C];
-    f32x2 A = {1.0f, 1.0f}, H = {0.0f, 0.0f}, K = {0.0f, 0.0f};
+    // Per step: the decay, and what G multiplies: m1 -> dx, m2 -> di, m3 -> dl (first
+    // what is subtracted there).  b = m1 x
+    f32x2 ga[C], m1[C], m2[C], m3[C], A = {1.0f, 1.0f}, H = {0.0f, 0.0f}, K = {0.0f, 0.0f};
 #pragma unroll
     for (int s = 0; s < C; ++s) {
-        const bool live = t0 + s < p.n, fr = (fresh >> s) & 1;
+        const f32x2 x = wide(rx[s]), r = wide(rr[s]), i = wide(ri[s]);
+        const bool live = PLAIN || s < w.live, fresh = !PLAIN && (w.fresh >> s) & 1;
+        const float start = fresh ? -__builtin_inff() : 0.0f;
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-            const float er = exp_neg<T>(rr[s][v]), ei = exp_neg<T>(ri[s][v]);
-            const float rh = rcp(1.0f + er), io = rcp(1.0f + ei);
-            float da, beta2;
-            decay(k[v] * rh, da, beta2);
-            const float beta = fr ? 1.0f : __builtin_amdgcn_sqrtf(beta2);
-            const float ix = io * rx[s][v];
-            const float b = beta * ix;
-            ga[s][v] = live ? (fr ? -0.0f : da) : 1.0f;
-            gb[s][v] = live ? b : 0.0f;
-            m1[s][v] = beta * io;
-            m2[s][v] = b * shut(ei, io);
-            w[s][v] = fr || beta == 0.0f ? 0.0f : ix * (da * da) * rcp(beta);
-            rho[s][v] = rh;
-            late[s][v] = shut(er, rh);
-            if (!live) g[s][v] = 0.0f;
-            H[v] = apply(ga[s][v], gb[s][v], H[v]);
-            A[v] = chain(A[v], ga[s][v]);
+            const Slopes o = slopes<T>(x[v], r[v], i[v], k[v], start);
+            ga[s][v] = !live ? 1.0f : fresh ? -0.0f : o.a;
+            m1[s][v] = o.x;
+            m2[s][v] = o.i;
+            m3[s][v] = o.l;
+            const float b = live ? o.b : 0.0f;
+            H[v] = PLAIN ? __builtin_fmaf(ga[s][v], H[v], b) : apply(ga[s][v], b, H[v]);
+            A[v] = PLAIN ? A[v] * ga[s][v] : chain(A[v], ga[s][v]);
         }
+        settle(ga[s]);
+        settle(m1[s]);
+        settle(m2[s]);
+        settle(m3[s]);
     }
-    sF[0][wv][lane] = A;
-    sF[1][wv][lane] = H;
-#pragma unroll
-    for (int s = C - 1; s >= 0; --s)
-#pragma unroll
-        for (int v = 0; v < 2; ++v) K[v] = clears(ga[s][v]) ? 0.0f : ga[s][v] * (g[s][v] + K[v]);
-    sh.A[pass][lane] = A;
-    sh.H[pass][lane] = K;
-    if (MULTI && threadIdx.x == 0) epoch_end(a.l.hd, ep, a.l.tiles * a.l.groups, sh.ticket);
-    __syncthreads();
-    for (int q = 0; q < wv; ++q) {
-        const f32x2 wA = sF[0][q][lane], wH = sF[1][q][lane];
-#pragma unroll
-        for (int v = 0; v < 2; ++v) h[v] = apply(wA[v], wH[v], h[v]);
-    }
-#pragma unroll
-    for (int s = 0; s < C; ++s)
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            const bool clear = clears(ga[s][v]);
-            const float ah = clear ? 0.0f : ga[s][v] * h[v];
-            w[s][v] = clear ? 0.0f : (ah - w[s][v]) * rho[s][v];
-            h[v] = ah + gb[s][v];
-        }
-    K = first;
-    if constexpr (MULTI) K = enter(a.l, sh, p.j, p.group, first);
-    for (int q = 0; q < pass; ++q) {
-        const f32x2 wA = sh.A[q][lane], wK = sh.H[q][lane];
-#pragma unroll
-        for (int v = 0; v < 2; ++v) K[v] = apply(wA[v], wK[v], K[v]);
-    }
-    T *dx = static_cast<T *>(a.dx) + p.b * a.T * a.D, *dr = static_cast<T *>(a.dr) + p.b * a.T * a.D;
-    T *di = static_cast<T *>(a.di) + p.b * a.T * a.D;
-    f32x2 sum = {0.0f, 0.0f};
+    // G times the decay, or nothing where that clears
+    auto back = [&](float decay, float G) { return !PLAIN && clears(decay) ? 0.0f : decay * G; };
 #pragma unroll
     for (int s = C - 1; s >= 0; --s) {
-        f32x2 ox, orr, oi;
-        const bool live = t0 + s < p.n;
+        const f32x2 g = again(rg[s]);
+#pragma unroll
+        for (int v = 0; v < 2; ++v) K[v] = back(ga[s][v], (PLAIN || s < w.live ? g[v] : 0.0f) + K[v]);
+    }
+    sh.F[0][wv][lane] = A;
+    sh.F[1][wv][lane] = H;
+    sh.s.A[pass][lane] = A;
+    sh.s.H[pass][lane] = K;
+    if (MULTI && threadIdx.x == 0) epoch_end(a.l.hd, ep, a.l.tiles * a.l.groups, sh.s.ticket);
+    __syncthreads();
+    if (pass == 1) {
+#pragma unroll
+        for (int q = 0; q < kWaves; ++q) {
+            const f32x2 fA = sh.F[0][q][lane], fH = sh.F[1][q][lane];
+            sh.F[1][q][lane] = state;
+            state = apply2(fA, fH, state);
+        }
+    }
+    K = enter<MULTI>(a.l, sh.s, p.j, p.group, pass, first);
+    f32x2 h = sh.F[1][wv][lane], sum = {0.0f, 0.0f};
+#pragma unroll
+    for (int s = 0; s < C; ++s) {
+        const f32x2 x = again(rx[s]);
 #pragma unroll
         for (int v = 0; v < 2; ++v) {
-            const float G = g[s][v] + K[v];
-            const float dl = G * w[s][v];
-            ox[v] = live ? G * m1[s][v] : 0.0f;
-            oi[v] = live ? G * m2[s][v] : 0.0f;
-            orr[v] = live ? dl * k[v] * late[s][v] : 0.0f;
-            sum[v] += live ? dl : 0.0f;
-            K[v] = clears(ga[s][v]) ? 0.0f : ga[s][v] * G;
-        }
-        if (t0 + s < a.T) {
-            store2<T, PAIRS>(dx + (t0 + s) * a.D, p.c, p.d, ox);
-            store2<T, PAIRS>(dr + (t0 + s) * a.D, p.c, p.d, orr);
-            store2<T, PAIRS>(di + (t0 + s) * a.D, p.c, p.d, oi);
+            const float b = PLAIN || s < w.live ? m1[s][v] * x[v] : 0.0f;
+            if constexpr (PLAIN) {
+                m3[s][v] = __builtin_fmaf(ga[s][v], h[v], -m3[s][v]);
+                h[v] = __builtin_fmaf(ga[s][v], h[v], b);
+            } else {
+                const float ah = back(ga[s][v], h[v]);
+                m3[s][v] = ah - m3[s][v];
+                h[v] = ah + b;
+            }
         }
     }
+    const f32x2 kn = k * 0.6931471805599453f;   // log a = kn rho
+#pragma unroll
+    for (int s = C - 1; s >= 0; --s) {
+        const f32x2 g = again(rg[s]), r = again(rr[s]);
+        const bool live = PLAIN || s < w.live;
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            const bool clear = !PLAIN && clears(ga[s][v]);
+            const float er = exp_neg<T>(r[v]), rho = rcp(1.0f + er);
+            const float G = (live ? g[v] : 0.0f) + K[v], dl = clear ? 0.0f : G * m3[s][v] * rho;   // (dl rho)
+            m1[s][v] *= G;
+            m2[s][v] *= G;
+            m3[s][v] = clear ? 0.0f : dl * kn[v] * shut(er, rho);
+            sum[v] += live ? dl : 0.0f;
+            K[v] = back(ga[s][v], G);
+        }
+    }
+    put_rows<T, C, PLAIN>(a.dx, a, p, w, two, [&](int s) { return m1[s]; });
+    put_rows<T, C, PLAIN>(a.dr, a, p, w, two, [&](int s) { return m3[s]; });
+    put_rows<T, C, PLAIN>(a.di, a, p, w, two, [&](int s) { return m2[s]; });
     if (a.dh0 && tile == 0 && wv == 0) store_f2(a.dh0 + p.b * a.D, p.c, p.d, K);
-    __syncthreads();
-    sF[0][wv][lane] = sum;
+    sh.sum[wv][lane] = sum;
     __syncthreads();
     if (wv == 0) {
-        for (int q = 1; q < kWaves; ++q) sum += sF[0][q][lane];
-        uint64_t *o = a.part + (p.b * a.l.tiles + tile) * a.D;
-        const uint32_t tag = MULTI ? sh.ticket[0] : 0;   // (never the tag of a later launch)
-#pragma unroll
-        for (int v = 0; v < 2; ++v)
-            if (p.c + v < p.d)
-                o[p.c + v] = (static_cast<uint64_t>(tag) << 32) | __float_as_uint(sum[v]);
+        for (int q = 1; q < kWaves; ++q) sum += sh.sum[q][lane];
+        put_part(a, p, tile, MULTI ? sh.s.ticket[0] : 0, sum);   // (0: never the tag of a later launch)
     }
+}
+
+template <typename T, bool PAIRS, bool MULTI>
+__global__ void __launch_bounds__(64 * kWaves, kBwdOccupancy) gated_bwd_kernel(GatedArgs a)
+{
+    __shared__ BwdShared sh;
+    const Place p = place(a);
+    const int64_t tile = static_cast<int64_t>(a.l.tiles) - 1 - p.j;
+    if (plain_tile<kBwdTile>(a, p, tile * kBwdTile))
+        bwd_tile<T, PAIRS, MULTI, true>(a, p, tile, sh);
+    else
+        bwd_tile<T, PAIRS, MULTI, false>(a, p, tile, sh);
 }
 
 // dlam: the partial sums of a channel in order, in fp64, over 16 waves' shares
@@ -540,25 +734,27 @@ template <typename T, bool PAIRS> __global__ void __launch_bounds__(256) gated_s
     const int64_t at = a.first + blockIdx.x, b = at / a.blocks_per_row;
     const int c = static_cast<int>(at - b * a.blocks_per_row) * 512 + 2 * threadIdx.x, d = static_cast<int>(a.D);
     if (c >= d) return;
+    const Lane<T, PAIRS> two(c, d);
     const int64_t slot = a.slots ? a.slots[b] : b;
-    T *y = static_cast<T *>(a.y) + b * a.D;
+    char *y = static_cast<char *>(a.y) + b * a.D * static_cast<int64_t>(sizeof(T));
     if (slot < 0 || slot >= a.n_slots) {
-        store2<T, PAIRS>(y, c, d, f32x2{0.0f, 0.0f});
+        two.store(y, f32x2{0.0f, 0.0f});
         return;
     }
-    const f32x2 x = load2<T, PAIRS>(static_cast<const T *>(a.x) + b * a.xs, c, d);
-    const f32x2 r = load2<T, PAIRS>(static_cast<const T *>(a.r) + b * a.rs, c, d);
-    const f32x2 i = load2<T, PAIRS>(static_cast<const T *>(a.i) + b * a.is, c, d);
+    auto row = [&](const void *p, int64_t stride) {
+        return wide(two.load(static_cast<const char *>(p) + b * stride * static_cast<int64_t>(sizeof(T))));
+    };
+    const f32x2 x = row(a.x, a.xs), r = row(a.r, a.rs), i = row(a.i, a.is);
     const f32x2 lam = load_f2(a.lam, c, d);
-    float *row = a.h + slot * a.D;
-    f32x2 h = load_f2(row, c, d);
+    float *state = a.h + slot * a.D;
+    f32x2 h = load_f2(state, c, d);
 #pragma unroll
     for (int v = 0; v < 2; ++v) {
-        const Gate g = gate<T>(x[v], r[v], i[v], slope(lam[v], a.rate), false);
+        const Gate g = gate<T>(x[v], r[v], i[v], slope2(lam[v], a.rate), 0.0f);
         h[v] = __builtin_fmaf(g.a, h[v], g.b);
     }
-    store_f2(row, c, d, h);
-    store2<T, PAIRS>(y, c, d, h);
+    store_f2(state, c, d, h);
+    two.store(y, h);
 }
 
 bool even(const int64_t *st, int n)
