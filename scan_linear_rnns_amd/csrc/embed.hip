@@ -78,20 +78,33 @@ struct LookupArgs {
     bool wide_ids, vec;
 };
 
-// `slabs` threads share a row
+// `slabs` threads share a row, and take kRows of them, their loads in flight together
+// (32768 rows of 2048, bf16: one row each 45 us)
+constexpr int kRows = 4;
+
 template <typename T> __global__ void __launch_bounds__(256) lookup_kernel(LookupArgs a)
 {
-    const int sub = threadIdx.x / a.slabs, t = threadIdx.x % a.slabs;
-    const int64_t n = (a.first + blockIdx.x) * (256 / a.slabs) + sub;
-    if (n >= a.n) return;
-    const int64_t id = id_at(a.ids, a.wide_ids, n);
-    const bool in = id >= 0 && id < a.vocab;
-    const T *row = static_cast<const T *>(a.W) + (in ? id : 0) * a.ws;
-    T *y = static_cast<T *>(a.y) + n * a.d;
+    const int per = 256 / a.slabs, sub = threadIdx.x / a.slabs, t = threadIdx.x % a.slabs;
+    const int64_t n0 = (a.first + blockIdx.x) * (per * kRows) + sub;
+    int64_t id[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+        const int64_t n = n0 + k * per;
+        id[k] = n < a.n ? id_at(a.ids, a.wide_ids, n) : -1;
+    }
     for (int64_t c = 8 * t; c < a.d; c += 8 * a.slabs) {
-        f8v v = {0, 0, 0, 0, 0, 0, 0, 0};
-        if (in) v = a.scale * load8(row, c, a.d, a.vec);
-        store8(y, c, a.d, a.vec, v);
+        f8v v[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            v[k] = f8v{0, 0, 0, 0, 0, 0, 0, 0};
+            if (id[k] >= 0 && id[k] < a.vocab)
+                v[k] = load8(static_cast<const T *>(a.W) + id[k] * a.ws, c, a.d, a.vec);
+        }
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const int64_t n = n0 + k * per;
+            if (n < a.n) store8(static_cast<T *>(a.y) + n * a.d, c, a.d, a.vec, a.scale * v[k]);
+        }
     }
 }
 
@@ -108,15 +121,35 @@ struct SortArgs {
     int64_t row_bytes;
 };
 
+// f(id, place) for the wave's places n0..n1-1, lane by lane, several loads in flight.  Ids
+// outside the table are -1, and so are places past the end (the wave stays whole)
+template <typename F> __device__ __forceinline__ void each_id(const SortArgs &a, int64_t n0, int64_t n1, F f)
+{
+    constexpr int kBatch = 8;
+    const int lane = threadIdx.x & 63;
+    for (int64_t n = n0; n < n1; n += 64 * kBatch) {
+        int64_t id[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            const int64_t at = n + 64 * k + lane;
+            id[k] = id_at(a.ids, a.wide_ids, at < n1 ? at : n1 - 1);
+            if (at >= n1 || id[k] < 0 || id[k] >= a.vocab) id[k] = -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) f(static_cast<int32_t>(id[k]), n + 64 * k + lane);
+    }
+}
+
 // Each wave takes an equal share of the places and counts its ids of the range in a
 // row of its own, so the second pass places them in order without a barrier.
 __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
 {
     __shared__ int32_t at[kSortWaves * kMaxRange];   // [wave][local id]: counts, then next places
+    __shared__ int32_t starts[kMaxRange];
     __shared__ int64_t below[kSortWaves];
     __shared__ int32_t scan[kSortWaves];
     const int lane = threadIdx.x & 63, wv = wave();
-    const int64_t lo = static_cast<int64_t>(blockIdx.x) * a.range;
+    const int32_t lo = static_cast<int32_t>(static_cast<int64_t>(blockIdx.x) * a.range);
     const int ids = static_cast<int>(a.vocab - lo < a.range ? a.vocab - lo : a.range);
     for (int i = threadIdx.x; i < kSortWaves * a.range; i += 64 * kSortWaves) at[i] = 0;
     __syncthreads();
@@ -124,21 +157,20 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
     const int64_t n0 = wv * share, n1 = n0 + share < a.n ? n0 + share : a.n;
     volatile int32_t *mine = at + wv * a.range;   // (its wave's lanes share it without barriers)
     int64_t smaller = 0;
-    for (int64_t n = n0 + lane; n < n1; n += 64) {
-        const int64_t id = id_at(a.ids, a.wide_ids, n);
+    each_id(a, n0, n1, [&](int32_t id, int64_t) {
         if (id >= 0 && id < lo) ++smaller;
-        if (id >= lo && id < lo + ids) atomicAdd(&at[wv * a.range + (id - lo)], 1);
-    }
+        if (id >= lo && id - lo < ids) atomicAdd(&at[wv * a.range + (id - lo)], 1);
+    });
     for (int off = 32; off; off >>= 1) smaller += __shfl_xor(smaller, off, 64);
     if (lane == 0) below[wv] = smaller;
     __syncthreads();
     int64_t base = 0;
     for (int w = 0; w < kSortWaves; ++w) base += below[w];
-    // exclusive sums over (id, wave): a thread takes neighbouring ids
-    const int per = (a.range + 64 * kSortWaves - 1) / (64 * kSortWaves);
-    const int i0 = threadIdx.x * per, i1 = i0 + per < ids ? i0 + per : ids;
+    // exclusive sums over (id, wave): a thread for each id
+    static_assert(kMaxRange <= 64 * kSortWaves, "a thread for each id");
+    const int i = threadIdx.x;
     int32_t sum = 0;
-    for (int i = i0; i < i1; ++i)
+    if (i < ids)
         for (int w = 0; w < kSortWaves; ++w) sum += at[w * a.range + i];
     int32_t before = sum;   // of the threads up to this one
     for (int off = 1; off < 64; off <<= 1) {
@@ -149,8 +181,9 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
     before -= sum;
     __syncthreads();
     for (int w = 0; w < wv; ++w) before += scan[w];
-    int32_t next = static_cast<int32_t>(base) + before;
-    for (int i = i0; i < i1; ++i) {
+    if (i < ids) {
+        int32_t next = static_cast<int32_t>(base) + before;
+        starts[i] = sum ? next : -1;   // -1: no place has this id
         a.first[lo + i] = next;
         for (int w = 0; w < kSortWaves; ++w) {
             const int32_t c = at[w * a.range + i];
@@ -163,9 +196,8 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
         }
     }
     __syncthreads();
-    for (int64_t n = n0 + lane; n - lane < n1; n += 64) {
-        const int64_t id = n < n1 ? id_at(a.ids, a.wide_ids, n) : -1;
-        int local = id >= lo && id < lo + ids ? static_cast<int>(id - lo) : -1;
+    each_id(a, n0, n1, [&](int32_t id, int64_t n) {
+        const int local = id >= lo && id - lo < ids ? id - lo : -1;
         // one round for each id among the lanes: its lanes in order
         for (uint64_t left = __ballot(local >= 0); left;) {
             const int now = __builtin_amdgcn_readlane(local, __builtin_ctzll(left));
@@ -174,18 +206,17 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
             if (local == now) {
                 const int32_t place = start + __popcll(same & ((1ull << lane) - 1));
                 a.row[place] = static_cast<int32_t>(n);
-                a.id[place] = static_cast<int32_t>(id);
+                a.id[place] = id;
             }
             if (lane == 0) mine[now] = start + __popcll(same);
             left &= ~same;
         }
-    }
+    });
     if (!a.clear) return;
-    __syncthreads();
-    // rows of no id: the last wave's next place is still the first one
-    for (int i = wv; i < ids; i += kSortWaves) {
-        if (at[(kSortWaves - 1) * a.range + i] != a.first[lo + i]) continue;
-        char *row = a.dW + (lo + i) * a.row_bytes;
+    // rows of no id
+    for (int k = wv; k < ids; k += kSortWaves) {
+        if (starts[k] >= 0) continue;
+        char *row = a.dW + (static_cast<int64_t>(lo) + k) * a.row_bytes;
         const int64_t head = (16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15;
         const int64_t wide = head < a.row_bytes ? (a.row_bytes - head) / 16 : 0;
         for (int64_t o = lane; o < wide; o += 64) {
@@ -226,30 +257,47 @@ __device__ __forceinline__ f8v *partial(const SumArgs &a, int64_t chunk, int whi
     return reinterpret_cast<f8v *>(a.part + (chunk * 2 + which) * width + c);
 }
 
-// `slabs` threads walk a chunk, 8 columns each
+// `slabs` threads walk a chunk, 8 columns each, eight rows in flight
 template <typename T, typename D> __global__ void __launch_bounds__(256) sum_kernel(SumArgs a)
 {
+    constexpr int kAhead = 8;
+    static_assert(kChunk % kAhead == 0, "whole batches");
     const int sub = threadIdx.x / a.slabs, t = threadIdx.x % a.slabs;
     const int64_t chunk = (a.block + blockIdx.x) * (256 / a.slabs) + sub, total = *a.count;
     const int64_t k0 = chunk * kChunk, k1 = k0 + kChunk < total ? k0 + kChunk : total;
     if (k0 >= k1) return;
+    const bool entered = k0 > 0 && a.id[k0 - 1] == a.id[k0];
     for (int64_t c = 8 * (t + static_cast<int64_t>(blockIdx.y) * a.slabs); c < a.d;
          c += 8 * static_cast<int64_t>(a.slabs) * gridDim.y) {
         f8v sum = {0, 0, 0, 0, 0, 0, 0, 0};
-        bool entered = k0 > 0 && a.id[k0 - 1] == a.id[k0];
-        for (int64_t k = k0; k < k1; ++k) {
-            const int32_t id = a.id[k];
-            sum += load8(static_cast<const T *>(a.dy) + a.row[k] * a.gs, c, a.d, a.vec_in);
-            const bool ends = k + 1 == total || a.id[k + 1] != id;
-            if (!ends && k + 1 < k1) continue;
-            if (entered)
-                *partial(a, chunk, 0, c) = sum;
-            else if (ends)
-                put<D>(a, id, c, sum);
-            else
-                *partial(a, chunk, 1, c) = sum;
-            entered = false;
-            sum = f8v{0, 0, 0, 0, 0, 0, 0, 0};
+        bool inside = entered;   // in the run that enters the chunk
+        for (int64_t k = k0; k < k1; k += kAhead) {
+            int32_t id[kAhead + 1], row[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                row[j] = a.row[k + j < k1 ? k + j : k1 - 1];
+                id[j] = a.id[k + j < k1 ? k + j : k1 - 1];
+            }
+            id[kAhead] = k + kAhead < total ? a.id[k + kAhead] : -1;
+            f8v v[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                v[j] = load8(static_cast<const T *>(a.dy) + row[j] * a.gs, c, a.d, a.vec_in);
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                if (k + j >= k1) break;
+                sum += v[j];
+                const bool ends = k + j + 1 == total || id[j + 1] != id[j];
+                if (!ends && k + j + 1 < k1) continue;
+                if (inside)
+                    *partial(a, chunk, 0, c) = sum;
+                else if (ends)
+                    put<D>(a, id[j], c, sum);
+                else
+                    *partial(a, chunk, 1, c) = sum;
+                inside = false;
+                sum = f8v{0, 0, 0, 0, 0, 0, 0, 0};
+            }
         }
     }
 }
@@ -336,7 +384,7 @@ hipError_t launch_embed_fwd(const void *ids, bool wide_ids, const void *W, void 
     const int size = dtype == MGS_BF16 ? 2 : 4;
     LookupArgs a{ids, W, y, 0, n, vocab, d, w_stride, slabs_of(d), scale, wide_ids,
                  whole8(W, d, w_stride, size) && whole8(y, d, d, size)};
-    const int per = 256 / a.slabs;
+    const int per = 256 / a.slabs * kRows;
     return launch_sliced((n + per - 1) / per, 256, [&](int64_t first, unsigned blocks) {
         a.first = first;
         if (dtype == MGS_BF16) lookup_kernel<__bf16><<<dim3(blocks), dim3(256), 0, s>>>(a);

@@ -29,15 +29,23 @@ namespace mgs {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kWaves = 8;                // per workgroup
 constexpr int kGroup = 128;              // channels of a workgroup
-constexpr int kFwdSteps = 16, kBwdSteps = 8;   // of a wave
-constexpr int kFwdOccupancy = 4, kBwdOccupancy = 4;   // waves of a SIMD
 constexpr int kUnit = 8;                 // tiles whose pairs a tile reads at most
-static_assert(kUnit <= kWaves, "each wave polls one tile");
-constexpr int kFwdTile = kWaves * kFwdSteps, kBwdTile = kWaves * kBwdSteps;
-static_assert(kFwdTile % MGS_GATED_CHUNK == 0 && kBwdTile % MGS_GATED_CHUNK == 0, "a tile starts at a saved state");
-static_assert(MGS_GATED_CHUNK % kFwdSteps == 0, "a wave saves the state ahead of it");
+// Waves of a workgroup, steps of a wave, and how many waves share a SIMD
+template <int WAVES, int STEPS, int OCCUPANCY> struct Shape {
+    static constexpr int W = WAVES, C = STEPS, occupancy = OCCUPANCY, tile = W * C;
+    static_assert(kUnit <= W, "each wave polls one tile");
+    static_assert(tile % MGS_GATED_CHUNK == 0, "a tile starts at a saved state");
+    static_assert(MGS_GATED_CHUNK % C == 0, "a wave saves the state ahead of it");
+};
+// Measured (us at 4 x 4096 x 4096, bf16, and 16 x 1024 x 1000, fp32).  Forward 8 waves
+// of 16 steps: 118 and 60; of 8 steps: 130 and 59 (and 74 against 57 on a ragged prompt);
+// 16 waves of 8: 162 and 74.  Backward 8 waves of 8 steps, 128 registers (the fp32 one
+// would spill, and takes 157, two waves a SIMD): 237 and 131; fp32 with 128: 141; bf16 with
+// 133: 314; 16 waves of 4 steps: 315 and 137; of 8: 281 and 165.
+template <typename T> struct Fwd : Shape<8, 16, 4> {};
+template <typename T> struct Bwd : Shape<8, 8, 2> {};
+template <> struct Bwd<__bf16> : Shape<8, 8, 4> {};
 
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float rcp(float x) { return __builtin_amdgcn_rcpf(x); }
@@ -208,8 +216,8 @@ struct Lookback {
     int local;                // every partner runs on this XCD (tagged_store)
 };
 
-struct Shared {
-    f32x2 A[kWaves][64], H[kWaves][64];      // the waves' pairs; then those of all waves ahead of each
+template <int W> struct Shared {
+    f32x2 A[W][64], H[W][64];      // the waves' pairs; then those of all waves ahead of each
     f32x2 pA[kUnit][64], pH[kUnit][64];      // the unit's tiles' pairs; pH[0]: the value that enters the unit
     float k[kGroup];                         // slope2
     uint32_t ticket[3];
@@ -248,8 +256,8 @@ __device__ __forceinline__ f32x2 await2(const Lookback &l, const uint64_t *p, ui
 // Whole-workgroup: the value that enters wave `pass` of tile j, from `first` at the
 // first one.  sh.A, sh.H hold the waves' pairs in the order of the pass (barrier and, with
 // MULTI, epoch_end done).  Publishes what later tiles read.
-template <bool MULTI>
-__device__ __forceinline__ f32x2 enter(const Lookback &l, Shared &sh, uint32_t j, uint32_t group, int pass, f32x2 first)
+template <bool MULTI, int W>
+__device__ __forceinline__ f32x2 enter(const Lookback &l, Shared<W> &sh, uint32_t j, uint32_t group, int pass, f32x2 first)
 {
     const int lane = threadIdx.x & 63;
     const uint32_t tag = sh.ticket[0], want = sh.ticket[1], limit = sh.ticket[2];
@@ -258,7 +266,7 @@ __device__ __forceinline__ f32x2 enter(const Lookback &l, Shared &sh, uint32_t j
     f32x2 TA = {1.0f, 1.0f}, TH = {0.0f, 0.0f};
     if (pass == 0) {
 #pragma unroll
-        for (int w = 0; w < kWaves; ++w) {
+        for (int w = 0; w < W; ++w) {
             const f32x2 A = sh.A[w][lane], H = sh.H[w][lane];
             sh.A[w][lane] = TA;
             sh.H[w][lane] = TH;
@@ -403,7 +411,7 @@ __device__ __forceinline__ void put_rows(void *base, const GatedArgs &a, const P
 
 // The channels' slope2 into LDS (a logarithm and two exponentials each: once per
 // workgroup, not once per wave)
-__device__ __forceinline__ void fill_slopes(const GatedArgs &a, const Place &p, Shared &sh)
+template <int W> __device__ __forceinline__ void fill_slopes(const GatedArgs &a, const Place &p, Shared<W> &sh)
 {
     if (threadIdx.x < kGroup) {
         const int64_t c = p.c - 2 * static_cast<int64_t>(threadIdx.x & 63) + threadIdx.x;
@@ -413,8 +421,8 @@ __device__ __forceinline__ void fill_slopes(const GatedArgs &a, const Place &p, 
 
 // A tile that lies past its sequence's length: hands on what enters it, `from` (or
 // zeros) at the first one, and returns it
-template <bool MULTI>
-__device__ __forceinline__ f32x2 pass_on(const GatedArgs &a, const Place &p, Shared &sh, int pass, const float *from)
+template <bool MULTI, int W>
+__device__ __forceinline__ f32x2 pass_on(const GatedArgs &a, const Place &p, Shared<W> &sh, int pass, const float *from)
 {
     const int lane = threadIdx.x & 63;
     Launch ep{0, 0};
@@ -453,14 +461,14 @@ template <int N, bool PLAIN> __device__ __forceinline__ void fold(const Steps &w
 }
 
 template <typename T, bool PAIRS, bool MULTI, bool PLAIN>
-__device__ __forceinline__ void fwd_tile(const GatedArgs &a, const Place &p, Shared &sh)
+__device__ __forceinline__ void fwd_tile(const GatedArgs &a, const Place &p, Shared<Fwd<T>::W> &sh)
 {
-    constexpr int C = kFwdSteps;
+    constexpr int C = Fwd<T>::C, W = Fwd<T>::W;
     const int lane = threadIdx.x & 63, wv = wave();
     const Lane<T, PAIRS> two(p.c, p.d);
-    const Steps w = steps<C>(a, p, static_cast<int64_t>(p.j) * kFwdTile + wv * C);
+    const Steps w = steps<C>(a, p, static_cast<int64_t>(p.j) * Fwd<T>::tile + wv * C);
     f32x2 h, ga[C], gb[C];
-    if (!PLAIN && static_cast<int64_t>(p.j) * kFwdTile >= p.n) {   // no step of the tile is live
+    if (!PLAIN && static_cast<int64_t>(p.j) * Fwd<T>::tile >= p.n) {   // no step of the tile is live
         h = pass_on<MULTI>(a, p, sh, wv, a.h0);
 #pragma unroll
         for (int s = 0; s < C; ++s) {
@@ -512,15 +520,15 @@ __device__ __forceinline__ void fwd_tile(const GatedArgs &a, const Place &p, Sha
         return h;
     });
     // (steps past the length leave it as it is)
-    if (a.hT && p.j + 1 == a.l.tiles && wv == kWaves - 1) store_f2(a.hT + p.b * a.D, p.c, p.d, h);
+    if (a.hT && p.j + 1 == a.l.tiles && wv == W - 1) store_f2(a.hT + p.b * a.D, p.c, p.d, h);
 }
 
 template <typename T, bool PAIRS, bool MULTI>
-__global__ void __launch_bounds__(64 * kWaves, kFwdOccupancy) gated_fwd_kernel(GatedArgs a)
+__global__ void __launch_bounds__(64 * Fwd<T>::W, Fwd<T>::occupancy) gated_fwd_kernel(GatedArgs a)
 {
-    __shared__ Shared sh;
+    __shared__ Shared<Fwd<T>::W> sh;
     const Place p = place(a);
-    if (plain_tile<kFwdTile>(a, p, static_cast<int64_t>(p.j) * kFwdTile))
+    if (plain_tile<Fwd<T>::tile>(a, p, static_cast<int64_t>(p.j) * Fwd<T>::tile))
         fwd_tile<T, PAIRS, MULTI, true>(a, p, sh);
     else
         fwd_tile<T, PAIRS, MULTI, false>(a, p, sh);
@@ -557,21 +565,21 @@ __device__ __forceinline__ void put_part(const GatedArgs &a, const Place &p, int
         if (p.c + v < p.d) o[p.c + v] = (static_cast<uint64_t>(tag) << 32) | __float_as_uint(sum[v]);
 }
 
-struct BwdShared {
-    Shared s;
-    f32x2 F[2][kWaves][64];   // the waves' pairs of the forward; then (second) the state ahead of each
-    f32x2 sum[kWaves][64];
+template <int W> struct BwdShared {
+    Shared<W> s;
+    f32x2 F[2][W][64];   // the waves' pairs of the forward; then (second) the state ahead of each
+    f32x2 sum[W][64];
 };
 
 template <typename T, bool PAIRS, bool MULTI, bool PLAIN>
-__device__ __forceinline__ void bwd_tile(const GatedArgs &a, const Place &p, int64_t tile, BwdShared &sh)
+__device__ __forceinline__ void bwd_tile(const GatedArgs &a, const Place &p, int64_t tile, BwdShared<Bwd<T>::W> &sh)
 {
-    constexpr int C = kBwdSteps;
+    constexpr int C = Bwd<T>::C, W = Bwd<T>::W;
     const int lane = threadIdx.x & 63;
-    const int pass = wave(), wv = kWaves - 1 - pass;   // in the order of the pass, and of the steps
+    const int pass = wave(), wv = W - 1 - pass;   // in the order of the pass, and of the steps
     const Lane<T, PAIRS> two(p.c, p.d);
-    const Steps w = steps<C>(a, p, tile * kBwdTile + wv * C);
-    if (!PLAIN && tile * kBwdTile >= p.n) {   // no step of the tile is live
+    const Steps w = steps<C>(a, p, tile * Bwd<T>::tile + wv * C);
+    if (!PLAIN && tile * Bwd<T>::tile >= p.n) {   // no step of the tile is live
         const f32x2 K = pass_on<MULTI>(a, p, sh.s, pass, a.dhT);
         for (void *o : {a.dx, a.dr, a.di})
             put_rows<T, C, false>(o, a, p, w, two, [](int) { return f32x2{0.0f, 0.0f}; });
@@ -589,7 +597,7 @@ __device__ __forceinline__ void bwd_tile(const GatedArgs &a, const Place &p, int
     f32x2 first = {0.0f, 0.0f}, state = {0.0f, 0.0f};
     if (a.dhT) first = load_f2(a.dhT + p.b * a.D, p.c, p.d);
     if (pass == 1)
-        state = load_f2(a.states + (p.b * a.chunks + tile * (kBwdTile / MGS_GATED_CHUNK)) * a.D, p.c, p.d);
+        state = load_f2(a.states + (p.b * a.chunks + tile * (Bwd<T>::tile / MGS_GATED_CHUNK)) * a.D, p.c, p.d);
     fill_slopes(a, p, sh.s);
     __syncthreads();
     const f32x2 k = {sh.s.k[2 * lane], sh.s.k[2 * lane + 1]};
@@ -634,7 +642,7 @@ __device__ __forceinline__ void bwd_tile(const GatedArgs &a, const Place &p, int
     __syncthreads();
     if (pass == 1) {
 #pragma unroll
-        for (int q = 0; q < kWaves; ++q) {
+        for (int q = 0; q < W; ++q) {
             const f32x2 fA = sh.F[0][q][lane], fH = sh.F[1][q][lane];
             sh.F[1][q][lane] = state;
             state = apply2(fA, fH, state);
@@ -682,18 +690,18 @@ __device__ __forceinline__ void bwd_tile(const GatedArgs &a, const Place &p, int
     sh.sum[wv][lane] = sum;
     __syncthreads();
     if (wv == 0) {
-        for (int q = 1; q < kWaves; ++q) sum += sh.sum[q][lane];
+        for (int q = 1; q < W; ++q) sum += sh.sum[q][lane];
         put_part(a, p, tile, MULTI ? sh.s.ticket[0] : 0, sum);   // (0: never the tag of a later launch)
     }
 }
 
 template <typename T, bool PAIRS, bool MULTI>
-__global__ void __launch_bounds__(64 * kWaves, kBwdOccupancy) gated_bwd_kernel(GatedArgs a)
+__global__ void __launch_bounds__(64 * Bwd<T>::W, Bwd<T>::occupancy) gated_bwd_kernel(GatedArgs a)
 {
-    __shared__ BwdShared sh;
+    __shared__ BwdShared<Bwd<T>::W> sh;
     const Place p = place(a);
     const int64_t tile = static_cast<int64_t>(a.l.tiles) - 1 - p.j;
-    if (plain_tile<kBwdTile>(a, p, tile * kBwdTile))
+    if (plain_tile<Bwd<T>::tile>(a, p, tile * Bwd<T>::tile))
         bwd_tile<T, PAIRS, MULTI, true>(a, p, tile, sh);
     else
         bwd_tile<T, PAIRS, MULTI, false>(a, p, tile, sh);
@@ -708,8 +716,14 @@ __global__ void __launch_bounds__(1024) gated_dlam_kernel(const uint64_t *part, 
     const int64_t c = (first + blockIdx.x) * 64 + lane, cc = c < D ? c : D - 1;
     const int64_t share = (rows + 15) / 16;
     double sum = 0.0;
-    for (int64_t i = wv * share; i < (wv + 1) * share && i < rows; ++i)
-        sum += static_cast<double>(tag_value(part[i * D + cc]));
+    const int64_t end = (wv + 1) * share < rows ? (wv + 1) * share : rows;
+    for (int64_t i = wv * share; i < end; i += 8) {
+        float v[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[e] = i + e < end ? tag_value(part[(i + e) * D + cc]) : 0.0f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += static_cast<double>(v[e]);
+    }
     s[wv][lane] = sum;
     __syncthreads();
     if (wv != 0 || c >= D) return;
@@ -801,7 +815,7 @@ GatedArgs arguments(const GatedGeom &g, const mgs_gated_desc &d, int64_t tiles, 
 
 template <typename T> hipError_t run_fwd(const GatedArgs &a, bool two, hipStream_t s)
 {
-    const dim3 grid(a.l.groups * a.l.tiles), block(64 * kWaves);
+    const dim3 grid(a.l.groups * a.l.tiles), block(64 * Fwd<T>::W);
     if (a.l.tiles > 1) {
         if (two) gated_fwd_kernel<T, true, true><<<grid, block, 0, s>>>(a);
         else gated_fwd_kernel<T, false, true><<<grid, block, 0, s>>>(a);
@@ -814,7 +828,7 @@ template <typename T> hipError_t run_fwd(const GatedArgs &a, bool two, hipStream
 
 template <typename T> hipError_t run_bwd(const GatedArgs &a, bool two, hipStream_t s)
 {
-    const dim3 grid(a.l.groups * a.l.tiles), block(64 * kWaves);
+    const dim3 grid(a.l.groups * a.l.tiles), block(64 * Bwd<T>::W);
     if (a.l.tiles > 1) {
         if (two) gated_bwd_kernel<T, true, true><<<grid, block, 0, s>>>(a);
         else gated_bwd_kernel<T, false, true><<<grid, block, 0, s>>>(a);
@@ -832,8 +846,10 @@ GatedGeom gated_geometry(const mgs_gated_desc &d, bool backward)
     GatedGeom g{};
     g.groups = d.B * ((d.D + kGroup - 1) / kGroup);
     // (no steps: one tile, which hands the state on)
-    g.tiles_f = std::max<int64_t>(1, (d.T + kFwdTile - 1) / kFwdTile);
-    g.tiles_b = std::max<int64_t>(1, (d.T + kBwdTile - 1) / kBwdTile);
+    const bool half = d.dtype == MGS_BF16;
+    const int64_t tf = half ? Fwd<__bf16>::tile : Fwd<float>::tile, tb = half ? Bwd<__bf16>::tile : Bwd<float>::tile;
+    g.tiles_f = std::max<int64_t>(1, (d.T + tf - 1) / tf);
+    g.tiles_b = std::max<int64_t>(1, (d.T + tb - 1) / tb);
     const int64_t tiles = backward ? std::max(g.tiles_f, g.tiles_b) : g.tiles_f;
     // every word behind the header is a tagged one, whatever call it is written by,
     // so that a call of other sizes takes none of them for its own
