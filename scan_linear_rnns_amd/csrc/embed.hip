@@ -3,14 +3,17 @@
 //
 //     y_n = scale W[id_n],      dW_v = scale sum over n with id_n = v of dy_n
 //
-// Gradient: three kernels.  The first sorts the places n by their ids: each
-// workgroup serves a range of ids, reads all of them (they stay in L2) and places the
-// ones in its range by counting, without a word to any other workgroup; it also writes
-// the zeros of the rows that no id points to, most of the traffic of a large table,
-// meanwhile.  The second walks the sorted places in chunks of equal length, so that
-// an id that makes up half of a text costs no workgroup more than the others, adds
-// the rows up in fp32 and writes each sum that lies inside a chunk; the third joins
-// the sums that cross chunks.  All orders are fixed by the ids.
+// Gradient: three kernels.  The first sorts the places n by their ids (equal ones next to
+// each other; the order of the ids does not matter): of 2^b workgroups each serves the
+// ids of one remainder, so that the low ids, which are most of a text in many
+// vocabularies, are spread over all of them (in ranges of ids, one workgroup had half
+// of the places: 32768 of them 243 us).  It reads all ids (they stay in L2) and places its
+// own by counting, without a word to any other workgroup.  The second walks the sorted
+// places in chunks of equal length, so that an id that makes up half of a text costs
+// no workgroup more than the others, adds the rows up in fp32 and writes each sum that
+// lies inside a chunk, while workgroups behind these write the zeros of the rows that no
+// id points to, most of the traffic of a large table; the third joins the sums that cross
+// chunks.  All orders are fixed by the ids.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -23,10 +26,9 @@
 namespace mgs {
 namespace {
 
-constexpr int kChunk = 32;        // sorted places of a workgroup
+constexpr int kMaxChunk = 32;     // sorted places of a workgroup (one more lane looks behind them)
 constexpr int kSortWaves = 16;
 constexpr int kMaxRange = 512;    // ids of a sorting workgroup
-constexpr int64_t kMinRange = 64;
 
 typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
 typedef float f8v __attribute__((ext_vector_type(8), aligned(16)));
@@ -109,16 +111,20 @@ template <typename T> __global__ void __launch_bounds__(256) lookup_kernel(Looku
 }
 
 // -------------------------------------------------------------------- sort
+// Where an id stands in the order: by its remainder, then its quotient
+__device__ __forceinline__ int64_t order_of(int32_t id, int bits, int range)
+{
+    return static_cast<int64_t>(id & ((1 << bits) - 1)) * range + (id >> bits);
+}
+
 struct SortArgs {
     const void *ids;
     int64_t n, vocab, d;
-    int range;
-    bool wide_ids, clear;
+    int bits, range;    // 2^bits workgroups, ids of each
+    bool wide_ids;
     int64_t *count;     // ids inside the table
-    int32_t *first;     // of each id, and one past the last
+    int32_t *first;     // the first place of each id, in their order, and one past the last
     int32_t *row, *id;  // sorted
-    char *dW;
-    int64_t row_bytes;
 };
 
 // f(id, place) for the wave's places n0..n1-1, lane by lane, several loads in flight.  Ids
@@ -145,12 +151,11 @@ template <typename F> __device__ __forceinline__ void each_id(const SortArgs &a,
 __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
 {
     __shared__ int32_t at[kSortWaves * kMaxRange];   // [wave][local id]: counts, then next places
-    __shared__ int32_t starts[kMaxRange];
     __shared__ int64_t below[kSortWaves];
     __shared__ int32_t scan[kSortWaves];
     const int lane = threadIdx.x & 63, wv = wave();
-    const int32_t lo = static_cast<int32_t>(static_cast<int64_t>(blockIdx.x) * a.range);
-    const int ids = static_cast<int>(a.vocab - lo < a.range ? a.vocab - lo : a.range);
+    const int32_t mask = (1 << a.bits) - 1, own = static_cast<int32_t>(blockIdx.x);
+    const int ids = a.range;   // (the last one may lie past the table)
     for (int i = threadIdx.x; i < kSortWaves * a.range; i += 64 * kSortWaves) at[i] = 0;
     __syncthreads();
     const int64_t share = (a.n + kSortWaves - 1) / kSortWaves;
@@ -158,8 +163,8 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
     volatile int32_t *mine = at + wv * a.range;   // (its wave's lanes share it without barriers)
     int64_t smaller = 0;
     each_id(a, n0, n1, [&](int32_t id, int64_t) {
-        if (id >= 0 && id < lo) ++smaller;
-        if (id >= lo && id - lo < ids) atomicAdd(&at[wv * a.range + (id - lo)], 1);
+        if (id >= 0 && (id & mask) < own) ++smaller;
+        if (id >= 0 && (id & mask) == own) atomicAdd(&at[wv * a.range + (id >> a.bits)], 1);
     });
     for (int off = 32; off; off >>= 1) smaller += __shfl_xor(smaller, off, 64);
     if (lane == 0) below[wv] = smaller;
@@ -183,21 +188,20 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
     for (int w = 0; w < wv; ++w) before += scan[w];
     if (i < ids) {
         int32_t next = static_cast<int32_t>(base) + before;
-        starts[i] = sum ? next : -1;   // -1: no place has this id
-        a.first[lo + i] = next;
+        a.first[static_cast<int64_t>(own) * a.range + i] = next;
         for (int w = 0; w < kSortWaves; ++w) {
             const int32_t c = at[w * a.range + i];
             at[w * a.range + i] = next;
             next += c;
         }
-        if (lo + i == a.vocab - 1) {
-            a.first[a.vocab] = next;
+        if (own == mask && i == ids - 1) {
+            a.first[static_cast<int64_t>(own + 1) * a.range] = next;
             *a.count = next;
         }
     }
     __syncthreads();
     each_id(a, n0, n1, [&](int32_t id, int64_t n) {
-        const int local = id >= lo && id - lo < ids ? id - lo : -1;
+        const int local = id >= 0 && (id & mask) == own ? id >> a.bits : -1;
         // one round for each id among the lanes: its lanes in order
         for (uint64_t left = __ballot(local >= 0); left;) {
             const int now = __builtin_amdgcn_readlane(local, __builtin_ctzll(left));
@@ -212,22 +216,6 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
             left &= ~same;
         }
     });
-    if (!a.clear) return;
-    // rows of no id
-    for (int k = wv; k < ids; k += kSortWaves) {
-        if (starts[k] >= 0) continue;
-        char *row = a.dW + (static_cast<int64_t>(lo) + k) * a.row_bytes;
-        const int64_t head = (16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15;
-        const int64_t wide = head < a.row_bytes ? (a.row_bytes - head) / 16 : 0;
-        for (int64_t o = lane; o < wide; o += 64) {
-            const f32x4 z = {0, 0, 0, 0};
-            __builtin_nontemporal_store(z, reinterpret_cast<f32x4 *>(row + head) + o);
-        }
-        if (head == 0 && 16 * wide == a.row_bytes) continue;
-        // the ends, in halves: an element is two or four bytes
-        for (int64_t o = 2 * lane; o < a.row_bytes; o += 128)
-            if (o < head || o >= head + 16 * wide) *reinterpret_cast<uint16_t *>(row + o) = 0;
-    }
 }
 
 // -------------------------------------------------------------------- sums
@@ -238,7 +226,9 @@ struct SumArgs {
     const void *dy;
     void *dW;
     int64_t block, d, gs;
-    int slabs;
+    int64_t blocks;    // that add up; the ones behind them clear rows
+    int64_t vocab, row_bytes;
+    int bits, range, slabs, chunk;
     float scale;
     bool add, vec_in, vec_out;
 };
@@ -257,47 +247,120 @@ __device__ __forceinline__ f8v *partial(const SumArgs &a, int64_t chunk, int whi
     return reinterpret_cast<f8v *>(a.part + (chunk * 2 + which) * width + c);
 }
 
-// `slabs` threads walk a chunk, 8 columns each, eight rows in flight
-template <typename T, typename D> __global__ void __launch_bounds__(256) sum_kernel(SumArgs a)
+// Eight elements as they are stored
+template <typename T> struct Raw8 {
+    typename Raw<T>::V v;
+    __device__ __forceinline__ void load(const T *row, int64_t c, int64_t d, bool vec)
+    {
+        v = typename Raw<T>::V{0, 0, 0, 0, 0, 0, 0, 0};
+        if (vec) {
+            if (c < d) v = *reinterpret_cast<const typename Raw<T>::V *>(row + c);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (c + i < d) v[i] = row[c + i];
+        }
+    }
+};
+
+// Zeros for the rows of no id among kClear ids of a wave
+constexpr int kClear = 16;
+
+__device__ __forceinline__ void clear_rows(const SumArgs &a, int64_t block)
 {
-    constexpr int kAhead = 8;
-    static_assert(kChunk % kAhead == 0, "whole batches");
-    const int sub = threadIdx.x / a.slabs, t = threadIdx.x % a.slabs;
+    const int lane = threadIdx.x & 63;
+    const int64_t id0 = (block * 4 + wave()) * kClear, mine = id0 + lane;
+    bool empty = false;
+    if (lane < kClear && mine < a.vocab) {
+        const int64_t o = order_of(static_cast<int32_t>(mine), a.bits, a.range);
+        empty = a.first[o] == a.first[o + 1];
+    }
+    for (uint64_t left = __ballot(empty); left; left &= left - 1) {
+        char *row = static_cast<char *>(a.dW) + (id0 + __builtin_ctzll(left)) * a.row_bytes;
+        const int64_t head = (16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15;
+        const int64_t wide = head < a.row_bytes ? (a.row_bytes - head) / 16 : 0;
+        for (int64_t o = lane; o < wide; o += 64) {
+            const f32x4 z = {0, 0, 0, 0};
+            __builtin_nontemporal_store(z, reinterpret_cast<f32x4 *>(row + head) + o);
+        }
+        if (head == 0 && 16 * wide == a.row_bytes) continue;
+        // the ends, in halves: an element is two or four bytes
+        for (int64_t o = 2 * lane; o < a.row_bytes; o += 128)
+            if (o < head || o >= head + 16 * wide) *reinterpret_cast<uint16_t *>(row + o) = 0;
+    }
+}
+
+// `slabs` threads walk a chunk, 8 columns each, kAhead rows in flight and as many on
+// their way.  WAVES: whole waves share a chunk, so that its places are scalars.
+template <typename T, typename D, bool WAVES> __global__ void __launch_bounds__(256) sum_kernel(SumArgs a)
+{
+    constexpr int kAhead = sizeof(T) == 2 ? 8 : 4;
+    if (a.block + blockIdx.x >= a.blocks) {
+        if (blockIdx.y == 0) clear_rows(a, a.block + blockIdx.x - a.blocks);
+        return;
+    }
+    int sub = threadIdx.x / a.slabs;
+    if constexpr (WAVES) sub = __builtin_amdgcn_readfirstlane(sub);
+    const int t = threadIdx.x % a.slabs;
     const int64_t chunk = (a.block + blockIdx.x) * (256 / a.slabs) + sub, total = *a.count;
-    const int64_t k0 = chunk * kChunk, k1 = k0 + kChunk < total ? k0 + kChunk : total;
+    const int64_t k0 = chunk * a.chunk, k1 = k0 + a.chunk < total ? k0 + a.chunk : total;
     if (k0 >= k1) return;
-    const bool entered = k0 > 0 && a.id[k0 - 1] == a.id[k0];
+    const int32_t *ids = a.id + k0, *rows = a.row + k0;
+    const int n = static_cast<int>(k1 - k0);
+    // lane k of each wave: the k-th place's row and id, lane n: the id behind the chunk, the
+    // one ahead of it
+    const int lane = threadIdx.x & 63;
+    int32_t lane_id = -1, lane_row = 0, ahead = -1;
+    if (WAVES) {
+        if (lane <= n && k0 + lane < total) lane_id = ids[lane];
+        if (lane < n) lane_row = rows[lane];
+        if (k0 > 0) ahead = ids[-1];
+    } else if (k0 > 0) {
+        ahead = ids[-1];
+    }
+    auto id_of = [&](int k) -> int32_t {   // k <= n; -1 past the last place
+        if constexpr (WAVES) return __builtin_amdgcn_readlane(lane_id, k);
+        return k0 + k < total ? ids[k] : -1;
+    };
+    auto row_of = [&](int k) -> int64_t {
+        if constexpr (WAVES) return __builtin_amdgcn_readlane(lane_row, k);
+        return rows[k];
+    };
+    const bool entered = ahead == id_of(0);
     for (int64_t c = 8 * (t + static_cast<int64_t>(blockIdx.y) * a.slabs); c < a.d;
          c += 8 * static_cast<int64_t>(a.slabs) * gridDim.y) {
-        f8v sum = {0, 0, 0, 0, 0, 0, 0, 0};
-        bool inside = entered;   // in the run that enters the chunk
-        for (int64_t k = k0; k < k1; k += kAhead) {
-            int32_t id[kAhead + 1], row[kAhead];
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j) {
-                row[j] = a.row[k + j < k1 ? k + j : k1 - 1];
-                id[j] = a.id[k + j < k1 ? k + j : k1 - 1];
-            }
-            id[kAhead] = k + kAhead < total ? a.id[k + kAhead] : -1;
-            f8v v[kAhead];
+        Raw8<T> v[2][kAhead];
+        auto fetch = [&](int k, Raw8<T> *to) {
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
-                v[j] = load8(static_cast<const T *>(a.dy) + row[j] * a.gs, c, a.d, a.vec_in);
+                to[j].load(static_cast<const T *>(a.dy) + row_of(k + j < n ? k + j : n - 1) * a.gs, c, a.d, a.vec_in);
+        };
+        f8v sum = {0, 0, 0, 0, 0, 0, 0, 0};
+        bool inside = entered;   // in the run that enters the chunk
+        auto add = [&](int k, const Raw8<T> *from) {
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                if (k + j >= k1) break;
-                sum += v[j];
-                const bool ends = k + j + 1 == total || id[j + 1] != id[j];
-                if (!ends && k + j + 1 < k1) continue;
+                if (k + j >= n) break;
+                sum += __builtin_convertvector(from[j].v, f8v);
+                const int32_t id = id_of(k + j);
+                const bool last = k + j + 1 == n, ends = id_of(k + j + 1) != id;
+                if (!ends && !last) continue;
                 if (inside)
                     *partial(a, chunk, 0, c) = sum;
                 else if (ends)
-                    put<D>(a, id[j], c, sum);
+                    put<D>(a, id, c, sum);
                 else
                     *partial(a, chunk, 1, c) = sum;
                 inside = false;
                 sum = f8v{0, 0, 0, 0, 0, 0, 0, 0};
             }
+        };
+        fetch(0, v[0]);
+        for (int k = 0; k < n; k += 2 * kAhead) {
+            if (k + kAhead < n) fetch(k + kAhead, v[1]);
+            add(k, v[0]);
+            if (k + 2 * kAhead < n) fetch(k + 2 * kAhead, v[0]);
+            add(k + kAhead, v[1]);
         }
     }
 }
@@ -308,11 +371,12 @@ template <typename D> __global__ void __launch_bounds__(256) join_kernel(SumArgs
 {
     __shared__ f8v s[4][64];
     const int64_t chunk = a.block + blockIdx.x, total = *a.count;
-    const int64_t k0 = chunk * kChunk, k1 = k0 + kChunk;
+    const int64_t k0 = chunk * a.chunk, k1 = k0 + a.chunk;
     if (k1 >= total) return;
     const int32_t id = a.id[k1 - 1];
-    if (a.id[k1] != id || a.first[id] < k0) return;
-    const int64_t last = (a.first[id + 1] - 1) / kChunk, many = last - chunk;   // chunks that it enters
+    const int64_t order = order_of(id, a.bits, a.range);
+    if (a.id[k1] != id || a.first[order] < k0) return;
+    const int64_t last = (a.first[order + 1] - 1) / a.chunk, many = last - chunk;   // chunks that it enters
     const int lane = threadIdx.x & 63, wv = wave();
     const int64_t share = (many + 3) / 4;
     const int64_t q0 = chunk + 1 + wv * share, q1 = q0 + share < last + 1 ? q0 + share : last + 1;
@@ -321,7 +385,14 @@ template <typename D> __global__ void __launch_bounds__(256) join_kernel(SumArgs
         f8v sum = {0, 0, 0, 0, 0, 0, 0, 0};
         if (c < a.d) {
             if (wv == 0) sum = *partial(a, chunk, 1, c);
-            for (int64_t q = q0; q < q1; ++q) sum += *partial(a, q, 0, c);
+            for (int64_t q = q0; q < q1; q += 4) {
+                f8v v[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[k] = *partial(a, q + k < q1 ? q + k : q1 - 1, 0, c);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (q + k < q1) sum += v[k];
+            }
         }
         s[wv][lane] = sum;
         __syncthreads();
@@ -348,9 +419,12 @@ hipError_t sums(SumArgs a, const EmbedGeom &g, hipStream_t s)
 {
     const unsigned cols = static_cast<unsigned>(std::min<int64_t>((a.d + 8 * a.slabs - 1) / (8 * a.slabs), 64));
     const int per = 256 / a.slabs;
-    hipError_t e = launch_sliced((g.chunks + per - 1) / per, 256, [&](int64_t first, unsigned blocks) {
+    a.blocks = (g.chunks + per - 1) / per;
+    const int64_t clearing = a.add ? 0 : (a.vocab + 4 * kClear - 1) / (4 * kClear);
+    hipError_t e = launch_sliced(a.blocks + clearing, 256, [&](int64_t first, unsigned blocks) {
         a.block = first;
-        sum_kernel<T, D><<<dim3(blocks, cols), dim3(256), 0, s>>>(a);
+        if (a.slabs >= 64) sum_kernel<T, D, true><<<dim3(blocks, cols), dim3(256), 0, s>>>(a);
+        else sum_kernel<T, D, false><<<dim3(blocks, cols), dim3(256), 0, s>>>(a);
     });
     if (e != hipSuccess || g.chunks < 2) return e;
     return launch_sliced(g.chunks - 1, 256, [&](int64_t first, unsigned blocks) {
@@ -364,13 +438,14 @@ hipError_t sums(SumArgs a, const EmbedGeom &g, hipStream_t s)
 EmbedGeom embed_geometry(int64_t n, int64_t vocab, int64_t d)
 {
     EmbedGeom g{};
-    int64_t range = kMinRange;   // about a workgroup for each of the 256 CUs
-    while (range < kMaxRange && range * 256 < vocab) range *= 2;
-    g.range = static_cast<int>(range);
-    g.ranges = (vocab + range - 1) / range;
-    g.chunks = (n + kChunk - 1) / kChunk;
+    // a workgroup for each of the 256 CUs, or for 16 ids where there are few
+    while (g.bits < 8 && (int64_t(16) << g.bits) < vocab) ++g.bits;
+    while ((int64_t(kMaxRange) << g.bits) < vocab) ++g.bits;
+    g.range = static_cast<int>((vocab + (int64_t(1) << g.bits) - 1) >> g.bits);
+    g.chunk = n <= 8192 ? 8 : n <= 16384 ? 16 : kMaxChunk;
+    g.chunks = (n + g.chunk - 1) / g.chunk;
     size_t off = 256;
-    g.off_first = off; off = align256(off + (static_cast<size_t>(vocab) + 1) * 4);
+    g.off_first = off; off = align256(off + ((static_cast<size_t>(g.range) << g.bits) + 1) * 4);
     g.off_row = off;   off = align256(off + static_cast<size_t>(n) * 4);
     g.off_id = off;    off = align256(off + static_cast<size_t>(n) * 4);
     g.off_part = off;  off = align256(off + static_cast<size_t>(g.chunks) * 2 * ((d + 7) / 8 * 8) * 4);
@@ -403,18 +478,16 @@ hipError_t launch_embed_bwd(const EmbedGeom &g, const void *ids, bool wide_ids, 
     a.n = n;
     a.vocab = vocab;
     a.d = d;
+    a.bits = g.bits;
     a.range = g.range;
     a.wide_ids = wide_ids;
-    a.clear = !accumulate;
     a.count = reinterpret_cast<int64_t *>(w);
     a.first = reinterpret_cast<int32_t *>(w + g.off_first);
     a.row = reinterpret_cast<int32_t *>(w + g.off_row);
     a.id = reinterpret_cast<int32_t *>(w + g.off_id);
-    a.dW = static_cast<char *>(dW);
-    a.row_bytes = d * out;
-    sort_kernel<<<dim3(static_cast<unsigned>(g.ranges)), dim3(64 * kSortWaves), 0, s>>>(a);
+    sort_kernel<<<dim3(1u << g.bits), dim3(64 * kSortWaves), 0, s>>>(a);
     const hipError_t e = hipGetLastError();
-    if (e != hipSuccess || n == 0) return e;
+    if (e != hipSuccess) return e;
     SumArgs b{};
     b.count = a.count;
     b.first = a.first;
@@ -424,8 +497,13 @@ hipError_t launch_embed_bwd(const EmbedGeom &g, const void *ids, bool wide_ids, 
     b.dy = dy;
     b.dW = dW;
     b.d = d;
+    b.vocab = vocab;
+    b.row_bytes = d * out;
     b.gs = dy_stride;
+    b.bits = g.bits;
+    b.range = g.range;
     b.slabs = slabs_of(d);
+    b.chunk = g.chunk;
     b.scale = scale;
     b.add = accumulate;
     b.vec_in = whole8(dy, d, dy_stride, size);

@@ -13,10 +13,11 @@ namespace mgs {
 
 // ---------------------------------------------------------------- embedding
 struct EmbedGeom {
-    int range;        // ids per sorting workgroup, a power of two
-    int64_t ranges, chunks;
-    // workspace byte offsets: the number of ids inside the table, each id's first
-    // sorted place, the sorted places' rows and ids, partial sums of runs of one id
+    int bits, range;   // 2^bits sorting workgroups, ids of each
+    int chunk;         // sorted places of a summing workgroup
+    int64_t chunks;
+    // workspace byte offsets (the number of ids inside the table comes first): each id's
+    // first sorted place, the sorted places' rows and ids, partial sums of runs of one id
     // that cross a chunk
     size_t off_first, off_row, off_id, off_part, bytes;
 };
