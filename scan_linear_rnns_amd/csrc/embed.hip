@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
     __syncthreads();
     const int64_t share = (a.n + kSortWaves - 1) / kSortWaves;
     const int64_t n0 = wv * share, n1 = n0 + share < a.n ? n0 + share : a.n;
-    volatile int32_t *mine = at + wv * a.range;   // (its wave's lanes share it without barriers)
+    int32_t *mine = at + wv * a.range;
     int64_t smaller = 0;
     each_id(a, n0, n1, [&](int32_t id, int64_t) {
         if (id >= 0 && (id & mask) < own) ++smaller;
@@ -213,6 +213,8 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
                 a.id[place] = id;
             }
             if (lane == 0) mine[now] = start + __popcll(same);
+            // (a wave's LDS accesses run in order: this holds the compiler to that)
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             left &= ~same;
         }
     });

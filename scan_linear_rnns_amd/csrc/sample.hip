@@ -35,8 +35,9 @@ constexpr int kBins = 2048;         // of 1/64: weights below e^-32 are less tha
 constexpr float kPerUnit = 64.0f;
 constexpr int kList = 4096;         // candidates that are sorted
 constexpr int kFixed = 43;          // a weight's bits behind the point: 2^20 of them fit 64 bits
+constexpr int kCounted = 256;       // up to here sorting counts the smaller ones
 constexpr int kMaxSlices = 64;
-constexpr float kInf = __builtin_inff();
+constexpr float kInf = __builtin_inff(), kMax = 3.4028234663852886e38f;
 
 struct SampleArgs {
     const void *logits;
@@ -72,7 +73,9 @@ enum { DONE = 0, GREEDY = 1, PLAIN = 2, TOP_K = 3, TOP_P = 4 };
 struct Row {
     int kind;
     int top_k;           // 0: off
-    float top;           // the largest logit
+    float max, top;      // the largest logit; the same, the largest number where it is infinite
+    float least;         // no smaller one passes min-p (the floor without it)
+    float floor;         // what is below has no weight: -inf, or all but +inf
     float inv;           // 1 / temperature
     double scale;        // log2 e / temperature
     double top_p, min_p;
@@ -87,40 +90,47 @@ __device__ __forceinline__ Row settings(const SampleArgs &a, int64_t b, float to
     const int k = a.top_k ? a.top_k[b] : a.k0;
     const float u = a.u[b];
     r.u = u > 0.0f ? (u < 1.0f ? u : 0.99999994f) : 0.0f;
-    r.top = top;
+    r.max = top;
+    r.top = fminf(top, kMax);
+    r.floor = top == kInf ? kInf : -kMax;
     r.inv = 1.0f / tau;
     r.scale = 1.4426950408889634 / static_cast<double>(tau);
     r.top_k = k > 0 && k < a.vocab ? k : 0;
     r.top_p = p < 1.0f ? (p > 0.0f ? p : 0.0f) : 1.0;
     r.min_p = m > 0.0f ? (m < 1.0f ? m : 1.0f) : 0.0f;
+    r.least = r.floor;
+    if (r.min_p > 0.0) {   // a little lower: the weight itself decides
+        const double x = r.top + static_cast<double>(tau) * log(r.min_p);
+        r.least = fmaxf(r.floor, static_cast<float>(x - 1e-6 * (fabs(x) + fabs(static_cast<double>(r.top)))));
+    }
     r.kind = !(top > -kInf) ? DONE : !(tau > 0.0f) ? GREEDY : r.top_k ? TOP_K : r.top_p < 1.0 ? TOP_P : PLAIN;
     return r;
 }
 
 // ------------------------------------------------------------------ weights
-// 2^(j/64), j = 0..63, for the function below
+constexpr int kRoots = 256;
+
+// 2^(j/256), for the function below
 __device__ __forceinline__ void fill_roots(double *roots)
 {
-    if (threadIdx.x < 64) roots[threadIdx.x] = exp2(static_cast<double>(threadIdx.x) / 64.0);
+    if (threadIdx.x < kRoots) roots[threadIdx.x] = exp2(static_cast<double>(threadIdx.x) / kRoots);
 }
 
-// e^((x - top) / temperature) in fp64: y = n + j/64 + s, |s| <= 1/128, 2^s by its
-// series to s^6 (the next term is below 2^-60 of it).  x <= top.
+// e^((x - top) / temperature) in fp64, x from the row's floor on: y = n + j/256 + s,
+// |s| <= 1/512, 2^s by its series to s^4 (the next term is below 2^-54).  What is below
+// 2^-999 is nothing.  (No branch: neighbouring values' chains run side by side.)
 __device__ __forceinline__ double weight(float x, const Row &r, const double *roots)
 {
-    constexpr double kShift = 1.5 * 70368744177664.0;   // 2^46: adding it rounds to 1/64
-    const double y = (static_cast<double>(x) - static_cast<double>(r.top)) * r.scale;
+    constexpr double kShift = 1.5 * 17592186044416.0;   // 2^44: adding it rounds to 1/256
+    const double y = fmax((static_cast<double>(fminf(x, kMax)) - static_cast<double>(r.top)) * r.scale, -1000.0);
     const double z = y + kShift, s = y - (z - kShift);
-    const int k = static_cast<int>(__double2loint(z));
-    double q = 1.5403530393381608e-4;
-    q = __builtin_fma(q, s, 1.3333558146428443e-3);
-    q = __builtin_fma(q, s, 9.6181291076284772e-3);
-    q = __builtin_fma(q, s, 5.5504108664821580e-2);
+    const int k = __double2loint(z);
+    double q = __builtin_fma(9.6181291076284772e-3, s, 5.5504108664821580e-2);
     q = __builtin_fma(q, s, 2.4022650695910071e-1);
     q = __builtin_fma(q, s, 6.9314718055994531e-1);
-    const double root = roots[k & 63];
-    const double w = ldexp(__builtin_fma(q * s, root, root), k >> 6);
-    return x == r.top ? 1.0 : !(y > -1100.0) ? 0.0 : w;   // (y is -inf or NaN next to infinities)
+    const double root = roots[k & (kRoots - 1)], w = __builtin_fma(q * s, root, root);
+    const double o = __hiloint2double(__double2hiint(w) + ((k >> 8) << 20), __double2loint(w));
+    return o > 0x1p-999 ? o : 0.0;
 }
 
 // w <= 1 as a multiple of 2^-43
@@ -132,11 +142,32 @@ __device__ __forceinline__ uint64_t fixed(double w)
 
 __device__ __forceinline__ double unfixed(uint64_t q) { return static_cast<double>(q) * 0x1p-43; }
 
-// The bin of x, kBins and more past the last one (-inf too); falls with x
+// The bin of x, kBins past the last one and below the floor; falls with x
 __device__ __forceinline__ int bin_of(float x, const Row &r)
 {
-    const float t = (r.top - x) * r.inv * kPerUnit;
-    return x == r.top ? 0 : t < static_cast<float>(kBins) && x > -kInf ? static_cast<int>(t) : kBins;
+    const float d = r.top - fminf(x, kMax), t = d * r.inv * kPerUnit;
+    const int bin = t < static_cast<float>(kBins) ? static_cast<int>(t) : kBins;
+    return x >= r.floor ? (d == 0.0f ? 0 : bin) : kBins;   // (0 times an infinite inv is no number)
+}
+
+// The least x whose bin is `bin` or less (bin < kBins), by the whole wave: 64 keys at a
+// time
+__device__ __forceinline__ float bin_floor(int bin, const Row &r)
+{
+    const uint32_t lane = threadIdx.x & 63;
+    uint32_t lo = key_of(r.floor), hi = key_of(r.floor == kInf ? kInf : r.top);   // hi's bin is 0
+    while (lo < hi) {
+        const uint32_t step = (hi - lo) / 64 + 1, at = hi - lo > lane * step ? lo + lane * step : hi;
+        const uint64_t in = __ballot(bin_of(of_key(at), r) <= bin);   // the lanes from some one on
+        if (in == 0) {
+            lo = __builtin_amdgcn_readlane(at, 63) + 1;
+            continue;
+        }
+        const int first = __builtin_ctzll(in);
+        hi = __builtin_amdgcn_readlane(at, first);
+        lo = first == 0 ? hi : __builtin_amdgcn_readlane(at, first - 1) + 1;
+    }
+    return of_key(hi);
 }
 
 // ------------------------------------------------------------ walking a row
@@ -179,6 +210,39 @@ template <typename T, typename F> __device__ __forceinline__ void walk(const T *
     }
 }
 
+// What a wave's lanes have written to LDS is there for its others (its LDS accesses run
+// in order: this holds the compiler to that)
+__device__ __forceinline__ void wave_order() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
+// Values of a wave's lanes that wait until there are 64 of them, so that what is done
+// with few of a row's values is done with whole waves
+struct Queue {
+    float *held;   // 128 of the wave's own, in LDS
+    int n = 0;
+
+    template <typename F> __device__ __forceinline__ void push(float v, bool in, F f)
+    {
+        const uint64_t who = __ballot(in);
+        if (!who) return;
+        const int lane = threadIdx.x & 63;
+        if (in) held[n + __popcll(who & ((1ull << lane) - 1))] = v;
+        n += __popcll(who);
+        if (n >= 64) {
+            n -= 64;
+            wave_order();
+            const float x = held[n + lane];
+            wave_order();
+            f(x);
+        }
+    }
+    template <typename F> __device__ __forceinline__ void rest(F f)
+    {
+        wave_order();
+        const int lane = threadIdx.x & 63;
+        if (lane < n) f(held[lane]);
+    }
+};
+
 // ------------------------------------------------------------ workgroup sums
 template <typename V> __device__ __forceinline__ V wave_sum(V v)
 {
@@ -209,11 +273,32 @@ template <typename V> __device__ __forceinline__ V scan_block(V v, V *lds, V &al
     return lane ? before + prev : before;
 }
 
-__device__ __forceinline__ void sort_list(uint64_t *list, int n)   // n: a power of two
+// Sorts n entries, all different but for ~0, n a power of two from 64 on.  Few: each
+// entry's place is the number of smaller ones, counted by kThreads / n threads (two
+// barriers, where sorting in steps takes some thirty; the reads grow with n^2: at 512
+// a row's last step took 61 us, in steps 36); many: in steps.
+__device__ __forceinline__ void sort_list(uint64_t *list, int n)
 {
+    __syncthreads();
+    if (n <= kCounted) {
+        const int each = kThreads / n, e = threadIdx.x / each, part = threadIdx.x % each;
+        const uint64_t own = list[e];
+        const int per = n / each;
+        int smaller = 0;
+#pragma unroll 8
+        for (int i = 0; i < per; ++i) {
+            const int at = part * per + i;
+            const uint64_t o = list[at];
+            smaller += o < own || (o == own && at < e);
+        }
+        for (int off = 1; off < each; off <<= 1) smaller += __shfl_xor(smaller, off, 64);
+        __syncthreads();
+        if (part == 0) list[smaller] = own;
+        __syncthreads();
+        return;
+    }
     for (int size = 2; size <= n; size *= 2)
         for (int step = size / 2; step; step /= 2) {
-            __syncthreads();
             for (int p = threadIdx.x; p < n / 2; p += kThreads) {
                 const int i = (p / step) * 2 * step + p % step, j = i + step;
                 const uint64_t x = list[i], y = list[j];
@@ -222,17 +307,18 @@ __device__ __forceinline__ void sort_list(uint64_t *list, int n)   // n: a power
                     list[j] = x;
                 }
             }
+            __syncthreads();
         }
-    __syncthreads();
 }
 
 // ------------------------------------------------------------- steps 1 to 3
 struct Shared {
     uint64_t mass[kBins];
-    uint32_t count[kBins];   // (right behind mass: see finish)
+    uint32_t count[kBins];
     uint64_t list[kList];
     double sub[kMaxSlices * kWaves];
-    double roots[64];
+    double roots[kRoots];
+    float queue[kWaves][128];
     double wd[kWaves];
     uint64_t wu[kWaves];
     float top[kWaves];
@@ -248,23 +334,27 @@ struct Slot {
     uint32_t *n;       // candidates
     uint32_t *count;
     uint64_t *mass, *list;
+    float *maxima;     // kGroups of each slice
     double *sub;
 };
 
+constexpr int kGroups = 64;   // of 16 threads
 constexpr size_t kSlotMass = 512, kSlotCount = kSlotMass + 8 * kBins, kSlotList = kSlotCount + 4 * kBins,
-                 kSlotSub = kSlotList + 8 * kList;
+                 kSlotMaxima = kSlotList + 8 * kList, kSlotSub = kSlotMaxima + 4 * kGroups * kMaxSlices;
 
 __device__ __forceinline__ Slot slot_of(const SampleArgs &a, int64_t b)
 {
     char *w = a.ws + b * a.slot;
     return Slot{reinterpret_cast<float *>(w), reinterpret_cast<uint32_t *>(w + 256),
                 reinterpret_cast<uint32_t *>(w + kSlotCount), reinterpret_cast<uint64_t *>(w + kSlotMass),
-                reinterpret_cast<uint64_t *>(w + kSlotList), reinterpret_cast<double *>(w + kSlotSub)};
+                reinterpret_cast<uint64_t *>(w + kSlotList), reinterpret_cast<float *>(w + kSlotMaxima),
+                reinterpret_cast<double *>(w + kSlotSub)};
 }
 
-// 1: the largest of a slice, NaN if it holds one, known to every thread
+// 1: the largest of a slice, NaN if it holds one, known to every thread; `own`: of the
+// values that this thread has read
 template <typename T>
-__device__ __forceinline__ float slice_top(const SampleArgs &a, const T *x, int lo, int hi, Shared &sh)
+__device__ __forceinline__ float slice_top(const SampleArgs &a, const T *x, int lo, int hi, Shared &sh, float &own)
 {
     float top = -kInf;
     bool nan = false;
@@ -272,6 +362,7 @@ __device__ __forceinline__ float slice_top(const SampleArgs &a, const T *x, int 
         top = fmaxf(top, v);
         nan |= v != v;
     });
+    own = top;
     if (nan) top = __builtin_nanf("");
     for (int off = 32; off; off >>= 1) {
         const float o = __shfl_xor(top, off, 64);
@@ -297,10 +388,8 @@ __device__ __forceinline__ void histogram(const SampleArgs &a, const Row &r, con
     else
         walk(x, lo, hi, a.vec, [&](float v, int) {
             const int bin = bin_of(v, r);
-            if (bin < kBins) {
-                atomicAdd(&sh.count[bin], 1u);
+            if (bin < kBins)
                 atomicAdd(reinterpret_cast<unsigned long long *>(&sh.mass[bin]), fixed(weight(v, r, sh.roots)));
-            }
         });
 }
 
@@ -341,23 +430,28 @@ __device__ __forceinline__ double gather(const SampleArgs &a, const Row &r, cons
 {
     double sum = 0.0;
     const int lane = threadIdx.x & 63;
+    auto add = [&](float v) {
+        const double w = weight(v, r, sh.roots);
+        sum += w >= r.min_p ? w : 0.0;
+    };
+    Queue queue{sh.queue[wave()]};
+    if (r.kind == PLAIN) {
+        if (r.min_p > 0.0)   // few pass it, as a rule: their weights are taken 64 at a time
+            walk(x, lo, hi, a.vec, [&](float v, int) { queue.push(v, v >= r.least, add); });
+        else
+            walk(x, lo, hi, a.vec, [&](float v, int) {
+                const double w = weight(v, r, sh.roots);
+                sum += v >= r.floor ? w : 0.0;
+            });
+        queue.rest(add);
+        return wave_sum(sum);
+    }
+    const bool share = r.kind == TOP_P && end > 0;
+    const float from = bin_floor(end < kBins ? end : kBins - 1, r);
+    const float past = share ? bin_floor(end - 1, r) : 0.0f, least = fmaxf(past, r.least);
     walk(x, lo, hi, a.vec, [&](float v, int i) {
-        bool in = false, candidate = false;
-        if (r.kind == PLAIN) {
-            in = v > -kInf;
-        } else {
-            const int bin = bin_of(v, r);
-            if (r.kind == TOP_K) {
-                candidate = bin <= end && bin < kBins;
-            } else {
-                in = bin < end;
-                candidate = bin == end && bin < kBins;
-            }
-        }
-        if (in) {
-            const double w = weight(v, r, sh.roots);
-            sum += w >= r.min_p ? w : 0.0;
-        }
+        if (share) queue.push(v, v >= least, add);
+        const bool candidate = v >= from && !(share && v >= past);
         const uint64_t who = __ballot(candidate);
         if (who) {
             uint32_t at = 0;
@@ -366,6 +460,7 @@ __device__ __forceinline__ double gather(const SampleArgs &a, const Row &r, cons
             if (candidate && at < kList) list[at] = (static_cast<uint64_t>(~key_of(v)) << 32) | static_cast<uint32_t>(i);
         }
     });
+    queue.rest(add);
     return wave_sum(sum);
 }
 
@@ -416,7 +511,7 @@ __device__ __forceinline__ void pick(const SampleArgs &a, const Row &r, int64_t 
     const int i0 = lo + static_cast<int>(threadIdx.x) * per, i1 = i0 + per < hi ? i0 + per : hi;
     auto weight_at = [&](int i) {
         const float v = static_cast<float>(x[i]);
-        if (v == -kInf || !kept(v, i, e)) return 0.0;
+        if (!(v >= r.floor) || !kept(v, i, e)) return 0.0;
         const double w = weight(v, r, sh.roots);
         return w >= r.min_p ? w : 0.0;
     };
@@ -424,31 +519,30 @@ __device__ __forceinline__ void pick(const SampleArgs &a, const Row &r, int64_t 
     for (int i = i0; i < i1; ++i) own += weight_at(i);
     const double ahead = start + scan_block(own, sh.wd, all);
     if (threadIdx.x == 0) {
-        sh.at = a.vocab;
+        sh.at = kThreads;
         sh.last = -1;
     }
     __syncthreads();
-    int at = -1, last = -1;
-    double run = ahead, w_at = 0.0, w_last = 0.0;
-    if (own > 0.0)
-        for (int i = i0; i < i1; ++i) {
-            const double w = weight_at(i);
-            if (!(w > 0.0)) continue;
-            run += w;
-            last = i;
-            w_last = w;
-            if (run > target) {
-                at = i;
-                w_at = w;
-                break;
-            }
-        }
-    if (at >= 0) atomicMin(&sh.at, at);
-    if (last >= 0) atomicMax(&sh.last, last);
+    const int me = static_cast<int>(threadIdx.x);
+    if (own > 0.0) {
+        if (ahead + own > target) atomicMin(&sh.at, me);
+        atomicMax(&sh.last, me);
+    }
     __syncthreads();
-    const int found = sh.at;
-    if (at >= 0 && at == found) emit(a, b, at, static_cast<float>(log(w_at / total)));
-    if (found == a.vocab && last >= 0 && last == sh.last) emit(a, b, last, static_cast<float>(log(w_last / total)));
+    // the first thread whose places pass the target (the last with any, where rounding has
+    // put it past all of them) finds the place: its last one, if none passes it
+    if (me != (sh.at < kThreads ? sh.at : sh.last)) return;
+    int at = -1;
+    double run = ahead, w_at = 0.0;
+    for (int i = i0; i < i1; ++i) {
+        const double w = weight_at(i);
+        if (!(w > 0.0)) continue;
+        run += w;
+        at = i;
+        w_at = w;
+        if (run > target) break;
+    }
+    emit(a, b, at, static_cast<float>(log(w_at / total)));
 }
 
 template <typename T>
@@ -461,7 +555,7 @@ __device__ __forceinline__ void pick_first(const SampleArgs &a, const Row &r, in
     const int lo = wv * per, hi = lo + per < a.vocab ? lo + per : a.vocab;
     int first = a.vocab;
     walk(x, lo, hi, a.vec, [&](float v, int i) {
-        if (v == r.top && i < first) first = i;
+        if (v == r.max && i < first) first = i;
     });
     if (first < a.vocab) atomicMin(&sh.at, first);
     __syncthreads();
@@ -474,28 +568,28 @@ struct Four {
     double w[4], before;
 };
 
-__device__ __forceinline__ Four weights4(const Row &r, int n, Shared &sh, double &all, bool by_index)
+__device__ __forceinline__ Four weights4(const Row &r, const uint64_t *list, int n, Shared &sh, double &all, bool by_index)
 {
     Four f;
     double sum = 0.0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int i = 4 * threadIdx.x + e;
-        const uint64_t c = sh.list[i < n ? i : 0];
+        const uint64_t c = list[i < n ? i : 0];
         const uint32_t key = by_index ? ~static_cast<uint32_t>(c) : ~static_cast<uint32_t>(c >> 32);
-        f.w[e] = i < n ? weight(of_key(key), r, sh.roots) : 0.0;
+        f.w[e] = i < n && c != ~0ull ? weight(of_key(key), r, sh.roots) : 0.0;
         sum += f.w[e];
     }
     f.before = scan_block(sum, sh.wd, all);
     return f;
 }
 
-__device__ __forceinline__ int pad_list(int n, Shared &sh)
+__device__ __forceinline__ int pad_list(uint64_t *list, int n)
 {
     int size = 64;
     while (size < n) size *= 2;
     __syncthreads();
-    for (int i = n + threadIdx.x; i < size; i += kThreads) sh.list[i] = ~0ull;
+    for (int i = n + threadIdx.x; i < size; i += kThreads) list[i] = ~0ull;
     return size;
 }
 
@@ -519,13 +613,95 @@ __device__ __forceinline__ int cut(const Four &f, int n, double ahead, double wa
     return sh.at;
 }
 
+// The edge of top-p among the n candidates, unsorted: the last that is entered with less
+// than `want` of the weight ahead of it (of them: `ahead` and the ones before), the first
+// at least.  Histograms over their order narrow it to a few, which are sorted.
+__device__ __forceinline__ Edge select(const Row &r, int n, double ahead, double want, Shared &sh)
+{
+    __syncthreads();   // (the histogram has been read)
+    uint64_t lo = 0, hi = ~0ull;   // the ones in question
+    uint64_t *few = sh.mass;
+    int left = n;
+    while (left > kCounted) {
+        uint64_t least = ~0ull, most = 0;
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            const uint64_t c = sh.list[i];
+            if (c < lo || c > hi) continue;
+            least = c < least ? c : least;
+            most = c > most ? c : most;
+        }
+        for (int off = 32; off; off >>= 1) {
+            const uint64_t o = __shfl_xor(least, off, 64), p = __shfl_xor(most, off, 64);
+            least = o < least ? o : least;
+            most = p > most ? p : most;
+        }
+        __syncthreads();
+        if ((threadIdx.x & 63) == 0) {
+            sh.wu[wave()] = least;
+            sh.wd[wave()] = __longlong_as_double(static_cast<long long>(most));
+        }
+        for (int i = threadIdx.x; i < kBins; i += kThreads) {
+            sh.count[i] = 0;
+            sh.mass[i] = 0;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+            const uint64_t o = sh.wu[w], p = static_cast<uint64_t>(__double_as_longlong(sh.wd[w]));
+            least = o < least ? o : least;
+            most = p > most ? p : most;
+        }
+        int shift = 0;
+        while (((most - least) >> shift) >= kBins) ++shift;
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            const uint64_t c = sh.list[i];
+            if (c < lo || c > hi) continue;
+            const int bin = static_cast<int>((c - least) >> shift);
+            atomicAdd(&sh.count[bin], 1u);
+            atomicAdd(reinterpret_cast<unsigned long long *>(&sh.mass[bin]),
+                      fixed(weight(of_key(~static_cast<uint32_t>(c >> 32)), r, sh.roots)));
+        }
+        if (threadIdx.x == 0) sh.bin = -1;
+        __syncthreads();
+        const int b = 2 * threadIdx.x;
+        const uint64_t v0 = sh.mass[b], v1 = sh.mass[b + 1];
+        const uint32_t c0 = sh.count[b], c1 = sh.count[b + 1];
+        uint64_t all;
+        const uint64_t sum = scan_block(v0 + v1, sh.wu, all);
+        auto less = [&](uint64_t m) { return ahead + unfixed(m) < want; };
+        if (c1 && less(sum + v0)) atomicMax(&sh.bin, b + 1);
+        else if (c0 && less(sum)) atomicMax(&sh.bin, b);
+        __syncthreads();
+        const int bin = sh.bin < 0 ? 0 : sh.bin;   // (the least is in the first)
+        if (b == (bin & ~1)) sh.ahead = bin & 1 ? sum + v0 : sum;
+        __syncthreads();
+        ahead += unfixed(sh.ahead);
+        lo = least + (static_cast<uint64_t>(bin) << shift);
+        hi = lo + ((1ull << shift) - 1);
+        left = static_cast<int>(sh.count[bin]);
+        __syncthreads();   // (the next histogram, or the few, take its place)
+    }
+    if (threadIdx.x == 0) sh.n = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint64_t c = sh.list[i];
+        if (c >= lo && c <= hi) few[atomicAdd(&sh.n, 1u)] = c;
+    }
+    sort_list(few, pad_list(few, left));
+    double all;
+    const Four f = weights4(r, few, left, sh, all, false);
+    const int m = cut(f, left, ahead, want, sh);
+    const uint64_t c = few[m > 1 ? m - 1 : 0];
+    return Edge{~static_cast<uint32_t>(c >> 32), static_cast<int>(static_cast<uint32_t>(c))};
+}
+
 // Top-k: the list holds all candidates, n of them; top-p, min-p and the draw are done on it
 __device__ __forceinline__ void finish_list(const SampleArgs &a, const Row &r, int64_t b, int n, Shared &sh)
 {
-    sort_list(sh.list, pad_list(n, sh));
+    sort_list(sh.list, pad_list(sh.list, n));
     n = n < r.top_k ? n : r.top_k;
     double all;
-    Four f = weights4(r, n, sh, all, false);
+    Four f = weights4(r, sh.list, n, sh, all, false);
     if (r.top_p < 1.0) {
         const int m = cut(f, n, 0.0, r.top_p * all, sh);
         n = m > 1 ? m : 1;
@@ -540,8 +716,8 @@ __device__ __forceinline__ void finish_list(const SampleArgs &a, const Row &r, i
             sh.list[i] = f.w[e] >= r.min_p ? (c << 32) | (c >> 32) : ~0ull;
         }
     }
-    sort_list(sh.list, pad_list(n, sh));
-    f = weights4(r, n, sh, all, true);   // (the dropped ones' key is a NaN's: no weight)
+    sort_list(sh.list, pad_list(sh.list, n));
+    f = weights4(r, sh.list, n, sh, all, true);   // (none of the dropped ones)
     const double target = static_cast<double>(r.u) * all;
     if (threadIdx.x == 0) sh.at = n;
     __syncthreads();
@@ -593,7 +769,7 @@ __device__ __forceinline__ Edge narrow(const SampleArgs &a, const Row &r, const 
         __syncthreads();
         walk(x, i0, i1, a.vec, [&](float v, int i) {
             const uint32_t k = key_of(v);
-            if (v == -kInf || k < lo || k > hi || !kept(v, i, before)) return;
+            if (!(v >= r.floor) || k < lo || k > hi || !kept(v, i, before)) return;
             const int bin = (hi - k) >> shift;
             atomicAdd(&sh.count[bin], 1u);
             if constexpr (MASS)
@@ -637,14 +813,14 @@ __device__ __forceinline__ Edge narrow(const SampleArgs &a, const Row &r, const 
             __syncthreads();
             walk(x, i0, i1, a.vec, [&](float v, int i) {
                 const uint32_t k = key_of(v);
-                if (v == -kInf || k < lo || k > hi || !kept(v, i, before)) return;
+                if (!(v >= r.floor) || k < lo || k > hi || !kept(v, i, before)) return;
                 sh.list[atomicAdd(&sh.n, 1u)] = (static_cast<uint64_t>(~k) << 32) | static_cast<uint32_t>(i);
             });
-            sort_list(sh.list, pad_list(n, sh));
+            sort_list(sh.list, pad_list(sh.list, n));
             int m;
             if constexpr (MASS) {
                 double sum4;
-                m = cut(weights4(r, n, sh, sum4, false), n, ahead, want, sh);
+                m = cut(weights4(r, sh.list, n, sh, sum4, false), n, ahead, want, sh);
             } else {
                 m = static_cast<int>(want - ahead);
                 m = m < n ? m : n;
@@ -698,7 +874,7 @@ __device__ __forceinline__ double kept_sums(const SampleArgs &a, const Row &r, c
         double sum = 0.0;
         const int lo = s * a.share, hi = lo + a.share < a.vocab ? lo + a.share : a.vocab;
         walk(x, lo, hi, a.vec, [&](float v, int i) {
-            if (v == -kInf || !kept(v, i, e)) return;
+            if (!(v >= r.floor) || !kept(v, i, e)) return;
             const double w = weight(v, r, sh.roots);
             sum += w >= r.min_p ? w : 0.0;
         });
@@ -716,7 +892,7 @@ template <typename T>
 __device__ __forceinline__ void solve_alone(const SampleArgs &a, Row r, int64_t b, const T *x, int subs, Shared &sh)
 {
     Edge e{0, a.vocab};
-    const uint32_t top = key_of(r.top);
+    const uint32_t top = key_of(r.max);
     const double min_p = r.min_p;
     if (r.top_k) e = narrow<T, false>(a, r, x, 1, top, 0.0, static_cast<double>(r.top_k), e, sh);
     if (r.top_p < 1.0) {
@@ -753,42 +929,25 @@ __device__ __forceinline__ void finish(const SampleArgs &a, const Row &r, int64_
         finish_list(a, r, b, n, sh);
         return;
     }
-    // top-p: the last of the sorted candidates that stays is the edge
-    sort_list(sh.list, pad_list(n, sh));
-    double all;
-    const Four f = weights4(r, n, sh, all, false);
-    const double ahead = unfixed(sh.ahead);
-    int m = cut(f, n, ahead, want, sh);
-    m = m > 1 ? m : 1;
-    const uint64_t c = sh.list[m - 1];
-    const Edge e{~static_cast<uint32_t>(c >> 32), static_cast<int>(static_cast<uint32_t>(c))};
+    const Edge e = select(r, n, unfixed(sh.ahead), want, sh);
+    // the weights of the kept ones into the sums of their shares: up to 2^12 multiples
+    // of 2^-51, whose sum no order changes
+    uint64_t *more = reinterpret_cast<uint64_t *>(sh.count);
+    static_assert(sizeof(sh.count) >= sizeof(uint64_t) * kMaxSlices * kWaves, "one for each share");
     __syncthreads();
-    // their weights into the sums of their shares, share by share in the candidates' order
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int i = 4 * threadIdx.x + k;
-        if (i < m) {
-            const uint64_t v = sh.list[i];
-            sh.list[i] = (v << 32) | (v >> 32);
-        }
-    }
-    sort_list(sh.list, pad_list(m, sh));
-    double *ws = reinterpret_cast<double *>(sh.mass);   // (the histogram has been read)
-    constexpr int kRoom = (sizeof(sh.mass) + sizeof(sh.count)) / sizeof(double);
-    auto weight_of = [&](int i) {
-        const double w = weight(of_key(~static_cast<uint32_t>(sh.list[i])), r, sh.roots);
-        return w >= r.min_p ? w : 0.0;
-    };
-    auto share_of = [&](int i) { return static_cast<int>(static_cast<uint32_t>(sh.list[i] >> 32) / a.share); };
-    for (int i = threadIdx.x; i < m && i < kRoom; i += kThreads) ws[i] = weight_of(i);
+    if (threadIdx.x < static_cast<unsigned>(subs)) more[threadIdx.x] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < m; i += kThreads) {
-        const int s = share_of(i);
-        if (i > 0 && share_of(i - 1) == s) continue;
-        double sum = sh.sub[s];   // the first of its share adds them up
-        for (int j = i; j < m && share_of(j) == s; ++j) sum += j < kRoom ? ws[j] : weight_of(j);
-        sh.sub[s] = sum;
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint64_t c = sh.list[i];
+        const float v = of_key(~static_cast<uint32_t>(c >> 32));
+        const int at = static_cast<int>(static_cast<uint32_t>(c));
+        const double w = weight(v, r, sh.roots);
+        if (kept(v, at, e) && w >= r.min_p)
+            atomicAdd(reinterpret_cast<unsigned long long *>(&more[at / a.share]),
+                      static_cast<unsigned long long>(w * 0x1p51));
     }
+    __syncthreads();
+    if (threadIdx.x < static_cast<unsigned>(subs)) sh.sub[threadIdx.x] += static_cast<double>(more[threadIdx.x]) * 0x1p-51;
     __syncthreads();
     pick(a, r, b, x, subs, e, sh);
 }
@@ -800,6 +959,18 @@ __device__ __forceinline__ void clear_histogram(Shared &sh)
         sh.mass[i] = 0;
     }
     if (threadIdx.x == 0) sh.n = 0;
+}
+
+// Whole workgroup: a bin up to which there are top_k logits at least: that many of the
+// threads' largest ones (`own`) are.  About as many logits are, where top_k is half of the
+// threads or less and they lie anywhere.  Whether there is such a bin.
+__device__ __forceinline__ bool end_of_maxima(const Row &r, float own, Shared &sh)
+{
+    const int bin = bin_of(own, r);
+    if (bin < kBins) atomicAdd(&sh.count[bin], 1u);
+    __syncthreads();
+    end_bin(r, sh.count, sh.mass, sh);
+    return sh.bin < kBins;
 }
 
 // top_p of the histogram's weight
@@ -819,7 +990,8 @@ template <typename T> __global__ void __launch_bounds__(kThreads) sample_row_ker
     const int hi = lo + a.share < a.vocab ? lo + a.share : a.vocab;
     fill_roots(sh.roots);
     clear_histogram(sh);
-    const Row r = settings(a, b, slice_top(a, x, lo, hi, sh));
+    float own;
+    const Row r = settings(a, b, slice_top(a, x, lo, hi, sh, own));
     if (r.kind == DONE) {
         if (threadIdx.x == 0) emit(a, b, -1, -kInf);
         return;
@@ -829,7 +1001,13 @@ template <typename T> __global__ void __launch_bounds__(kThreads) sample_row_ker
         return;
     }
     double want = 0.0;
-    if (r.kind != PLAIN) {
+    bool known = r.kind == PLAIN;
+    if (r.kind == TOP_K && r.top_k <= kThreads / 2) {
+        known = end_of_maxima(r, own, sh);
+        if (!known) clear_histogram(sh);
+        __syncthreads();
+    }
+    if (!known) {
         histogram(a, r, x, lo, hi, sh);
         __syncthreads();
         end_bin(r, sh.count, sh.mass, sh);
@@ -867,13 +1045,20 @@ __device__ __forceinline__ float row_top(const SampleArgs &a, const Slot &s)
     return top;
 }
 
+// Whether top_k's end comes of the groups' largest logits (as end_of_maxima says), and not
+// of a histogram of all
+__device__ __forceinline__ bool by_maxima(const SampleArgs &a, const Row &r) { return r.top_k <= kGroups / 2 * a.slices; }
+
 template <typename T> __global__ void __launch_bounds__(kThreads) sample_top_kernel(SampleArgs a)
 {
     __shared__ Shared sh;
     const Piece p = piece(a);
     const Slot s = slot_of(a, p.b);
-    const float top = slice_top(a, static_cast<const T *>(a.logits) + p.b * a.stride, p.lo, p.hi, sh);
+    float own;
+    const float top = slice_top(a, static_cast<const T *>(a.logits) + p.b * a.stride, p.lo, p.hi, sh, own);
     if (threadIdx.x == 0) s.top[p.slice] = top;
+    for (int off = 1; off < kThreads / kGroups; off <<= 1) own = fmaxf(own, __shfl_xor(own, off, 64));
+    if (threadIdx.x % (kThreads / kGroups) == 0) s.maxima[p.slice * kGroups + threadIdx.x / (kThreads / kGroups)] = own;
     for (int i = p.slice * kThreads + threadIdx.x; i < kBins; i += a.slices * kThreads) {
         s.count[i] = 0;
         s.mass[i] = 0;
@@ -887,16 +1072,15 @@ template <typename T> __global__ void __launch_bounds__(kThreads) sample_bins_ke
     const Piece p = piece(a);
     const Slot s = slot_of(a, p.b);
     const Row r = settings(a, p.b, row_top(a, s));
-    if (r.kind != TOP_K && r.kind != TOP_P) return;
+    if ((r.kind != TOP_K || by_maxima(a, r)) && r.kind != TOP_P) return;
     fill_roots(sh.roots);
     clear_histogram(sh);
     __syncthreads();
     histogram(a, r, static_cast<const T *>(a.logits) + p.b * a.stride, p.lo, p.hi, sh);
     __syncthreads();
     for (int i = threadIdx.x; i < kBins; i += kThreads) {
-        if (!sh.count[i]) continue;
-        atomicAdd(&s.count[i], sh.count[i]);
-        if (r.kind == TOP_P) atomicAdd(reinterpret_cast<unsigned long long *>(&s.mass[i]), sh.mass[i]);
+        if (r.kind == TOP_K && sh.count[i]) atomicAdd(&s.count[i], sh.count[i]);
+        if (r.kind == TOP_P && sh.mass[i]) atomicAdd(reinterpret_cast<unsigned long long *>(&s.mass[i]), sh.mass[i]);
     }
 }
 
@@ -908,8 +1092,19 @@ template <typename T> __global__ void __launch_bounds__(kThreads) sample_gather_
     const Row r = settings(a, p.b, row_top(a, s));
     if (r.kind == DONE || r.kind == GREEDY) return;
     fill_roots(sh.roots);
+    if (r.kind == TOP_K && by_maxima(a, r)) {
+        clear_histogram(sh);
+        __syncthreads();
+        for (int i = threadIdx.x; i < kGroups * a.slices; i += kThreads) {
+            const int bin = bin_of(s.maxima[i], r);
+            if (bin < kBins) atomicAdd(&sh.count[bin], 1u);
+        }
+        __syncthreads();
+        end_bin(r, sh.count, sh.mass, sh);
+    } else if (r.kind != PLAIN) {
+        end_bin(r, s.count, s.mass, sh);
+    }
     __syncthreads();
-    if (r.kind != PLAIN) end_bin(r, s.count, s.mass, sh);
     const double sum = gather(a, r, static_cast<const T *>(a.logits) + p.b * a.stride, p.lo, p.hi, sh.bin, sh, s.n, s.list);
     if ((threadIdx.x & 63) == 0) s.sub[p.slice * kWaves + wave()] = sum;
 }
@@ -936,8 +1131,10 @@ template <typename T> __global__ void __launch_bounds__(kThreads) sample_pick_ke
     if (r.kind != PLAIN) {
         for (int i = threadIdx.x; i < n && i < kList; i += kThreads) sh.list[i] = s.list[i];
         __syncthreads();
-        end_bin(r, s.count, s.mass, sh);
-        if (r.kind == TOP_P) want = wanted(r, s.mass, sh);
+        if (r.kind == TOP_P) {
+            end_bin(r, s.count, s.mass, sh);
+            want = wanted(r, s.mass, sh);
+        }
     }
     __syncthreads();
     finish(a, r, b, x, subs, n, want, sh);
@@ -954,7 +1151,7 @@ SampleGeom sample_geometry(const mgs_sample_desc &d)
     const int64_t step = 64 * (d.dtype == MGS_BF16 ? 8 : 4);   // what a wave reads at once
     const int64_t steps = (d.vocab + step - 1) / step;
     // workgroups for every CU, no more than there are waves' steps
-    int64_t s = std::min<int64_t>((steps + kWaves - 1) / kWaves, d.B > 0 ? 512 / d.B : 1);
+    int64_t s = std::min<int64_t>((steps + kWaves - 1) / kWaves, d.B > 0 ? 256 / d.B : 1);
     s = std::max<int64_t>(1, std::min<int64_t>(s, kMaxSlices));
     g.slices = static_cast<int>(s);
     g.share = static_cast<int>((steps + s * kWaves - 1) / (s * kWaves) * step);
@@ -969,7 +1166,9 @@ template <typename T> hipError_t run(const SampleArgs &a, unsigned rows, hipStre
         return hipGetLastError();
     }
     const dim3 grid(rows * a.slices), block(kThreads);
-    const bool filters = a.top_k || a.top_p || (a.k0 > 0 && a.k0 < a.vocab) || a.p0 < 1.0f;
+    // one top_k for all rows that the groups' largest logits serve needs no histogram
+    const bool k = a.k0 > 0 && a.k0 < a.vocab;
+    const bool filters = a.top_k || (k ? a.k0 > kGroups / 2 * a.slices : a.top_p || a.p0 < 1.0f);
     sample_top_kernel<T><<<grid, block, 0, s>>>(a);
     if (filters) sample_bins_kernel<T><<<grid, block, 0, s>>>(a);
     sample_gather_kernel<T><<<grid, block, 0, s>>>(a);
