@@ -31,7 +31,7 @@ namespace mgs {
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kBins = 2048;         // of 1/64: weights below e^-32 are less than a step
+constexpr int kBinBits = 11, kBins = 1 << kBinBits;   // of 1/64: weights below e^-32 are less than a step
 constexpr float kPerUnit = 64.0f;
 constexpr int kList = 4096;         // candidates that are sorted
 constexpr int kFixed = 43;          // a weight's bits behind the point: 2^20 of them fit 64 bits
@@ -76,6 +76,7 @@ struct Row {
     float max, top;      // the largest logit; the same, the largest number where it is infinite
     float least;         // no smaller one passes min-p (the floor without it)
     float floor;         // what is below has no weight: -inf, or all but +inf
+    float nothing;       // what is below has a weight of less than 2^-1000, or is below the floor
     float inv;           // 1 / temperature
     double scale;        // log2 e / temperature
     double top_p, min_p;
@@ -95,6 +96,7 @@ __device__ __forceinline__ Row settings(const SampleArgs &a, int64_t b, float to
     r.floor = top == kInf ? kInf : -kMax;
     r.inv = 1.0f / tau;
     r.scale = 1.4426950408889634 / static_cast<double>(tau);
+    r.nothing = fmaxf(r.floor, static_cast<float>(static_cast<double>(r.top) - 1000.0 / r.scale));
     r.top_k = k > 0 && k < a.vocab ? k : 0;
     r.top_p = p < 1.0f ? (p > 0.0f ? p : 0.0f) : 1.0;
     r.min_p = m > 0.0f ? (m < 1.0f ? m : 1.0f) : 0.0f;
@@ -116,21 +118,25 @@ __device__ __forceinline__ void fill_roots(double *roots)
     if (threadIdx.x < kRoots) roots[threadIdx.x] = exp2(static_cast<double>(threadIdx.x) / kRoots);
 }
 
-// e^((x - top) / temperature) in fp64, x from the row's floor on: y = n + j/256 + s,
+// e^((x - top) / temperature) in fp64, x not above the largest: y = n + j/256 + s,
 // |s| <= 1/512, 2^s by its series to s^4 (the next term is below 2^-54).  What is below
-// 2^-999 is nothing.  (No branch: neighbouring values' chains run side by side.)
+// r.nothing is nothing.  No branches: neighbouring values' chains run side by side (with a
+// branch for that, 256 rows of 128000 without filters took 64 us, now 52; the fp64
+// operations, eight cycles each, are two thirds of it).
 __device__ __forceinline__ double weight(float x, const Row &r, const double *roots)
 {
     constexpr double kShift = 1.5 * 17592186044416.0;   // 2^44: adding it rounds to 1/256
-    const double y = fmax((static_cast<double>(fminf(x, kMax)) - static_cast<double>(r.top)) * r.scale, -1000.0);
+    const bool some = x >= r.nothing;
+    const float v = some ? fminf(x, kMax) : r.top;
+    const double y = (static_cast<double>(v) - static_cast<double>(r.top)) * r.scale;
     const double z = y + kShift, s = y - (z - kShift);
     const int k = __double2loint(z);
     double q = __builtin_fma(9.6181291076284772e-3, s, 5.5504108664821580e-2);
     q = __builtin_fma(q, s, 2.4022650695910071e-1);
     q = __builtin_fma(q, s, 6.9314718055994531e-1);
     const double root = roots[k & (kRoots - 1)], w = __builtin_fma(q * s, root, root);
-    const double o = __hiloint2double(__double2hiint(w) + ((k >> 8) << 20), __double2loint(w));
-    return o > 0x1p-999 ? o : 0.0;
+    const int hi = __double2hiint(w) + ((k >> 8) << 20), lo = __double2loint(w);
+    return __hiloint2double(some ? hi : 0, some ? lo : 0);
 }
 
 // w <= 1 as a multiple of 2^-43
@@ -181,9 +187,10 @@ template <> struct Wide<__bf16> {
     static constexpr int N = 8;
 };
 
-// f(value, index) for the places lo..hi-1, hi <= V, of a row, spread over a wave's
-// lanes; lo is a multiple of what it reads at once.  -inf stands for places past hi.
-template <typename T, typename F> __device__ __forceinline__ void walk(const T *x, int lo, int hi, bool vec, F f)
+// f(values, index of the first) for the places lo..hi-1, hi <= V, of a row, four
+// neighbours a lane at a time; lo is a multiple of what a wave reads at once.  -inf stands
+// for places past hi.  The wave stays whole.
+template <typename T, typename F> __device__ __forceinline__ void walk4(const T *x, int lo, int hi, bool vec, F f)
 {
     constexpr int N = Wide<T>::N, U = 4;
     const int lane = threadIdx.x & 63;
@@ -205,9 +212,18 @@ template <typename T, typename F> __device__ __forceinline__ void walk(const T *
         for (int j = 0; j < U; ++j) {
             if (base + j * 64 * N >= hi) break;
 #pragma unroll
-            for (int e = 0; e < N; ++e) f(v[j][e], base + (j * 64 + lane) * N + e);
+            for (int e = 0; e < N; e += 4) f(&v[j][e], base + (j * 64 + lane) * N + e);
         }
     }
+}
+
+// The same one by one: f(value, index)
+template <typename T, typename F> __device__ __forceinline__ void walk(const T *x, int lo, int hi, bool vec, F f)
+{
+    walk4(x, lo, hi, vec, [&](const float *v, int i) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f(v[e], i + e);
+    });
 }
 
 // What a wave's lanes have written to LDS is there for its others (its LDS accesses run
@@ -215,25 +231,33 @@ template <typename T, typename F> __device__ __forceinline__ void walk(const T *
 __device__ __forceinline__ void wave_order() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
 
 // Values of a wave's lanes that wait until there are 64 of them, so that what is done
-// with few of a row's values is done with whole waves
+// with few of a row's values is done with whole waves.  Four a lane are taken in at once.
+constexpr int kQueue = 63 + 4 * 64;
+
 struct Queue {
-    float *held;   // 128 of the wave's own, in LDS
+    float *held;   // kQueue of the wave's own, in LDS
     int n = 0;
 
-    template <typename F> __device__ __forceinline__ void push(float v, bool in, F f)
+    template <typename P, typename F> __device__ __forceinline__ void push4(const float *v, P in, F f)
     {
-        const uint64_t who = __ballot(in);
-        if (!who) return;
+        uint64_t who[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) who[e] = __ballot(in(v[e]));
+        if ((who[0] | who[1] | who[2] | who[3]) == 0) return;
         const int lane = threadIdx.x & 63;
-        if (in) held[n + __popcll(who & ((1ull << lane) - 1))] = v;
-        n += __popcll(who);
-        if (n >= 64) {
-            n -= 64;
-            wave_order();
-            const float x = held[n + lane];
-            wave_order();
-            f(x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int before = __builtin_amdgcn_mbcnt_hi(static_cast<uint32_t>(who[e] >> 32),
+                                                         __builtin_amdgcn_mbcnt_lo(static_cast<uint32_t>(who[e]), 0));
+            if (in(v[e])) held[n + before] = v[e];
+            n += __popcll(who[e]);
         }
+        wave_order();
+        for (; n >= 64;) {
+            n -= 64;
+            f(held[n + lane]);
+        }
+        wave_order();
     }
     template <typename F> __device__ __forceinline__ void rest(F f)
     {
@@ -318,7 +342,6 @@ struct Shared {
     uint64_t list[kList];
     double sub[kMaxSlices * kWaves];
     double roots[kRoots];
-    float queue[kWaves][128];
     double wd[kWaves];
     uint64_t wu[kWaves];
     float top[kWaves];
@@ -386,10 +409,18 @@ __device__ __forceinline__ void histogram(const SampleArgs &a, const Row &r, con
             if (bin < kBins) atomicAdd(&sh.count[bin], 1u);
         });
     else
-        walk(x, lo, hi, a.vec, [&](float v, int) {
-            const int bin = bin_of(v, r);
-            if (bin < kBins)
-                atomicAdd(reinterpret_cast<unsigned long long *>(&sh.mass[bin]), fixed(weight(v, r, sh.roots)));
+        walk4(x, lo, hi, a.vec, [&](const float *v, int) {
+            // all four chains side by side, ahead of the branches
+            int bin[4];
+            uint64_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                bin[e] = bin_of(v[e], r);
+                w[e] = fixed(weight(v[e], r, sh.roots));
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (bin[e] < kBins) atomicAdd(reinterpret_cast<unsigned long long *>(&sh.mass[bin[e]]), w[e]);
         });
 }
 
@@ -434,10 +465,14 @@ __device__ __forceinline__ double gather(const SampleArgs &a, const Row &r, cons
         const double w = weight(v, r, sh.roots);
         sum += w >= r.min_p ? w : 0.0;
     };
-    Queue queue{sh.queue[wave()]};
+    // (the histogram has been read)
+    static_assert(sizeof(sh.mass) + sizeof(sh.count) >= sizeof(float) * kQueue * kWaves, "room for the queues");
+    Queue queue{reinterpret_cast<float *>(sh.mass) + wave() * kQueue};
     if (r.kind == PLAIN) {
         if (r.min_p > 0.0)   // few pass it, as a rule: their weights are taken 64 at a time
-            walk(x, lo, hi, a.vec, [&](float v, int) { queue.push(v, v >= r.least, add); });
+            walk4(x, lo, hi, a.vec, [&](const float *v, int) {
+                queue.push4(v, [&](float y) { return y >= r.least; }, add);
+            });
         else
             walk(x, lo, hi, a.vec, [&](float v, int) {
                 const double w = weight(v, r, sh.roots);
@@ -449,15 +484,19 @@ __device__ __forceinline__ double gather(const SampleArgs &a, const Row &r, cons
     const bool share = r.kind == TOP_P && end > 0;
     const float from = bin_floor(end < kBins ? end : kBins - 1, r);
     const float past = share ? bin_floor(end - 1, r) : 0.0f, least = fmaxf(past, r.least);
-    walk(x, lo, hi, a.vec, [&](float v, int i) {
-        if (share) queue.push(v, v >= least, add);
-        const bool candidate = v >= from && !(share && v >= past);
-        const uint64_t who = __ballot(candidate);
-        if (who) {
+    auto candidate = [&](float y) { return y >= from && !(share && y >= past); };
+    walk4(x, lo, hi, a.vec, [&](const float *v, int i) {
+        if (share) queue.push4(v, [&](float y) { return y >= least; }, add);
+        if (__ballot(candidate(v[0]) || candidate(v[1]) || candidate(v[2]) || candidate(v[3])) == 0) return;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint64_t who = __ballot(candidate(v[e]));
+            if (!who) continue;
             uint32_t at = 0;
             if (lane == __builtin_ctzll(who)) at = atomicAdd(n, static_cast<uint32_t>(__popcll(who)));
             at = __builtin_amdgcn_readlane(at, __builtin_ctzll(who)) + __popcll(who & ((1ull << lane) - 1));
-            if (candidate && at < kList) list[at] = (static_cast<uint64_t>(~key_of(v)) << 32) | static_cast<uint32_t>(i);
+            if (candidate(v[e]) && at < kList)
+                list[at] = (static_cast<uint64_t>(~key_of(v[e])) << 32) | static_cast<uint32_t>(i + e);
         }
     });
     queue.rest(add);
@@ -651,8 +690,7 @@ __device__ __forceinline__ Edge select(const Row &r, int n, double ahead, double
             least = o < least ? o : least;
             most = p > most ? p : most;
         }
-        int shift = 0;
-        while (((most - least) >> shift) >= kBins) ++shift;
+        const int bits = 64 - __builtin_clzll((most - least) | 1), shift = bits > kBinBits ? bits - kBinBits : 0;
         for (int i = threadIdx.x; i < n; i += kThreads) {
             const uint64_t c = sh.list[i];
             if (c < lo || c > hi) continue;
@@ -759,8 +797,7 @@ __device__ __forceinline__ Edge narrow(const SampleArgs &a, const Row &r, const 
     const int i0 = wave() * per, i1 = i0 + per < a.vocab ? i0 + per : a.vocab;
     for (;;) {
         // histogram of lo..hi, largest first
-        int shift = 0;
-        while (((hi - lo) >> shift) >= kBins) ++shift;
+        const int bits = 32 - __builtin_clz((hi - lo) | 1), shift = bits > kBinBits ? bits - kBinBits : 0;
         __syncthreads();
         for (int i = threadIdx.x; i < kBins; i += kThreads) {
             sh.count[i] = 0;
@@ -1150,8 +1187,11 @@ SampleGeom sample_geometry(const mgs_sample_desc &d)
     SampleGeom g{};
     const int64_t step = 64 * (d.dtype == MGS_BF16 ? 8 : 4);   // what a wave reads at once
     const int64_t steps = (d.vocab + step - 1) / step;
-    // workgroups for every CU, no more than there are waves' steps
-    int64_t s = std::min<int64_t>((steps + kWaves - 1) / kWaves, d.B > 0 ? 256 / d.B : 1);
+    // Workgroups for every CU, no more than there are waves' steps.  Rows of up to four
+    // steps a wave stay with one (32000, bf16, all filters: 1 row 21 us, cut in four 26; 128
+    // rows of mixed settings 44, in two 55); longer ones are cut (8 rows of 128000: 52, whole
+    // or in four 72 and 57).
+    int64_t s = steps <= 4 * kWaves || d.B <= 0 ? 1 : std::min<int64_t>((steps + kWaves - 1) / kWaves, 256 / d.B);
     s = std::max<int64_t>(1, std::min<int64_t>(s, kMaxSlices));
     g.slices = static_cast<int>(s);
     g.share = static_cast<int>((steps + s * kWaves - 1) / (s * kWaves) * step);
