@@ -119,7 +119,7 @@ __device__ __forceinline__ int64_t order_of(int32_t id, int bits, int range)
 
 struct SortArgs {
     const void *ids;
-    int64_t n, vocab, d;
+    int64_t block, n, vocab, d;
     int bits, range;    // 2^bits workgroups, ids of each
     bool wide_ids;
     int64_t *count;     // ids inside the table
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
     __shared__ int64_t below[kSortWaves];
     __shared__ int32_t scan[kSortWaves];
     const int lane = threadIdx.x & 63, wv = wave();
-    const int32_t mask = (1 << a.bits) - 1, own = static_cast<int32_t>(blockIdx.x);
+    const int32_t mask = (1 << a.bits) - 1, own = static_cast<int32_t>(a.block + blockIdx.x);
     const int ids = a.range;   // (the last one may lie past the table)
     for (int i = threadIdx.x; i < kSortWaves * a.range; i += 64 * kSortWaves) at[i] = 0;
     __syncthreads();
@@ -487,8 +487,10 @@ hipError_t launch_embed_bwd(const EmbedGeom &g, const void *ids, bool wide_ids, 
     a.first = reinterpret_cast<int32_t *>(w + g.off_first);
     a.row = reinterpret_cast<int32_t *>(w + g.off_row);
     a.id = reinterpret_cast<int32_t *>(w + g.off_id);
-    sort_kernel<<<dim3(1u << g.bits), dim3(64 * kSortWaves), 0, s>>>(a);
-    const hipError_t e = hipGetLastError();
+    const hipError_t e = launch_sliced(int64_t(1) << g.bits, 64 * kSortWaves, [&](int64_t first, unsigned blocks) {
+        a.block = first;
+        sort_kernel<<<dim3(blocks), dim3(64 * kSortWaves), 0, s>>>(a);
+    });
     if (e != hipSuccess) return e;
     SumArgs b{};
     b.count = a.count;

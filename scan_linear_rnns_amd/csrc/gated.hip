@@ -59,8 +59,9 @@ template <typename T> struct Two;
 template <> struct Two<float> { using V = f32x2; };
 template <> struct Two<__bf16> { using V = bf2v; };
 
-// A lane's two channels, c and c + 1: byte offsets into a row of T, past the last
-// channel the last one's (that lane's results are not stored).
+// A lane's two channels, c and c + 1 of the d that its workgroup has: byte offsets from
+// the first of them, past the last channel the last one's (those results are not
+// stored).
 template <typename T, bool PAIRS> struct Lane {
     uint32_t at, next;
     bool in, both;
@@ -318,7 +319,8 @@ struct GatedArgs {
 struct Place {
     int64_t b;
     uint32_t group, j;   // j: tile in the direction of the pass
-    int c, d;          // this lane's first channel, of d
+    int64_t at;        // the workgroup's first channel
+    int c, d;          // of its d channels, this lane's first
     int64_t n;         // live steps of the sequence
 };
 
@@ -329,8 +331,9 @@ __device__ __forceinline__ Place place(const GatedArgs &a)
     p.group = blockIdx.x - p.j * a.l.groups;
     const uint32_t b = p.group / a.per_seq;
     p.b = b;
-    p.c = static_cast<int>(p.group - b * a.per_seq) * kGroup + 2 * (threadIdx.x & 63);
-    p.d = static_cast<int>(a.D);
+    p.at = static_cast<int64_t>(p.group - b * a.per_seq) * kGroup;
+    p.c = 2 * (threadIdx.x & 63);
+    p.d = static_cast<int>(a.D - p.at < kGroup ? a.D - p.at : kGroup);
     p.n = a.T;
     if (a.lengths) {
         const int64_t n = a.lengths[p.b];
@@ -384,7 +387,7 @@ __device__ __forceinline__ void rows(const void *base, const int64_t *stride, co
 {
     const int64_t step = stride[1] * static_cast<int64_t>(sizeof(T));
     const int64_t t = PLAIN || w.live > 0 ? w.t0 : p.n - 1;
-    const char *row = static_cast<const char *>(base) + p.b * stride[0] * static_cast<int64_t>(sizeof(T)) + t * step;
+    const char *row = static_cast<const char *>(base) + (p.b * stride[0] + p.at) * static_cast<int64_t>(sizeof(T)) + t * step;
 #pragma unroll
     for (int s = 0; s < N; ++s) {
         out[s] = lane.load(row);
@@ -397,7 +400,7 @@ template <typename T, int N, bool PLAIN, typename L, typename F>
 __device__ __forceinline__ void put_rows(void *base, const GatedArgs &a, const Place &p, const Steps &w, const L &lane, F f)
 {
     const int64_t step = a.D * static_cast<int64_t>(sizeof(T));
-    char *row = static_cast<char *>(base) + (p.b * a.T + w.t0) * step;
+    char *row = static_cast<char *>(base) + (p.b * a.T + w.t0) * step + p.at * static_cast<int64_t>(sizeof(T));
     if (!lane.in) return;
 #pragma unroll
     for (int s = 0; s < N; ++s) {
@@ -414,7 +417,7 @@ __device__ __forceinline__ void put_rows(void *base, const GatedArgs &a, const P
 template <int W> __device__ __forceinline__ void fill_slopes(const GatedArgs &a, const Place &p, Shared<W> &sh)
 {
     if (threadIdx.x < kGroup) {
-        const int64_t c = p.c - 2 * static_cast<int64_t>(threadIdx.x & 63) + threadIdx.x;
+        const int64_t c = p.at + threadIdx.x;
         sh.k[threadIdx.x] = slope2(a.lam[c < a.D ? c : a.D - 1], a.rate);
     }
 }
@@ -428,7 +431,7 @@ __device__ __forceinline__ f32x2 pass_on(const GatedArgs &a, const Place &p, Sha
     Launch ep{0, 0};
     if constexpr (MULTI) ep = epoch_begin(a.l.hd);
     f32x2 first = {0.0f, 0.0f};
-    if (from) first = load_f2(from + p.b * a.D, p.c, p.d);
+    if (from) first = load_f2(from + p.b * a.D + p.at, p.c, p.d);
     sh.A[pass][lane] = f32x2{1.0f, 1.0f};
     sh.H[pass][lane] = f32x2{0.0f, 0.0f};
     if (MULTI && threadIdx.x == 0) epoch_end(a.l.hd, ep, a.l.tiles * a.l.groups, sh.ticket);
@@ -483,25 +486,33 @@ __device__ __forceinline__ void fwd_tile(const GatedArgs &a, const Place &p, Sha
         Launch ep{0, 0};
         if constexpr (MULTI) ep = epoch_begin(a.l.hd);
         f32x2 first = {0.0f, 0.0f};
-        if (a.h0) first = load_f2(a.h0 + p.b * a.D, p.c, p.d);
+        if (a.h0) first = load_f2(a.h0 + p.b * a.D + p.at, p.c, p.d);
         fill_slopes(a, p, sh);
         __syncthreads();
         const f32x2 k = {sh.k[2 * lane], sh.k[2 * lane + 1]};
         f32x2 A = {1.0f, 1.0f}, H = {0.0f, 0.0f};
+        if (!PLAIN && w.live == 0) {   // (a short sequence: most of the tile's waves)
 #pragma unroll
-        for (int s = 0; s < C; ++s) {
-            const f32x2 x = wide(rx[s]), r = wide(rr[s]), i = wide(ri[s]);
-            const float start = !PLAIN && (w.fresh >> s) & 1 ? -__builtin_inff() : 0.0f;
-#pragma unroll
-            for (int v = 0; v < 2; ++v) {
-                const Gate g = gate<T>(x[v], r[v], i[v], k[v], start);
-                ga[s][v] = g.a;
-                gb[s][v] = g.b;
+            for (int s = 0; s < C; ++s) {
+                ga[s] = f32x2{1.0f, 1.0f};
+                gb[s] = f32x2{0.0f, 0.0f};
             }
-            settle(ga[s]);
-            settle(gb[s]);
+        } else {
+#pragma unroll
+            for (int s = 0; s < C; ++s) {
+                const f32x2 x = wide(rx[s]), r = wide(rr[s]), i = wide(ri[s]);
+                const float start = !PLAIN && (w.fresh >> s) & 1 ? -__builtin_inff() : 0.0f;
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const Gate g = gate<T>(x[v], r[v], i[v], k[v], start);
+                    ga[s][v] = g.a;
+                    gb[s][v] = g.b;
+                }
+                settle(ga[s]);
+                settle(gb[s]);
+            }
+            fold<C, PLAIN>(w, ga, gb, A, H);
         }
-        fold<C, PLAIN>(w, ga, gb, A, H);
         sh.A[wv][lane] = A;
         sh.H[wv][lane] = H;
         if (MULTI && threadIdx.x == 0) epoch_end(a.l.hd, ep, a.l.tiles * a.l.groups, sh.ticket);
@@ -509,7 +520,7 @@ __device__ __forceinline__ void fwd_tile(const GatedArgs &a, const Place &p, Sha
         h = enter<MULTI>(a.l, sh, p.j, p.group, wv, first);
     }
     if (a.states && w.t0 % MGS_GATED_CHUNK == 0 && (PLAIN || w.t0 < a.T))
-        store_f2(a.states + (p.b * a.chunks + w.t0 / MGS_GATED_CHUNK) * a.D, p.c, p.d, h);
+        store_f2(a.states + (p.b * a.chunks + w.t0 / MGS_GATED_CHUNK) * a.D + p.at, p.c, p.d, h);
     put_rows<T, C, PLAIN>(a.y, a, p, w, two, [&](int s) {
         if constexpr (PLAIN) {
 #pragma unroll
@@ -520,7 +531,7 @@ __device__ __forceinline__ void fwd_tile(const GatedArgs &a, const Place &p, Sha
         return h;
     });
     // (steps past the length leave it as it is)
-    if (a.hT && p.j + 1 == a.l.tiles && wv == W - 1) store_f2(a.hT + p.b * a.D, p.c, p.d, h);
+    if (a.hT && p.j + 1 == a.l.tiles && wv == W - 1) store_f2(a.hT + p.b * a.D + p.at, p.c, p.d, h);
 }
 
 template <typename T, bool PAIRS, bool MULTI>
@@ -559,7 +570,7 @@ template <typename T> __device__ __forceinline__ Slopes slopes(float x, float r,
 // A tile's sums of dl rho, for dlam
 __device__ __forceinline__ void put_part(const GatedArgs &a, const Place &p, int64_t tile, uint32_t tag, f32x2 sum)
 {
-    uint64_t *o = a.part + (p.b * a.l.tiles + tile) * a.D;
+    uint64_t *o = a.part + (p.b * a.l.tiles + tile) * a.D + p.at;
 #pragma unroll
     for (int v = 0; v < 2; ++v)
         if (p.c + v < p.d) o[p.c + v] = (static_cast<uint64_t>(tag) << 32) | __float_as_uint(sum[v]);
@@ -583,7 +594,7 @@ __device__ __forceinline__ void bwd_tile(const GatedArgs &a, const Place &p, int
         const f32x2 K = pass_on<MULTI>(a, p, sh.s, pass, a.dhT);
         for (void *o : {a.dx, a.dr, a.di})
             put_rows<T, C, false>(o, a, p, w, two, [](int) { return f32x2{0.0f, 0.0f}; });
-        if (a.dh0 && tile == 0 && wv == 0) store_f2(a.dh0 + p.b * a.D, p.c, p.d, K);
+        if (a.dh0 && tile == 0 && wv == 0) store_f2(a.dh0 + p.b * a.D + p.at, p.c, p.d, K);
         if (wv == 0) put_part(a, p, tile, MULTI ? sh.s.ticket[0] : 0, f32x2{0.0f, 0.0f});
         return;
     }
@@ -595,9 +606,9 @@ __device__ __forceinline__ void bwd_tile(const GatedArgs &a, const Place &p, int
     Launch ep{0, 0};
     if constexpr (MULTI) ep = epoch_begin(a.l.hd);
     f32x2 first = {0.0f, 0.0f}, state = {0.0f, 0.0f};
-    if (a.dhT) first = load_f2(a.dhT + p.b * a.D, p.c, p.d);
+    if (a.dhT) first = load_f2(a.dhT + p.b * a.D + p.at, p.c, p.d);
     if (pass == 1)
-        state = load_f2(a.states + (p.b * a.chunks + tile * (Bwd<T>::tile / MGS_GATED_CHUNK)) * a.D, p.c, p.d);
+        state = load_f2(a.states + (p.b * a.chunks + tile * (Bwd<T>::tile / MGS_GATED_CHUNK)) * a.D + p.at, p.c, p.d);
     fill_slopes(a, p, sh.s);
     __syncthreads();
     const f32x2 k = {sh.s.k[2 * lane], sh.s.k[2 * lane + 1]};
@@ -605,26 +616,34 @@ __device__ __forceinline__ void bwd_tile(const GatedArgs &a, const Place &p, int
     // Per step: the decay, and what G multiplies: m1 -> dx, m2 -> di, m3 -> dl (first
     // what is subtracted there).  b = m1 x
     f32x2 ga[C], m1[C], m2[C], m3[C], A = {1.0f, 1.0f}, H = {0.0f, 0.0f}, K = {0.0f, 0.0f};
+    if (!PLAIN && w.live == 0) {   // (a short sequence: most of the tile's waves)
 #pragma unroll
-    for (int s = 0; s < C; ++s) {
-        const f32x2 x = wide(rx[s]), r = wide(rr[s]), i = wide(ri[s]);
-        const bool live = PLAIN || s < w.live, fresh = !PLAIN && (w.fresh >> s) & 1;
-        const float start = fresh ? -__builtin_inff() : 0.0f;
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            const Slopes o = slopes<T>(x[v], r[v], i[v], k[v], start);
-            ga[s][v] = !live ? 1.0f : fresh ? -0.0f : o.a;
-            m1[s][v] = o.x;
-            m2[s][v] = o.i;
-            m3[s][v] = o.l;
-            const float b = live ? o.b : 0.0f;
-            H[v] = PLAIN ? __builtin_fmaf(ga[s][v], H[v], b) : apply(ga[s][v], b, H[v]);
-            A[v] = PLAIN ? A[v] * ga[s][v] : chain(A[v], ga[s][v]);
+        for (int s = 0; s < C; ++s) {
+            ga[s] = f32x2{1.0f, 1.0f};
+            m1[s] = m2[s] = m3[s] = f32x2{0.0f, 0.0f};
         }
-        settle(ga[s]);
-        settle(m1[s]);
-        settle(m2[s]);
-        settle(m3[s]);
+    } else {
+#pragma unroll
+        for (int s = 0; s < C; ++s) {
+            const f32x2 x = wide(rx[s]), r = wide(rr[s]), i = wide(ri[s]);
+            const bool live = PLAIN || s < w.live, fresh = !PLAIN && (w.fresh >> s) & 1;
+            const float start = fresh ? -__builtin_inff() : 0.0f;
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const Slopes o = slopes<T>(x[v], r[v], i[v], k[v], start);
+                ga[s][v] = !live ? 1.0f : fresh ? -0.0f : o.a;
+                m1[s][v] = o.x;
+                m2[s][v] = o.i;
+                m3[s][v] = o.l;
+                const float b = live ? o.b : 0.0f;
+                H[v] = PLAIN ? __builtin_fmaf(ga[s][v], H[v], b) : apply(ga[s][v], b, H[v]);
+                A[v] = PLAIN ? A[v] * ga[s][v] : chain(A[v], ga[s][v]);
+            }
+            settle(ga[s]);
+            settle(m1[s]);
+            settle(m2[s]);
+            settle(m3[s]);
+        }
     }
     // G times the decay, or nothing where that clears
     auto back = [&](float decay, float G) { return !PLAIN && clears(decay) ? 0.0f : decay * G; };
@@ -686,7 +705,7 @@ __device__ __forceinline__ void bwd_tile(const GatedArgs &a, const Place &p, int
     put_rows<T, C, PLAIN>(a.dx, a, p, w, two, [&](int s) { return m1[s]; });
     put_rows<T, C, PLAIN>(a.dr, a, p, w, two, [&](int s) { return m3[s]; });
     put_rows<T, C, PLAIN>(a.di, a, p, w, two, [&](int s) { return m2[s]; });
-    if (a.dh0 && tile == 0 && wv == 0) store_f2(a.dh0 + p.b * a.D, p.c, p.d, K);
+    if (a.dh0 && tile == 0 && wv == 0) store_f2(a.dh0 + p.b * a.D + p.at, p.c, p.d, K);
     sh.sum[wv][lane] = sum;
     __syncthreads();
     if (wv == 0) {
@@ -746,21 +765,22 @@ struct StepArgs {
 template <typename T, bool PAIRS> __global__ void __launch_bounds__(256) gated_step_kernel(StepArgs a)
 {
     const int64_t at = a.first + blockIdx.x, b = at / a.blocks_per_row;
-    const int c = static_cast<int>(at - b * a.blocks_per_row) * 512 + 2 * threadIdx.x, d = static_cast<int>(a.D);
+    const int64_t from = (at - b * a.blocks_per_row) * 512;   // this workgroup's first channel
+    const int c = 2 * threadIdx.x, d = static_cast<int>(a.D - from < 512 ? a.D - from : 512);
     if (c >= d) return;
     const Lane<T, PAIRS> two(c, d);
     const int64_t slot = a.slots ? a.slots[b] : b;
-    char *y = static_cast<char *>(a.y) + b * a.D * static_cast<int64_t>(sizeof(T));
+    char *y = static_cast<char *>(a.y) + (b * a.D + from) * static_cast<int64_t>(sizeof(T));
     if (slot < 0 || slot >= a.n_slots) {
         two.store(y, f32x2{0.0f, 0.0f});
         return;
     }
     auto row = [&](const void *p, int64_t stride) {
-        return wide(two.load(static_cast<const char *>(p) + b * stride * static_cast<int64_t>(sizeof(T))));
+        return wide(two.load(static_cast<const char *>(p) + (b * stride + from) * static_cast<int64_t>(sizeof(T))));
     };
     const f32x2 x = row(a.x, a.xs), r = row(a.r, a.rs), i = row(a.i, a.is);
-    const f32x2 lam = load_f2(a.lam, c, d);
-    float *state = a.h + slot * a.D;
+    const f32x2 lam = load_f2(a.lam + from, c, d);
+    float *state = a.h + slot * a.D + from;
     f32x2 h = load_f2(state, c, d);
 #pragma unroll
     for (int v = 0; v < 2; ++v) {

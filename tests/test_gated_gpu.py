@@ -293,3 +293,44 @@ def test_empty_batch(gpu):
         a = make(gpu, 0, T, 9, seed=14)
         got = run(a)
         assert got["dlam"].shape == (9,) and got["dlam"].count_nonzero() == 0
+
+
+def test_step_of_more_channels_than_bytes_fit_32_bits(gpu):
+    """2^30 and some channels of four bytes: the ends and the 32-bit seam are what those channels give alone."""
+    import gc
+    import scan_linear_rnns_amd as mgs
+    D = (1 << 30) + 10
+    say(f"gated step D={D}")
+    g = torch.Generator(gpu).manual_seed(1)
+    rand = lambda n: torch.randn(n, D, generator=g, device=gpu)  # noqa: E731
+    x, r, i, h, lam = rand(1), rand(1), rand(1), rand(1), rand(1)[0].sub_(4)
+    at = torch.tensor([0, 1, 511, 512, (1 << 29) - 1, 1 << 29, (1 << 30) - 1, 1 << 30, D - 2, D - 1], device=gpu)
+    small = h[:, at].clone()
+    want = mgs.mgs_gated_step(*(t[:, at].contiguous() for t in (x, r, i)), lam[at].contiguous(), small)
+    y = mgs.mgs_gated_step(x, r, i, lam, h)
+    assert torch.equal(y[:, at], want) and torch.equal(h[:, at], small)
+    del x, r, i, h, lam, y
+    gc.collect()
+    torch.cuda.empty_cache()
+
+
+def test_far_offsets(gpu):
+    """Rows whose strides put them past 2^32 bytes from the first."""
+    say("gated far rows")
+    a = make(gpu, 2, 70, 128, "bf16", seed=15)
+    one = run(a)
+    b = dict(a)
+    room = torch.empty((1 << 31) + 70 * 130, dtype=torch.bfloat16, device=gpu)
+    b["x"] = room.as_strided((2, 70, 128), (1 << 31, 130, 1))
+    b["x"].copy_(a["x"])
+    got = run(b)
+    for n in NAMES:
+        assert torch.equal(got[n], one[n]), n
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [9, 200])
+def test_many_short_sequences(gpu, T, dtype):
+    say(f"gated 40 x {T} {dtype}")
+    a = make(gpu, 40, T, 70, dtype, lengths=[(7 * b) % (T + 1) for b in range(40)], reset=0.1, seed=T)
+    check(run(a), reference(a))
