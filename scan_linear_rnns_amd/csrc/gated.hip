@@ -30,12 +30,12 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kGroup = 128;              // channels of a workgroup
-constexpr int kUnit = 8;                 // tiles whose pairs a tile reads at most
+constexpr int kPollers = 7;              // waves of a workgroup that read other tiles' pairs
 // Waves of a workgroup, steps of a wave, and how many waves share a SIMD
 template <int WAVES, int STEPS, int OCCUPANCY> struct Shape {
     static constexpr int W = WAVES, C = STEPS, occupancy = OCCUPANCY, tile = W * C;
-    static_assert(kUnit <= W, "each wave polls one tile");
-    static_assert(tile % MGS_GATED_CHUNK == 0, "a tile starts at a saved state");
+    static constexpr bool several = W > kPollers;   // serves several tiles along T
+    static_assert(!several || tile % MGS_GATED_CHUNK == 0, "a tile starts at a saved state");
     static_assert(MGS_GATED_CHUNK % C == 0, "a wave saves the state ahead of it");
 };
 // Measured (us at 4 x 4096 x 4096, bf16, and 16 x 1024 x 1000, fp32).  Forward 8 waves
@@ -46,6 +46,11 @@ template <int WAVES, int STEPS, int OCCUPANCY> struct Shape {
 template <typename T> struct Fwd : Shape<8, 16, 4> {};
 template <typename T> struct Bwd : Shape<8, 8, 2> {};
 template <> struct Bwd<__bf16> : Shape<8, 8, 4> {};
+
+// Sequences of up to 16 steps (64 of 4 x 4096, bf16: 27 and 36 us with the shapes above)
+constexpr int kShort = 16;
+struct FwdShort : Shape<1, kShort, 4> {};
+struct BwdShort : Shape<2, kShort / 2, 2> {};
 
 __device__ __forceinline__ float ex2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float rcp(float x) { return __builtin_amdgcn_rcpf(x); }
@@ -203,23 +208,24 @@ __device__ __forceinline__ f32x2 apply2(f32x2 A, f32x2 H, f32x2 h)
 }
 
 // ------------------------------------------------------------- look-back
-// Tiles of one channel group pass on their pairs in units of kUnit tiles: the
-// last tile of a unit publishes the value that leaves it, the others their pair,
-// and a tile reads the value that left the unit before it and the pairs of the
-// tiles ahead of it in its unit, and folds them in order: results do not depend
-// on which tile was early.  Wave q polls for the q-th of these, so a tile waits for
-// the slowest of them once.  Words are tagged (device.hpp).  Tile indices run in the
+// Tiles of one channel group pass on their pairs in units of l.unit tiles: the last
+// tile of a unit publishes the value that leaves it, the others their pair, and a tile
+// reads the value that left the unit before it and the pairs of the tiles ahead of it in
+// its unit, and folds them in order: results do not depend on which tile was early.
+// Wave 0 polls for the first, the others for l.per pairs each, so a tile waits for the
+// slowest of them once.  Words are tagged (device.hpp).  Tile indices run in the
 // direction of the pass; tiles wait for smaller blockIdx only.
 struct Lookback {
     WsHeader *hd;
     uint64_t *agg, *incl;     // [tile][2][group channels], [unit][group channels], per group
     uint32_t groups, tiles;   // tiles of one group
+    uint32_t unit, per;
     int local;                // every partner runs on this XCD (tagged_store)
 };
 
 template <int W> struct Shared {
     f32x2 A[W][64], H[W][64];      // the waves' pairs; then those of all waves ahead of each
-    f32x2 pA[kUnit][64], pH[kUnit][64];      // the unit's tiles' pairs; pH[0]: the value that enters the unit
+    f32x2 pA[kPollers + 1][64], pH[kPollers + 1][64];   // the unit's pairs, each of l.per tiles; pH[0]: what enters it
     float k[kGroup];                         // slope2
     uint32_t ticket[3];
 };
@@ -262,8 +268,8 @@ __device__ __forceinline__ f32x2 enter(const Lookback &l, Shared<W> &sh, uint32_
 {
     const int lane = threadIdx.x & 63;
     const uint32_t tag = sh.ticket[0], want = sh.ticket[1], limit = sh.ticket[2];
-    const uint32_t unit = j / kUnit, at = j % kUnit;
-    const bool closes = at == kUnit - 1;
+    const uint32_t unit = MULTI ? j / l.unit : 0, at = j - unit * l.unit;
+    const bool closes = at == l.unit - 1;
     f32x2 TA = {1.0f, 1.0f}, TH = {0.0f, 0.0f};
     if (pass == 0) {
 #pragma unroll
@@ -279,20 +285,30 @@ __device__ __forceinline__ f32x2 enter(const Lookback &l, Shared<W> &sh, uint32_
             publish2(p + kGroup, tag, TH, l.local);
         }
     }
-    if (MULTI && pass <= static_cast<int>(at)) {
+    if constexpr (MULTI) {
         if (pass == 0) {
             sh.pH[0][lane] = unit == 0 ? first : await2(l, incl_at(l, unit - 1, group) + 2 * lane, want, limit);
-        } else {
-            const uint64_t *p = agg_at(l, static_cast<int64_t>(unit) * kUnit + pass - 1, group) + 2 * lane;
-            sh.pA[pass][lane] = await2(l, p, want, limit);
-            sh.pH[pass][lane] = await2(l, p + kGroup, want, limit);
+        } else if (pass <= kPollers) {
+            const uint32_t end = pass * l.per < at ? pass * l.per : at;
+            uint32_t q = (pass - 1) * l.per;
+            f32x2 A = {1.0f, 1.0f}, H = {0.0f, 0.0f};
+            const bool any = q < end;
+            for (; q < end; ++q) {
+                const uint64_t *p = agg_at(l, static_cast<int64_t>(unit) * l.unit + q, group) + 2 * lane;
+                const f32x2 A2 = await2(l, p, want, limit), H2 = await2(l, p + kGroup, want, limit);
+                append(A, H, A2, H2);
+            }
+            if (any) {
+                sh.pA[pass][lane] = A;
+                sh.pH[pass][lane] = H;
+            }
         }
     }
     __syncthreads();
     f32x2 c = first;
     if constexpr (MULTI) {
         c = sh.pH[0][lane];
-        for (uint32_t q = 1; q <= at; ++q) c = apply2(sh.pA[q][lane], sh.pH[q][lane], c);
+        for (uint32_t q = 1; (q - 1) * l.per < at; ++q) c = apply2(sh.pA[q][lane], sh.pH[q][lane], c);
         if (pass == 0 && closes && j + 1 < l.tiles)
             publish2(incl_at(l, unit, group) + 2 * lane, tag, apply2(TA, TH, c), l.local);
     }
@@ -369,25 +385,23 @@ template <int N> __device__ __forceinline__ Steps steps(const GatedArgs &a, cons
 // workgroup takes one of two bodies by this
 template <int N> __device__ __forceinline__ bool plain_tile(const GatedArgs &a, const Place &p, int64_t t)
 {
-    static_assert(N % 64 == 0, "whole words of a wave");
     if (t + N > p.n) return false;
     if (!a.reset) return true;
-    const uint8_t *from = a.reset + p.b * a.T + t + (threadIdx.x & 63);
+    const uint8_t *from = a.reset + p.b * a.T + t;
     int any = 0;
 #pragma unroll
-    for (int i = 0; i < N; i += 64) any |= from[i];
+    for (int i = 0; i < N; i += 64) any |= from[(i + (threadIdx.x & 63)) % N];
     return __ballot(any != 0) == 0;
 }
 
 // The wave's N rows of a (B,T,...) tensor; past the last live one, that one again
-// (p.n > 0)
+// (there is one)
 template <typename T, int N, bool PLAIN, typename L>
 __device__ __forceinline__ void rows(const void *base, const int64_t *stride, const Place &p, const Steps &w, const L &lane,
                                      typename Two<T>::V *out)
 {
     const int64_t step = stride[1] * static_cast<int64_t>(sizeof(T));
-    const int64_t t = PLAIN || w.live > 0 ? w.t0 : p.n - 1;
-    const char *row = static_cast<const char *>(base) + (p.b * stride[0] + p.at) * static_cast<int64_t>(sizeof(T)) + t * step;
+    const char *row = static_cast<const char *>(base) + (p.b * stride[0] + p.at) * static_cast<int64_t>(sizeof(T)) + w.t0 * step;
 #pragma unroll
     for (int s = 0; s < N; ++s) {
         out[s] = lane.load(row);
@@ -416,9 +430,9 @@ __device__ __forceinline__ void put_rows(void *base, const GatedArgs &a, const P
 // workgroup, not once per wave)
 template <int W> __device__ __forceinline__ void fill_slopes(const GatedArgs &a, const Place &p, Shared<W> &sh)
 {
-    if (threadIdx.x < kGroup) {
-        const int64_t c = p.at + threadIdx.x;
-        sh.k[threadIdx.x] = slope2(a.lam[c < a.D ? c : a.D - 1], a.rate);
+    for (int i = threadIdx.x; i < kGroup; i += 64 * W) {
+        const int64_t c = p.at + i;
+        sh.k[i] = slope2(a.lam[c < a.D ? c : a.D - 1], a.rate);
     }
 }
 
@@ -463,15 +477,15 @@ template <int N, bool PLAIN> __device__ __forceinline__ void fold(const Steps &w
     }
 }
 
-template <typename T, bool PAIRS, bool MULTI, bool PLAIN>
-__device__ __forceinline__ void fwd_tile(const GatedArgs &a, const Place &p, Shared<Fwd<T>::W> &sh)
+template <typename T, typename S, bool PAIRS, bool MULTI, bool PLAIN>
+__device__ __forceinline__ void fwd_tile(const GatedArgs &a, const Place &p, Shared<S::W> &sh)
 {
-    constexpr int C = Fwd<T>::C, W = Fwd<T>::W;
+    constexpr int C = S::C, W = S::W;
     const int lane = threadIdx.x & 63, wv = wave();
     const Lane<T, PAIRS> two(p.c, p.d);
-    const Steps w = steps<C>(a, p, static_cast<int64_t>(p.j) * Fwd<T>::tile + wv * C);
+    const Steps w = steps<C>(a, p, static_cast<int64_t>(p.j) * S::tile + wv * C);
     f32x2 h, ga[C], gb[C];
-    if (!PLAIN && static_cast<int64_t>(p.j) * Fwd<T>::tile >= p.n) {   // no step of the tile is live
+    if (!PLAIN && static_cast<int64_t>(p.j) * S::tile >= p.n) {   // no step of the tile is live
         h = pass_on<MULTI>(a, p, sh, wv, a.h0);
 #pragma unroll
         for (int s = 0; s < C; ++s) {
@@ -480,9 +494,11 @@ __device__ __forceinline__ void fwd_tile(const GatedArgs &a, const Place &p, Sha
         }
     } else {
         typename Two<T>::V rx[C], rr[C], ri[C];
-        rows<T, C, PLAIN>(a.x, a.xs, p, w, two, rx);
-        rows<T, C, PLAIN>(a.r, a.rs, p, w, two, rr);
-        rows<T, C, PLAIN>(a.i, a.is, p, w, two, ri);
+        if (PLAIN || w.live > 0) {
+            rows<T, C, PLAIN>(a.x, a.xs, p, w, two, rx);
+            rows<T, C, PLAIN>(a.r, a.rs, p, w, two, rr);
+            rows<T, C, PLAIN>(a.i, a.is, p, w, two, ri);
+        }
         Launch ep{0, 0};
         if constexpr (MULTI) ep = epoch_begin(a.l.hd);
         f32x2 first = {0.0f, 0.0f};
@@ -534,15 +550,16 @@ __device__ __forceinline__ void fwd_tile(const GatedArgs &a, const Place &p, Sha
     if (a.hT && p.j + 1 == a.l.tiles && wv == W - 1) store_f2(a.hT + p.b * a.D + p.at, p.c, p.d, h);
 }
 
-template <typename T, bool PAIRS, bool MULTI>
-__global__ void __launch_bounds__(64 * Fwd<T>::W, Fwd<T>::occupancy) gated_fwd_kernel(GatedArgs a)
+template <typename T, typename S, bool PAIRS, bool MULTI>
+__global__ void __launch_bounds__(64 * S::W, S::occupancy) gated_fwd_kernel(GatedArgs a)
 {
-    __shared__ Shared<Fwd<T>::W> sh;
+    __shared__ Shared<S::W> sh;
     const Place p = place(a);
-    if (plain_tile<Fwd<T>::tile>(a, p, static_cast<int64_t>(p.j) * Fwd<T>::tile))
-        fwd_tile<T, PAIRS, MULTI, true>(a, p, sh);
+    static_assert(S::several || !MULTI, "enough waves to wait for other tiles");
+    if (plain_tile<S::tile>(a, p, static_cast<int64_t>(p.j) * S::tile))
+        fwd_tile<T, S, PAIRS, MULTI, true>(a, p, sh);
     else
-        fwd_tile<T, PAIRS, MULTI, false>(a, p, sh);
+        fwd_tile<T, S, PAIRS, MULTI, false>(a, p, sh);
 }
 
 // One step of the backward from its inputs
@@ -582,15 +599,15 @@ template <int W> struct BwdShared {
     f32x2 sum[W][64];
 };
 
-template <typename T, bool PAIRS, bool MULTI, bool PLAIN>
-__device__ __forceinline__ void bwd_tile(const GatedArgs &a, const Place &p, int64_t tile, BwdShared<Bwd<T>::W> &sh)
+template <typename T, typename S, bool PAIRS, bool MULTI, bool PLAIN>
+__device__ __forceinline__ void bwd_tile(const GatedArgs &a, const Place &p, int64_t tile, BwdShared<S::W> &sh)
 {
-    constexpr int C = Bwd<T>::C, W = Bwd<T>::W;
+    constexpr int C = S::C, W = S::W;
     const int lane = threadIdx.x & 63;
     const int pass = wave(), wv = W - 1 - pass;   // in the order of the pass, and of the steps
     const Lane<T, PAIRS> two(p.c, p.d);
-    const Steps w = steps<C>(a, p, tile * Bwd<T>::tile + wv * C);
-    if (!PLAIN && tile * Bwd<T>::tile >= p.n) {   // no step of the tile is live
+    const Steps w = steps<C>(a, p, tile * S::tile + wv * C);
+    if (!PLAIN && tile * S::tile >= p.n) {   // no step of the tile is live
         const f32x2 K = pass_on<MULTI>(a, p, sh.s, pass, a.dhT);
         for (void *o : {a.dx, a.dr, a.di})
             put_rows<T, C, false>(o, a, p, w, two, [](int) { return f32x2{0.0f, 0.0f}; });
@@ -599,16 +616,18 @@ __device__ __forceinline__ void bwd_tile(const GatedArgs &a, const Place &p, int
         return;
     }
     typename Two<T>::V rx[C], rr[C], ri[C], rg[C];
-    rows<T, C, PLAIN>(a.x, a.xs, p, w, two, rx);
-    rows<T, C, PLAIN>(a.r, a.rs, p, w, two, rr);
-    rows<T, C, PLAIN>(a.i, a.is, p, w, two, ri);
-    rows<T, C, PLAIN>(a.dy, a.gs, p, w, two, rg);
+    if (PLAIN || w.live > 0) {
+        rows<T, C, PLAIN>(a.x, a.xs, p, w, two, rx);
+        rows<T, C, PLAIN>(a.r, a.rs, p, w, two, rr);
+        rows<T, C, PLAIN>(a.i, a.is, p, w, two, ri);
+        rows<T, C, PLAIN>(a.dy, a.gs, p, w, two, rg);
+    }
     Launch ep{0, 0};
     if constexpr (MULTI) ep = epoch_begin(a.l.hd);
     f32x2 first = {0.0f, 0.0f}, state = {0.0f, 0.0f};
     if (a.dhT) first = load_f2(a.dhT + p.b * a.D + p.at, p.c, p.d);
     if (pass == 1)
-        state = load_f2(a.states + (p.b * a.chunks + tile * (Bwd<T>::tile / MGS_GATED_CHUNK)) * a.D + p.at, p.c, p.d);
+        state = load_f2(a.states + (p.b * a.chunks + tile * S::tile / MGS_GATED_CHUNK) * a.D + p.at, p.c, p.d);
     fill_slopes(a, p, sh.s);
     __syncthreads();
     const f32x2 k = {sh.s.k[2 * lane], sh.s.k[2 * lane + 1]};
@@ -714,16 +733,17 @@ __device__ __forceinline__ void bwd_tile(const GatedArgs &a, const Place &p, int
     }
 }
 
-template <typename T, bool PAIRS, bool MULTI>
-__global__ void __launch_bounds__(64 * Bwd<T>::W, Bwd<T>::occupancy) gated_bwd_kernel(GatedArgs a)
+template <typename T, typename S, bool PAIRS, bool MULTI>
+__global__ void __launch_bounds__(64 * S::W, S::occupancy) gated_bwd_kernel(GatedArgs a)
 {
-    __shared__ BwdShared<Bwd<T>::W> sh;
+    __shared__ BwdShared<S::W> sh;
     const Place p = place(a);
     const int64_t tile = static_cast<int64_t>(a.l.tiles) - 1 - p.j;
-    if (plain_tile<Bwd<T>::tile>(a, p, tile * Bwd<T>::tile))
-        bwd_tile<T, PAIRS, MULTI, true>(a, p, tile, sh);
+    static_assert(S::several || !MULTI, "enough waves to wait for other tiles");
+    if (plain_tile<S::tile>(a, p, tile * S::tile))
+        bwd_tile<T, S, PAIRS, MULTI, true>(a, p, tile, sh);
     else
-        bwd_tile<T, PAIRS, MULTI, false>(a, p, tile, sh);
+        bwd_tile<T, S, PAIRS, MULTI, false>(a, p, tile, sh);
 }
 
 // dlam: the partial sums of a channel in order, in fp64, over 16 waves' shares
@@ -827,36 +847,40 @@ GatedArgs arguments(const GatedGeom &g, const mgs_gated_desc &d, int64_t tiles, 
     a.l.incl = reinterpret_cast<uint64_t *>(w + g.off_incl);
     a.part = reinterpret_cast<uint64_t *>(w + g.off_part);
     a.l.groups = static_cast<uint32_t>(g.groups);
+    a.l.unit = static_cast<uint32_t>(g.unit);
+    a.l.per = static_cast<uint32_t>((g.unit - 1 + kPollers - 1) / kPollers + (g.unit == 1));
     a.l.tiles = static_cast<uint32_t>(tiles);
     const int xcds = xcd_count();
     a.l.local = xcds > 0 && g.groups % xcds == 0;
     return a;
 }
 
+template <typename T, typename S, bool MULTI> hipError_t run_fwd_as(const GatedArgs &a, bool two, hipStream_t s)
+{
+    const dim3 grid(a.l.groups * a.l.tiles), block(64 * S::W);
+    if (two) gated_fwd_kernel<T, S, true, MULTI><<<grid, block, 0, s>>>(a);
+    else gated_fwd_kernel<T, S, false, MULTI><<<grid, block, 0, s>>>(a);
+    return hipGetLastError();
+}
+
 template <typename T> hipError_t run_fwd(const GatedArgs &a, bool two, hipStream_t s)
 {
-    const dim3 grid(a.l.groups * a.l.tiles), block(64 * Fwd<T>::W);
-    if (a.l.tiles > 1) {
-        if (two) gated_fwd_kernel<T, true, true><<<grid, block, 0, s>>>(a);
-        else gated_fwd_kernel<T, false, true><<<grid, block, 0, s>>>(a);
-    } else {
-        if (two) gated_fwd_kernel<T, true, false><<<grid, block, 0, s>>>(a);
-        else gated_fwd_kernel<T, false, false><<<grid, block, 0, s>>>(a);
-    }
+    if (a.T <= kShort) return run_fwd_as<T, FwdShort, false>(a, two, s);
+    return a.l.tiles > 1 ? run_fwd_as<T, Fwd<T>, true>(a, two, s) : run_fwd_as<T, Fwd<T>, false>(a, two, s);
+}
+
+template <typename T, typename S, bool MULTI> hipError_t run_bwd_as(const GatedArgs &a, bool two, hipStream_t s)
+{
+    const dim3 grid(a.l.groups * a.l.tiles), block(64 * S::W);
+    if (two) gated_bwd_kernel<T, S, true, MULTI><<<grid, block, 0, s>>>(a);
+    else gated_bwd_kernel<T, S, false, MULTI><<<grid, block, 0, s>>>(a);
     return hipGetLastError();
 }
 
 template <typename T> hipError_t run_bwd(const GatedArgs &a, bool two, hipStream_t s)
 {
-    const dim3 grid(a.l.groups * a.l.tiles), block(64 * Bwd<T>::W);
-    if (a.l.tiles > 1) {
-        if (two) gated_bwd_kernel<T, true, true><<<grid, block, 0, s>>>(a);
-        else gated_bwd_kernel<T, false, true><<<grid, block, 0, s>>>(a);
-    } else {
-        if (two) gated_bwd_kernel<T, true, false><<<grid, block, 0, s>>>(a);
-        else gated_bwd_kernel<T, false, false><<<grid, block, 0, s>>>(a);
-    }
-    return hipGetLastError();
+    if (a.T <= kShort) return run_bwd_as<T, BwdShort, false>(a, two, s);
+    return a.l.tiles > 1 ? run_bwd_as<T, Bwd<T>, true>(a, two, s) : run_bwd_as<T, Bwd<T>, false>(a, two, s);
 }
 
 }  // namespace
@@ -870,14 +894,23 @@ GatedGeom gated_geometry(const mgs_gated_desc &d, bool backward)
     const int64_t tf = half ? Fwd<__bf16>::tile : Fwd<float>::tile, tb = half ? Bwd<__bf16>::tile : Bwd<float>::tile;
     g.tiles_f = std::max<int64_t>(1, (d.T + tf - 1) / tf);
     g.tiles_b = std::max<int64_t>(1, (d.T + tb - 1) / tb);
+    // A unit is one hop of 1.2 us along a sequence: enough tiles that the hops do not take
+    // longer than the data, and no more, for a tile reads half a unit's pairs.  Measured, us
+    // forward / backward, bf16, with units of 1, 2, 4, 8, 22, 36, 64 tiles:
+    //   128 groups (4 x 4096 steps)  112/220 114/232 117/233 118/237 129/256 139/266 145/300
+    //   16 (2 x 32768)               144/327 113/251 116/252 120/256 130/275 135/297 147/329
+    //   8 (65536)                    240/514 160/358 113/270 116/260 127/286 135/309 149/346
+    //   2 (262144)                   1440/3063 801/1725 497/1092 322/732 161/425 157/416 171/442
+    //   1 (1048576)                  5686/12184 3107/6731 1774/3962 1201/2808 490/1394 328/1084 291/1031
+    g.unit = static_cast<int>(std::max<int64_t>(1, 64 / std::max<int64_t>(1, g.groups)));
     const int64_t tiles = backward ? std::max(g.tiles_f, g.tiles_b) : g.tiles_f;
     // every word behind the header is a tagged one, whatever call it is written by,
     // so that a call of other sizes takes none of them for its own
     size_t off = sizeof(WsHeader);
     g.off_agg = off;
-    if (tiles > 1) off = align256(off + static_cast<size_t>(tiles) * g.groups * 2 * kGroup * 8);
+    if (tiles > 1 && g.unit > 1) off = align256(off + static_cast<size_t>(tiles) * g.groups * 2 * kGroup * 8);
     g.off_incl = off;
-    if (tiles > 1) off = align256(off + static_cast<size_t>(tiles / kUnit) * g.groups * kGroup * 8);
+    if (tiles > 1) off = align256(off + static_cast<size_t>(tiles / g.unit) * g.groups * kGroup * 8);
     g.off_part = off;
     if (backward) off = align256(off + static_cast<size_t>(g.tiles_b) * d.B * d.D * 8);
     g.bytes = off;

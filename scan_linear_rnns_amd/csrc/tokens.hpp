@@ -34,6 +34,7 @@ hipError_t launch_embed_bwd(const EmbedGeom &g, const void *ids, bool wide_ids, 
 struct GatedGeom {
     int64_t groups;       // of channels, over all sequences
     int64_t tiles_f, tiles_b;     // along T, forward and backward
+    int unit;             // tiles of a look-back's unit
     size_t off_agg, off_incl, off_part, bytes;   // tagged words
 };
 
