@@ -190,3 +190,25 @@ def test_empty_batch(gpu):
     import scan_linear_rnns_amd as mgs
     token, logp = mgs.mgs_sample(torch.empty(0, 10, device=gpu), torch.empty(0, device=gpu))
     assert token.shape == logp.shape == (0,)
+
+
+def test_the_largest_batch(gpu):
+    import scan_linear_rnns_amd as mgs
+    B, V = (1 << 22) - 1, 5
+    say(f"sample B={B}")
+    g = torch.Generator(gpu).manual_seed(9)
+    x, u = torch.randn(B, V, generator=g, device=gpu), torch.rand(B, generator=g, device=gpu)
+    token, logp = mgs.mgs_sample(x, u, top_k=3)
+    at = torch.tensor([0, 1, 255, 256, B // 2, B - 2, B - 1], device=gpu)
+    one = mgs.mgs_sample(x[at], u[at], top_k=3)
+    assert torch.equal(token[at], one[0]) and torch.equal(logp[at], one[1])
+    assert int(token.min()) >= 0 and int(token.max()) < V and bool((logp <= 0).all())
+
+
+def test_the_largest_vocabulary(gpu):
+    say("sample vocabulary of 2^20")
+    for B in (1, 3):
+        x, u = draw(gpu, B, 1 << 20, "bf16", B)
+        for i, fixed in enumerate([dict(top_k=0, top_p=1.0, min_p=0.0), dict(top_k=0, min_p=0.0), {}]):
+            s = settings(B, i, **fixed)
+            check(x, u, s, *run(x, u, s), who=fixed)
