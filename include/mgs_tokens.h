@@ -13,7 +13,8 @@
  * buffers and workspaces, no allocation, arguments checked before any HIP call.
  * The workspaces carry nothing from one call to the next and need not be
  * zero-filled, but for mgs_gated_*'s, which has to be once, as those of mgs.h.
- * Calls that share a workspace must not run concurrently.
+ * Calls that share a workspace must not run concurrently.  A workspace for B sequences or
+ * rows, T steps or n ids serves calls of fewer too.
  */
 #ifndef MGS_TOKENS_H
 #define MGS_TOKENS_H

@@ -450,7 +450,10 @@ EmbedGeom embed_geometry(int64_t n, int64_t vocab, int64_t d)
     g.off_first = off; off = align256(off + ((static_cast<size_t>(g.range) << g.bits) + 1) * 4);
     g.off_row = off;   off = align256(off + static_cast<size_t>(n) * 4);
     g.off_id = off;    off = align256(off + static_cast<size_t>(n) * 4);
-    g.off_part = off;  off = align256(off + static_cast<size_t>(g.chunks) * 2 * ((d + 7) / 8 * 8) * 4);
+    g.off_part = off;
+    // (fewer ids, in shorter chunks, may have more of them: room for these too)
+    const int64_t room = std::max(g.chunks, std::min<int64_t>((n + 7) / 8, 1024));
+    off = align256(off + static_cast<size_t>(room) * 2 * ((d + 7) / 8 * 8) * 4);
     g.bytes = off;
     return g;
 }

@@ -910,7 +910,10 @@ GatedGeom gated_geometry(const mgs_gated_desc &d, bool backward)
     g.off_agg = off;
     if (tiles > 1 && g.unit > 1) off = align256(off + static_cast<size_t>(tiles) * g.groups * 2 * kGroup * 8);
     g.off_incl = off;
-    if (tiles > 1) off = align256(off + static_cast<size_t>(tiles / g.unit) * g.groups * kGroup * 8);
+    // (32 groups need 2 1/2 words a tile and channel, their units being of two tiles; more
+    // groups with units of one have room for a call of those too)
+    const int64_t lines = g.unit > 1 ? tiles / g.unit * g.groups : tiles * std::max<int64_t>(g.groups, 80);
+    if (tiles > 1) off = align256(off + static_cast<size_t>(lines) * kGroup * 8);
     g.off_part = off;
     if (backward) off = align256(off + static_cast<size_t>(g.tiles_b) * d.B * d.D * 8);
     g.bytes = off;

@@ -37,6 +37,7 @@ constexpr int kList = 4096;         // candidates that are sorted
 constexpr int kFixed = 43;          // a weight's bits behind the point: 2^20 of them fit 64 bits
 constexpr int kCounted = 256;       // up to here sorting counts the smaller ones
 constexpr int kMaxSlices = 64;
+constexpr int kWorkgroups = 256;    // that rows are cut into: one for each CU
 constexpr float kInf = __builtin_inff(), kMax = 3.4028234663852886e38f;
 
 struct SampleArgs {
@@ -1191,7 +1192,7 @@ SampleGeom sample_geometry(const mgs_sample_desc &d)
     // steps a wave stay with one (32000, bf16, all filters: 1 row 21 us, cut in four 26; 128
     // rows of mixed settings 44, in two 55); longer ones are cut (8 rows of 128000: 52, whole
     // or in four 72 and 57).
-    int64_t s = steps <= 4 * kWaves || d.B <= 0 ? 1 : std::min<int64_t>((steps + kWaves - 1) / kWaves, 256 / d.B);
+    int64_t s = steps <= 4 * kWaves || d.B <= 0 ? 1 : std::min<int64_t>((steps + kWaves - 1) / kWaves, kWorkgroups / d.B);
     s = std::max<int64_t>(1, std::min<int64_t>(s, kMaxSlices));
     g.slices = static_cast<int>(s);
     g.share = static_cast<int>((steps + s * kWaves - 1) / (s * kWaves) * step);
@@ -1220,8 +1221,10 @@ template <typename T> hipError_t run(const SampleArgs &a, unsigned rows, hipStre
 
 size_t sample_workspace(const mgs_sample_desc &d)
 {
-    const SampleGeom g = sample_geometry(d);
-    return 256 + g.slot * static_cast<size_t>(d.B);
+    // (more rows than this are not cut; the bytes of fewer grow with their number)
+    mgs_sample_desc cut = d;
+    cut.B = std::min<int64_t>(d.B, kWorkgroups / 2);
+    return 256 + sample_geometry(cut).slot * static_cast<size_t>(cut.B);
 }
 
 hipError_t launch_sample(const mgs_sample_desc &d, const void *logits, const float *u, const float *temperature,

@@ -46,6 +46,12 @@ def test_embed_workspace(lib):
     assert embed_size(lib, n=0)[0] == OK and embed_size(lib, vocab=0)[0] == OK
 
 
+def test_an_embed_workspace_serves_fewer_ids(lib):
+    for d in (1, 64, 2050):
+        sizes = [embed_size(lib, n=n, vocab=700, d=d)[1] for n in range(0, 40000, 13)]
+        assert sizes == sorted(sizes), d
+
+
 def test_embed_fwd_refusals(lib):
     def fwd(ids=fake(0), bits=64, W=fake(1), y=fake(2), n=100, vocab=50, d=64, stride=64, dtype=1):
         return lib.mgs_embed_fwd(ids, bits, W, y, n, vocab, d, stride, 1.0, dtype, None)
@@ -103,6 +109,17 @@ def test_gated_workspace(lib):
     # a workspace of the forward and backward of a size is one of either alone
     for T in (1, 64, 65, 128, 129, 1000, 5000):
         assert gated_size(lib, gated(T=T), 1)[1] >= gated_size(lib, gated(T=T))[1]
+
+
+@pytest.mark.parametrize("backward", [0, 1])
+def test_a_gated_workspace_serves_fewer_sequences_and_steps(lib, backward):
+    for D in (1, 128, 300, 1024, 5000):
+        for T in (64, 65, 129, 1000, 40000):
+            sizes = [gated_size(lib, gated(B=B, T=T, D=D), backward)[1] for B in range(100)]
+            assert sizes == sorted(sizes), (D, T)
+        for B in (1, 3, 40):
+            sizes = [gated_size(lib, gated(B=B, T=T, D=D), backward)[1] for T in range(0, 3000, 7)]
+            assert sizes == sorted(sizes), (D, B)
 
 
 def test_gated_fwd_refusals(lib):
@@ -184,6 +201,18 @@ def test_sample_workspace(lib):
     for bad in (dict(dtype=2), dict(vocab=(1 << 20) + 1), dict(B=1 << 22), dict(B=BIG)):
         assert size(sampling(**bad))[0] == UNSUPPORTED, bad
     assert size(sampling(vocab=1 << 20))[0] == OK
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+def test_a_sample_workspace_serves_fewer_rows(lib, dtype):
+    out = ctypes.c_size_t(0)
+    for vocab in (1000, 16385, 32769, 40000, 128000, 1 << 20):
+        sizes = []
+        for B in range(300):
+            d = sampling(B=B, vocab=vocab, stride=vocab, dtype=dtype)
+            assert lib.mgs_sample_workspace_size(ctypes.byref(d), ctypes.byref(out)) == OK
+            sizes.append(out.value)
+        assert sizes == sorted(sizes), vocab
 
 
 def test_sample_refusals(lib):
