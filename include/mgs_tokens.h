@@ -139,8 +139,10 @@ mgs_status mgs_gated_step(const mgs_gated_desc *desc, const void *x, const void 
  * -inf is a forbidden token.  A row of nothing else, or with a NaN, has token -1
  * and logp -inf; where the largest is +inf, those that are share all the weight.
  * Weights and sums are fp64 (the ones that top_p compares, multiples of 2^-43 of
- * the largest weight), so that an answer does not depend on the batch; a weight below
- * 2^-1000 of the largest counts as none.
+ * the largest weight, whose sums are exact); a weight below 2^-1000 of the largest
+ * counts as none.  A call's answers are the same every time; those of other batch
+ * sizes and row strides may differ where u times the sum is within fp64's rounding of
+ * a token's end.
  * Envelope: vocab <= 2^20, B < 2^22.
  */
 typedef struct {

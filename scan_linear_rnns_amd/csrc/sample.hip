@@ -5,9 +5,9 @@
 // what is kept is an edge: everything above its value, and its equals up to an index.
 // A row goes through
 //   1. its largest logit;
-//   2. a histogram over (largest - x) / temperature in steps of 1/64: of the counts
-//      for top-k, of the weights, as multiples of 2^-43, for top-p (integers: their sums
-//      do not depend on the order of the atomics);
+//   2. a histogram over (largest - x) / temperature, in steps of 1/64 to e^-16, wider ones
+//      to where no weight is left: of the counts for top-k, of the weights, as multiples of
+//      2^-43, for top-p (integers: their sums do not depend on the order of the atomics);
 //   3. the few that lie in the bin where the filter ends (for top-k, all up to there),
 //      gathered and sorted, and the sums of the weights ahead of that bin, a sum for
 //      each wave's share of the row;
@@ -31,8 +31,8 @@ namespace mgs {
 namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
-constexpr int kBinBits = 11, kBins = 1 << kBinBits;   // of 1/64: weights below e^-32 are less than a step
-constexpr float kPerUnit = 64.0f;
+constexpr int kBinBits = 11, kBins = 1 << kBinBits;
+constexpr float kPerUnit = 64.0f, kFar = 43.0f;   // half of the bins of 1/64, half of 43/64: to e^-704, less than 2^-1000
 constexpr int kList = 4096;         // candidates that are sorted
 constexpr int kFixed = 43;          // a weight's bits behind the point: 2^20 of them fit 64 bits
 constexpr int kCounted = 256;       // up to here sorting counts the smaller ones
@@ -75,6 +75,7 @@ struct Row {
     int kind;
     int top_k;           // 0: off
     float max, top;      // the largest logit; the same, the largest number where it is infinite
+    float half;          // of top
     float least;         // no smaller one passes min-p (the floor without it)
     float floor;         // what is below has no weight: -inf, or all but +inf
     float nothing;       // what is below has a weight of less than 2^-1000, or is below the floor
@@ -94,10 +95,14 @@ __device__ __forceinline__ Row settings(const SampleArgs &a, int64_t b, float to
     r.u = u > 0.0f ? (u < 1.0f ? u : 0.99999994f) : 0.0f;
     r.max = top;
     r.top = fminf(top, kMax);
+    r.half = 0.5f * r.top;
     r.floor = top == kInf ? kInf : -kMax;
     r.inv = 1.0f / tau;
     r.scale = 1.4426950408889634 / static_cast<double>(tau);
-    r.nothing = fmaxf(r.floor, static_cast<float>(static_cast<double>(r.top) - 1000.0 / r.scale));
+    // (rounded up: were it down, a value between could have a weight below 2^-1022)
+    const double end = static_cast<double>(r.top) - 1000.0 / r.scale;
+    const float near = static_cast<float>(end);
+    r.nothing = fmaxf(r.floor, static_cast<double>(near) < end ? of_key(key_of(near) + 1) : near);
     r.top_k = k > 0 && k < a.vocab ? k : 0;
     r.top_p = p < 1.0f ? (p > 0.0f ? p : 0.0f) : 1.0;
     r.min_p = m > 0.0f ? (m < 1.0f ? m : 1.0f) : 0.0f;
@@ -149,10 +154,13 @@ __device__ __forceinline__ uint64_t fixed(double w)
 
 __device__ __forceinline__ double unfixed(uint64_t q) { return static_cast<double>(q) * 0x1p-43; }
 
-// The bin of x, kBins past the last one and below the floor; falls with x
+// The bin of x, kBins past the last one and below the floor; falls with x.  (Of half the
+// distance, which is finite: a temperature may be as large.)
 __device__ __forceinline__ int bin_of(float x, const Row &r)
 {
-    const float d = r.top - fminf(x, kMax), t = d * r.inv * kPerUnit;
+    constexpr float kBend = kBins / 2 - kBins / 2 / kFar;
+    const float d = __builtin_fmaf(-0.5f, fminf(x, kMax), r.half), far = d * r.inv * (2.0f * kPerUnit);
+    const float t = fminf(far, __builtin_fmaf(far, 1.0f / kFar, kBend));
     const int bin = t < static_cast<float>(kBins) ? static_cast<int>(t) : kBins;
     return x >= r.floor ? (d == 0.0f ? 0 : bin) : kBins;   // (0 times an infinite inv is no number)
 }

@@ -160,6 +160,38 @@ def test_far_tails(gpu):
             check(logits, u, s, *run(logits, u, s), who=fixed)
 
 
+def test_neighbouring_numbers_and_small_temperatures(gpu):
+    """Logits one or two roundings below the largest, at temperatures that put them around 2^-1000 of its weight."""
+    say("sample neighbours")
+    for top in (10.0, 1.0, -3.0, 2.0 ** -20, 5e30):
+        x = np.full(300, top, np.float32)
+        for i in range(1, 300):
+            x[i] = np.nextafter(x[i - 1] if i < 4 else x[3], np.float32(-np.inf))
+        step = float(x[0]) - float(x[1])
+        for k in (0.3, 0.5001, 0.75, 0.999, 1.4, 1.5001, 1.9, 2.6, 700.0):   # steps to 2^-1000
+            logits = torch.from_numpy(np.tile(x[::-1].copy(), (8, 1))).to(gpu)
+            u = torch.linspace(0, 0.9999, 8, device=gpu)
+            for fixed in (dict(), dict(top_k=3), dict(top_p=0.7), dict(min_p=0.5)):
+                full = dict(dict(temperature=k * step * 1.4426950408889634 / 1000, top_k=0, top_p=1.0, min_p=0.0), **fixed)
+                s = settings(8, 0, **full)
+                check(logits, u, s, *run(logits, u, s), who=(top, k, fixed))
+
+
+def test_logits_over_the_whole_range(gpu):
+    """Distances past the largest number, at temperatures that large: their weights are not small."""
+    say("sample whole range")
+    g = torch.Generator().manual_seed(11)
+    for V in (500, 20000):
+        x = (6.6e38 * (torch.rand(12, V, generator=g, dtype=torch.float64) - 0.5)).float()
+        x[:, :40] = -3.4e38
+        x[::2, 40:43] = 3.4e38
+        x, u = x.to(gpu), torch.rand(12, generator=g).to(gpu)
+        for tau in (1e36, 1e38, 3e38, float("inf")):
+            for i, fixed in enumerate([dict(top_k=0, top_p=1.0), dict(top_k=0, min_p=0.0), dict(min_p=0.0)]):
+                s = settings(12, i, temperature=tau, **fixed)
+                check(x, u, s, *run(x, u, s), who=(V, tau, fixed))
+
+
 def test_strides(gpu):
     """Rows apart, a vocabulary inside a padded one, rows that no wide access can take."""
     say("sample strides")

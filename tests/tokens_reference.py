@@ -116,6 +116,7 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
         return int(np.argmax(x)), 0.0, 1.0
     with np.errstate(invalid="ignore"):
         w = np.where(x == top, 1.0, np.where((x == -np.inf) | (top == np.inf), 0.0, np.exp((x - top) / temperature)))
+    w = np.where(w < 2.0 ** -1000, 0.0, w)   # (as the operator is defined)
     order = np.argsort(-x, kind="stable")
     margin = 1.0
     if top_k > 0:
