@@ -12,7 +12,9 @@
  * count elements and may be 0 but not negative, device pointers, caller-owned
  * buffers and workspaces, no allocation, arguments checked before any HIP call.
  * The workspaces carry nothing from one call to the next and need not be
- * zero-filled, but for mgs_gated_*'s, which has to be once, as those of mgs.h.
+ * zero-filled, but for mgs_gated_*'s, which has to be once, as those of mgs.h, and
+ * which calls that fill theirs with other things (mgs_embed_bwd, mgs_sample, those of
+ * mgs_layers.h) must not have written to since.
  * Calls that share a workspace must not run concurrently.  A workspace for B sequences or
  * rows, T steps or n ids serves calls of fewer too.
  */
@@ -140,9 +142,8 @@ mgs_status mgs_gated_step(const mgs_gated_desc *desc, const void *x, const void 
  * and logp -inf; where the largest is +inf, those that are share all the weight.
  * Weights and sums are fp64 (the ones that top_p compares, multiples of 2^-43 of
  * the largest weight, whose sums are exact); a weight below 2^-1000 of the largest
- * counts as none.  A call's answers are the same every time; those of other batch
- * sizes and row strides may differ where u times the sum is within fp64's rounding of
- * a token's end.
+ * counts as none.  A call's answers are the same every time; in a batch of another size
+ * they may differ where u times the sum is within fp64's rounding of a token's end.
  * Envelope: vocab <= 2^20, B < 2^22.
  */
 typedef struct {

@@ -89,6 +89,42 @@ def test_graph_replays(gpu, name):
             assert torch.equal(x, y), n
 
 
+def test_two_graphs_on_one_workspace(gpu):
+    """Calls of two sizes, captured into a graph each, all on one workspace, replayed in turn with eager calls between."""
+    import scan_linear_rnns_amd as mgs
+    say("tokens two graphs")
+    both = [inputs(gpu, seed=1), inputs(gpu, B=1, T=5000, D=70, V=40000, dt=torch.float32, seed=2)]
+    sizes = [mgs.mgs_gated_workspace_size(3, 700, 320, backward=True),
+             mgs.mgs_gated_workspace_size(1, 5000, 70, backward=True),
+             mgs.mgs_embed_workspace_size(2100, 1000, 320), mgs.mgs_embed_workspace_size(5000, 40000, 70),
+             mgs.mgs_sample_workspace_size(3, 1000), mgs.mgs_sample_workspace_size(1, 40000)]
+    # (the recurrence's words are tagged: its workspace is its own)
+    spaces = {"gated": mgs.workspace(max(sizes[:2]), gpu), "other": mgs.workspace(max(sizes[2:]), gpu)}
+    use = {"table": "other", "gated": "gated", "gated_bwd": "gated", "sample": "other"}
+
+    def run(a):
+        return [t for name, ws in use.items() for t in calls(mgs, a)[name](ws=spaces[ws])]
+
+    want = [[t.clone() for t in run(a)] for a in both]
+    torch.cuda.synchronize()
+    graphs, outs = [torch.cuda.CUDAGraph() for _ in both], []
+    for graph, a in zip(graphs, both):
+        with torch.cuda.graph(graph):
+            outs.append(run(a))
+    for n in range(4):
+        for k in ((0, 1), (1, 0), (0, 0), (1, 1))[n]:
+            for o in outs[k]:
+                o.fill_(-7)
+            graphs[k].replay()
+            got = run(both[1 - k])   # eager, on the same workspaces
+            torch.cuda.synchronize()
+            for x, y in zip(outs[k], want[k]):
+                assert torch.equal(x, y), (n, k)
+            for x, y in zip(got, want[1 - k]):
+                assert torch.equal(x, y), (n, k)
+    assert mgs.mgs_workspace_check(spaces["gated"]) == 0
+
+
 def test_two_streams_at_once(gpu):
     """The same operators on two streams, a workspace each, interleaved."""
     import scan_linear_rnns_amd as mgs
