@@ -100,7 +100,7 @@ __device__ __forceinline__ Row settings(const SampleArgs &a, int64_t b, float to
     r.inv = 1.0f / tau;
     r.scale = 1.4426950408889634 / static_cast<double>(tau);
     // (rounded up: were it down, a value between could have a weight below 2^-1022)
-    const double end = static_cast<double>(r.top) - 1000.0 / r.scale;
+    const double end = static_cast<double>(r.top) - 693.1471805599453 * static_cast<double>(tau);
     const float near = static_cast<float>(end);
     r.nothing = fmaxf(r.floor, static_cast<double>(near) < end ? of_key(key_of(near) + 1) : near);
     r.top_k = k > 0 && k < a.vocab ? k : 0;
@@ -593,21 +593,21 @@ __device__ __forceinline__ void pick(const SampleArgs &a, const Row &r, int64_t 
     emit(a, b, at, static_cast<float>(log(w_at / total)));
 }
 
+// The first of the largest, which is among the places from..to-1
 template <typename T>
-__device__ __forceinline__ void pick_first(const SampleArgs &a, const Row &r, int64_t b, const T *x, Shared &sh)
+__device__ __forceinline__ void pick_first(const SampleArgs &a, const Row &r, int64_t b, const T *x, int from, int to, int &at)
 {
-    if (threadIdx.x == 0) sh.at = a.vocab;
+    if (threadIdx.x == 0) at = to;
     __syncthreads();
-    const int wv = wave();
-    const int per = (a.vocab + kWaves * 512 - 1) / (kWaves * 512) * 512;
-    const int lo = wv * per, hi = lo + per < a.vocab ? lo + per : a.vocab;
-    int first = a.vocab;
+    const int per = (to - from + kWaves * 512 - 1) / (kWaves * 512) * 512;
+    const int lo = from + wave() * per, hi = lo + per < to ? lo + per : to;
+    int first = to;
     walk(x, lo, hi, a.vec, [&](float v, int i) {
         if (v == r.max && i < first) first = i;
     });
-    if (first < a.vocab) atomicMin(&sh.at, first);
+    if (first < to) atomicMin(&at, first);
     __syncthreads();
-    if (threadIdx.x == 0) emit(a, b, sh.at, 0.0f);
+    if (threadIdx.x == 0) emit(a, b, at, 0.0f);
 }
 
 // Sorted candidates' weights: the sum over the places before `i`, thread by thread; a
@@ -1027,11 +1027,9 @@ __device__ __forceinline__ double wanted(const Row &r, const uint64_t *mass, Sha
     return r.top_p * unfixed(all);
 }
 
-template <typename T> __global__ void __launch_bounds__(kThreads) sample_row_kernel(SampleArgs a)
+// A row from its logits
+template <typename T> __device__ __forceinline__ void by_sorting(const SampleArgs &a, int64_t b, const T *x, Shared &sh)
 {
-    __shared__ Shared sh;
-    const int64_t b = blockIdx.x;
-    const T *x = static_cast<const T *>(a.logits) + b * a.stride;
     const int lo = wave() * a.share < a.vocab ? wave() * a.share : a.vocab;
     const int hi = lo + a.share < a.vocab ? lo + a.share : a.vocab;
     fill_roots(sh.roots);
@@ -1043,7 +1041,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) sample_row_ker
         return;
     }
     if (r.kind == GREEDY) {
-        pick_first(a, r, b, x, sh);
+        pick_first(a, r, b, x, 0, a.vocab, sh.at);
         return;
     }
     double want = 0.0;
@@ -1063,6 +1061,441 @@ template <typename T> __global__ void __launch_bounds__(kThreads) sample_row_ker
     if ((threadIdx.x & 63) == 0) sh.sub[wave()] = sum;
     __syncthreads();
     finish(a, r, b, x, kWaves, static_cast<int>(sh.n), want, sh);
+}
+
+template <typename T> __global__ void __launch_bounds__(kThreads) sample_row_kernel(SampleArgs a)
+{
+    __shared__ Shared sh;
+    const int64_t b = blockIdx.x;
+    by_sorting(a, b, static_cast<const T *>(a.logits) + b * a.stride, sh);
+}
+
+// ------------------------------------------------ rows counted by their values
+// bf16 has so few values between 2^-13 and 2^10 that a workgroup counts each, for a share
+// of the row and another: one pass over the row, then all filters end at a value and a
+// number of its equals, the shares' sums are products of counts and weights, and the
+// token's share alone is read again.  Values nearer to 0 count together, their weights one
+// by one; a row where a filter ends among them, or with values past 2^10 that matter, goes
+// by sorting.
+constexpr int kTallies = 4;                       // shares
+constexpr int kFirstMag = 114 << 7, kSide = 23 << 7;   // 2^-13 as bits; values of a sign
+constexpr int kMiddle = kSide, kValues = 2 * kSide + 1;   // from the largest to the smallest
+constexpr int kEach = (kValues + kThreads - 1) / kThreads;
+constexpr int kOthers = 512;
+constexpr uint32_t kStop = 1, kLow = 2;           // a value that counting does not serve; one of -2^10 or less
+
+struct Tally {
+    alignas(16) uint32_t count[kTallies][kEach * kThreads];
+    double w[kEach * kThreads];         // of the values ahead of the edge; 0 for the others, and the middle
+    double roots[kRoots];
+    uint32_t others[kOthers];   // bits, share << 16
+    uint64_t wu[kWaves], mid, mid_sum[kTallies];
+    double wd[kWaves], part[kTallies][kWaves], w_edge;
+    uint32_t eq[kWaves];
+    uint32_t n, flags, m;
+    int top, edge, at;
+};
+
+__device__ __forceinline__ float value_of(int pos)
+{
+    const int c = pos < kMiddle ? kMiddle - pos : pos - kMiddle;
+    return __uint_as_float(static_cast<uint32_t>(kFirstMag - 1 + c) << 16 | (pos < kMiddle ? 0u : 0x80000000u));
+}
+
+// How far a value is from the middle, the one with these bits: 0 for the middle's, above
+// kSide outside
+__device__ __forceinline__ int distance(uint32_t bits)
+{
+    const int over = static_cast<int>(bits & 0x7FFFu) - (kFirstMag - 1);
+    return over > 0 ? over : 0;
+}
+
+__device__ __forceinline__ int place_of(uint32_t bits, int distance)
+{
+    return kMiddle + (bits & 0x8000u ? distance : -distance);
+}
+
+typedef uint32_t Bits8 __attribute__((ext_vector_type(4)));
+
+// Eight values from place i on; -inf stands for places from hi on
+__device__ __forceinline__ Bits8 load_bits(const __bf16 *x, int i, int hi, bool vec)
+{
+    const uint16_t *bits = reinterpret_cast<const uint16_t *>(x);
+    if (vec && i + 8 <= hi) return *reinterpret_cast<const Bits8 *>(bits + i);
+    Bits8 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const uint32_t low = i + 2 * e < hi ? bits[i + 2 * e] : 0xFF80u;
+        v[e] = low | static_cast<uint32_t>(i + 2 * e + 1 < hi ? bits[i + 2 * e + 1] : 0xFF80u) << 16;
+    }
+    return v;
+}
+
+__device__ __forceinline__ uint32_t bits_of(const Bits8 &v, int e) { return e & 1 ? v[e / 2] >> 16 : v[e / 2] & 0xFFFFu; }
+
+// f(eight values) for the places lo..hi-1 of a row, a wave's
+template <typename F> __device__ __forceinline__ void walk_bits(const __bf16 *x, int lo, int hi, bool vec, F f)
+{
+    constexpr int U = 4;
+    const int lane = threadIdx.x & 63;
+    for (int base = lo; base < hi; base += 512 * U) {
+        Bits8 v[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) v[j] = load_bits(x, base + (j * 64 + lane) * 8, hi, vec);
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            if (base + j * 512 >= hi) break;
+            f(v[j]);
+        }
+    }
+}
+
+// The kept weight of a value, but for the edge's; `middle`: whether values near 0 stay
+__device__ __forceinline__ double weight_of(uint32_t bits, bool middle, const Row &r, const Tally &t, int &pos)
+{
+    const int c = distance(bits);
+    pos = c <= kSide ? place_of(bits, c) : kMiddle;   // (what is outside has no weight)
+    double w = t.w[pos];
+    if (middle && c == 0) {
+        w = weight(__uint_as_float(bits << 16), r, t.roots);
+        w = w >= r.min_p ? w : 0.0;
+    }
+    return w;
+}
+
+// The token, when all is counted: it is in share s, with `ahead` of the kept weight ahead
+// of it, and the share's first m values equal to the edge stay
+__device__ __forceinline__ void pick_in(const SampleArgs &a, const Row &r, int64_t b, const __bf16 *x, int s, double ahead,
+                                        double total, double target, int edge, uint32_t m, Tally &t)
+{
+    const int whole = a.share * (kWaves / kTallies), sub = a.share / kTallies, lane = threadIdx.x & 63;
+    const int from = s * whole, to = from + whole < a.vocab ? from + whole : a.vocab;
+    const bool middle = edge > kMiddle && t.n > 0;
+    const double each = t.w_edge;
+    // each wave's part of the share
+    const int own = from + wave() * sub;
+    double sum = 0.0;
+    uint32_t equal = 0;
+    walk_bits(x, own < to ? own : to, own + sub < to ? own + sub : to, a.vec, [&](const Bits8 &v) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            int pos;
+            sum += weight_of(bits_of(v, e), middle, r, t, pos);
+            equal += pos == edge;
+        }
+    });
+    sum = wave_sum(sum);
+    equal = wave_sum(equal);
+    if (lane == 0) {
+        t.wd[wave()] = sum;
+        t.eq[wave()] = equal;
+    }
+    __syncthreads();
+    int part = 0;   // (the last with any weight, where rounding has put the target past all)
+    double run = ahead, start = ahead;
+    uint32_t rest = m, left = m;
+    bool found = false;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        const uint32_t stay = t.eq[w] < rest ? t.eq[w] : rest;
+        const double mine = t.wd[w] + stay * each;
+        if (mine > 0.0 && !found) {
+            part = w;
+            start = run;
+            left = rest;
+            found = run + mine > target;
+        }
+        run += mine;
+        rest -= stay;
+    }
+    if (wave() != part) return;
+    // its wave finds the place
+    run = start;
+    int last = -1;
+    double w_last = 0.0;
+    const int lo = from + part * sub, hi = lo + sub < to ? lo + sub : to;
+    for (int base = lo; base < hi; base += 512) {
+        const int i = base + lane * 8;
+        const Bits8 v = load_bits(x, i, hi, a.vec);
+        double w[8], mine = 0.0;
+        bool same[8];
+        uint32_t equals = 0;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            int pos;
+            w[e] = weight_of(bits_of(v, e), middle, r, t, pos);
+            same[e] = pos == edge;
+            equals += same[e];
+        }
+        if (__ballot(equals != 0) && left) {
+            uint32_t up = equals;
+            for (int off = 1; off < 64; off <<= 1) {
+                const uint32_t o = __shfl_up(up, off, 64);
+                if (lane >= off) up += o;
+            }
+            uint32_t before = up - equals;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (same[e] && before < left) w[e] = each;
+                before += same[e];
+            }
+            const uint32_t seen = __builtin_amdgcn_readlane(up, 63);
+            left -= seen < left ? seen : left;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            mine += w[e];
+            if (w[e] > 0.0) {
+                last = i + e;
+                w_last = w[e];
+            }
+        }
+        double up = mine;
+        for (int off = 1; off < 64; off <<= 1) {
+            const double o = __shfl_up(up, off, 64);
+            if (lane >= off) up += o;
+        }
+        const uint64_t past = __ballot(mine > 0.0 && run + up > target);
+        if (past) {
+            if (lane != __builtin_ctzll(past)) return;
+            double at = run + (up - mine), w_at = 0.0;
+            int chosen = -1;
+            bool over = false;   // (the last one, if rounding leaves none)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                if (w[e] > 0.0 && !over) {
+                    chosen = i + e;
+                    w_at = w[e];
+                }
+                at += w[e];
+                over |= at > target;
+            }
+            emit(a, b, chosen, static_cast<float>(log(w_at / total)));
+            return;
+        }
+        run += __shfl(up, 63, 64);
+    }
+    int most = last;
+    for (int off = 32; off; off >>= 1) {
+        const int o = __shfl_xor(most, off, 64);
+        most = o > most ? o : most;
+    }
+    if (last == most && last >= 0) emit(a, b, last, static_cast<float>(log(w_last / total)));
+}
+
+// A row by counting; false (for the whole workgroup) where that does not serve it
+__device__ __forceinline__ bool by_counting(const SampleArgs &a, int64_t b, const __bf16 *x, Tally &t)
+{
+    const int s_own = wave() / (kWaves / kTallies), me = static_cast<int>(threadIdx.x);
+    fill_roots(t.roots);
+    for (int i = me; i < static_cast<int>(sizeof(t.count) / 16); i += kThreads)
+        reinterpret_cast<f32x4 *>(&t.count[0][0])[i] = f32x4{0, 0, 0, 0};
+    if (me < kTallies) t.mid_sum[me] = 0;
+    if (me == 0) {
+        t.mid = 0;
+        t.w_edge = 0.0;
+        t.n = t.flags = t.m = 0;
+        t.top = kValues;
+        t.edge = -1;
+    }
+    __syncthreads();
+    {
+        const int lo = wave() * a.share < a.vocab ? wave() * a.share : a.vocab;
+        const int hi = lo + a.share < a.vocab ? lo + a.share : a.vocab;
+        uint32_t *count = t.count[s_own], flags = 0;
+        walk_bits(x, lo, hi, a.vec, [&](const Bits8 &v) {
+            int least = kSide, most = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t o = bits_of(v, e);
+                const int c = distance(o);
+                least = c < least ? c : least;
+                most = c > most ? c : most;
+                if (c <= kSide) atomicAdd(&count[place_of(o, c)], 1u);
+            }
+            if (__ballot(least == 0 || most > kSide) == 0) return;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t o = bits_of(v, e);
+                const int c = distance(o);
+                if (c > kSide && o != 0xFF80u) flags |= o > 0x8000u && o < 0xFF80u ? kLow : kStop;
+                if (c == 0) {
+                    const uint32_t at = atomicAdd(&t.n, 1u);
+                    if (at < kOthers) t.others[at] = o | static_cast<uint32_t>(s_own) << 16;
+                }
+            }
+        });
+        if (flags) atomicOr(&t.flags, flags);
+    }
+    __syncthreads();
+    if ((t.flags & kStop) || t.n > kOthers) return false;
+
+    // this thread's neighbouring values
+    uint32_t n[kEach];
+    int first = kValues;
+#pragma unroll
+    for (int e = kEach - 1; e >= 0; --e) {
+        const int pos = me * kEach + e;
+        n[e] = 0;
+#pragma unroll
+        for (int s = 0; s < kTallies; ++s) n[e] += t.count[s][pos];
+        if (n[e]) first = pos;
+    }
+    if (first < kValues) atomicMin(&t.top, first);
+    __syncthreads();
+    const int top = t.top;
+    if (top == kMiddle || top == kValues) return false;
+    const Row r = settings(a, b, value_of(top));
+    if (r.kind == GREEDY) {
+        int s = 0;
+        while (t.count[s][top] == 0) ++s;
+        const int whole = a.share * (kWaves / kTallies), from = s * whole;
+        pick_first(a, r, b, x, from, from + whole < a.vocab ? from + whole : a.vocab, t.at);
+        return true;
+    }
+    if ((t.flags & kLow) && !(r.nothing > -1024.0f)) return false;
+    double w[kEach];
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const int pos = me * kEach + e;
+        w[e] = weight(value_of(pos < kValues ? pos : kValues - 1), r, t.roots);
+    }
+    for (int i = me; i < static_cast<int>(t.n); i += kThreads) {
+        const double o = weight(__uint_as_float(t.others[i] << 16), r, t.roots);
+        atomicAdd(reinterpret_cast<unsigned long long *>(&t.mid), static_cast<unsigned long long>(fixed(o)));
+        if (o >= r.min_p)
+            atomicAdd(reinterpret_cast<unsigned long long *>(&t.mid_sum[t.others[i] >> 16]),
+                      static_cast<unsigned long long>(o * 0x1p51));
+    }
+    // how many of each value stay, and the last of them
+    uint64_t all;
+    bool stop = false;
+    int last = -1;
+    if (r.top_k) {
+        uint64_t sum = 0;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) sum += n[e];
+        uint64_t before = scan_block(sum, t.wu, all);
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            const uint64_t k = static_cast<uint64_t>(r.top_k), room = before < k ? k - before : 0;
+            before += n[e];
+            stop |= me * kEach + e == kMiddle && room > 0 && room < n[e];
+            n[e] = n[e] < room ? n[e] : static_cast<uint32_t>(room);
+        }
+    }
+    __syncthreads();
+    if (r.top_p < 1.0) {
+        uint64_t q[kEach], sum = 0;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            q[e] = fixed(w[e]) * n[e];
+            if (me * kEach + e == kMiddle) q[e] = n[e] ? t.mid : 0;
+            sum += q[e];
+        }
+        uint64_t before = scan_block(sum, t.wu, all);
+        // (those with less than `want` ahead of them; the first at least)
+        const double exact = ceil(r.top_p * static_cast<double>(all));
+        const uint64_t want = exact > 1.0 ? static_cast<uint64_t>(exact) : 1;
+        uint64_t left = 0, one = 0;
+        uint32_t most = 0;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+            if (n[e] && before < want) {
+                last = me * kEach + e;
+                left = want - 1 - before;
+                one = fixed(w[e]);
+                most = n[e];
+            }
+            before += q[e];
+        }
+        if (last >= 0) atomicMax(&t.edge, last);
+        __syncthreads();
+        if (last >= 0 && last == t.edge) t.m = one && left / one < most ? static_cast<uint32_t>(left / one) + 1 : most;
+    } else if (r.top_k) {
+        uint32_t most = 0;
+#pragma unroll
+        for (int e = 0; e < kEach; ++e)
+            if (n[e]) {
+                last = me * kEach + e;
+                most = n[e];
+            }
+        if (last >= 0) atomicMax(&t.edge, last);
+        __syncthreads();
+        if (last >= 0 && last == t.edge) t.m = most;
+    }
+    if (stop) atomicOr(&t.flags, kStop);
+    __syncthreads();
+    const int edge = t.edge < 0 ? kValues : t.edge;
+    if (edge == kMiddle || (t.flags & kStop)) return false;
+    const uint32_t m = t.m;
+    // the shares' kept weights
+    double sums[kTallies] = {};
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+        const int pos = me * kEach + e;
+        uint32_t rest = pos < edge ? 0xFFFFFFFFu : pos == edge ? m : 0;
+        const double each = w[e] >= r.min_p && pos != kMiddle ? w[e] : 0.0;
+        t.w[pos] = pos < edge ? each : 0.0;
+        if (pos == edge) t.w_edge = each;
+#pragma unroll
+        for (int s = 0; s < kTallies; ++s) {
+            const uint32_t c = t.count[s][pos], stay = c < rest ? c : rest;
+            rest -= stay;
+            sums[s] += stay * each;
+        }
+    }
+    // (a quarter of the lanes for each share)
+    const int lane = me & 63, quarter = lane >> 4;
+    static_assert(kTallies == 4 && kWaves == 16, "a lane for each share's wave");
+    auto halves = [&](double low, double high, int bit) {   // of the other lanes too: low where the bit is not set
+        return (lane & bit ? high : low) + __shfl_xor(lane & bit ? low : high, bit, 64);
+    };
+    auto within = [&](double v) {
+        for (int off = 8; off; off >>= 1) v += __shfl_xor(v, off, 64);
+        return v;
+    };
+    const double wave_part = within(halves(halves(sums[0], sums[2], 32), halves(sums[1], sums[3], 32), 16));
+    if ((lane & 15) == 0) t.part[quarter][wave()] = wave_part;
+    __syncthreads();
+    const double share_sum = within(t.part[quarter][lane & 15]);
+    double total = 0.0;
+#pragma unroll
+    for (int s = 0; s < kTallies; ++s) {
+        sums[s] = __shfl(share_sum, 16 * s, 64) + (edge > kMiddle ? static_cast<double>(t.mid_sum[s]) * 0x1p-51 : 0.0);
+        total += sums[s];
+    }
+    const double target = static_cast<double>(r.u) * total;
+    int in = 0;
+    double ahead = 0.0, run = 0.0;
+    bool found = false;
+#pragma unroll
+    for (int s = 0; s < kTallies; ++s) {   // (the last one, where rounding has put the target past all)
+        if (sums[s] > 0.0 && !found) {
+            in = s;
+            ahead = run;
+            found = run + sums[s] > target;
+        }
+        run += sums[s];
+    }
+    uint32_t left = m;
+    if (edge < kValues)
+        for (int s = 0; s < in; ++s) left -= t.count[s][edge] < left ? t.count[s][edge] : left;
+    pick_in(a, r, b, x, in, ahead, total, target, edge, left, t);
+    return true;
+}
+
+__global__ void __launch_bounds__(kThreads) sample_count_kernel(SampleArgs a)
+{
+    __shared__ union Either {
+        Shared sh;
+        Tally t;
+    } u;
+    const int64_t b = blockIdx.x;
+    const __bf16 *x = static_cast<const __bf16 *>(a.logits) + b * a.stride;
+    if (by_counting(a, b, x, u.t)) return;
+    __syncthreads();
+    by_sorting(a, b, x, u.sh);
 }
 
 // ------------------------------------------------------ rows cut into slices
@@ -1167,7 +1600,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) sample_pick_ke
         return;
     }
     if (r.kind == GREEDY) {
-        pick_first(a, r, b, x, sh);
+        pick_first(a, r, b, x, 0, a.vocab, sh.at);
         return;
     }
     fill_roots(sh.roots);
@@ -1211,7 +1644,8 @@ SampleGeom sample_geometry(const mgs_sample_desc &d)
 template <typename T> hipError_t run(const SampleArgs &a, unsigned rows, hipStream_t s)
 {
     if (a.slices == 1) {
-        sample_row_kernel<T><<<dim3(rows), dim3(kThreads), 0, s>>>(a);
+        if constexpr (sizeof(T) == 2) sample_count_kernel<<<dim3(rows), dim3(kThreads), 0, s>>>(a);
+        else sample_row_kernel<T><<<dim3(rows), dim3(kThreads), 0, s>>>(a);
         return hipGetLastError();
     }
     const dim3 grid(rows * a.slices), block(kThreads);
