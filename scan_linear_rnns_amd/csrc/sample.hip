@@ -16,8 +16,9 @@
 // A row without top-k and top-p needs 1, the sums of 3, and 4.  Where a bin holds too
 // many to sort (equal logits by the thousand), its values are split again, one
 // histogram after another, by the row's workgroup alone.
-// Large batches take a workgroup a row for all of it; for small ones a row is cut into
-// slices, each step a launch.
+// Large batches take a workgroup a row for all of it; for small ones a long row is cut into
+// slices, each step a launch.  Rows of bf16 logits that need 2 are counted by value instead
+// (below).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -1624,16 +1625,24 @@ struct SampleGeom {
     size_t slot;
 };
 
-SampleGeom sample_geometry(const mgs_sample_desc &d)
+constexpr int kShort = 4 * kWaves;   // what waves read at once, of a row that is not cut
+
+int64_t wave_steps(const mgs_sample_desc &d)
+{
+    const int64_t step = 64 * (d.dtype == MGS_BF16 ? 8 : 4);
+    return (d.vocab + step - 1) / step;
+}
+
+// cut: whether rows may be cut at all
+SampleGeom sample_geometry(const mgs_sample_desc &d, bool cut)
 {
     SampleGeom g{};
-    const int64_t step = 64 * (d.dtype == MGS_BF16 ? 8 : 4);   // what a wave reads at once
-    const int64_t steps = (d.vocab + step - 1) / step;
+    const int64_t step = 64 * (d.dtype == MGS_BF16 ? 8 : 4), steps = wave_steps(d);
     // Workgroups for every CU, no more than there are waves' steps.  Rows of up to four
     // steps a wave stay with one (32000, bf16, all filters: 1 row 21 us, cut in four 26; 128
     // rows of mixed settings 44, in two 55); longer ones are cut (8 rows of 128000: 52, whole
     // or in four 72 and 57).
-    int64_t s = steps <= 4 * kWaves || d.B <= 0 ? 1 : std::min<int64_t>((steps + kWaves - 1) / kWaves, kWorkgroups / d.B);
+    int64_t s = !cut || steps <= kShort || d.B <= 0 ? 1 : std::min<int64_t>((steps + kWaves - 1) / kWaves, kWorkgroups / d.B);
     s = std::max<int64_t>(1, std::min<int64_t>(s, kMaxSlices));
     g.slices = static_cast<int>(s);
     g.share = static_cast<int>((steps + s * kWaves - 1) / (s * kWaves) * step);
@@ -1641,19 +1650,37 @@ SampleGeom sample_geometry(const mgs_sample_desc &d)
     return g;
 }
 
+// Whether some row's filter ends where only a histogram tells; one top_k for all rows that
+// the threads' largest logits serve needs none
+bool histograms(const SampleArgs &a)
+{
+    if (a.top_k) return true;
+    if (a.k0 > 0 && a.k0 < a.vocab) return a.k0 > (a.slices > 1 ? kGroups / 2 * a.slices : kThreads / 2);
+    return a.top_p || a.p0 < 1.0f;
+}
+
+// Whether bf16 rows are counted.  Measured, us, counted / otherwise: with a histogram, 1 and
+// 256 rows of 32000 by top-p 21/37 and 22/43, mixed settings 22/32 and 24/47, 8 of 128000 39/52,
+// 256 mixed 45/120, but 8 of 262144 mixed 65/53; without one, 1 row of 32000 18/17, by min-p
+// 19/13, 1 of 128000 36/21, 256 of them 40/52, by top-k 41/38, by min-p 40/34.
+bool counted(const mgs_sample_desc &d, const SampleArgs &a)
+{
+    if (d.dtype != MGS_BF16) return false;
+    const int64_t steps = wave_steps(d);
+    if (histograms(a)) return a.slices == 1 || steps <= 4 * kShort;
+    const bool plain = !(a.k0 > 0 && a.k0 < a.vocab) && !a.min_p && !(a.m0 > 0.0f);
+    return plain && a.slices == 1 && steps > kShort;
+}
+
 template <typename T> hipError_t run(const SampleArgs &a, unsigned rows, hipStream_t s)
 {
     if (a.slices == 1) {
-        if constexpr (sizeof(T) == 2) sample_count_kernel<<<dim3(rows), dim3(kThreads), 0, s>>>(a);
-        else sample_row_kernel<T><<<dim3(rows), dim3(kThreads), 0, s>>>(a);
+        sample_row_kernel<T><<<dim3(rows), dim3(kThreads), 0, s>>>(a);
         return hipGetLastError();
     }
     const dim3 grid(rows * a.slices), block(kThreads);
-    // one top_k for all rows that the groups' largest logits serve needs no histogram
-    const bool k = a.k0 > 0 && a.k0 < a.vocab;
-    const bool filters = a.top_k || (k ? a.k0 > kGroups / 2 * a.slices : a.top_p || a.p0 < 1.0f);
     sample_top_kernel<T><<<grid, block, 0, s>>>(a);
-    if (filters) sample_bins_kernel<T><<<grid, block, 0, s>>>(a);
+    if (histograms(a)) sample_bins_kernel<T><<<grid, block, 0, s>>>(a);
     sample_gather_kernel<T><<<grid, block, 0, s>>>(a);
     sample_pick_kernel<T><<<dim3(rows), block, 0, s>>>(a);
     return hipGetLastError();
@@ -1666,20 +1693,27 @@ size_t sample_workspace(const mgs_sample_desc &d)
     // (more rows than this are not cut; the bytes of fewer grow with their number)
     mgs_sample_desc cut = d;
     cut.B = std::min<int64_t>(d.B, kWorkgroups / 2);
-    return 256 + sample_geometry(cut).slot * static_cast<size_t>(cut.B);
+    return 256 + sample_geometry(cut, true).slot * static_cast<size_t>(cut.B);
 }
 
 hipError_t launch_sample(const mgs_sample_desc &d, const void *logits, const float *u, const float *temperature,
                          const int32_t *top_k, const float *top_p, const float *min_p, int64_t *token, float *logp,
                          void *ws, hipStream_t s)
 {
-    const SampleGeom g = sample_geometry(d);
+    SampleGeom g = sample_geometry(d, true);
     const int size = d.dtype == MGS_BF16 ? 2 : 4;
     const bool vec = (reinterpret_cast<uintptr_t>(logits) & 15) == 0 && (d.B == 1 || (d.logits_stride * size) % 16 == 0);
-    const SampleArgs a{logits, u, temperature, top_p, min_p, top_k, token, logp, d.logits_stride,
+    SampleArgs a{logits, u, temperature, top_p, min_p, top_k, token, logp, d.logits_stride,
                        static_cast<char *>(ws), g.slot, static_cast<int>(d.vocab), g.slices, g.share, d.top_k,
                        d.temperature, d.top_p, d.min_p, vec};
     const unsigned rows = static_cast<unsigned>(d.B);
+    if (counted(d, a)) {
+        g = sample_geometry(d, false);
+        a.slices = g.slices;
+        a.share = g.share;
+        sample_count_kernel<<<dim3(rows), dim3(kThreads), 0, s>>>(a);
+        return hipGetLastError();
+    }
     return d.dtype == MGS_BF16 ? run<__bf16>(a, rows, s) : run<float>(a, rows, s);
 }
 

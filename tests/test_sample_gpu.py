@@ -89,6 +89,57 @@ def test_numbers_for_all_rows(gpu):
         check(x, u, settings(9, 0, **dict(full, top_k=min(full["top_k"], 2 ** 31 - 1))), *mgs.mgs_sample(x, u, **fixed))
 
 
+@pytest.mark.parametrize("B, V", [(3, 800), (2, 32000), (2, 50001), (2, 200000), (130, 40000)])
+def test_numbers_for_all_rows_bf16(gpu, B, V):
+    """(Other kernels than a tensor of settings takes.)"""
+    import scan_linear_rnns_amd as mgs
+    say(f"sample numbers bf16 {B} x {V}")
+    x, u = draw(gpu, B, V, "bf16", V)
+    for fixed in (dict(), dict(top_k=5), dict(top_k=700), dict(top_p=0.8), dict(min_p=0.1),
+                  dict(temperature=0.9, top_k=40, top_p=0.9, min_p=0.05), dict(temperature=0.0)):
+        full = dict(dict(temperature=1.0, top_k=0, top_p=1.0, min_p=0.0), **fixed)
+        rows = slice(0, min(B, 6))
+        token, logp = mgs.mgs_sample(x, u, **fixed)
+        check(x[rows], u[rows], settings(B, 0, **full), token[rows], logp[rows], who=fixed)
+
+
+def test_bf16_values_that_are_rare(gpu):
+    """Near 0 (many of them, filters that end among them), 2^10 and more, -2^10 and less at temperatures where that has
+    weight, the lowest number as a mask, infinities and NaN."""
+    say("sample rare bf16")
+    inf, nan = float("inf"), float("nan")
+    g = torch.Generator().manual_seed(12)
+    for V in (600, 40000):
+        base = torch.randn(14, V, generator=g)
+        rows = base.clone()
+        rows[0, ::3] = 0.0
+        rows[1] = -rows[1].abs()
+        rows[1, 5:40] = 2.0 ** -15 * torch.randn(35, generator=g)     # the largest are near 0
+        rows[2] = 2.0 ** -14 * rows[2]
+        rows[3] = 1e-30 * rows[3]
+        rows[4] = 400 * rows[4]
+        rows[5] = 2000 + rows[5]
+        rows[6] = -3000 + 16 * rows[6]
+        rows[7, 7:] = torch.finfo(torch.bfloat16).min
+        rows[8, :V - 3] = -1024.0
+        rows[8, V - 3:] = 1.0
+        rows[9, 3] = inf
+        rows[10, V - 1] = nan
+        rows[11] = torch.where(rows[11] > 0, -0.0, 0.0)
+        rows[12] = rows[12].clamp(max=2.0 ** -20)
+        rows[13, :] = -2.0 ** -13
+        rows[13, 9] = 2.0 ** -13
+        x, u = rows.bfloat16().to(gpu), torch.rand(14, generator=g).to(gpu)
+        for i, fixed in enumerate([dict(top_k=0, min_p=0.0), dict(top_p=1.0, min_p=0.0), dict(min_p=0.0),
+                                   dict(temperature=1e4, top_k=0), dict(temperature=1e-3), dict(temperature=0.0), {}]):
+            s = settings(14, i, **fixed)
+            if i == 1:
+                s["top_k"][:] = [7, 20, 40, 2, 9, 3, 5, 8, 2, 1, 4, V // 2, V // 2 + 17, 3]
+            if i == 2:
+                s["top_k"][:] = V - 5
+            check(x, u, s, *run(x, u, s), who=(V, i))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_ties(gpu, dtype):
     """Equal logits by the thousand: of equals the first by index stay."""
