@@ -29,6 +29,7 @@ namespace {
 constexpr int kMaxChunk = 32;     // sorted places of a workgroup (one more lane looks behind them)
 constexpr int kSortWaves = 16;
 constexpr int kMaxRange = 512;    // ids of a sorting workgroup
+constexpr int kHeld = 256;        // places of its ids that a sorting wave remembers
 
 typedef __bf16 bf8v __attribute__((ext_vector_type(8)));
 typedef float f8v __attribute__((ext_vector_type(8), aligned(16)));
@@ -147,12 +148,15 @@ template <typename F> __device__ __forceinline__ void each_id(const SortArgs &a,
 }
 
 // Each wave takes an equal share of the places and counts its ids of the range in a
-// row of its own, so the second pass places them in order without a barrier.
+// row of its own, so that it places them in order without a barrier afterwards: from
+// what it remembers of them, or, if they are more, by reading its share again (32768
+// ids, all read twice: 22 us).
 __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
 {
     __shared__ int32_t at[kSortWaves * kMaxRange];   // [wave][local id]: counts, then next places
     __shared__ int64_t below[kSortWaves];
     __shared__ int32_t scan[kSortWaves];
+    __shared__ int2 held[kSortWaves][kHeld];         // id, place
     const int lane = threadIdx.x & 63, wv = wave();
     const int32_t mask = (1 << a.bits) - 1, own = static_cast<int32_t>(a.block + blockIdx.x);
     const int ids = a.range;   // (the last one may lie past the table)
@@ -162,9 +166,18 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
     const int64_t n0 = wv * share, n1 = n0 + share < a.n ? n0 + share : a.n;
     int32_t *mine = at + wv * a.range;
     int64_t smaller = 0;
-    each_id(a, n0, n1, [&](int32_t id, int64_t) {
+    int many = 0;
+    each_id(a, n0, n1, [&](int32_t id, int64_t n) {
         if (id >= 0 && (id & mask) < own) ++smaller;
-        if (id >= 0 && (id & mask) == own) atomicAdd(&at[wv * a.range + (id >> a.bits)], 1);
+        const bool hit = id >= 0 && (id & mask) == own;
+        const uint64_t who = __ballot(hit);
+        if (!who) return;
+        if (hit) {
+            atomicAdd(&at[wv * a.range + (id >> a.bits)], 1);
+            const int i = many + __popcll(who & ((1ull << lane) - 1));
+            if (i < kHeld) held[wv][i] = int2{id, static_cast<int32_t>(n)};
+        }
+        many += __popcll(who);
     });
     for (int off = 32; off; off >>= 1) smaller += __shfl_xor(smaller, off, 64);
     if (lane == 0) below[wv] = smaller;
@@ -200,7 +213,7 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
         }
     }
     __syncthreads();
-    each_id(a, n0, n1, [&](int32_t id, int64_t n) {
+    auto put = [&](int32_t id, int64_t n) {
         const int local = id >= 0 && (id & mask) == own ? id >> a.bits : -1;
         // one round for each id among the lanes: its lanes in order
         for (uint64_t left = __ballot(local >= 0); left;) {
@@ -217,7 +230,15 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
             left &= ~same;
         }
-    });
+    };
+    if (many > kHeld) {
+        each_id(a, n0, n1, put);
+        return;
+    }
+    for (int i = 0; i < many; i += 64) {
+        const int2 h = held[wv][i + lane];   // (a multiple of 64 has room)
+        put(i + lane < many ? h.x : -1, h.y);
+    }
 }
 
 // -------------------------------------------------------------------- sums

@@ -756,12 +756,13 @@ __global__ void __launch_bounds__(1024) gated_dlam_kernel(const uint64_t *part, 
     const int64_t share = (rows + 15) / 16;
     double sum = 0.0;
     const int64_t end = (wv + 1) * share < rows ? (wv + 1) * share : rows;
-    for (int64_t i = wv * share; i < end; i += 8) {
-        float v[8];
+    constexpr int U = 16;   // loads in flight
+    for (int64_t i = wv * share; i < end; i += U) {
+        float v[U];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = i + e < end ? tag_value(part[(i + e) * D + cc]) : 0.0f;
+        for (int e = 0; e < U; ++e) v[e] = tag_value(part[(i + e < end ? i + e : end - 1) * D + cc]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += static_cast<double>(v[e]);
+        for (int e = 0; e < U; ++e) sum += i + e < end ? static_cast<double>(v[e]) : 0.0;
     }
     s[wv][lane] = sum;
     __syncthreads();
