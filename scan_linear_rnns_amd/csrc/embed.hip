@@ -122,7 +122,6 @@ struct SortArgs {
     const void *ids;
     int64_t block, n, vocab, d;
     int bits, range;    // 2^bits workgroups, ids of each
-    bool wide_ids;
     int64_t *count;     // ids inside the table
     int32_t *first;     // the first place of each id, in their order, and one past the last
     int32_t *row, *id;  // sorted
@@ -130,20 +129,18 @@ struct SortArgs {
 
 // f(id, place) for the wave's places n0..n1-1, lane by lane, several loads in flight.  Ids
 // outside the table are -1, and so are places past the end (the wave stays whole)
-template <typename F> __device__ __forceinline__ void each_id(const SortArgs &a, int64_t n0, int64_t n1, F f)
+template <typename I, typename F> __device__ __forceinline__ void each_id(const SortArgs &a, uint32_t n0, uint32_t n1, F f)
 {
-    constexpr int kBatch = 8;
-    const int lane = threadIdx.x & 63;
-    for (int64_t n = n0; n < n1; n += 64 * kBatch) {
-        int64_t id[kBatch];
+    constexpr int kBatch = 4;
+    const I *ids = static_cast<const I *>(a.ids);
+    const I vocab = static_cast<I>(a.vocab);   // (unsigned: what is negative is past it)
+    for (uint32_t n = n0 + (threadIdx.x & 63); n - (threadIdx.x & 63) < n1; n += 64 * kBatch) {
+        I id[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const int64_t at = n + 64 * k + lane;
-            id[k] = id_at(a.ids, a.wide_ids, at < n1 ? at : n1 - 1);
-            if (at >= n1 || id[k] < 0 || id[k] >= a.vocab) id[k] = -1;
-        }
+        for (int k = 0; k < kBatch; ++k) id[k] = ids[n + 64 * k < n1 ? n + 64 * k : n1 - 1];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) f(static_cast<int32_t>(id[k]), n + 64 * k + lane);
+        for (int k = 0; k < kBatch; ++k)
+            f(id[k] < vocab && n + 64 * k < n1 ? static_cast<int32_t>(id[k]) : -1, n + 64 * k);
     }
 }
 
@@ -151,10 +148,10 @@ template <typename F> __device__ __forceinline__ void each_id(const SortArgs &a,
 // row of its own, so that it places them in order without a barrier afterwards: from
 // what it remembers of them, or, if they are more, by reading its share again (32768
 // ids, all read twice: 22 us).
-__global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
+template <typename I> __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
 {
     __shared__ int32_t at[kSortWaves * kMaxRange];   // [wave][local id]: counts, then next places
-    __shared__ int64_t below[kSortWaves];
+    __shared__ int32_t below[kSortWaves];
     __shared__ int32_t scan[kSortWaves];
     __shared__ int2 held[kSortWaves][kHeld];         // id, place
     const int lane = threadIdx.x & 63, wv = wave();
@@ -162,14 +159,15 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
     const int ids = a.range;   // (the last one may lie past the table)
     for (int i = threadIdx.x; i < kSortWaves * a.range; i += 64 * kSortWaves) at[i] = 0;
     __syncthreads();
-    const int64_t share = (a.n + kSortWaves - 1) / kSortWaves;
-    const int64_t n0 = wv * share, n1 = n0 + share < a.n ? n0 + share : a.n;
+    const uint32_t count = static_cast<uint32_t>(a.n), share = (count + kSortWaves - 1) / kSortWaves;
+    const uint32_t n0 = wv * share < count ? wv * share : count, n1 = share < count - n0 ? n0 + share : count;
     int32_t *mine = at + wv * a.range;
-    int64_t smaller = 0;
+    int32_t smaller = 0;
     int many = 0;
-    each_id(a, n0, n1, [&](int32_t id, int64_t n) {
-        if (id >= 0 && (id & mask) < own) ++smaller;
-        const bool hit = id >= 0 && (id & mask) == own;
+    each_id<I>(a, n0, n1, [&](int32_t id, uint32_t n) {
+        const int32_t rest = id >= 0 ? id & mask : mask + 1;
+        smaller += rest < own;
+        const bool hit = rest == own;
         const uint64_t who = __ballot(hit);
         if (!who) return;
         if (hit) {
@@ -182,7 +180,7 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
     for (int off = 32; off; off >>= 1) smaller += __shfl_xor(smaller, off, 64);
     if (lane == 0) below[wv] = smaller;
     __syncthreads();
-    int64_t base = 0;
+    int32_t base = 0;
     for (int w = 0; w < kSortWaves; ++w) base += below[w];
     // exclusive sums over (id, wave): a thread for each id
     static_assert(kMaxRange <= 64 * kSortWaves, "a thread for each id");
@@ -200,7 +198,7 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
     __syncthreads();
     for (int w = 0; w < wv; ++w) before += scan[w];
     if (i < ids) {
-        int32_t next = static_cast<int32_t>(base) + before;
+        int32_t next = base + before;
         a.first[static_cast<int64_t>(own) * a.range + i] = next;
         for (int w = 0; w < kSortWaves; ++w) {
             const int32_t c = at[w * a.range + i];
@@ -213,7 +211,7 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
         }
     }
     __syncthreads();
-    auto put = [&](int32_t id, int64_t n) {
+    auto put = [&](int32_t id, uint32_t n) {
         const int local = id >= 0 && (id & mask) == own ? id >> a.bits : -1;
         // one round for each id among the lanes: its lanes in order
         for (uint64_t left = __ballot(local >= 0); left;) {
@@ -232,7 +230,7 @@ __global__ void __launch_bounds__(64 * kSortWaves) sort_kernel(SortArgs a)
         }
     };
     if (many > kHeld) {
-        each_id(a, n0, n1, put);
+        each_id<I>(a, n0, n1, put);
         return;
     }
     for (int i = 0; i < many; i += 64) {
@@ -506,14 +504,14 @@ hipError_t launch_embed_bwd(const EmbedGeom &g, const void *ids, bool wide_ids, 
     a.d = d;
     a.bits = g.bits;
     a.range = g.range;
-    a.wide_ids = wide_ids;
     a.count = reinterpret_cast<int64_t *>(w);
     a.first = reinterpret_cast<int32_t *>(w + g.off_first);
     a.row = reinterpret_cast<int32_t *>(w + g.off_row);
     a.id = reinterpret_cast<int32_t *>(w + g.off_id);
     const hipError_t e = launch_sliced(int64_t(1) << g.bits, 64 * kSortWaves, [&](int64_t first, unsigned blocks) {
         a.block = first;
-        sort_kernel<<<dim3(blocks), dim3(64 * kSortWaves), 0, s>>>(a);
+        if (wide_ids) sort_kernel<uint64_t><<<dim3(blocks), dim3(64 * kSortWaves), 0, s>>>(a);
+        else sort_kernel<uint32_t><<<dim3(blocks), dim3(64 * kSortWaves), 0, s>>>(a);
     });
     if (e != hipSuccess) return e;
     SumArgs b{};
