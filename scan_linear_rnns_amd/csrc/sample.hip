@@ -52,7 +52,7 @@ struct SampleArgs {
     size_t slot;     // workspace bytes of a row
     int vocab, slices, share, k0;
     float t0, p0, m0;
-    bool vec;
+    bool vec, plain;     // plain: no row has a filter
 };
 
 __device__ __forceinline__ int wave() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
@@ -197,29 +197,41 @@ template <> struct Wide<__bf16> {
     static constexpr int N = 8;
 };
 
+// What a wave reads at once from place `base` of a row on, before hi: four times N
+// neighbours a lane; -inf stands for places from hi on
+constexpr int kLoads = 4;
+
+template <typename T>
+__device__ __forceinline__ void load_some(const T *x, int base, int hi, bool vec, float (&v)[kLoads][Wide<T>::N])
+{
+    constexpr int N = Wide<T>::N;
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+        const int i = base + (j * 64 + lane) * N;
+        if (vec && i + N <= hi) {
+            const typename Wide<T>::V w = *reinterpret_cast<const typename Wide<T>::V *>(x + i);
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[j][e] = static_cast<float>(w[e]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e) v[j][e] = i + e < hi ? static_cast<float>(x[i + e]) : -kInf;
+        }
+    }
+}
+
 // f(values, index of the first) for the places lo..hi-1, hi <= V, of a row, four
 // neighbours a lane at a time; lo is a multiple of what a wave reads at once.  -inf stands
 // for places past hi.  The wave stays whole.
 template <typename T, typename F> __device__ __forceinline__ void walk4(const T *x, int lo, int hi, bool vec, F f)
 {
-    constexpr int N = Wide<T>::N, U = 4;
+    constexpr int N = Wide<T>::N;
     const int lane = threadIdx.x & 63;
-    for (int base = lo; base < hi; base += 64 * N * U) {
-        float v[U][N];
+    for (int base = lo; base < hi; base += 64 * N * kLoads) {
+        float v[kLoads][N];
+        load_some(x, base, hi, vec, v);
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            const int i = base + (j * 64 + lane) * N;
-            if (vec && i + N <= hi) {
-                const typename Wide<T>::V w = *reinterpret_cast<const typename Wide<T>::V *>(x + i);
-#pragma unroll
-                for (int e = 0; e < N; ++e) v[j][e] = static_cast<float>(w[e]);
-            } else {
-#pragma unroll
-                for (int e = 0; e < N; ++e) v[j][e] = i + e < hi ? static_cast<float>(x[i + e]) : -kInf;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < U; ++j) {
+        for (int j = 0; j < kLoads; ++j) {
             if (base + j * 64 * N >= hi) break;
 #pragma unroll
             for (int e = 0; e < N; e += 4) f(&v[j][e], base + (j * 64 + lane) * N + e);
@@ -1028,6 +1040,54 @@ __device__ __forceinline__ double wanted(const Row &r, const uint64_t *mass, Sha
     return r.top_p * unfixed(all);
 }
 
+// Without filters, 1 and 3 at once: the sum of the weights of a wave's share, as parts of
+// the share's own largest (`top`; NaN if it holds one), which is 1 of them
+template <typename T>
+__device__ __forceinline__ double share_sum(const SampleArgs &a, int64_t b, const T *x, int lo, int hi, const double *roots,
+                                            float &top)
+{
+    constexpr int N = Wide<T>::N;
+    double sum = 0.0;
+    bool nan = false;
+    Row r{};
+    top = -kInf;
+    for (int base = lo; base < hi; base += 64 * N * kLoads) {
+        float v[kLoads][N], most = -kInf;
+        load_some(x, base, hi, a.vec, v);
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                most = fmaxf(most, v[j][e]);
+                nan |= v[j][e] != v[j][e];
+            }
+        for (int off = 32; off; off >>= 1) most = fmaxf(most, __shfl_xor(most, off, 64));
+        if (most > top) {
+            r = settings(a, b, most);
+            if (r.kind == PLAIN) sum *= weight(top, r, roots);
+            top = most;
+        }
+        if (!(top > -kInf) || r.kind != PLAIN) continue;
+#pragma unroll
+        for (int j = 0; j < kLoads; ++j) {
+            if (base + j * 64 * N >= hi) break;
+#pragma unroll
+            for (int e = 0; e < N; ++e) sum += weight(v[j][e], r, roots);
+        }
+    }
+    if (__ballot(nan)) top = __builtin_nanf("");
+    return wave_sum(sum);
+}
+
+// The shares' sums as parts of the row's largest.  (One of a share whose own largest has no
+// weight is nothing: its token could not be found.)
+__device__ __forceinline__ void scale_sums(const Row &r, int subs, const double *sums, const float *tops, int stride, Shared &sh)
+{
+    for (int i = threadIdx.x; i < subs; i += kThreads)
+        sh.sub[i] = sums[i] * weight(tops[i / kWaves * stride + i % kWaves], r, sh.roots);
+    __syncthreads();
+}
+
 // A row from its logits
 template <typename T> __device__ __forceinline__ void by_sorting(const SampleArgs &a, int64_t b, const T *x, Shared &sh)
 {
@@ -1069,6 +1129,36 @@ template <typename T> __global__ void __launch_bounds__(kThreads) sample_row_ker
     __shared__ Shared sh;
     const int64_t b = blockIdx.x;
     by_sorting(a, b, static_cast<const T *>(a.logits) + b * a.stride, sh);
+}
+
+template <typename T> __global__ void __launch_bounds__(kThreads) sample_plain_kernel(SampleArgs a)
+{
+    __shared__ Shared sh;
+    const int64_t b = blockIdx.x;
+    const T *x = static_cast<const T *>(a.logits) + b * a.stride;
+    const int lo = wave() * a.share < a.vocab ? wave() * a.share : a.vocab;
+    fill_roots(sh.roots);
+    __syncthreads();
+    float top;
+    const double sum = share_sum(a, b, x, lo, lo + a.share < a.vocab ? lo + a.share : a.vocab, sh.roots, top);
+    if ((threadIdx.x & 63) == 0) {
+        sh.top[wave()] = top;
+        sh.wd[wave()] = sum;
+    }
+    __syncthreads();
+    top = sh.top[0];
+    for (int w = 1; w < kWaves; ++w) top = top != top || sh.top[w] != sh.top[w] ? __builtin_nanf("") : fmaxf(top, sh.top[w]);
+    const Row r = settings(a, b, top);
+    if (r.kind == DONE) {
+        if (threadIdx.x == 0) emit(a, b, -1, -kInf);
+        return;
+    }
+    if (r.kind == GREEDY) {
+        pick_first(a, r, b, x, 0, a.vocab, sh.at);
+        return;
+    }
+    scale_sums(r, kWaves, sh.wd, sh.top, kWaves, sh);
+    pick(a, r, b, x, kWaves, Edge{0, a.vocab}, sh);
 }
 
 // ------------------------------------------------ rows counted by their values
@@ -1534,8 +1624,25 @@ template <typename T> __global__ void __launch_bounds__(kThreads) sample_top_ker
     __shared__ Shared sh;
     const Piece p = piece(a);
     const Slot s = slot_of(a, p.b);
+    const T *x = static_cast<const T *>(a.logits) + p.b * a.stride;
+    if (a.plain) {
+        fill_roots(sh.roots);
+        __syncthreads();
+        float most;
+        const double sum = share_sum(a, p.b, x, p.lo, p.hi, sh.roots, most);
+        if ((threadIdx.x & 63) == 0) {
+            s.sub[p.slice * kWaves + wave()] = sum;
+            s.maxima[p.slice * kGroups + wave()] = sh.top[wave()] = most;
+        }
+        __syncthreads();
+        if (threadIdx.x != 0) return;
+        for (int w = 0; w < kWaves; ++w)
+            most = most != most || sh.top[w] != sh.top[w] ? __builtin_nanf("") : fmaxf(most, sh.top[w]);
+        s.top[p.slice] = most;
+        return;
+    }
     float own;
-    const float top = slice_top(a, static_cast<const T *>(a.logits) + p.b * a.stride, p.lo, p.hi, sh, own);
+    const float top = slice_top(a, x, p.lo, p.hi, sh, own);
     if (threadIdx.x == 0) s.top[p.slice] = top;
     for (int off = 1; off < kThreads / kGroups; off <<= 1) own = fmaxf(own, __shfl_xor(own, off, 64));
     if (threadIdx.x % (kThreads / kGroups) == 0) s.maxima[p.slice * kGroups + threadIdx.x / (kThreads / kGroups)] = own;
@@ -1605,7 +1712,14 @@ template <typename T> __global__ void __launch_bounds__(kThreads) sample_pick_ke
         return;
     }
     fill_roots(sh.roots);
-    const int subs = a.slices * kWaves, n = static_cast<int>(*s.n);
+    const int subs = a.slices * kWaves;
+    if (a.plain) {
+        __syncthreads();
+        scale_sums(r, subs, s.sub, s.maxima, kGroups, sh);
+        pick(a, r, b, x, subs, Edge{0, a.vocab}, sh);
+        return;
+    }
+    const int n = static_cast<int>(*s.n);
     for (int i = threadIdx.x; i < subs; i += kThreads) sh.sub[i] = s.sub[i];
     double want = 0.0;
     if (r.kind != PLAIN) {
@@ -1668,20 +1782,20 @@ bool counted(const mgs_sample_desc &d, const SampleArgs &a)
     if (d.dtype != MGS_BF16) return false;
     const int64_t steps = wave_steps(d);
     if (histograms(a)) return a.slices == 1 || steps <= 4 * kShort;
-    const bool plain = !(a.k0 > 0 && a.k0 < a.vocab) && !a.min_p && !(a.m0 > 0.0f);
-    return plain && a.slices == 1 && steps > kShort;
+    return a.plain && a.slices == 1 && steps > kShort;
 }
 
 template <typename T> hipError_t run(const SampleArgs &a, unsigned rows, hipStream_t s)
 {
     if (a.slices == 1) {
-        sample_row_kernel<T><<<dim3(rows), dim3(kThreads), 0, s>>>(a);
+        if (a.plain) sample_plain_kernel<T><<<dim3(rows), dim3(kThreads), 0, s>>>(a);
+        else sample_row_kernel<T><<<dim3(rows), dim3(kThreads), 0, s>>>(a);
         return hipGetLastError();
     }
     const dim3 grid(rows * a.slices), block(kThreads);
     sample_top_kernel<T><<<grid, block, 0, s>>>(a);
     if (histograms(a)) sample_bins_kernel<T><<<grid, block, 0, s>>>(a);
-    sample_gather_kernel<T><<<grid, block, 0, s>>>(a);
+    if (!a.plain) sample_gather_kernel<T><<<grid, block, 0, s>>>(a);
     sample_pick_kernel<T><<<dim3(rows), block, 0, s>>>(a);
     return hipGetLastError();
 }
@@ -1705,7 +1819,8 @@ hipError_t launch_sample(const mgs_sample_desc &d, const void *logits, const flo
     const bool vec = (reinterpret_cast<uintptr_t>(logits) & 15) == 0 && (d.B == 1 || (d.logits_stride * size) % 16 == 0);
     SampleArgs a{logits, u, temperature, top_p, min_p, top_k, token, logp, d.logits_stride,
                        static_cast<char *>(ws), g.slot, static_cast<int>(d.vocab), g.slices, g.share, d.top_k,
-                       d.temperature, d.top_p, d.min_p, vec};
+                       d.temperature, d.top_p, d.min_p, vec, false};
+    a.plain = !histograms(a) && !(a.k0 > 0 && a.k0 < a.vocab) && !a.min_p && !(a.m0 > 0.0f);
     const unsigned rows = static_cast<unsigned>(d.B);
     if (counted(d, a)) {
         g = sample_geometry(d, false);

@@ -103,6 +103,32 @@ def test_numbers_for_all_rows_bf16(gpu, B, V):
         check(x[rows], u[rows], settings(B, 0, **full), token[rows], logp[rows], who=fixed)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [1, 70, 5000, 40000, 150000])
+def test_no_filters(gpu, V, dtype):
+    """Whole rows and cut ones; a largest logit at the end, far ahead of the others, infinite; rows with none."""
+    import scan_linear_rnns_amd as mgs
+    say(f"sample without filters V={V} {dtype}")
+    inf, nan = float("inf"), float("nan")
+    x, _ = draw(gpu, 12, V, dtype, V)
+    x[1, V - 1] = 200.0
+    x[2, :V // 2] = 1000.0
+    x[2, 0] = -1000.0
+    x[3] = torch.linspace(-3000, 3000, V, device=gpu)
+    x[4] = -inf
+    x[5, V // 3] = nan
+    x[6, V // 2] = x[6, 0] = inf
+    x[7] = -inf
+    x[7, V - 1] = -5.0
+    x[8] = 0.0
+    temperature = torch.tensor([1.0, 0.5, 1.0, 2.0, 1.0, 1.0, 1.0, 0.7, 1.0, 0.0, 1e-30, inf], device=gpu)
+    s = settings(12, 0, top_k=0, top_p=1.0, min_p=0.0)
+    s["temperature"] = temperature.cpu().numpy()
+    for value in (0.0, 1e-9, 0.37, 0.9999999):
+        u = torch.full((12,), value, device=gpu)
+        check(x, u, s, *mgs.mgs_sample(x, u, temperature=temperature), who=value)
+
+
 def test_bf16_values_that_are_rare(gpu):
     """Near 0 (many of them, filters that end among them), 2^10 and more, -2^10 and less at temperatures where that has
     weight, the lowest number as a mask, infinities and NaN."""
