@@ -13,12 +13,20 @@
 //      each wave's share of the row;
 //   4. the edge, from the sorted ones; the share in which the running sum passes u
 //      times the total; the token in that share.
-// A row without top-k and top-p needs 1, the sums of 3, and 4.  Where a bin holds too
-// many to sort (equal logits by the thousand), its values are split again, one
-// histogram after another, by the row's workgroup alone.
+// A row without top-k and top-p needs 1, the sums of 3, and 4; without min-p too, 1 and 3
+// are one pass.  Where a bin holds too many to sort (equal logits by the thousand), its
+// values are split again, one histogram after another, by the row's workgroup alone.
 // Large batches take a workgroup a row for all of it; for small ones a long row is cut into
 // slices, each step a launch.  Rows of bf16 logits that need 2 are counted by value instead
 // (below).
+//
+// What bounds it: for few rows the chain of barriers and launches (1 row of 32000, bf16,
+// all filters 21 us, of them 3 for the launch; 37 of 50001, fp32, no filter 9.6 + 9.2, with
+// 1.5 us of bytes); for many the weights' fp64 operations and LDS atomics.  256 rows of
+// 128000, bf16, mixed settings, are 65.5 MB, 13 us at a copy's rate: 45 counted (24 until
+// all is counted, 8 for the ends and sums, 10 for the token), 120 by histograms of weights
+// and sorting (13 the largest, 42 histogram, 33 gathering, 18 the edge, 10 the token); 256 of
+// 128000, fp32, by top-p 121, without filters 52 of 26.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -33,9 +41,9 @@ namespace {
 
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kBinBits = 11, kBins = 1 << kBinBits;
-constexpr float kPerUnit = 64.0f, kFar = 43.0f;   // half of the bins of 1/64, half of 43/64: to e^-704, less than 2^-1000
+// half of the bins are of 1/64, half of 43/64: to e^-704, less than 2^-1000
+constexpr float kPerUnit = 64.0f, kFar = 43.0f;
 constexpr int kList = 4096;         // candidates that are sorted
-constexpr int kFixed = 43;          // a weight's bits behind the point: 2^20 of them fit 64 bits
 constexpr int kCounted = 256;       // up to here sorting counts the smaller ones
 constexpr int kMaxSlices = 64;
 constexpr int kWorkgroups = 256;    // that rows are cut into: one for each CU
@@ -67,6 +75,12 @@ __device__ __forceinline__ uint32_t key_of(float x)
 __device__ __forceinline__ float of_key(uint32_t k)
 {
     return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
+// The larger of two, NaN if one is
+__device__ __forceinline__ float larger(float x, float y)
+{
+    return x != x || y != y ? __builtin_nanf("") : fmaxf(x, y);
 }
 
 // ---------------------------------------------------------- a row's settings
@@ -146,7 +160,8 @@ __device__ __forceinline__ double weight(float x, const Row &r, const double *ro
     return __hiloint2double(some ? hi : 0, some ? lo : 0);
 }
 
-// w <= 1 as a multiple of 2^-43
+// w <= 1 as a multiple of 2^-43 (rounded: 2^20 of them fit 64 bits, and are off by 2^-24 in
+// sum at the very most, a number u's own step)
 __device__ __forceinline__ uint64_t fixed(double w)
 {
     constexpr double kOne = 768.0;   // 1.5 * 2^(52 - 43)
@@ -411,13 +426,13 @@ __device__ __forceinline__ float slice_top(const SampleArgs &a, const T *x, int 
     if (nan) top = __builtin_nanf("");
     for (int off = 32; off; off >>= 1) {
         const float o = __shfl_xor(top, off, 64);
-        top = top != top || o != o ? __builtin_nanf("") : fmaxf(top, o);
+        top = larger(top, o);
     }
     __syncthreads();
     if ((threadIdx.x & 63) == 0) sh.top[wave()] = top;
     __syncthreads();
     top = sh.top[0];
-    for (int w = 1; w < kWaves; ++w) top = top != top || sh.top[w] != sh.top[w] ? __builtin_nanf("") : fmaxf(top, sh.top[w]);
+    for (int w = 1; w < kWaves; ++w) top = larger(top, sh.top[w]);
     return top;
 }
 
@@ -1147,7 +1162,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) sample_plain_k
     }
     __syncthreads();
     top = sh.top[0];
-    for (int w = 1; w < kWaves; ++w) top = top != top || sh.top[w] != sh.top[w] ? __builtin_nanf("") : fmaxf(top, sh.top[w]);
+    for (int w = 1; w < kWaves; ++w) top = larger(top, sh.top[w]);
     const Row r = settings(a, b, top);
     if (r.kind == DONE) {
         if (threadIdx.x == 0) emit(a, b, -1, -kInf);
@@ -1611,7 +1626,7 @@ __device__ __forceinline__ Piece piece(const SampleArgs &a)
 __device__ __forceinline__ float row_top(const SampleArgs &a, const Slot &s)
 {
     float top = -kInf;
-    for (int i = 0; i < a.slices; ++i) top = top != top || s.top[i] != s.top[i] ? __builtin_nanf("") : fmaxf(top, s.top[i]);
+    for (int i = 0; i < a.slices; ++i) top = larger(top, s.top[i]);
     return top;
 }
 
@@ -1636,8 +1651,7 @@ template <typename T> __global__ void __launch_bounds__(kThreads) sample_top_ker
         }
         __syncthreads();
         if (threadIdx.x != 0) return;
-        for (int w = 0; w < kWaves; ++w)
-            most = most != most || sh.top[w] != sh.top[w] ? __builtin_nanf("") : fmaxf(most, sh.top[w]);
+        for (int w = 0; w < kWaves; ++w) most = larger(most, sh.top[w]);
         s.top[p.slice] = most;
         return;
     }
@@ -1773,16 +1787,16 @@ bool histograms(const SampleArgs &a)
     return a.top_p || a.p0 < 1.0f;
 }
 
-// Whether bf16 rows are counted.  Measured, us, counted / otherwise: with a histogram, 1 and
+// Whether bf16 rows are counted.  Measured, us, counted / otherwise.  With a histogram, 1 and
 // 256 rows of 32000 by top-p 21/37 and 22/43, mixed settings 22/32 and 24/47, 8 of 128000 39/52,
-// 256 mixed 45/120, but 8 of 262144 mixed 65/53; without one, 1 row of 32000 18/17, by min-p
-// 19/13, 1 of 128000 36/21, 256 of them 40/52, by top-k 41/38, by min-p 40/34.
+// 256 mixed 45/120, but 8 of 262144 mixed 65/53.  Without one: 1 row of 32000 18/17, 256 of
+// 50001 37/34, of 128000 40/46; 1 of 128000 36/17; by top-k 256 of 128000 41/38, by min-p 40/34.
 bool counted(const mgs_sample_desc &d, const SampleArgs &a)
 {
     if (d.dtype != MGS_BF16) return false;
     const int64_t steps = wave_steps(d);
     if (histograms(a)) return a.slices == 1 || steps <= 4 * kShort;
-    return a.plain && a.slices == 1 && steps > kShort;
+    return a.plain && a.slices == 1 && steps > 2 * kShort;
 }
 
 template <typename T> hipError_t run(const SampleArgs &a, unsigned rows, hipStream_t s)
