@@ -1408,8 +1408,9 @@ __device__ __forceinline__ bool by_counting(const SampleArgs &a, int64_t b, cons
     {
         const int lo = wave() * a.share < a.vocab ? wave() * a.share : a.vocab;
         const int hi = lo + a.share < a.vocab ? lo + a.share : a.vocab;
-        uint32_t *count = t.count[s_own], flags = 0;
+        uint32_t *count = t.count[s_own], flags = 0, seen = 0;
         walk_bits(x, lo, hi, a.vec, [&](const Bits8 &v) {
+            if (seen > kOthers) return;   // (it goes by sorting)
             int least = kSide, most = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
@@ -1425,10 +1426,13 @@ __device__ __forceinline__ bool by_counting(const SampleArgs &a, int64_t b, cons
                 const uint32_t o = bits_of(v, e);
                 const int c = distance(o);
                 if (c > kSide && o != 0xFF80u) flags |= o > 0x8000u && o < 0xFF80u ? kLow : kStop;
-                if (c == 0) {
-                    const uint32_t at = atomicAdd(&t.n, 1u);
-                    if (at < kOthers) t.others[at] = o | static_cast<uint32_t>(s_own) << 16;
-                }
+                const uint64_t who = __ballot(c == 0);
+                if (!who) continue;
+                uint32_t at = 0;
+                if ((me & 63) == __builtin_ctzll(who)) at = atomicAdd(&t.n, static_cast<uint32_t>(__popcll(who)));
+                at = __builtin_amdgcn_readlane(at, __builtin_ctzll(who)) + __popcll(who & ((1ull << (me & 63)) - 1));
+                if (c == 0 && at < kOthers) t.others[at] = o | static_cast<uint32_t>(s_own) << 16;
+                seen += __popcll(who);
             }
         });
         if (flags) atomicOr(&t.flags, flags);
@@ -1469,9 +1473,10 @@ __device__ __forceinline__ bool by_counting(const SampleArgs &a, int64_t b, cons
     for (int i = me; i < static_cast<int>(t.n); i += kThreads) {
         const double o = weight(__uint_as_float(t.others[i] << 16), r, t.roots);
         atomicAdd(reinterpret_cast<unsigned long long *>(&t.mid), static_cast<unsigned long long>(fixed(o)));
+        // (one step at least: a share with a token in it has a sum)
+        const unsigned long long steps = o * 0x1p51 > 1.0 ? static_cast<unsigned long long>(o * 0x1p51) : o > 0.0;
         if (o >= r.min_p)
-            atomicAdd(reinterpret_cast<unsigned long long *>(&t.mid_sum[t.others[i] >> 16]),
-                      static_cast<unsigned long long>(o * 0x1p51));
+            atomicAdd(reinterpret_cast<unsigned long long *>(&t.mid_sum[t.others[i] >> 16]), steps);
     }
     // how many of each value stay, and the last of them
     uint64_t all;

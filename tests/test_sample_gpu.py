@@ -269,6 +269,21 @@ def test_logits_over_the_whole_range(gpu):
                 check(x, u, s, *run(x, u, s), who=(V, tau, fixed))
 
 
+def test_a_small_weight_ahead_of_all_others(gpu):
+    """u = 0 takes the first token with any weight, here one near 0, alone in its part of the row."""
+    say("sample first weight")
+    for dt in ("f32", "bf16"):
+        for V in (3000, 90000):
+            x = torch.full((3, V), float("-inf"))
+            x[:, 5] = torch.tensor([0.0, 1e-20, -2.0 ** -14])
+            x[:, V - 400:] = 60.0
+            x, u = x.to(DT[dt]).to(gpu), torch.zeros(3, device=gpu)
+            s = settings(3, 0, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0)
+            token, logp = run(x, u, s)
+            check(x, u, s, token, logp)
+            assert (token == 5).all()
+
+
 def test_strides(gpu):
     """Rows apart, a vocabulary inside a padded one, rows that no wide access can take."""
     say("sample strides")
