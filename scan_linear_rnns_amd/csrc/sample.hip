@@ -844,10 +844,15 @@ __device__ __forceinline__ Edge narrow(const SampleArgs &a, const Row &r, const 
         walk(x, i0, i1, a.vec, [&](float v, int i) {
             const uint32_t k = key_of(v);
             if (!(v >= r.floor) || k < lo || k > hi || !kept(v, i, before)) return;
+            // (many are equal here: one addition for the lanes with the first one's value)
+            const uint64_t same = __ballot(k == __builtin_amdgcn_readfirstlane(k));
+            const bool mine = k == __builtin_amdgcn_readfirstlane(k);
+            if (mine && (threadIdx.x & 63) != __builtin_ctzll(same)) return;
+            const uint32_t many = mine ? __popcll(same) : 1;
             const int bin = (hi - k) >> shift;
-            atomicAdd(&sh.count[bin], 1u);
+            atomicAdd(&sh.count[bin], many);
             if constexpr (MASS)
-                atomicAdd(reinterpret_cast<unsigned long long *>(&sh.mass[bin]), fixed(weight(v, r, sh.roots)));
+                atomicAdd(reinterpret_cast<unsigned long long *>(&sh.mass[bin]), fixed(weight(v, r, sh.roots)) * many);
         });
         __syncthreads();
         const int b = 2 * threadIdx.x;
@@ -1180,19 +1185,20 @@ template <typename T> __global__ void __launch_bounds__(kThreads) sample_plain_k
 // bf16 has so few values between 2^-13 and 2^10 that a workgroup counts each, for a share
 // of the row and another: one pass over the row, then all filters end at a value and a
 // number of its equals, the shares' sums are products of counts and weights, and the
-// token's share alone is read again.  Values nearer to 0 count together, their weights one
-// by one; a row where a filter ends among them, or with values past 2^10 that matter, goes
-// by sorting.
+// token's share alone is read again.  Values nearer to 0, but not 0, are listed, their weights
+// taken one by one; a row where a filter ends among them, or with values past 2^10 that
+// matter, goes by sorting.
 constexpr int kTallies = 4;                       // shares
 constexpr int kFirstMag = 114 << 7, kSide = 23 << 7;   // 2^-13 as bits; values of a sign
-constexpr int kMiddle = kSide, kValues = 2 * kSide + 1;   // from the largest to the smallest
+constexpr int kMiddle = kSide, kValues = 2 * kSide + 1;   // from the largest to the smallest; 0 is the middle
+constexpr int kOutside = kValues + 1;                     // of no weight
 constexpr int kEach = (kValues + kThreads - 1) / kThreads;
 constexpr int kOthers = 512;
 constexpr uint32_t kStop = 1, kLow = 2;           // a value that counting does not serve; one of -2^10 or less
 
 struct Tally {
     alignas(16) uint32_t count[kTallies][kEach * kThreads];
-    double w[kEach * kThreads];         // of the values ahead of the edge; 0 for the others, and the middle
+    double w[kEach * kThreads];         // of the values ahead of the edge; 0 for the others
     double roots[kRoots];
     uint32_t others[kOthers];   // bits, share << 16
     uint64_t wu[kWaves], mid, mid_sum[kTallies];
@@ -1205,11 +1211,14 @@ struct Tally {
 __device__ __forceinline__ float value_of(int pos)
 {
     const int c = pos < kMiddle ? kMiddle - pos : pos - kMiddle;
-    return __uint_as_float(static_cast<uint32_t>(kFirstMag - 1 + c) << 16 | (pos < kMiddle ? 0u : 0x80000000u));
+    const float v = __uint_as_float(static_cast<uint32_t>(kFirstMag - 1 + c) << 16 | (pos < kMiddle ? 0u : 0x80000000u));
+    return c == 0 ? 0.0f : v;
 }
 
-// How far a value is from the middle, the one with these bits: 0 for the middle's, above
-// kSide outside
+// Whether a value, the one with these bits, is listed
+__device__ __forceinline__ bool listed(uint32_t bits) { return (bits & 0x7FFFu) - 1u < kFirstMag - 1u; }
+
+// How far it is from the middle, if it is not: above kSide outside
 __device__ __forceinline__ int distance(uint32_t bits)
 {
     const int over = static_cast<int>(bits & 0x7FFFu) - (kFirstMag - 1);
@@ -1256,13 +1265,14 @@ template <typename F> __device__ __forceinline__ void walk_bits(const __bf16 *x,
     }
 }
 
-// The kept weight of a value, but for the edge's; `middle`: whether values near 0 stay
+// The kept weight of a value, but for the edge's; `middle`: whether there are listed ones that
+// stay
 __device__ __forceinline__ double weight_of(uint32_t bits, bool middle, const Row &r, const Tally &t, int &pos)
 {
     const int c = distance(bits);
-    pos = c <= kSide ? place_of(bits, c) : kMiddle;   // (what is outside has no weight)
+    pos = c <= kSide && !listed(bits) ? place_of(bits, c) : kOutside;
     double w = t.w[pos];
-    if (middle && c == 0) {
+    if (middle && listed(bits)) {
         w = weight(__uint_as_float(bits << 16), r, t.roots);
         w = w >= r.min_p ? w : 0.0;
     }
@@ -1411,28 +1421,33 @@ __device__ __forceinline__ bool by_counting(const SampleArgs &a, int64_t b, cons
         uint32_t *count = t.count[s_own], flags = 0, seen = 0;
         walk_bits(x, lo, hi, a.vec, [&](const Bits8 &v) {
             if (seen > kOthers) return;   // (it goes by sorting)
-            int least = kSide, most = 0;
+            uint32_t least = ~0u;
+            int most = 0;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const uint32_t o = bits_of(v, e);
+                const uint32_t o = bits_of(v, e), m = (o & 0x7FFFu) - 1u;
                 const int c = distance(o);
-                least = c < least ? c : least;
+                least = m < least ? m : least;
                 most = c > most ? c : most;
-                if (c <= kSide) atomicAdd(&count[place_of(o, c)], 1u);
+                if (c <= kSide) atomicAdd(&count[place_of(o, c)], 1u);   // (what is listed is taken back)
             }
-            if (__ballot(least == 0 || most > kSide) == 0) return;
+            if (__ballot(least < kFirstMag - 1u || most > kSide) == 0) return;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const uint32_t o = bits_of(v, e);
                 const int c = distance(o);
                 if (c > kSide && o != 0xFF80u) flags |= o > 0x8000u && o < 0xFF80u ? kLow : kStop;
-                const uint64_t who = __ballot(c == 0);
+                const uint64_t who = __ballot(listed(o));
                 if (!who) continue;
                 uint32_t at = 0;
-                if ((me & 63) == __builtin_ctzll(who)) at = atomicAdd(&t.n, static_cast<uint32_t>(__popcll(who)));
+                const uint32_t many = static_cast<uint32_t>(__popcll(who));
+                if ((me & 63) == __builtin_ctzll(who)) {
+                    at = atomicAdd(&t.n, many);
+                    atomicSub(&count[kMiddle], many);
+                }
                 at = __builtin_amdgcn_readlane(at, __builtin_ctzll(who)) + __popcll(who & ((1ull << (me & 63)) - 1));
-                if (c == 0 && at < kOthers) t.others[at] = o | static_cast<uint32_t>(s_own) << 16;
-                seen += __popcll(who);
+                if (listed(o) && at < kOthers) t.others[at] = o | static_cast<uint32_t>(s_own) << 16;
+                seen += many;
             }
         });
         if (flags) atomicOr(&t.flags, flags);
@@ -1454,7 +1469,8 @@ __device__ __forceinline__ bool by_counting(const SampleArgs &a, int64_t b, cons
     if (first < kValues) atomicMin(&t.top, first);
     __syncthreads();
     const int top = t.top;
-    if (top == kMiddle || top == kValues) return false;
+    const uint32_t others = t.n;
+    if (top == kValues || (top >= kMiddle && others)) return false;
     const Row r = settings(a, b, value_of(top));
     if (r.kind == GREEDY) {
         int s = 0;
@@ -1470,7 +1486,7 @@ __device__ __forceinline__ bool by_counting(const SampleArgs &a, int64_t b, cons
         const int pos = me * kEach + e;
         w[e] = weight(value_of(pos < kValues ? pos : kValues - 1), r, t.roots);
     }
-    for (int i = me; i < static_cast<int>(t.n); i += kThreads) {
+    for (int i = me; i < static_cast<int>(others); i += kThreads) {
         const double o = weight(__uint_as_float(t.others[i] << 16), r, t.roots);
         atomicAdd(reinterpret_cast<unsigned long long *>(&t.mid), static_cast<unsigned long long>(fixed(o)));
         // (one step at least: a share with a token in it has a sum)
@@ -1478,7 +1494,8 @@ __device__ __forceinline__ bool by_counting(const SampleArgs &a, int64_t b, cons
         if (o >= r.min_p)
             atomicAdd(reinterpret_cast<unsigned long long *>(&t.mid_sum[t.others[i] >> 16]), steps);
     }
-    // how many of each value stay, and the last of them
+    // how many of each value stay, and the last of them (what is listed goes with 0)
+    if (me == kMiddle / kEach) n[kMiddle % kEach] += others;
     uint64_t all;
     bool stop = false;
     int last = -1;
@@ -1491,7 +1508,7 @@ __device__ __forceinline__ bool by_counting(const SampleArgs &a, int64_t b, cons
         for (int e = 0; e < kEach; ++e) {
             const uint64_t k = static_cast<uint64_t>(r.top_k), room = before < k ? k - before : 0;
             before += n[e];
-            stop |= me * kEach + e == kMiddle && room > 0 && room < n[e];
+            stop |= me * kEach + e == kMiddle && others && room > 0 && room < n[e];
             n[e] = n[e] < room ? n[e] : static_cast<uint32_t>(room);
         }
     }
@@ -1501,7 +1518,7 @@ __device__ __forceinline__ bool by_counting(const SampleArgs &a, int64_t b, cons
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             q[e] = fixed(w[e]) * n[e];
-            if (me * kEach + e == kMiddle) q[e] = n[e] ? t.mid : 0;
+            if (me * kEach + e == kMiddle && others && n[e]) q[e] += t.mid - fixed(w[e]) * others;
             sum += q[e];
         }
         uint64_t before = scan_block(sum, t.wu, all);
@@ -1538,7 +1555,7 @@ __device__ __forceinline__ bool by_counting(const SampleArgs &a, int64_t b, cons
     if (stop) atomicOr(&t.flags, kStop);
     __syncthreads();
     const int edge = t.edge < 0 ? kValues : t.edge;
-    if (edge == kMiddle || (t.flags & kStop)) return false;
+    if ((edge == kMiddle && others) || (t.flags & kStop)) return false;
     const uint32_t m = t.m;
     // the shares' kept weights
     double sums[kTallies] = {};
@@ -1546,7 +1563,7 @@ __device__ __forceinline__ bool by_counting(const SampleArgs &a, int64_t b, cons
     for (int e = 0; e < kEach; ++e) {
         const int pos = me * kEach + e;
         uint32_t rest = pos < edge ? 0xFFFFFFFFu : pos == edge ? m : 0;
-        const double each = w[e] >= r.min_p && pos != kMiddle ? w[e] : 0.0;
+        const double each = w[e] >= r.min_p ? w[e] : 0.0;
         t.w[pos] = pos < edge ? each : 0.0;
         if (pos == edge) t.w_edge = each;
 #pragma unroll
