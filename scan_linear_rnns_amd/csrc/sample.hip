@@ -1000,6 +1000,20 @@ __device__ __forceinline__ void finish(const SampleArgs &a, const Row &r, int64_
         pick(a, r, b, x, subs, Edge{0, a.vocab}, sh);
         return;
     }
+    if (n > kList && r.kind == TOP_P) {
+        // the end's bin is known, and the weight ahead of it
+        const int end = sh.bin;
+        const double ahead = unfixed(sh.ahead);
+        const uint32_t top = key_of(r.max), lo = key_of(bin_floor(end, r));
+        const uint32_t hi = end > 0 ? key_of(bin_floor(end - 1, r)) - 1 : top;
+        const Edge whole{0, a.vocab};
+        Edge e = narrow<T, true>(a, r, x, lo, hi, ahead, want, whole, sh);
+        if (e.limit < 0) e = narrow<T, false>(a, r, x, top, top, 0.0, 1.0, whole, sh);
+        kept_sums(a, r, x, subs, e, sh);
+        __syncthreads();
+        pick(a, r, b, x, subs, e, sh);
+        return;
+    }
     if (n > kList) {
         solve_alone(a, r, b, x, subs, sh);
         return;
