@@ -1661,8 +1661,10 @@ __device__ __forceinline__ Piece piece(const SampleArgs &a)
 
 __device__ __forceinline__ float row_top(const SampleArgs &a, const Slot &s)
 {
-    float top = -kInf;
-    for (int i = 0; i < a.slices; ++i) top = larger(top, s.top[i]);
+    static_assert(kMaxSlices <= 64, "a lane for each");
+    const int lane = threadIdx.x & 63;
+    float top = lane < a.slices ? s.top[lane] : -kInf;
+    for (int off = 32; off; off >>= 1) top = larger(top, __shfl_xor(top, off, 64));
     return top;
 }
 

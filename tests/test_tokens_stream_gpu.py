@@ -14,7 +14,7 @@ def inputs(dev, B=3, T=700, D=320, V=1000, dt=torch.bfloat16, seed=0):
     return dict(ids=torch.randint(-1, V, (B, T), generator=g, device=dev), W=rand(V, D).to(dt),
                 x=rand(B, T, D).to(dt), r=rand(B, T, D).to(dt), i=rand(B, T, D).to(dt), dy=rand(B, T, D).to(dt),
                 lam=rand(D) - 4, h=rand(B, D), logits=3 * rand(B, V), u=torch.rand(B, generator=g, device=dev),
-                states=rand(B, -(-T // 64), D))
+                states=rand(B, -(-T // 64), D), logits16=3 * rand(B, V).bfloat16())
 
 
 def calls(mgs, a):
@@ -27,10 +27,11 @@ def calls(mgs, a):
         "gated_bwd": lambda **k: mgs.mgs_gated_bwd(*gates, a["dy"], a["states"], **k),
         "step": lambda **k: (mgs.mgs_gated_step(*(t[:, 0] for t in gates[:3]), a["lam"], a["h"], **k),),
         "sample": lambda **k: mgs.mgs_sample(a["logits"], a["u"], top_k=50, top_p=0.9, **k),
+        "sample_bf16": lambda **k: mgs.mgs_sample(a["logits16"], a["u"], top_p=0.9, min_p=0.01, **k),
     }
 
 
-NAMES = ["lookup", "table", "gated", "gated_bwd", "step", "sample"]
+NAMES = ["lookup", "table", "gated", "gated_bwd", "step", "sample", "sample_bf16"]
 
 
 @pytest.mark.parametrize("name", NAMES)
