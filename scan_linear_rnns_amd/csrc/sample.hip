@@ -21,7 +21,7 @@
 // (below).
 //
 // What bounds it: for few rows the chain of barriers and launches (1 row of 32000, bf16,
-// all filters 21 us, of them 3 for the launch; 37 of 50001, fp32, no filter 9.6 + 9.2, with
+// all filters 21 us, of them 3 for the launch; 37 of 50001, fp32, no filter 8.6 + 8.6, with
 // 1.5 us of bytes); for many the weights' fp64 operations and LDS atomics.  256 rows of
 // 128000, bf16, mixed settings, are 65.5 MB, 13 us at a copy's rate: 45 counted (24 until
 // all is counted, 8 for the ends and sums, 10 for the token), 120 by histograms of weights
@@ -1825,15 +1825,16 @@ bool histograms(const SampleArgs &a)
     return a.top_p || a.p0 < 1.0f;
 }
 
-// Whether bf16 rows are counted.  Measured, us, counted / otherwise.  With a histogram, 1 and
-// 256 rows of 32000 by top-p 21/37 and 22/43, mixed settings 22/32 and 24/47, 8 of 128000 39/52,
-// 256 mixed 45/120, but 8 of 262144 mixed 65/53.  Without one: 1 row of 32000 18/17, 256 of
-// 50001 37/34, of 128000 40/46; 1 of 128000 36/17; by top-k 256 of 128000 41/38, by min-p 40/34.
+// Whether bf16 rows are counted.  Measured, us, counted / otherwise.  With a histogram, by
+// top-p: 1 and 256 rows of 32000 21/37 and 23/43, 1 and 8 of 131072 40/39 and 41/45, 256 of
+// 128000 with mixed settings 45/120; of 262144 8 rows 66/56, 32 69/70, 64 70/92; 64 and 128 of
+// 2^20 237/231 and 245/417.  Without one: 1 row of 32000 18/17, 256 of 50001 37/34, of 128000
+// 40/46; 1 of 128000 36/15; by top-k 256 of 128000 41/38, by min-p 40/33.
 bool counted(const mgs_sample_desc &d, const SampleArgs &a)
 {
     if (d.dtype != MGS_BF16) return false;
     const int64_t steps = wave_steps(d);
-    if (histograms(a)) return a.slices == 1 || steps <= 4 * kShort;
+    if (histograms(a)) return a.slices <= 4 || steps <= 4 * kShort;
     return a.plain && a.slices == 1 && steps > 2 * kShort;
 }
 

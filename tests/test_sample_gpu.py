@@ -89,7 +89,7 @@ def test_numbers_for_all_rows(gpu):
         check(x, u, settings(9, 0, **dict(full, top_k=min(full["top_k"], 2 ** 31 - 1))), *mgs.mgs_sample(x, u, **fixed))
 
 
-@pytest.mark.parametrize("B, V", [(3, 800), (2, 32000), (2, 50001), (2, 200000), (130, 40000)])
+@pytest.mark.parametrize("B, V", [(3, 800), (2, 32000), (2, 50001), (2, 200000), (130, 40000), (70, 200000)])
 def test_numbers_for_all_rows_bf16(gpu, B, V):
     """(Other kernels than a tensor of settings takes.)"""
     import scan_linear_rnns_amd as mgs
