@@ -1805,8 +1805,8 @@ SampleGeom sample_geometry(const mgs_sample_desc &d, bool cut)
     SampleGeom g{};
     const int64_t step = 64 * (d.dtype == MGS_BF16 ? 8 : 4), steps = wave_steps(d);
     // Workgroups for every CU, no more than there are waves' steps.  Rows of up to four
-    // steps a wave stay with one (32000, bf16, all filters: 1 row 21 us, cut in four 26; 128
-    // rows of mixed settings 44, in two 55); longer ones are cut (8 rows of 128000: 52, whole
+    // steps a wave stay with one (32000, bf16, by sorting, all filters: 1 row 21 us, cut in four
+    // 26; 128 rows of mixed settings 44, in two 55); longer ones are cut (8 rows of 128000: 52, whole
     // or in four 72 and 57).
     int64_t s = !cut || steps <= kShort || d.B <= 0 ? 1 : std::min<int64_t>((steps + kWaves - 1) / kWaves, kWorkgroups / d.B);
     s = std::max<int64_t>(1, std::min<int64_t>(s, kMaxSlices));
