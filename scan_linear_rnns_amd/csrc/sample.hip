@@ -1498,7 +1498,8 @@ __device__ __forceinline__ bool by_counting(const SampleArgs &a, int64_t b, cons
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
         const int pos = me * kEach + e;
-        w[e] = weight(value_of(pos < kValues ? pos : kValues - 1), r, t.roots);
+        // (not of one above the largest: none has it, and none times a weight past the numbers is NaN)
+        w[e] = weight(fminf(value_of(pos < kValues ? pos : kValues - 1), r.top), r, t.roots);
     }
     for (int i = me; i < static_cast<int>(others); i += kThreads) {
         const double o = weight(__uint_as_float(t.others[i] << 16), r, t.roots);
