@@ -168,7 +168,13 @@ __device__ __forceinline__ uint64_t fixed(double w)
     return __double_as_longlong(w + kOne) - __double_as_longlong(kOne);
 }
 
-__device__ __forceinline__ double unfixed(uint64_t q) { return static_cast<double>(q) * 0x1p-43; }
+// The weight that top-p asks for, of `all`, in these steps: of the order, the ones with less
+// ahead of them stay (so the first does)
+__device__ __forceinline__ uint64_t needed(const Row &r, uint64_t all)
+{
+    const double want = ceil(r.top_p * static_cast<double>(all));
+    return want > 1.0 ? static_cast<uint64_t>(want) : 1;
+}
 
 // The bin of x, kBins past the last one and below the floor; falls with x.  (Of half the
 // distance, which is finite: a temperature may be as large.)
@@ -463,8 +469,8 @@ __device__ __forceinline__ void histogram(const SampleArgs &a, const Row &r, con
 
 // Whole workgroup: the bin in which the filter ends, from the row's histogram: the first
 // at whose end there are top_k, or top_p of the weight.  -> sh.bin, what is ahead of
-// it -> sh.ahead.  kBins where all are kept.
-__device__ __forceinline__ void end_bin(const Row &r, const uint32_t *count, const uint64_t *mass, Shared &sh)
+// it -> sh.ahead.  kBins where all are kept.  How many, or how much, are wanted.
+__device__ __forceinline__ uint64_t end_bin(const Row &r, const uint32_t *count, const uint64_t *mass, Shared &sh)
 {
     const int b = 2 * threadIdx.x;
     uint64_t v0, v1, all;
@@ -477,16 +483,15 @@ __device__ __forceinline__ void end_bin(const Row &r, const uint32_t *count, con
     }
     if (threadIdx.x == 0) sh.bin = kBins;
     const uint64_t before = scan_block(v0 + v1, sh.wu, all);
-    const double want = r.kind == TOP_K ? static_cast<double>(r.top_k) : r.top_p * unfixed(all) * 0x1p43;
-    auto less = [&](uint64_t m) { return static_cast<double>(m) < want; };
-    // (the first bin is never empty: the largest is in it)
-    const bool e0 = (b == 0 || less(before)) && !less(before + v0);
-    const bool e1 = less(before + v0) && !less(before + v0 + v1);
+    const uint64_t want = r.kind == TOP_K ? static_cast<uint64_t>(r.top_k) : needed(r, all);
+    const bool e0 = before < want && before + v0 >= want;
+    const bool e1 = before + v0 < want && before + v0 + v1 >= want;
     if (e0 || e1) {
         sh.bin = e0 ? b : b + 1;
         sh.ahead = e0 ? before : before + v0;
     }
     __syncthreads();
+    return want;
 }
 
 // 3: candidates into the list (`n` and `list` in LDS or the workspace), and the sum of
@@ -638,26 +643,31 @@ __device__ __forceinline__ void pick_first(const SampleArgs &a, const Row &r, in
     if (threadIdx.x == 0) emit(a, b, at, 0.0f);
 }
 
-// Sorted candidates' weights: the sum over the places before `i`, thread by thread; a
-// thread holds four neighbours
+// Sorted candidates' weights: a thread holds four neighbours
 struct Four {
-    double w[4], before;
+    double w[4];
 };
 
-__device__ __forceinline__ Four weights4(const Row &r, const uint64_t *list, int n, Shared &sh, double &all, bool by_index)
+__device__ __forceinline__ Four weights4(const Row &r, const uint64_t *list, int n, Shared &sh, bool by_index)
 {
     Four f;
-    double sum = 0.0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int i = 4 * threadIdx.x + e;
         const uint64_t c = list[i < n ? i : 0];
         const uint32_t key = by_index ? ~static_cast<uint32_t>(c) : ~static_cast<uint32_t>(c >> 32);
         f.w[e] = i < n && c != ~0ull ? weight(of_key(key), r, sh.roots) : 0.0;
-        sum += f.w[e];
     }
-    f.before = scan_block(sum, sh.wd, all);
     return f;
+}
+
+// Of the weights as top-p compares them, those of the threads before this one, and all
+__device__ __forceinline__ uint64_t ahead4(const Four &f, Shared &sh, uint64_t &all)
+{
+    uint64_t sum = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum += fixed(f.w[e]);
+    return scan_block(sum, sh.wu, all);
 }
 
 __device__ __forceinline__ int pad_list(uint64_t *list, int n)
@@ -670,19 +680,18 @@ __device__ __forceinline__ int pad_list(uint64_t *list, int n)
 }
 
 // How many of the n sorted candidates stay: those with less than `want` of the weight
-// ahead of them, one at least
-__device__ __forceinline__ int cut(const Four &f, int n, double ahead, double want, Shared &sh)
+// ahead of them, `run` of it ahead of this thread's
+__device__ __forceinline__ int cut(const Four &f, int n, uint64_t run, uint64_t want, Shared &sh)
 {
     __syncthreads();
     if (threadIdx.x == 0) sh.at = 0;
     __syncthreads();
-    double run = ahead + f.before;
     int most = 0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int i = 4 * threadIdx.x + e;
         if (i < n && run < want) most = i + 1;
-        run += f.w[e];
+        run += fixed(f.w[e]);
     }
     if (most) atomicMax(&sh.at, most);
     __syncthreads();
@@ -690,9 +699,9 @@ __device__ __forceinline__ int cut(const Four &f, int n, double ahead, double wa
 }
 
 // The edge of top-p among the n candidates, unsorted: the last that is entered with less
-// than `want` of the weight ahead of it (of them: `ahead` and the ones before), the first
-// at least.  Histograms over their order narrow it to a few, which are sorted.
-__device__ __forceinline__ Edge select(const Row &r, int n, double ahead, double want, Shared &sh)
+// than `want` of the weight ahead of it (of them: `ahead`, which is less, and the ones
+// before).  Histograms over their order narrow it to a few, which are sorted.
+__device__ __forceinline__ Edge select(const Row &r, int n, uint64_t ahead, uint64_t want, Shared &sh)
 {
     __syncthreads();   // (the histogram has been read)
     uint64_t lo = 0, hi = ~0ull;   // the ones in question
@@ -736,21 +745,20 @@ __device__ __forceinline__ Edge select(const Row &r, int n, double ahead, double
             atomicAdd(reinterpret_cast<unsigned long long *>(&sh.mass[bin]),
                       fixed(weight(of_key(~static_cast<uint32_t>(c >> 32)), r, sh.roots)));
         }
-        if (threadIdx.x == 0) sh.bin = -1;
+        if (threadIdx.x == 0) sh.bin = 0;   // (the least is in it)
         __syncthreads();
         const int b = 2 * threadIdx.x;
         const uint64_t v0 = sh.mass[b], v1 = sh.mass[b + 1];
         const uint32_t c0 = sh.count[b], c1 = sh.count[b + 1];
         uint64_t all;
         const uint64_t sum = scan_block(v0 + v1, sh.wu, all);
-        auto less = [&](uint64_t m) { return ahead + unfixed(m) < want; };
-        if (c1 && less(sum + v0)) atomicMax(&sh.bin, b + 1);
-        else if (c0 && less(sum)) atomicMax(&sh.bin, b);
+        if (c1 && ahead + sum + v0 < want) atomicMax(&sh.bin, b + 1);
+        else if (c0 && ahead + sum < want) atomicMax(&sh.bin, b);
         __syncthreads();
-        const int bin = sh.bin < 0 ? 0 : sh.bin;   // (the least is in the first)
+        const int bin = sh.bin;
         if (b == (bin & ~1)) sh.ahead = bin & 1 ? sum + v0 : sum;
         __syncthreads();
-        ahead += unfixed(sh.ahead);
+        ahead += sh.ahead;
         lo = least + (static_cast<uint64_t>(bin) << shift);
         hi = lo + ((1ull << shift) - 1);
         left = static_cast<int>(sh.count[bin]);
@@ -763,9 +771,9 @@ __device__ __forceinline__ Edge select(const Row &r, int n, double ahead, double
         if (c >= lo && c <= hi) few[atomicAdd(&sh.n, 1u)] = c;
     }
     sort_list(few, pad_list(few, left));
-    double all;
-    const Four f = weights4(r, few, left, sh, all, false);
-    const int m = cut(f, left, ahead, want, sh);
+    uint64_t all;
+    const Four f = weights4(r, few, left, sh, false);
+    const int m = cut(f, left, ahead + ahead4(f, sh, all), want, sh);
     const uint64_t c = few[m > 1 ? m - 1 : 0];
     return Edge{~static_cast<uint32_t>(c >> 32), static_cast<int>(static_cast<uint32_t>(c))};
 }
@@ -775,11 +783,11 @@ __device__ __forceinline__ void finish_list(const SampleArgs &a, const Row &r, i
 {
     sort_list(sh.list, pad_list(sh.list, n));
     n = n < r.top_k ? n : r.top_k;
-    double all;
-    Four f = weights4(r, sh.list, n, sh, all, false);
+    Four f = weights4(r, sh.list, n, sh, false);
     if (r.top_p < 1.0) {
-        const int m = cut(f, n, 0.0, r.top_p * all, sh);
-        n = m > 1 ? m : 1;
+        uint64_t mass;
+        const uint64_t ahead = ahead4(f, sh, mass);
+        n = cut(f, n, ahead, needed(r, mass), sh);
     }
     __syncthreads();
     // by index; what min-p drops goes to the end
@@ -792,11 +800,11 @@ __device__ __forceinline__ void finish_list(const SampleArgs &a, const Row &r, i
         }
     }
     sort_list(sh.list, pad_list(sh.list, n));
-    f = weights4(r, sh.list, n, sh, all, true);   // (none of the dropped ones)
+    f = weights4(r, sh.list, n, sh, true);   // (none of the dropped ones)
+    double all, run = scan_block(((f.w[0] + f.w[1]) + f.w[2]) + f.w[3], sh.wd, all);
     const double target = static_cast<double>(r.u) * all;
     if (threadIdx.x == 0) sh.at = n;
     __syncthreads();
-    double run = f.before;
     int at = -1, last = -1;
     double w_at = 0.0, w_last = 0.0;
 #pragma unroll
@@ -824,11 +832,11 @@ __device__ __forceinline__ void finish_list(const SampleArgs &a, const Row &r, i
 
 // ---------------------------------------------- rows with too many candidates
 // The edge of a filter over what `before` keeps, by the row's workgroup alone: want
-// (a count, or a weight) is reached within the keys lo..hi, with `ahead` above hi.
-// The range is split by histograms until it is short enough to sort or one value.
+// (a count, or a weight) is reached within the keys lo..hi, with `ahead`, which is less,
+// above hi.  The range is split by histograms until it is short enough to sort or one value.
 template <typename T, bool MASS>
-__device__ __forceinline__ Edge narrow(const SampleArgs &a, const Row &r, const T *x, uint32_t lo, uint32_t hi, double ahead,
-                                       double want, const Edge &before, Shared &sh)
+__device__ __forceinline__ Edge narrow(const SampleArgs &a, const Row &r, const T *x, uint32_t lo, uint32_t hi, uint64_t ahead,
+                                       uint64_t want, const Edge &before, Shared &sh)
 {
     const int per = (a.vocab + kWaves * 512 - 1) / (kWaves * 512) * 512;
     const int i0 = wave() * per, i1 = i0 + per < a.vocab ? i0 + per : a.vocab;
@@ -859,27 +867,21 @@ __device__ __forceinline__ Edge narrow(const SampleArgs &a, const Row &r, const 
         const uint64_t v0 = MASS ? sh.mass[b] : sh.count[b], v1 = MASS ? sh.mass[b + 1] : sh.count[b + 1];
         uint64_t all;
         const uint64_t sum = scan_block(v0 + v1, sh.wu, all);
-        const double unit = MASS ? 0x1p-43 : 1.0;
-        auto less = [&](uint64_t m) { return ahead + static_cast<double>(m) * unit < want; };
         if (threadIdx.x == 0) {
-            sh.bin = -1;
+            sh.bin = 0;
             sh.last = -1;
         }
         __syncthreads();
-        // the last bin that is entered with less than `want` ahead, and is not empty
+        // the last bin that is entered with less than `want` ahead, and is not empty (the
+        // first that is not empty is such a one)
         const uint32_t c0 = sh.count[b], c1 = sh.count[b + 1];
-        if (c1 && less(sum + v0)) atomicMax(&sh.bin, b + 1);
-        else if (c0 && less(sum)) atomicMax(&sh.bin, b);
+        if (c1 && ahead + sum + v0 < want) atomicMax(&sh.bin, b + 1);
+        else if (c0 && ahead + sum < want) atomicMax(&sh.bin, b);
         __syncthreads();
         const int bin = sh.bin;
-        if (bin < 0) {   // nothing may follow what is ahead: the largest alone
-            sh.n = 0;
-            __syncthreads();
-            return Edge{hi, -1};
-        }
         if (b == (bin & ~1)) sh.ahead = bin & 1 ? sum + v0 : sum;
         __syncthreads();
-        ahead += static_cast<double>(sh.ahead) * unit;
+        ahead += sh.ahead;
         const uint32_t top = hi - (static_cast<uint32_t>(bin) << shift);
         const uint32_t span = (1u << shift) - 1;
         lo = top - lo > span ? top - span : lo;
@@ -898,13 +900,12 @@ __device__ __forceinline__ Edge narrow(const SampleArgs &a, const Row &r, const 
             sort_list(sh.list, pad_list(sh.list, n));
             int m;
             if constexpr (MASS) {
-                double sum4;
-                m = cut(weights4(r, sh.list, n, sh, sum4, false), n, ahead, want, sh);
+                uint64_t in;
+                const Four f = weights4(r, sh.list, n, sh, false);
+                m = cut(f, n, ahead + ahead4(f, sh, in), want, sh);
             } else {
-                m = static_cast<int>(want - ahead);
-                m = m < n ? m : n;
+                m = want - ahead < static_cast<uint64_t>(n) ? static_cast<int>(want - ahead) : n;
             }
-            m = m > 1 ? m : 1;
             const uint64_t c = sh.list[m - 1];
             __syncthreads();
             return Edge{~static_cast<uint32_t>(c >> 32), static_cast<int>(static_cast<uint32_t>(c))};
@@ -912,17 +913,12 @@ __device__ __forceinline__ Edge narrow(const SampleArgs &a, const Row &r, const 
         if (lo == hi) {
             // one value: the first few of its places
             int m = n;
+            uint64_t places = want - ahead;
             if constexpr (MASS) {
-                const double w = weight(of_key(lo), r, sh.roots);
-                int low = 1;   // the smallest number that is not followed
-                while (low < m) {
-                    const int mid = low + (m - low) / 2;
-                    if (ahead + static_cast<double>(mid) * w < want) low = mid + 1;
-                    else m = mid;
-                }
-            } else {
-                m = want - ahead < n ? static_cast<int>(want - ahead) : n;
+                const uint64_t w = fixed(weight(of_key(lo), r, sh.roots));
+                places = w ? (places - 1) / w + 1 : n;
             }
+            if (places < static_cast<uint64_t>(n)) m = static_cast<int>(places);
             // the index of the m-th: counted by threads' neighbouring places
             const int each = (a.vocab + kThreads - 1) / kThreads;
             const int j0 = threadIdx.x * each, j1 = j0 + each < a.vocab ? j0 + each : a.vocab;
@@ -946,9 +942,8 @@ __device__ __forceinline__ Edge narrow(const SampleArgs &a, const Row &r, const 
 
 // Kept weights of all of a row, into the shares' sums
 template <typename T>
-__device__ __forceinline__ double kept_sums(const SampleArgs &a, const Row &r, const T *x, int subs, const Edge &e, Shared &sh)
+__device__ __forceinline__ void kept_sums(const SampleArgs &a, const Row &r, const T *x, int subs, const Edge &e, Shared &sh)
 {
-    double mine = 0.0;
     for (int s = wave(); s < subs; s += kWaves) {
         double sum = 0.0;
         const int lo = s * a.share, hi = lo + a.share < a.vocab ? lo + a.share : a.vocab;
@@ -958,35 +953,33 @@ __device__ __forceinline__ double kept_sums(const SampleArgs &a, const Row &r, c
             sum += w >= r.min_p ? w : 0.0;
         });
         sum = wave_sum(sum);
-        mine += sum;
         if ((threadIdx.x & 63) == 0) sh.sub[s] = sum;
     }
     __syncthreads();
-    double all;
-    scan_block((threadIdx.x & 63) == 0 ? mine : 0.0, sh.wd, all);
+}
+
+// The weight that the edge keeps, as top-p compares it
+template <typename T>
+__device__ __forceinline__ uint64_t kept_mass(const SampleArgs &a, const Row &r, const T *x, const Edge &e, Shared &sh)
+{
+    const int per = (a.vocab + kWaves * 512 - 1) / (kWaves * 512) * 512;
+    const int i0 = wave() * per, i1 = i0 + per < a.vocab ? i0 + per : a.vocab;
+    uint64_t sum = 0, all;
+    walk(x, i0, i1, a.vec, [&](float v, int i) {
+        if (v >= r.floor && kept(v, i, e)) sum += fixed(weight(v, r, sh.roots));
+    });
+    scan_block(sum, sh.wu, all);
     return all;
 }
 
 template <typename T>
-__device__ __forceinline__ void solve_alone(const SampleArgs &a, Row r, int64_t b, const T *x, int subs, Shared &sh)
+__device__ __forceinline__ void solve_alone(const SampleArgs &a, const Row &r, int64_t b, const T *x, int subs, Shared &sh)
 {
     Edge e{0, a.vocab};
     const uint32_t top = key_of(r.max);
-    const double min_p = r.min_p;
-    if (r.top_k) e = narrow<T, false>(a, r, x, 1, top, 0.0, static_cast<double>(r.top_k), e, sh);
-    if (r.top_p < 1.0) {
-        r.min_p = 0.0;
-        const double want = r.top_p * kept_sums(a, r, x, subs, e, sh);
-        const Edge f = narrow<T, true>(a, r, x, 1, top, 0.0, want, e, sh);
-        if (f.limit >= 0) {
-            e = f;
-        } else {   // want is nothing: the first of the largest
-            e = narrow<T, false>(a, r, x, top, top, 0.0, 1.0, e, sh);
-        }
-        r.min_p = min_p;
-    }
+    if (r.top_k) e = narrow<T, false>(a, r, x, 1, top, 0, static_cast<uint64_t>(r.top_k), e, sh);
+    if (r.top_p < 1.0) e = narrow<T, true>(a, r, x, 1, top, 0, needed(r, kept_mass(a, r, x, e, sh)), e, sh);
     kept_sums(a, r, x, subs, e, sh);
-    __syncthreads();
     pick(a, r, b, x, subs, e, sh);
 }
 
@@ -994,7 +987,7 @@ __device__ __forceinline__ void solve_alone(const SampleArgs &a, Row r, int64_t 
 // sh.list with `n` found in all, sh.sub)
 template <typename T>
 __device__ __forceinline__ void finish(const SampleArgs &a, const Row &r, int64_t b, const T *x, int subs, int n,
-                                       double want, Shared &sh)
+                                       uint64_t want, Shared &sh)
 {
     if (r.kind == PLAIN) {
         pick(a, r, b, x, subs, Edge{0, a.vocab}, sh);
@@ -1003,14 +996,11 @@ __device__ __forceinline__ void finish(const SampleArgs &a, const Row &r, int64_
     if (n > kList && r.kind == TOP_P) {
         // the end's bin is known, and the weight ahead of it
         const int end = sh.bin;
-        const double ahead = unfixed(sh.ahead);
-        const uint32_t top = key_of(r.max), lo = key_of(bin_floor(end, r));
-        const uint32_t hi = end > 0 ? key_of(bin_floor(end - 1, r)) - 1 : top;
-        const Edge whole{0, a.vocab};
-        Edge e = narrow<T, true>(a, r, x, lo, hi, ahead, want, whole, sh);
-        if (e.limit < 0) e = narrow<T, false>(a, r, x, top, top, 0.0, 1.0, whole, sh);
+        const uint64_t ahead = sh.ahead;
+        const uint32_t lo = key_of(bin_floor(end, r));
+        const uint32_t hi = end > 0 ? key_of(bin_floor(end - 1, r)) - 1 : key_of(r.max);
+        const Edge e = narrow<T, true>(a, r, x, lo, hi, ahead, want, Edge{0, a.vocab}, sh);
         kept_sums(a, r, x, subs, e, sh);
-        __syncthreads();
         pick(a, r, b, x, subs, e, sh);
         return;
     }
@@ -1022,7 +1012,7 @@ __device__ __forceinline__ void finish(const SampleArgs &a, const Row &r, int64_
         finish_list(a, r, b, n, sh);
         return;
     }
-    const Edge e = select(r, n, unfixed(sh.ahead), want, sh);
+    const Edge e = select(r, n, sh.ahead, want, sh);
     // the weights of the kept ones into the sums of their shares: up to 2^12 multiples
     // of 2^-51, whose sum no order changes
     uint64_t *more = reinterpret_cast<uint64_t *>(sh.count);
@@ -1064,14 +1054,6 @@ __device__ __forceinline__ bool end_of_maxima(const Row &r, float own, Shared &s
     __syncthreads();
     end_bin(r, sh.count, sh.mass, sh);
     return sh.bin < kBins;
-}
-
-// top_p of the histogram's weight
-__device__ __forceinline__ double wanted(const Row &r, const uint64_t *mass, Shared &sh)
-{
-    uint64_t all;
-    scan_block(mass[2 * threadIdx.x] + mass[2 * threadIdx.x + 1], sh.wu, all);
-    return r.top_p * unfixed(all);
 }
 
 // Without filters, 1 and 3 at once: the sum of the weights of a wave's share, as parts of
@@ -1139,7 +1121,7 @@ template <typename T> __device__ __forceinline__ void by_sorting(const SampleArg
         pick_first(a, r, b, x, 0, a.vocab, sh.at);
         return;
     }
-    double want = 0.0;
+    uint64_t want = 0;
     bool known = r.kind == PLAIN;
     if (r.kind == TOP_K && r.top_k <= kThreads / 2) {
         known = end_of_maxima(r, own, sh);
@@ -1149,8 +1131,7 @@ template <typename T> __device__ __forceinline__ void by_sorting(const SampleArg
     if (!known) {
         histogram(a, r, x, lo, hi, sh);
         __syncthreads();
-        end_bin(r, sh.count, sh.mass, sh);
-        if (r.kind == TOP_P) want = wanted(r, sh.mass, sh);
+        want = end_bin(r, sh.count, sh.mass, sh);
     }
     const double sum = gather(a, r, x, lo, hi, sh.bin, sh, &sh.n, sh.list);
     if ((threadIdx.x & 63) == 0) sh.sub[wave()] = sum;
@@ -1537,9 +1518,7 @@ __device__ __forceinline__ bool by_counting(const SampleArgs &a, int64_t b, cons
             sum += q[e];
         }
         uint64_t before = scan_block(sum, t.wu, all);
-        // (those with less than `want` ahead of them; the first at least)
-        const double exact = ceil(r.top_p * static_cast<double>(all));
-        const uint64_t want = exact > 1.0 ? static_cast<uint64_t>(exact) : 1;
+        const uint64_t want = needed(r, all);
         uint64_t left = 0, one = 0;
         uint32_t most = 0;
 #pragma unroll
@@ -1774,14 +1753,11 @@ template <typename T> __global__ void __launch_bounds__(kThreads) sample_pick_ke
     }
     const int n = static_cast<int>(*s.n);
     for (int i = threadIdx.x; i < subs; i += kThreads) sh.sub[i] = s.sub[i];
-    double want = 0.0;
+    uint64_t want = 0;
     if (r.kind != PLAIN) {
         for (int i = threadIdx.x; i < n && i < kList; i += kThreads) sh.list[i] = s.list[i];
         __syncthreads();
-        if (r.kind == TOP_P) {
-            end_bin(r, s.count, s.mass, sh);
-            want = wanted(r, s.mass, sh);
-        }
+        if (r.kind == TOP_P) want = end_bin(r, s.count, s.mass, sh);
     }
     __syncthreads();
     finish(a, r, b, x, subs, n, want, sh);

@@ -29,3 +29,63 @@ def test_small_temperatures_of_counted_rows(gpu, tau, top):
         token, logp = (torch.full((6,), -7, dtype=t, device=gpu) for t in (torch.int64, torch.float32))
         mgs.mgs_sample(x, u, **full, token=token, logp=logp)
         check(x, u, settings(6, 0, **full), token, logp, who=fixed)
+
+
+def by_multiples(x, u, top_k, top_p):
+    """(token, logp) of a row at temperature 1 where top-p compares the weights rounded to multiples of 2^-43."""
+    x = np.asarray(x, np.float64)
+    w = np.exp(x - x.max())
+    order = np.argsort(-x, kind="stable")
+    if top_k > 0:
+        order = order[:top_k]
+    q = np.rint(w[order] * 2.0 ** 43).astype(np.int64)
+    ahead = np.cumsum(q) - q
+    want = max(1, ceil(Fraction(float(np.float32(top_p))) * int(q.sum())))
+    ids = np.sort(order[ahead < want])
+    run = np.cumsum(w[ids])
+    at = int((run <= u * run[-1]).sum())
+    return int(ids[at]), float(np.log(w[ids[at]] / run[-1]))
+
+
+def same(token, logp, want, who):
+    assert int(token) == want[0], (who, int(token), want)
+    assert abs(float(logp) - want[1]) <= 2.0 ** -24 * abs(want[1]) + 2.0 ** -23, (who, float(logp), want)
+
+
+@pytest.mark.parametrize("dtype, B", [(torch.float32, 1), (torch.float32, 130), (torch.bfloat16, 1), (torch.bfloat16, 64)])
+def test_top_p_ends_in_a_field_of_tiny_weights(gpu, dtype, B):
+    """All but one token weigh 0.64 times 2^-43, one step where top-p compares: half of them are kept by the largest
+    top_p below 1 (of the weights themselves it would be a quarter; of weights compared with steps, four fifths)."""
+    import scan_linear_rnns_amd as mgs
+    say(f"sample tiny weights {dtype} B={B}")
+    V = 1 << 20
+    row = torch.full((V,), -30.25)
+    row[V - 1] = 0.0
+    x = row.to(dtype).to(gpu).expand(B, V)
+    for top_k in (0, V - 5):
+        for share in (0.3, 0.5, 0.72):   # of 2^-24: the kept ones hold 0.64 of that
+            u = float(np.float32(share * 2.0 ** -24))
+            token, logp = mgs.mgs_sample(x, torch.full((B,), u, device=gpu), top_k=top_k, top_p=0.99999994)
+            want = by_multiples(row, u, top_k, 0.99999994)
+            for b in {0, B - 1}:
+                same(token[b], logp[b], want, (top_k, share, b))
+
+
+# Rows of three logits for which 2^-43's multiples end top-p (a share near that of the first one or two) elsewhere than
+# 64-bit weights do: top_p times the sum is a fifth of a step or more from the deciding weight on either side
+THREE = [(3, -0.00803716015, -2.61609435, 0.484242082), (3, -0.00227771816, -2.0928452, 0.47146225),
+         (3, -0.0132342903, -1.87472475, 0.467235118), (0, -0.00210684282, -0.0105585232, 0.668775678),
+         (0, -0.00217477302, -0.0129938666, 0.669307411), (0, -0.00421557622, -0.0108519839, 0.668607473)]
+
+
+@pytest.mark.parametrize("top_k, second, third, top_p", THREE)
+def test_top_p_compares_multiples(gpu, top_k, second, third, top_p):
+    """In a short row and in one that is cut into slices; of more logits, the others forbidden."""
+    import scan_linear_rnns_amd as mgs
+    say(f"sample multiples {top_p}")
+    u = torch.tensor([0.999], device=gpu)
+    for V in (4, 100000):
+        x = torch.full((1, V), float("-inf"))
+        x[0, [0, V // 2, V - 1]] = torch.tensor([0.0, second, third])
+        token, logp = mgs.mgs_sample(x.to(gpu), u, top_k=top_k, top_p=top_p)
+        same(token, logp, by_multiples(x[0], float(u), top_k, top_p), V)
