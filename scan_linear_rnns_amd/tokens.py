@@ -232,11 +232,11 @@ def mgs_sample_workspace_size(B, vocab, dtype=None):
 
 
 def _setting(torch, name, value, dtype, B, dev, off):
-    """A setting as the desc's number and a pointer to one for each row, or None."""
+    """A setting as the desc's number (the nearest that its type holds) and a pointer to one for each row, or None."""
     if isinstance(value, torch.Tensor):
         _tensor(name, value, (B,), dtype, dev)
         return off, value.data_ptr()
-    return value, None
+    return max(0, min(value, 2 ** 31 - 1)) if dtype is torch.int32 else value, None
 
 
 def mgs_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=None, logp=None, ws=None, stream=None):
@@ -265,7 +265,7 @@ def mgs_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=
     token = _out(torch, "token", token, (B,), torch.int64, dev)
     logp = _out(torch, "logp", logp, (B,), f32, dev)
     ws = _scratch(torch, ws, lambda: mgs_sample_workspace_size(B, vocab, logits.dtype), dev)
-    d = _pack_sample(B, vocab, logits.stride(0), code, min(k, vocab), tau, p, m)
+    d = _pack_sample(B, vocab, logits.stride(0), code, k, tau, p, m)
     check(load().mgs_sample(d, logits.data_ptr(), u.data_ptr(), taus, ks, ps, ms, token.data_ptr(), logp.data_ptr(),
                             ws.data_ptr(), ws.numel(), _raw_stream(torch, dev)), "mgs_sample")
     return token, logp

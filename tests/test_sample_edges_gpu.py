@@ -89,3 +89,17 @@ def test_top_p_compares_multiples(gpu, top_k, second, third, top_p):
         x[0, [0, V // 2, V - 1]] = torch.tensor([0.0, second, third])
         token, logp = mgs.mgs_sample(x.to(gpu), u, top_k=top_k, top_p=top_p)
         same(token, logp, by_multiples(x[0], float(u), top_k, top_p), V)
+
+
+def test_numbers_past_their_types_range(gpu):
+    """They count as the nearest number that the type holds."""
+    import scan_linear_rnns_amd as mgs
+    say("sample numbers past the range")
+    inf = float("inf")
+    x = torch.randn(40, 300, generator=torch.Generator().manual_seed(2)).to(gpu)
+    u = torch.linspace(0, 0.999, 40, device=gpu)
+    for given, meant in ((dict(top_k=-2 ** 40), dict()), (dict(top_k=2 ** 40), dict()), (dict(temperature=1e39), dict(temperature=inf)),
+                         (dict(temperature=-1e39), dict(temperature=0.0)), (dict(top_p=1e39), dict()),
+                         (dict(min_p=1e39), dict(min_p=1.0)), (dict(min_p=-1e39), dict())):
+        for got, want in zip(mgs.mgs_sample(x, u, **given), mgs.mgs_sample(x, u, **meant)):
+            assert torch.equal(got, want), given
