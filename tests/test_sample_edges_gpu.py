@@ -103,3 +103,52 @@ def test_numbers_past_their_types_range(gpu):
                          (dict(min_p=1e39), dict(min_p=1.0)), (dict(min_p=-1e39), dict())):
         for got, want in zip(mgs.mgs_sample(x, u, **given), mgs.mgs_sample(x, u, **meant)):
             assert torch.equal(got, want), given
+
+
+# Rows of which a wave reads its share in several rounds: whole rows, rows cut in two slices, and bf16 rows long enough to
+# be counted without a filter.  (B, V, type, places of a round, of a share)
+LONG = [(130, 40000, torch.float32, 1024, 2560), (100, 200000, torch.float32, 1024, 6400),
+        (130, 70001, torch.bfloat16, 2048, 4608)]
+
+
+@pytest.mark.parametrize("B, V, dtype, step, share", LONG)
+def test_shares_read_in_rounds(gpu, B, V, dtype, step, share):
+    """The largest logit, a NaN and an infinity in a share's later rounds, behind smaller ones and ahead of them; numbers
+    for all rows, each filter alone and together; a temperature of 0 for some."""
+    import scan_linear_rnns_amd as mgs
+    say(f"sample rounds {B} x {V} {dtype}")
+    inf, nan = float("inf"), float("nan")
+    g = torch.Generator().manual_seed(V)
+    x = 2.0 * torch.randn(B, V, generator=g)
+    late = 3 * share + step + 77   # in the second round of a share
+    x[0, late] = 30.0
+    x[1, late:late + 3] = torch.tensor([9.0, 25.0, 9.5])
+    x[2, :late] -= 40.0
+    x[3, :step] = -inf
+    x[4, late] = nan
+    x[5, late + 5] = inf
+    x[6, :] = -inf
+    x[6, late + 9] = -7.0
+    x[7] = torch.linspace(-60, 60, V)     # each round's largest is larger
+    x[8] = torch.linspace(60, -60, V)
+    x[9, V - 1] = 20.0
+    x = x.to(dtype).to(gpu)
+    u = torch.rand(B, generator=g)
+    u[:4] = torch.tensor([0.0, 0.4, 0.99999, 0.5])
+    u = u.to(gpu)
+    rows = slice(0, 14)
+    for fixed in (dict(), dict(top_k=5), dict(top_k=700), dict(top_p=0.8), dict(min_p=0.1), dict(temperature=0.0),
+                  dict(temperature=0.9, top_k=40, top_p=0.9, min_p=0.05), dict(temperature=30.0)):
+        full = dict(dict(temperature=1.0, top_k=0, top_p=1.0, min_p=0.0), **fixed)
+        token, logp = mgs.mgs_sample(x, u, **fixed)
+        check(x[rows], u[rows], settings(14, 0, **full), token[rows], logp[rows], who=fixed)
+    # temperatures of their own, without filters: a largest one of 0 in a share's later rounds too
+    s = settings(B, 3, top_k=0, top_p=1.0, min_p=0.0)
+    s["temperature"][[0, 7, 10]] = 0.0
+    s["temperature"][[8, 11]] = np.inf
+    token, logp = mgs.mgs_sample(x, u, temperature=torch.from_numpy(s["temperature"]).to(gpu))
+    check(x[rows], u[rows], {k: v[rows] for k, v in s.items()}, token[rows], logp[rows], who="own temperatures")
+    for i, fixed in enumerate([dict(top_k=0, min_p=0.0), dict(top_p=1.0, min_p=0.0), {}]):
+        s = settings(B, i, **fixed)
+        token, logp = mgs.mgs_sample(x, u, **{k: torch.from_numpy(v).to(gpu) for k, v in s.items()})
+        check(x[rows], u[rows], {k: v[rows] for k, v in s.items()}, token[rows], logp[rows], who=("own", fixed))
