@@ -470,7 +470,8 @@ EmbedGeom embed_geometry(int64_t n, int64_t vocab, int64_t d)
     g.range = static_cast<int>((vocab + (int64_t(1) << g.bits) - 1) >> g.bits);
     g.chunk = n <= 8192 ? 8 : n <= 16384 ? 16 : kMaxChunk;
     g.chunks = (n + g.chunk - 1) / g.chunk;
-    size_t off = 256;
+    size_t off = kHeader;
+    g.off_count = off; off += 256;
     g.off_first = off; off = align256(off + ((static_cast<size_t>(g.range) << g.bits) + 1) * 4);
     g.off_row = off;   off = align256(off + static_cast<size_t>(n) * 4);
     g.off_id = off;    off = align256(off + static_cast<size_t>(n) * 4);
@@ -509,7 +510,7 @@ hipError_t launch_embed_bwd(const EmbedGeom &g, const void *ids, bool wide_ids, 
     a.d = d;
     a.bits = g.bits;
     a.range = g.range;
-    a.count = reinterpret_cast<int64_t *>(w);
+    a.count = reinterpret_cast<int64_t *>(w + g.off_count);
     a.first = reinterpret_cast<int32_t *>(w + g.off_first);
     a.row = reinterpret_cast<int32_t *>(w + g.off_row);
     a.id = reinterpret_cast<int32_t *>(w + g.off_id);

@@ -410,7 +410,7 @@ constexpr size_t kSlotMass = 512, kSlotCount = kSlotMass + 8 * kBins, kSlotList 
 
 __device__ __forceinline__ Slot slot_of(const SampleArgs &a, int64_t b)
 {
-    char *w = a.ws + b * a.slot;
+    char *w = a.ws + kHeader + b * a.slot;
     return Slot{reinterpret_cast<float *>(w), reinterpret_cast<uint32_t *>(w + 256),
                 reinterpret_cast<uint32_t *>(w + kSlotCount), reinterpret_cast<uint64_t *>(w + kSlotMass),
                 reinterpret_cast<uint64_t *>(w + kSlotList), reinterpret_cast<float *>(w + kSlotMaxima),
@@ -1837,7 +1837,7 @@ size_t sample_workspace(const mgs_sample_desc &d)
     // (more rows than this are not cut; the bytes of fewer grow with their number)
     mgs_sample_desc cut = d;
     cut.B = std::min<int64_t>(d.B, kWorkgroups / 2);
-    return 256 + sample_geometry(cut, true).slot * static_cast<size_t>(cut.B);
+    return kHeader + sample_geometry(cut, true).slot * static_cast<size_t>(cut.B);
 }
 
 hipError_t launch_sample(const mgs_sample_desc &d, const void *logits, const float *u, const float *temperature,

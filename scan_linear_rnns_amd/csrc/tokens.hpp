@@ -11,15 +11,19 @@
 
 namespace mgs {
 
+// Bytes at a workspace's start that sampling and the table's gradient leave alone: the
+// recurrence's launch words and the limit of its waits, were it given the same one (its
+// results are wrong then, but every wait ends)
+constexpr size_t kHeader = 256;
+
 // ---------------------------------------------------------------- embedding
 struct EmbedGeom {
     int bits, range;   // 2^bits sorting workgroups, ids of each
     int chunk;         // sorted places of a summing workgroup
     int64_t chunks;
-    // workspace byte offsets (the number of ids inside the table comes first): each id's
-    // first sorted place, the sorted places' rows and ids, partial sums of runs of one id
-    // that cross a chunk
-    size_t off_first, off_row, off_id, off_part, bytes;
+    // workspace byte offsets: the number of ids inside the table, each id's first sorted
+    // place, the sorted places' rows and ids, partial sums of runs of one id that cross a chunk
+    size_t off_count, off_first, off_row, off_id, off_part, bytes;
 };
 
 EmbedGeom embed_geometry(int64_t n, int64_t vocab, int64_t d);
