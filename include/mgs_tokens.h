@@ -12,9 +12,9 @@
  * count elements and may be 0 but not negative, device pointers, caller-owned
  * buffers and workspaces, no allocation, arguments checked before any HIP call.
  * The workspaces carry nothing from one call to the next and need not be
- * zero-filled, but for mgs_gated_*'s, which has to be once, as those of mgs.h, and
- * which calls that fill theirs with other things (mgs_embed_bwd, mgs_sample, those of
- * mgs_layers.h) must not have written to since.
+ * zero-filled, but for mgs_gated_*'s.  That one has to be zero-filled once, as those of
+ * mgs.h, and again after any other operator's call has had it, and before one of mgs.h has
+ * it: results may be wrong otherwise, with no error to show it.
  * Calls that share a workspace must not run concurrently.  A workspace for B sequences or
  * rows, T steps or n ids serves calls of fewer too.
  */
@@ -94,8 +94,8 @@ mgs_status mgs_gated_fwd(const mgs_gated_desc *desc, const void *x, const void *
  * Gradients of mgs_gated_fwd for L = sum_t <dy_t, y_t> + <dhT, h_T>.  With
  * G_t = dy_t + a_{t+1} G_{t+1} (dhT added at the last step), beta = sqrt(1 - a^2):
  *     dx = G beta iota,      di = G beta x iota (1 - iota),
- *     dl = G (a h_{t-1} - iota x a^2 / beta)     (of log a; 0 where a document starts
- *                                                 and where beta == 0),
+ *     dl = G (a h_{t-1} - iota x a^2 / beta)     (of log a; 0 where a document starts;
+ *                                                 without the quotient where beta == 0),
  *     dr = dl log a (1 - rho),   dlam = -rate sigmoid(lam) sum dl rho,   dh0 = a_1 G_1.
  *   dy   : (B,T,D), strides dy_stride;  dhT : (B,D) fp32 or NULL;
  *   states : the forward's;
@@ -140,10 +140,12 @@ mgs_status mgs_gated_step(const mgs_gated_desc *desc, const void *x, const void 
  *   logp : (B) fp32 out or NULL: the log of the token's share of the kept weight.
  * -inf is a forbidden token.  A row of nothing else, or with a NaN, has token -1
  * and logp -inf; where the largest is +inf, those that are share all the weight.
- * Weights and sums are fp64 (the ones that top_p compares, multiples of 2^-43 of
- * the largest weight, whose sums are exact); a weight below 2^-1000 of the largest
- * counts as none.  A call's answers are the same every time; in a batch of another size
- * they may differ where u times the sum is within fp64's rounding of a token's end.
+ * Weights and sums are fp64, in units of the largest weight.  Those that top_p compares are
+ * rounded to multiples of 2^-43, whose sums are exact; of a row's kept weights up to 4096 go
+ * into the sum that u is compared with as multiples of 2^-51, rounded down (2^-39 in all at
+ * most); a weight below 2^-1000 counts as none.  A call's answers are the same every time; in a
+ * batch of another size, or of the other type, they may differ where u times the sum is within
+ * 2^-39 of a token's end.
  * Envelope: vocab <= 2^20, B < 2^22.
  */
 typedef struct {

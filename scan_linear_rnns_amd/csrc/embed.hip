@@ -16,9 +16,9 @@
 // chunks.  All orders are fixed by the ids.
 //
 // What bounds it: bytes, where there are many.  32768 rows of 2048 of 128000, bf16: lookup
-// 39 us (220 MB reach HBM: 5.4 TB/s), the gradient 12.5 + 132 + 6, where 660 MB of rows and
-// table move at 5.0 TB/s.  4095 rows of 1000 of 5003, fp32: 8, and 5.4 + 9 + 4.5, of it some 3
-// a launch.
+// 40 us (220 MB reach HBM: 5.5 TB/s), the gradient 12.7 + 135 + 6.6, where 667 MB of rows and
+// table move at 4.9 TB/s; added to the table 59 in all (11766 rows occur).  4095 rows of 1000 of
+// 5003, fp32: 8.2, and 5.8 + 9.6 + 4.8, of it some 3 a launch; added 18.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>

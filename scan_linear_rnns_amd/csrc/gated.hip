@@ -18,10 +18,10 @@
 //
 // What bounds it: HBM, and in the bf16 backward the gates' operations beside it (35 an
 // element forward, 77 backward, the reciprocals, exponentials and roots among them a
-// quarter as fast as the others).  1 x 65536 x 1024, bf16: 115 us, 4.8 TB/s (a copy: 5.0);
-// 4 x 4096 x 4096, bf16: 111 and 219 + 6 for dlam, 5.0 and 4.7 TB/s, the VALU 59 and 68 %
-// busy; 16 x 1024 x 1000, fp32: 58 and 112 + 5, 5.2 and 4.6 TB/s.  A step of 256 x 4096: 7 us,
-// of it 3 for the launch and 3.3 for the bytes.
+// quarter as fast as the others).  Medians of kernels: 1 x 65536 x 1024, bf16: 118 us, 4.7
+// TB/s (a copy: 5.0); 4 x 4096 x 4096, bf16: 117 and 231 + 6 for dlam, 4.7 and 4.5 TB/s, the
+// VALU 60 and 69 % busy (the shortest 111 and 213); 16 x 1024 x 1000, fp32: 59 and 113 + 5, 5.1
+// and 4.6 TB/s.  A step of 256 x 4096: 7.5 us, of it 3 for the launch and 3.3 for the bytes.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -55,7 +55,8 @@ template <typename T> struct Fwd : Shape<8, 16, 4> {};
 template <typename T> struct Bwd : Shape<8, 8, 2> {};
 template <> struct Bwd<__bf16> : Shape<8, 8, 4> {};
 
-// Sequences of up to 16 steps (64 of 4 x 4096, bf16: 27 and 36 us with the shapes above)
+// Sequences of up to 16 steps (64 of 4 x 4096, bf16: 11 and 17 us, with the shapes above 27
+// and 36).  Shorter ones load and evaluate 16 too, the last live one again.
 constexpr int kShort = 16;
 struct FwdShort : Shape<1, kShort, 4> {};
 struct BwdShort : Shape<2, kShort / 2, 2> {};
@@ -160,9 +161,10 @@ template <typename T> __device__ __forceinline__ float exp_neg(float z)
 // 1 - s of s = 1 / (1 + e), without cancellation; e may be infinite
 __device__ __forceinline__ float shut(float e, float s) { return e > 0x1p100f ? 1.0f : e * s; }
 
-// a = 2^l and beta^2 = 1 - a^2 for l <= 0 (log2 a; -inf where a document starts).  1 - a loses what a rounds away
-// where a is near 1; below |l| = 1/16 (2^-20 of it) the series of 1 - 2^l takes its
-// place, four terms, off by 2^-23 at most.
+// a = 2^l and beta^2 = 1 - a^2 for l <= 0 (log2 a; -inf where a document starts).  1 - a loses
+// what a rounds away where a is near 1: 2^-20.4 of it at |l| = 1/16 with an a that is rounded
+// once, 2^-19.4 with one that is an ulp off.  Below that the series of 1 - 2^l takes its place,
+// four terms, off by 2^-22.5 at most.
 __device__ __forceinline__ void decay(float l, float &a, float &beta2)
 {
     a = ex2(l);
@@ -904,8 +906,10 @@ GatedGeom gated_geometry(const mgs_gated_desc &d, bool backward)
     g.tiles_f = std::max<int64_t>(1, (d.T + tf - 1) / tf);
     g.tiles_b = std::max<int64_t>(1, (d.T + tb - 1) / tb);
     // A unit is one hop of 1.2 us along a sequence: enough tiles that the hops do not take
-    // longer than the data, and no more, for a tile reads half a unit's pairs.  Measured, us
-    // forward / backward, bf16, with units of 1, 2, 4, 8, 22, 36, 64 tiles:
+    // longer than the data, and no more, for a tile reads half a unit's pairs.  Measured on
+    // 4096 forward tiles in all, us forward / backward, bf16, with units of 1, 2, 4, 8, 22, 36,
+    // 64 tiles (not on few tiles, where the hops are most of the time: 2048 steps of 20 groups
+    // are five of them, 18 / 31 with 8.4 / 15 of bytes):
     //   128 groups (4 x 4096 steps)  112/220 114/232 117/233 118/237 129/256 139/266 145/300
     //   16 (2 x 32768)               144/327 113/251 116/252 120/256 130/275 135/297 147/329
     //   8 (65536)                    240/514 160/358 113/270 116/260 127/286 135/309 149/346

@@ -21,12 +21,14 @@
 // (below).
 //
 // What bounds it: for few rows the chain of barriers and launches (1 row of 32000, bf16,
-// all filters 21 us, of them 3 for the launch; 37 of 50001, fp32, no filter 8.6 + 8.6, with
-// 1.5 us of bytes); for many the weights' fp64 operations and LDS atomics.  256 rows of
-// 128000, bf16, mixed settings, are 65.5 MB, 13 us at a copy's rate: 45 counted (24 until
-// all is counted, 8 for the ends and sums, 10 for the token), 120 by histograms of weights
-// and sorting (13 the largest, 42 histogram, 33 gathering, 18 the edge, 10 the token); 256 of
-// 128000, fp32, by top-p 121, without filters 52 of 26.
+// all filters 21 us, of them 3 for the launch; 37 of 50001, fp32, no filter 8.7 + 9.2, with
+// 1.5 us of bytes).  256 rows of 128000, bf16, mixed settings, are 65.5 MB, 13 us at a copy's
+// rate: 46 counted, 26 until all is counted, 10 for the ends and sums, 11 for the token.
+// Without the additions to LDS the first takes as long: a wave reads its share in four rounds
+// and waits for each (56 % of the waves' cycles), the VALU is busy half of the time, the
+// LDS a fifth.  The same in fp32, 26 us of bytes, goes by weights' fp64 operations: by top-p
+// 110 to 115 (26 the largest, 46 histogram, 29 gathering, 6 the edge, 8 the token), without
+// filters 52, mixed 133.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -1014,7 +1016,8 @@ __device__ __forceinline__ void finish(const SampleArgs &a, const Row &r, int64_
     }
     const Edge e = select(r, n, sh.ahead, want, sh);
     // the weights of the kept ones into the sums of their shares: up to 2^12 multiples
-    // of 2^-51, whose sum no order changes
+    // of 2^-51, rounded down, whose sum no order changes (each is 2^-44 or more, so that a
+    // share with a kept one has a sum)
     uint64_t *more = reinterpret_cast<uint64_t *>(sh.count);
     static_assert(sizeof(sh.count) >= sizeof(uint64_t) * kMaxSlices * kWaves, "one for each share");
     __syncthreads();

@@ -59,7 +59,8 @@ def mgs_embed_workspace_size(n, vocab, d):
 def mgs_embed_bwd(ids, dy, vocab, scale=1.0, dW=None, accumulate=False, dtype=None, ws=None, stream=None):
     """dW (vocab,d): for each id, scale times the sum of its rows of dy (...,d), zeros for ids that do not occur, in
     `dtype` (float32 by default; dW's own where it is given).  accumulate=True adds to dW and touches the rows that
-    occur only.  Sums are float32 and run in an order that the ids fix."""
+    occur only.  Sums are float32 and run in an order that the ids fix.  ws: any memory, but not the recurrence's
+    workspace, which this overwrites."""
     if stream is not None:
         return _on(stream, mgs_embed_bwd, ids, dy, vocab, scale, dW, accumulate, dtype, ws)
     import torch
@@ -132,7 +133,7 @@ def mgs_gated_fwd(x, r, i, lam, h0=None, lengths=None, reset=None, rate=8.0, y=N
     (B,D) or None (zeros) float32.  lengths (B,) int32 or None: later steps are not read, leave the state as it is and
     give zeros.  reset (B,T) bool or uint8, or None: steps that start a document, which nothing before them reaches.
     states (want_states): what mgs_gated_bwd reads.  ws: a workspace (see `workspace`), zero-filled before its first
-    use."""
+    use, and again after any other operator's call has had it."""
     if stream is not None:
         return _on(stream, mgs_gated_fwd, x, r, i, lam, h0, lengths, reset, rate, y, hT, states, ws, want_state,
                    want_states)
@@ -160,7 +161,7 @@ def mgs_gated_bwd(x, r, i, lam, dy, states, dhT=None, lengths=None, reset=None, 
                   want_dh0=True, stream=None):
     """(dx, dr, di, dlam, dh0) for L = sum(dy * y) + sum(dhT * h_T), from the forward's states; dlam (D,) and dh0 (B,D)
     (None without want_dh0) are float32.  dy (B,T,D) may be strided as x may.  out: the five outputs, dense (dh0 may be
-    None there)."""
+    None there).  ws: as mgs_gated_fwd's."""
     if stream is not None:
         return _on(stream, mgs_gated_bwd, x, r, i, lam, dy, states, dhT, lengths, reset, rate, out, ws, want_dh0)
     import torch
@@ -247,7 +248,8 @@ def mgs_sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, token=
     in order of their logits, the first top_k (0: all) stay, of these the fewest that hold top_p of their weight, of
     these the ones of at least min_p times the largest weight; the token is the first, by index, at which the kept
     weight exceeds u times its sum.  temperature 0 takes the largest.  logp: the log of the token's share of the kept
-    weight.  A row with nothing but -inf, or with a NaN, gives -1 and -inf."""
+    weight.  A row with nothing but -inf, or with a NaN, gives -1 and -inf.  Numbers count as float32 holds them (0.8 is
+    0.800000012).  ws: any memory, but not the recurrence's workspace, which this overwrites."""
     if stream is not None:
         return _on(stream, mgs_sample, logits, u, temperature, top_k, top_p, min_p, token, logp, ws)
     import torch
