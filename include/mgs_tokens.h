@@ -67,7 +67,8 @@ mgs_status mgs_embed_bwd(const void *ids, int id_bits, const void *dy, void *dW,
  *   states : (B, ceil(T / MGS_GATED_CHUNK), D) fp32 out, or NULL: the states
  *          ahead of steps 1, MGS_GATED_CHUNK + 1, ..., which the backward reads.
  * A value that is not finite reaches its own channel only, from its step to the
- * next document (an infinity may come out as NaN).
+ * next document (an infinity may come out as NaN).  A sigmoid or a 1 - a^2 below 2^-126
+ * counts as 0.
  * The workspace is zero-filled once before its first use; it serves forward and
  * backward calls of any sizes that fit it.
  * Envelope: B ceil(D / 128) ceil(T / 64) < 2^23.
@@ -142,8 +143,8 @@ mgs_status mgs_gated_step(const mgs_gated_desc *desc, const void *x, const void 
  * and logp -inf; where the largest is +inf, those that are share all the weight.
  * Weights and sums are fp64, in units of the largest weight.  Those that top_p compares are
  * rounded to multiples of 2^-43, whose sums are exact; of a row's kept weights up to 4096 go
- * into the sum that u is compared with as multiples of 2^-51, rounded down (2^-39 in all at
- * most); a weight below 2^-1000 counts as none.  A call's answers are the same every time; in a
+ * into the sum that u is compared with as multiples of 2^-51 (off by 2^-39 in all at most);
+ * a weight below 2^-1000 counts as none.  A call's answers are the same every time; in a
  * batch of another size, or of the other type, they may differ where u times the sum is within
  * 2^-39 of a token's end.
  * Envelope: vocab <= 2^20, B < 2^22.
